@@ -368,6 +368,69 @@ int convrot_guard_configure(double tol, int log_to_stderr);
 enum convrot_fault { CONVROT_FAULT_NONE = 0, CONVROT_FAULT_MISMATCH = 1, CONVROT_FAULT_KERNEL = 2 };
 int convrot_guard_inject(int device, int fault);
 
+/* ---------------------------------------------------------------- between two blocks
+ * The step between two blocks of a transformer in one launch: norm of a
+ * block's output (or of the weighted sum of the rows its experts wrote),
+ * gate, residual scale and residual sum, then the next block's norm with its
+ * scale and shift.  Per token m, in fp32:
+ *   u  = U[m]                                       (n_routes = 0)
+ *      = sum_j route_weight[m][j] * U[route_row[m][j]]      (n_routes > 0)
+ *   p  = post(u)
+ *   h' = rnd(residual_scale * h[m] + gate[r] * p)       -> h_out[m]
+ *   z  = pre(h') * (1 + scale[r]) + shift[r]
+ *   out[m] = rnd(z)                                 (group = 0)
+ *          = codes and scale of z rotated           (group = 128 or 256)
+ * with r = mod_index[m] and, for post and pre (weight 1 where NULL):
+ *   CONVROT_NORM_NONE   v
+ *   CONVROT_NORM_RMS    v * weight / sqrt(mean(v^2) + eps)
+ *   CONVROT_NORM_LAYER  (v - mean(v)) * weight / sqrt(mean((v - mean(v))^2) + eps)
+ * The norm of h' is that of its stored, rounded values; z is not rounded
+ * before it is rotated, and its codes and scale follow convrot_rotate_quant's
+ * definitions.  A row holding infinities or NaN gives what the formulas give
+ * (its codes are then unspecified); other rows are untouched by it. */
+enum convrot_norm { CONVROT_NORM_NONE = 0, CONVROT_NORM_RMS = 1, CONVROT_NORM_LAYER = 2 };
+
+typedef struct convrot_block {
+    int            io_dtype;        /* CONVROT_BF16 or CONVROT_F16: every void * below except coded out */
+    int            group;           /* 0: out holds 16-bit values; 128 or 256: codes of that rotation */
+    int            post_norm;       /* enum convrot_norm, of u */
+    int            pre_norm;        /* enum convrot_norm, of h' */
+    int            n_routes;        /* rows of u summed per token, 0 to 64; 0: u is [M, K] */
+    float          eps;             /* finite, >= 0 */
+    float          residual_scale;  /* finite */
+    int64_t        M, K;            /* K a multiple of 8 (of group where coded), at most 32768 */
+    const void    *h;               /* [M, K] stream */
+    const void    *u;               /* [M, K], or [u_rows, K] with routes; NULL: no block before, h' = h
+                                       (post_norm, gate, residual_scale and routes then have to be unset:
+                                       CONVROT_NORM_NONE, NULL, 1 and 0) */
+    int64_t        u_rows;          /* rows of u (with routes; else not read) */
+    const int32_t *route_row;       /* [M, n_routes]; a row outside [0, u_rows) is left out of the sum */
+    const float   *route_weight;    /* [M, n_routes] */
+    const void    *post_weight;     /* [K] or NULL */
+    const void    *pre_weight;      /* [K] or NULL */
+    const void    *gate;            /* [n_mod, K] each, rows mod_stride elements apart (a multiple of 8,   */
+    const void    *scale;           /* at least K): parts of one [n_mod, 3 K] projection, say; NULL: 1, 0, */
+    const void    *shift;           /* 0                                                                   */
+    int64_t        n_mod;           /* rows of gate, scale and shift; 0 if all are NULL */
+    int64_t        mod_stride;
+    const int32_t *mod_index;       /* [M] row of gate, scale and shift for each token, NULL: row 0 for all;
+                                       a token whose index is outside [0, n_mod) has gate 1, scale and shift 0 */
+    void          *h_out;           /* [M, K]; may be h itself; not written (and may be NULL) without u */
+    void          *out;             /* [M, K] 16-bit values or int8 codes; NULL: only h_out is wanted */
+    float         *out_scale;       /* [M], coded out only */
+} convrot_block;
+
+/* b is a host pointer, read during the call only.  Rows are contiguous;
+ * h, u, h_out, out, the weights, gate, scale and shift are 16-byte aligned
+ * (CONVROT_EALIGN).  Outputs must not overlap each other or any input, except
+ * h_out = h.  No workspace.  M = 0 is a no-op; no entry point of the library
+ * trains, so there is no gradient.
+ * Errors: NULL or missing pointers, sizes, eps or residual_scale out of range,
+ * nothing to do (u and out both NULL) -> CONVROT_EINVAL; io_dtype, group or
+ * norm unknown, K > 32768 -> CONVROT_EUNSUPPORTED; alignment ->
+ * CONVROT_EALIGN; launch -> CONVROT_EHIP. */
+int convrot_block_norm(const convrot_block *b, void *stream);
+
 /* ---------------------------------------------------------------- measurement aid
  * Not a step of the layer and defined by no page: it exists so that a
  * benchmark can state the rate the matrix cores sustain on this machine,

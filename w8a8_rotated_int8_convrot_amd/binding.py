@@ -55,6 +55,7 @@ SIGNATURES = {
     "convrot_guard_reset": ([_I], _I),
     "convrot_guard_configure": ([ctypes.c_double, _I], _I),
     "convrot_guard_inject": ([_I, _I], _I),
+    "convrot_block_norm": ([_P, _P], _I),
 }
 
 CONVROT_FAULT_NONE = 0
@@ -543,3 +544,122 @@ def convrot_guard_inject(device: int, fault: str) -> None:
     if fault not in codes:
         raise ValueError("convrot_guard_inject: fault is 'none', 'mismatch' or 'kernel'")
     _call("convrot_guard_inject", device, codes[fault])
+
+
+# ---------------------------------------------------------------- operators around the layer
+
+def _call_on(t, name, *args):
+    """``_call`` with t's device current (the library launches on the current one)."""
+    if t.device.index == torch.cuda.current_device():
+        return _call(name, *args)
+    with torch.cuda.device(t.device):
+        return _call(name, *args)
+
+
+def _need_on(t, dev, dtype, name, shape):
+    """A contiguous CUDA tensor of this type and shape, on dev."""
+    if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on {dev}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+
+
+class Block(ctypes.Structure):
+    """Mirror of ``convrot_block`` (include/convrot.h)."""
+    _fields_ = [("io_dtype", _I), ("group", _I), ("post_norm", _I), ("pre_norm", _I), ("n_routes", _I),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float), ("M", _I64), ("K", _I64), ("h", _P),
+                ("u", _P), ("u_rows", _I64), ("route_row", _P), ("route_weight", _P), ("post_weight", _P),
+                ("pre_weight", _P), ("gate", _P), ("scale", _P), ("shift", _P), ("n_mod", _I64), ("mod_stride", _I64),
+                ("mod_index", _P), ("h_out", _P), ("out", _P), ("out_scale", _P)]
+
+
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _norm_of(kind, name):
+    if kind not in _NORMS:
+        raise ValueError(f"{name}: 'none', 'rms' or 'layer', got {kind!r}")
+    return _NORMS[kind]
+
+
+def convrot_block_norm(h, u=None, routes=None, post_norm="none", post_weight=None, gate=None, residual_scale=1.0,
+                       pre_norm="rms", pre_weight=None, scale=None, shift=None, mod_index=None, eps=1e-6, group=0,
+                       h_out=None, out=None, out_scale=None, want_out=True):
+    """The step between two blocks (see include/convrot.h): bf16 or fp16 stream h [M, K] and
+    block output u -> (h_out, out), or (h_out, codes, scales) with a rotation group.
+
+    u is [M, K], or with ``routes`` = (int32 rows [M, t], fp32 weights [M, t]) the [P, K] rows to
+    sum for each token; without u the stream is only normed (h_out is h).  gate, scale and
+    shift are [n, K] tensors with contiguous rows and one common row stride (chunks of one
+    projection, say), each token's row named by the int32 mod_index [M] (row 0 without it).
+    h_out may be h.  want_out=False stops after h_out and returns it alone."""
+    io = _io_of(h, "h")
+    _need(h, h.dtype, "h", 2)
+    dev, dt = h.device, h.dtype
+    M, K = h.shape
+    b = Block(io, group, _norm_of(post_norm, "post_norm"), _norm_of(pre_norm, "pre_norm"), 0, eps, residual_scale, M, K,
+              h.data_ptr())
+    if routes is not None:
+        if u is None:
+            raise ValueError("convrot_block_norm: routes without u")
+        row, weight = routes
+        _need(u, dt, "u", 2)
+        if row.dim() != 2 or row.shape[1] < 1:
+            raise ValueError("convrot_block_norm: route rows are [M, t], t >= 1")
+        t = row.shape[1]
+        _need_on(u, dev, dt, "u", (u.shape[0], K))
+        _need_on(row, dev, torch.int32, "route rows", (M, t))
+        _need_on(weight, dev, torch.float32, "route weights", (M, t))
+        b.n_routes, b.u_rows, b.route_row, b.route_weight = t, u.shape[0], row.data_ptr(), weight.data_ptr()
+        # no rows at all: every route is out of range, but u still has to be there
+        b.u = u.data_ptr() or h.data_ptr()
+    elif u is not None:
+        _need_on(u, dev, dt, "u", (M, K))
+        b.u = u.data_ptr()
+    if post_weight is not None:
+        _need_on(post_weight, dev, dt, "post_weight", (K,))
+        b.post_weight = post_weight.data_ptr()
+    if pre_weight is not None:
+        _need_on(pre_weight, dev, dt, "pre_weight", (K,))
+        b.pre_weight = pre_weight.data_ptr()
+    mods = [(n, m) for n, m in (("gate", gate), ("scale", scale), ("shift", shift)) if m is not None]
+    for n, m in mods:
+        if m.dtype != dt or m.device != dev or m.dim() != 2 or m.shape[1] != K or m.shape[0] < 1 or m.stride(1) != 1:
+            raise ValueError(f"{n}: expected {dt} [n, {K}] on {dev} with contiguous rows, got {m.dtype} "
+                             f"{list(m.shape)} on {m.device}")
+        # one row has no neighbour, whatever stride it carries
+        stride = m.stride(0) if m.shape[0] > 1 else K
+        if b.n_mod and (m.shape[0] != b.n_mod or stride != b.mod_stride):
+            raise ValueError("convrot_block_norm: gate, scale and shift must have the same rows and row stride")
+        b.n_mod, b.mod_stride = m.shape[0], stride
+        setattr(b, n, m.data_ptr())
+    if mod_index is not None:
+        if not mods:
+            raise ValueError("convrot_block_norm: mod_index without gate, scale or shift")
+        _need_on(mod_index, dev, torch.int32, "mod_index", (M,))
+        b.mod_index = mod_index.data_ptr()
+    if u is None:
+        if h_out is not None:
+            raise ValueError("convrot_block_norm: h_out without u")
+        h_out = h
+    else:
+        if h_out is None:
+            h_out = torch.empty_like(h)
+        else:
+            _need_on(h_out, dev, dt, "h_out", (M, K))
+        b.h_out = h_out.data_ptr()
+    if want_out:
+        if out is None:
+            out = torch.empty((M, K), dtype=torch.int8 if group else dt, device=dev)
+        else:
+            _need_on(out, dev, torch.int8 if group else dt, "out", (M, K))
+        b.out = out.data_ptr()
+        if group:
+            if out_scale is None:
+                out_scale = torch.empty(M, dtype=torch.float32, device=dev)
+            else:
+                _need_on(out_scale, dev, torch.float32, "out_scale", (M,))
+            b.out_scale = out_scale.data_ptr()
+    _call_on(h, "convrot_block_norm", ctypes.byref(b), _stream(h))
+    if not want_out:
+        return h_out
+    return (h_out, out, out_scale) if group else (h_out, out)

@@ -5,14 +5,17 @@ The library is placed next to this file, where ``binding`` looks for it.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libconvrot.so")
-SOURCES = ("convrot_api.hip", "rotate_quant.hip", "gemm_i8.hip", "default_path.hip", "mfma_probe.hip")
+SOURCES = ("convrot_api.hip", "rotate_quant.hip", "gemm_i8.hip", "default_path.hip", "block_norm.hip",
+           "operators_api.hip", "mfma_probe.hip")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -20,7 +23,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # every float operation is one IEEE operation in the written order: the
     # rotation must reproduce the same sums bit for bit, and fused multiply-adds
     # are written out explicitly where wanted
@@ -34,22 +36,31 @@ FLAGS = [
     "-mllvm", "-disable-promote-alloca-to-lds",
     "-Wall",
 ]
+LINK_FLAGS = ["--offload-arch=gfx950", "-fPIC", "-shared"]
 
 
 def build(verbose: bool = False) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, *FLAGS, "-o", tmp, *srcs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    # the host pass warns that it does not know the packed-fp32 feature
-    noise = "is not a recognized feature for this target"
-    msgs = [l for l in (res.stdout + res.stderr).splitlines() if noise not in l]
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
-    if verbose and msgs:
-        print("\n".join(msgs), flush=True)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        # the host pass warns that it does not know the packed-fp32 feature
+        noise = "is not a recognized feature for this target"
+        msgs = [l for l in (res.stdout + res.stderr).splitlines() if noise not in l]
+        if res.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
+        if verbose and msgs:
+            print("\n".join(msgs), flush=True)
+
+    # the sources side by side, then one link
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, s.replace(".hip", ".o")) for s in SOURCES]
+        cmds = [[HIPCC, *FLAGS, "-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objs)]
+        with concurrent.futures.ThreadPoolExecutor(min(len(SOURCES), 8)) as pool:
+            list(pool.map(run, cmds))
+        run([HIPCC, *LINK_FLAGS, "-o", tmp, *objs])
     os.replace(tmp, LIB)
     return LIB
 

@@ -2,9 +2,10 @@
 // the C ABI).  Kernels live in rotate_quant.hip (rotation + quantization, and
 // the default path's weight unpacking), gemm_i8.hip (the int8 GEMM with its
 // epilogues, and the default path's bf16/fp16 product on the same tiles),
-// default_path.hip (the guarded layer's check) and mfma_probe.hip (two
-// measurement aids); argument checking, dispatch and the guard state live in
-// convrot_api.hip.
+// default_path.hip (the guarded layer's check), block_norm.hip (the step
+// between two blocks) and mfma_probe.hip (two measurement aids); argument
+// checking, dispatch and the guard state live in convrot_api.hip, the entry
+// points of the operators around the layer in operators_api.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -85,6 +86,32 @@ hipError_t launch_compare_rows(const uint16_t* y, const uint16_t* ydef, bool f16
 __host__ __device__ inline int64_t sample_row(int i, int R, int64_t M) {
   return R > 1 ? static_cast<int64_t>(i) * (M - 1) / (R - 1) : 0;
 }
+
+// ---------------------------------------------------------------- between two blocks
+// (block_norm.hip)
+
+constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;
+// The longest row the kernel holds in its registers (1024 threads of four
+// 8-element chunks).
+constexpr int64_t kMaxNormK = 32768;
+
+// Arguments as in convrot_block_norm (16-bit values behind void pointers); a
+// null u leaves the stream as it is, a null out ends after h_out.
+struct BlockNorm {
+  int K, n_routes, post_norm, pre_norm;
+  const void *h, *u;
+  const int32_t* route_row;
+  const float* route_weight;
+  int64_t u_rows;
+  const void *post_weight, *pre_weight, *gate, *scale, *shift;
+  const int32_t* mod_index;
+  int64_t n_mod, mod_stride;
+  float residual_scale, eps;
+  void *h_out, *out;
+  float* out_scale;
+};
+// group: 128 or 256 for codes, 0 for 16-bit values.
+hipError_t launch_block_norm(const BlockNorm& p, int64_t M, int group, bool f16, hipStream_t stream);
 
 // ---------------------------------------------------------------- measurement aid
 

@@ -1,0 +1,120 @@
+// rotate_device.hpp -- device code shared by the kernels that rotate rows held
+// in registers (rotate_quant.hip, block_norm.hip): 16-bit loads widened to
+// fp32, the butterfly of one 8-element chunk of a g-group spread over g/8
+// lanes, and the int8 code of a value.
+#pragma once
+
+#include "convrot_internal.hpp"
+
+namespace convrot {
+namespace {
+
+// The float nearest to 1/sqrt(g): 2^-3.5 rounds to 0x3db504f3 for g = 128;
+// 2^-4 is exact for g = 256.
+template <int G> struct RotScale;
+template <> struct RotScale<128> { static constexpr float value = 0x1.6a09e6p-4f; };
+template <> struct RotScale<256> { static constexpr float value = 0x1p-4f; };
+
+__device__ inline float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ inline float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// IEEE binary16 -> fp32 is exact (v_cvt_f32_f16)
+__device__ inline float f16_lo(uint32_t w) {
+  return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w)));
+}
+__device__ inline float f16_hi(uint32_t w) {
+  return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w >> 16)));
+}
+// the two 16-bit input formats: bf16 bits (uint16_t) and IEEE binary16 (_Float16)
+template <typename In> __device__ inline float in_lo(uint32_t w);
+template <typename In> __device__ inline float in_hi(uint32_t w);
+template <> __device__ inline float in_lo<uint16_t>(uint32_t w) { return bf16_lo(w); }
+template <> __device__ inline float in_hi<uint16_t>(uint32_t w) { return bf16_hi(w); }
+template <> __device__ inline float in_lo<_Float16>(uint32_t w) { return f16_lo(w); }
+template <> __device__ inline float in_hi<_Float16>(uint32_t w) { return f16_hi(w); }
+
+// Load 8 consecutive inputs as fp32.
+template <typename In16>
+__device__ inline void load8_16(const In16* p, float (&v)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  v[0] = in_lo<In16>(w.x); v[1] = in_hi<In16>(w.x);
+  v[2] = in_lo<In16>(w.y); v[3] = in_hi<In16>(w.y);
+  v[4] = in_lo<In16>(w.z); v[5] = in_hi<In16>(w.z);
+  v[6] = in_lo<In16>(w.w); v[7] = in_hi<In16>(w.w);
+}
+__device__ inline void load8(const uint16_t* p, float (&v)[8]) { load8_16(p, v); }
+__device__ inline void load8(const _Float16* p, float (&v)[8]) { load8_16(p, v); }
+__device__ inline void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  const float4 b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// v of lane (this lane ^ T).  Inside a 16-lane row DPP moves do it: xor 1
+// and xor 2 are quad permutations, xor 4 is the quad reversal (xor 3)
+// followed by the half-row mirror (xor 7), xor 8 is a rotation of the row by
+// 8; wider distances go through ds_bpermute.
+template <int T>
+__device__ inline float lane_xor(float v) {
+  const int b = __float_as_int(v);
+  if constexpr (T == 1) return __int_as_float(__builtin_amdgcn_mov_dpp(b, 0xB1, 0xF, 0xF, true));
+  else if constexpr (T == 2) return __int_as_float(__builtin_amdgcn_mov_dpp(b, 0x4E, 0xF, 0xF, true));
+  else if constexpr (T == 4)
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(b, 0x1B, 0xF, 0xF, true), 0x141, 0xF, 0xF, true));
+  else if constexpr (T == 8) return __int_as_float(__builtin_amdgcn_mov_dpp(b, 0x128, 0xF, 0xF, true));
+  else return __shfl_xor(v, T);
+}
+
+// One butterfly stage between lanes T apart: the lower element keeps
+// RN(a + b), the upper RN(a - b) (a = lower), each as RN(own * sgn + partner)
+// with sgn = -1 on the upper lane.
+template <int T>
+__device__ inline void lane_stage(float (&v)[8], int lane_in_group) {
+  const float sgn = (lane_in_group & T) != 0 ? -1.0f : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], sgn, lane_xor<T>(v[i]));
+}
+
+// Butterfly of one 8-element chunk that is part of a g-group spread over g/8
+// lanes; `lane_in_group` is this lane's index inside the group.
+template <int G>
+__device__ inline void rotate_chunk(float (&v)[8], int lane_in_group) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i & h) == 0) {
+        const float a = v[i], b = v[i + h];
+        v[i] = a + b;
+        v[i + h] = a - b;
+      }
+    }
+  }
+  lane_stage<1>(v, lane_in_group);
+  lane_stage<2>(v, lane_in_group);
+  lane_stage<4>(v, lane_in_group);
+  lane_stage<8>(v, lane_in_group);
+  if constexpr (G == 256) lane_stage<16>(v, lane_in_group);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = v[i] * RotScale<G>::value;
+}
+
+__device__ inline int quant_code(float v, float s) {
+  float r = __builtin_rintf(v / s);
+  r = fminf(fmaxf(r, -127.0f), 127.0f);
+  return static_cast<int>(r);
+}
+
+__device__ inline uint2 pack8(const float (&v)[8], float s) {
+  uint32_t lo = 0, hi = 0;
+  if (s != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lo |= (static_cast<uint32_t>(quant_code(v[i], s)) & 0xffu) << (8 * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) hi |= (static_cast<uint32_t>(quant_code(v[4 + i], s)) & 0xffu) << (8 * i);
+  }
+  return make_uint2(lo, hi);
+}
+
+}  // namespace
+}  // namespace convrot
