@@ -431,6 +431,46 @@ typedef struct convrot_block {
  * CONVROT_EALIGN; launch -> CONVROT_EHIP. */
 int convrot_block_norm(const convrot_block *b, void *stream);
 
+/* ---------------------------------------------------------------- experts
+ * The layer grouped by expert: a router has sent each token to some of
+ * n_experts layers of one shape, and the rows of one expert are neighbours.
+ *   for expert e and p in [offsets[e], offsets[e+1]):
+ *     y[p] = the layer of expert e on token m,  m = rows[p]  (m = p without rows)
+ * with convrot_linear_ex's definitions (codes and scale of token m, the
+ * product, bias and rounding), so y[p] has the bytes convrot_linear_ex gives
+ * for that token and that expert's weight.  Each token is coded once, however
+ * many experts it goes to. */
+
+/* Workspace bytes convrot_grouped_linear needs: codes and scales of M tokens.
+ * 0 for a bad size. */
+size_t convrot_grouped_workspace(int64_t M, int64_t K);
+
+/*   x        [M, K] activation in io_dtype (CONVROT_BF16 or CONVROT_F16).
+ *   wq       [n_experts, N, K] int8, each as written by convrot_prepare_weight_ex
+ *            with this group.
+ *   w_scale  [n_experts] (CONVROT_SCALE_TENSOR) or [n_experts, N]
+ *            (CONVROT_SCALE_ROW).
+ *   bias     [n_experts, N] in io_dtype or NULL.
+ *   offsets  DEVICE int32 [n_experts + 1], ascending; an expert may have no
+ *            rows.  Values are clamped to [0, P] and to the value before.
+ *   rows     DEVICE int32 [P], the token of each row, any order, a token as
+ *            often as wanted; NULL: row p is token p, and P has to be M.
+ *   y        [P, N] in io_dtype.  Rows outside [offsets[0], offsets[n_experts])
+ *            and rows whose token is outside [0, M) are left as they were.
+ *            Must not overlap the inputs.
+ *   workspace at least convrot_grouped_workspace(M, K) bytes.
+ * The offsets are read by the kernel only: the call does not wait for the
+ * router's, and one captured into a graph takes whatever they then hold.
+ * N >= 1, 1 <= n_experts <= 65536, M and P in [0, 2^30], and at most 2^31
+ * workgroups of 16 rows and 16 channels, one more of them for each expert
+ * (CONVROT_EINVAL).  P = 0 is a no-op.  x, wq, y and workspace are 16-byte
+ * aligned.  Other errors as convrot_linear_ex.  Two launches: rotate + quant
+ * of the M tokens, then the product. */
+int convrot_grouped_linear(const void *x, int io_dtype, int64_t M, int64_t K, const int8_t *wq,
+                           const float *w_scale, int scale_mode, int64_t n_experts, int64_t N, int group,
+                           const void *bias, const int32_t *offsets, const int32_t *rows, int64_t P,
+                           void *y, void *workspace, size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------- measurement aid
  * Not a step of the layer and defined by no page: it exists so that a
  * benchmark can state the rate the matrix cores sustain on this machine,

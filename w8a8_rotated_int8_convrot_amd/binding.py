@@ -56,6 +56,8 @@ SIGNATURES = {
     "convrot_guard_configure": ([ctypes.c_double, _I], _I),
     "convrot_guard_inject": ([_I, _I], _I),
     "convrot_block_norm": ([_P, _P], _I),
+    "convrot_grouped_workspace": ([_I64, _I64], _SZ),
+    "convrot_grouped_linear": ([_P, _I, _I64, _I64, _P, _P, _I, _I64, _I64, _I, _P, _P, _P, _I64, _P, _P, _SZ, _P], _I),
 }
 
 CONVROT_FAULT_NONE = 0
@@ -663,3 +665,49 @@ def convrot_block_norm(h, u=None, routes=None, post_norm="none", post_weight=Non
     if not want_out:
         return h_out
     return (h_out, out, out_scale) if group else (h_out, out)
+
+
+def convrot_grouped_workspace(M: int, K: int) -> int:
+    return lib().convrot_grouped_workspace(M, K)
+
+
+def convrot_grouped_linear(x, wq, w_scale, group, offsets, rows=None, bias=None, out=None,
+                           workspace=None) -> torch.Tensor:
+    """The layer grouped by expert (see include/convrot.h): bf16 or fp16 x [M, K], int8 wq
+    [E, N, K] with fp32 scales [E] or [E, N], optional bias [E, N] -> y [P, N].
+
+    offsets: int32 [E + 1] on the GPU, expert e's rows of y being offsets[e] to
+    offsets[e + 1]; rows: int32 [P] on the GPU, the token of each row (row p is token p
+    without it).  Rows of no expert, and rows whose token is outside x, are left as they
+    were (unset in an ``out`` allocated here)."""
+    who = "convrot_grouped_linear"
+    io = _io_of(x, "x")
+    _need(x, x.dtype, "x", 2)
+    dev, dt = x.device, x.dtype
+    M, K = x.shape
+    if wq.dim() != 3:
+        raise ValueError(f"wq: expected 3 dimensions, got {wq.dim()}")
+    E, N = wq.shape[:2]
+    _need_on(wq, dev, torch.int8, "wq", (E, N, K))
+    per_row = w_scale.dim() == 2
+    _need_on(w_scale, dev, torch.float32, "w_scale", (E, N) if per_row else (E,))
+    _need_on(offsets, dev, torch.int32, "offsets", (E + 1,))
+    P = M
+    if rows is not None:
+        _need(rows, torch.int32, "rows", 1)
+        P = rows.shape[0]
+        _need_on(rows, dev, torch.int32, "rows", (P,))
+    if bias is not None:
+        _need_on(bias, dev, dt, "bias", (E, N))
+    if out is None:
+        out = torch.empty((P, N), dtype=dt, device=dev)
+    else:
+        _need_on(out, dev, dt, "out", (P, N))
+    if workspace is None:
+        workspace = torch.empty(max(convrot_grouped_workspace(M, K), 1), dtype=torch.uint8, device=dev)
+    else:
+        _need_on(workspace, dev, torch.uint8, "workspace", (workspace.numel(),))
+    _call_on(x, who, _ptr(x), io, M, K, _ptr(wq), _ptr(w_scale), CONVROT_SCALE_ROW if per_row else CONVROT_SCALE_TENSOR,
+             E, N, group, _ptr(bias), _ptr(offsets), _ptr(rows), P, _ptr(out), _ptr(workspace), workspace.numel(),
+             _stream(x))
+    return out

@@ -1,7 +1,8 @@
 // convrot_internal.hpp -- shared declarations of the HIP library (not part of
 // the C ABI).  Kernels live in rotate_quant.hip (rotation + quantization, and
-// the default path's weight unpacking), gemm_i8.hip (the int8 GEMM with its
+// the default path's weight unpacking), gemm_core.hpp (the int8 GEMM with its
 // epilogues, and the default path's bf16/fp16 product on the same tiles),
+// launched by gemm_i8.hip and, per expert, by gemm_grouped.hip,
 // default_path.hip (the guarded layer's check), block_norm.hip (the step
 // between two blocks) and mfma_probe.hip (two measurement aids); argument
 // checking, dispatch and the guard state live in convrot_api.hip, the entry
@@ -69,6 +70,17 @@ hipError_t launch_gemm_i32(const int8_t* xq, const int8_t* wq, int32_t* acc,
 // operands x [M, K] and wu [N, K] with an fp32 accumulator.  K % 64 == 0.
 hipError_t launch_gemm_default(const uint16_t* x, const uint16_t* wu, const uint16_t* bias, uint16_t* y,
                                bool f16, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+// The product per expert (gemm_grouped.hip): rows [offsets[e], offsets[e+1])
+// of y [P, N] are those of expert e (wq [experts, N, K], w_scale [experts] or
+// with row_scale [experts, N], bias [experts, N] or null), row p made from row
+// rows[p] of xq [x_rows, K] (null: p).  offsets and rows are device memory.
+// hipErrorInvalidConfiguration where the grid could pass kMaxGroupedTiles.
+constexpr int64_t kMaxGroupedTiles = (int64_t{1} << 31) - 1;
+hipError_t launch_gemm_grouped(const int8_t* xq, const float* x_scale, int64_t x_rows, const int8_t* wq,
+                               const float* w_scale, bool row_scale, const uint16_t* bias, uint16_t* y, bool f16,
+                               const int32_t* offsets, const int32_t* rows, int64_t experts, int64_t P, int64_t N,
+                               int64_t K, hipStream_t stream);
 
 // ---------------------------------------------------------------- guard check
 // (default_path.hip)

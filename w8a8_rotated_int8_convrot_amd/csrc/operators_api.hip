@@ -13,12 +13,20 @@ namespace {
 using namespace convrot;
 
 constexpr int kMaxRoutes = 64;
+constexpr int64_t kMaxExperts = 65536;
 
 int check_norm(int kind, const char* what, const char* who) {
   if (kind != CONVROT_NORM_NONE && kind != CONVROT_NORM_RMS && kind != CONVROT_NORM_LAYER)
     return fail(CONVROT_EUNSUPPORTED, "%s: %s %d (CONVROT_NORM_NONE, CONVROT_NORM_RMS or CONVROT_NORM_LAYER)", who,
                 what, kind);
   return CONVROT_OK;
+}
+
+hipError_t rotate_quant(const void* x, bool f16, int64_t M, int64_t K, int group, int8_t* xq, float* xs,
+                        hipStream_t stream) {
+  const auto* xb = static_cast<const uint16_t*>(x);
+  return f16 ? launch_rotate_quant_f16(xb, M, K, group, xq, xs, stream)
+             : launch_rotate_quant(xb, M, K, group, xq, xs, stream);
 }
 
 }  // namespace
@@ -73,6 +81,50 @@ int convrot_block_norm(const convrot_block* b, void* stream) {
                     mods ? b->mod_index : nullptr, b->n_mod, b->mod_stride, b->residual_scale, b->eps, b->h_out, b->out,
                     b->out_scale};
   return hip_status(launch_block_norm(p, b->M, b->group, b->io_dtype == CONVROT_F16, static_cast<hipStream_t>(stream)),
+                    who);
+}
+
+size_t convrot_grouped_workspace(int64_t M, int64_t K) {
+  if (M < 0 || K < 1) return 0;
+  return round_up(static_cast<size_t>(M) * static_cast<size_t>(K), 256) + static_cast<size_t>(M) * 4;
+}
+
+int convrot_grouped_linear(const void* x, int io_dtype, int64_t M, int64_t K, const int8_t* wq, const float* w_scale,
+                           int scale_mode, int64_t n_experts, int64_t N, int group, const void* bias,
+                           const int32_t* offsets, const int32_t* rows, int64_t P, void* y, void* workspace,
+                           size_t ws_bytes, void* stream) {
+  const char* who = "convrot_grouped_linear";
+  if (int rc = check_group(group, K, who)) return rc;
+  if (int rc = check_mn(M, N, who)) return rc;
+  if (int rc = check_io(io_dtype, who)) return rc;
+  if (int rc = check_scale_mode(scale_mode, who)) return rc;
+  if (n_experts < 1 || n_experts > kMaxExperts)
+    return fail(CONVROT_EINVAL, "%s: n_experts=%lld must be in [1, %lld]", who, static_cast<long long>(n_experts),
+                static_cast<long long>(kMaxExperts));
+  if (P < 0 || P > (int64_t(1) << 30))
+    return fail(CONVROT_EINVAL, "%s: P=%lld must be in [0, 2^30]", who, static_cast<long long>(P));
+  if (!rows && P != M)
+    return fail(CONVROT_EINVAL, "%s: without rows P=%lld has to be M=%lld", who, static_cast<long long>(P),
+                static_cast<long long>(M));
+  if (P == 0) return ok();
+  if (M == 0) return fail(CONVROT_EINVAL, "%s: P=%lld rows of no tokens", who, static_cast<long long>(P));
+  if ((P / 16 + n_experts) * ((N + 15) / 16) >= (int64_t(1) << 31))
+    return fail(CONVROT_EINVAL, "%s: P=%lld, n_experts=%lld and N=%lld make too many tiles", who,
+                static_cast<long long>(P), static_cast<long long>(n_experts), static_cast<long long>(N));
+  if (!x || !wq || !w_scale || !offsets || !y) return fail(CONVROT_EINVAL, "%s: NULL pointer", who);
+  if (!aligned16(x) || !aligned16(wq) || !aligned16(y) || (workspace && !aligned16(workspace)))
+    return fail(CONVROT_EALIGN, "%s: x, wq, y and workspace must be 16-byte aligned", who);
+  if (!workspace || ws_bytes < convrot_grouped_workspace(M, K))
+    return fail(CONVROT_EWORKSPACE, "%s: workspace of %zu bytes needed (convrot_grouped_workspace)", who,
+                convrot_grouped_workspace(M, K));
+  auto* xq = static_cast<int8_t*>(workspace);
+  auto* xs = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(static_cast<size_t>(M) * K, 256));
+  const bool f16 = io_dtype == CONVROT_F16;
+  auto s = static_cast<hipStream_t>(stream);
+  if (hipError_t e = rotate_quant(x, f16, M, K, group, xq, xs, s); e != hipSuccess) return hip_status(e, who);
+  return hip_status(launch_gemm_grouped(xq, xs, M, wq, w_scale, scale_mode == CONVROT_SCALE_ROW,
+                                        static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), f16, offsets,
+                                        rows, n_experts, P, N, K, s),
                     who);
 }
 
