@@ -471,6 +471,47 @@ int convrot_grouped_linear(const void *x, int io_dtype, int64_t M, int64_t K, co
                            const void *bias, const int32_t *offsets, const int32_t *rows, int64_t P,
                            void *y, void *workspace, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------- low-rank adapters
+ * The layer with the low-rank adapters of many requests beside it (page "int8
+ * Compute": adapters run beside the int8 layer in the compute precision and
+ * are never coded).  Token m, with adapter a = index[m] of rank
+ * offsets[a+1] - offsets[a]:
+ *   t_m  = rnd(lora_scale[a] * A_a x_m)        A_a: rows offsets[a] .. of lora_a [R, K]
+ *   y[m] = rnd(l_m + t_m B_a)                  B_a: the same rows of lora_b [R, N]
+ * with l_m the layer's fp32 result (convrot_linear_ex's before its rounding)
+ * and the products summed in fp32; rnd: to io_dtype.  x_m enters A_a x_m as it
+ * is, neither rotated nor coded.  A token whose index is outside
+ * [0, n_adapters) has no adapter and gets convrot_linear_ex's bytes, and a
+ * token's result does not depend on the other tokens' adapters.  A given shape
+ * repeats its bytes from call to call. */
+
+/* Workspace bytes convrot_linear_lora needs: convrot_linear's for its slices
+ * of min(M, 2N) tokens and their t_m.  0 for a bad size. */
+size_t convrot_lora_workspace(int64_t M, int64_t K, int64_t N, int64_t max_rank);
+
+/* Arguments as convrot_linear_ex, and
+ *   lora_a      [R, K], lora_b [R, N] in io_dtype: the adapters' rows one after
+ *               another, both rank-major, so that an adapter is a range of rows
+ *               of both.
+ *   R           their rows (>= 0; 0: no adapter has any).
+ *   lora_scale  [n_adapters] fp32.
+ *   offsets     DEVICE int32 [n_adapters + 1], ascending (clamped to [0, R] and
+ *               to the value before); an adapter may have rank 0.
+ *   n_adapters  1 to 65536.
+ *   max_rank    1 to 512: the largest rank; rows of an adapter past it are
+ *               not used.
+ *   index       DEVICE int32 [M], any order (neighbours sharing an adapter are
+ *               faster).
+ * lora_a is 16-byte aligned (CONVROT_EALIGN), offsets, index and lora_scale
+ * are read by the kernels only.  Errors as convrot_linear_ex, except that the
+ * workspace has to hold convrot_lora_workspace bytes.  Per slice: rotate +
+ * quant, the adapters' first product, the layer's product with the second. */
+int convrot_linear_lora(const void *x, int io_dtype, int64_t M, int64_t K, const int8_t *wq,
+                        const float *w_scale, int scale_mode, int64_t N, int group, const void *bias,
+                        const void *lora_a, const void *lora_b, int64_t R, const float *lora_scale,
+                        const int32_t *offsets, int64_t n_adapters, int64_t max_rank, const int32_t *index,
+                        void *y, void *workspace, size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------- measurement aid
  * Not a step of the layer and defined by no page: it exists so that a
  * benchmark can state the rate the matrix cores sustain on this machine,

@@ -56,6 +56,9 @@ SIGNATURES = {
     "convrot_guard_configure": ([ctypes.c_double, _I], _I),
     "convrot_guard_inject": ([_I, _I], _I),
     "convrot_block_norm": ([_P, _P], _I),
+    "convrot_lora_workspace": ([_I64, _I64, _I64, _I64], _SZ),
+    "convrot_linear_lora": ([_P, _I, _I64, _I64, _P, _P, _I, _I64, _I, _P, _P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P,
+                             _SZ, _P], _I),
     "convrot_grouped_workspace": ([_I64, _I64], _SZ),
     "convrot_grouped_linear": ([_P, _I, _I64, _I64, _P, _P, _I, _I64, _I64, _I, _P, _P, _P, _I64, _P, _P, _SZ, _P], _I),
 }
@@ -711,3 +714,41 @@ def convrot_grouped_linear(x, wq, w_scale, group, offsets, rows=None, bias=None,
              E, N, group, _ptr(bias), _ptr(offsets), _ptr(rows), P, _ptr(out), _ptr(workspace), workspace.numel(),
              _stream(x))
     return out
+
+
+def convrot_lora_workspace(M: int, K: int, N: int, max_rank: int) -> int:
+    return lib().convrot_lora_workspace(M, K, N, max_rank)
+
+
+def convrot_linear_lora(x, wq, w_scale, group, lora_a, lora_b, lora_scale, offsets, index, max_rank, bias=None,
+                        out=None, workspace=None) -> torch.Tensor:
+    """The layer with the low-rank adapters of many requests beside it (see
+    include/convrot.h): bf16 or fp16 x [M, K], int8 wq [N, K] with 1 or N scales -> y [M, N].
+
+    lora_a [R, K] and lora_b [R, N] in x's dtype hold the adapters' rows one after
+    another (an adapter's B is stored rank-major, the transpose of an nn.Linear
+    weight), adapter a being rows offsets[a] to offsets[a + 1] of both; offsets int32
+    [n + 1], lora_scale fp32 [n] and index int32 [M] (each token's adapter, outside
+    [0, n) for none) are on the GPU; max_rank is the largest rank."""
+    who = "convrot_linear_lora"
+    io, M, K, N, mode, y = _layer_args(who, x, wq, w_scale, bias, out)
+    dev, dt = x.device, x.dtype
+    R = lora_a.shape[0]
+    _need_on(lora_a, dev, dt, "lora_a", (R, K))
+    _need_on(lora_b, dev, dt, "lora_b", (R, N))
+    _need(lora_scale, torch.float32, "lora_scale", 1)
+    n = lora_scale.shape[0]
+    _need_on(lora_scale, dev, torch.float32, "lora_scale", (n,))
+    _need_on(offsets, dev, torch.int32, "offsets", (n + 1,))
+    _need_on(index, dev, torch.int32, "index", (M,))
+    for name, o in (("wq", wq), ("w_scale", w_scale), ("bias", bias), ("out", y)):
+        if o is not None and o.device != dev:
+            raise ValueError(f"{name}: expected a tensor on {dev}, got one on {o.device}")
+    if workspace is None:
+        workspace = torch.empty(max(convrot_lora_workspace(M, K, N, max_rank), 1), dtype=torch.uint8, device=dev)
+    else:
+        _need_on(workspace, dev, torch.uint8, "workspace", (workspace.numel(),))
+    _call_on(x, who, _ptr(x), io, M, K, _ptr(wq), _ptr(w_scale), mode, N, group, _ptr(bias), _ptr(lora_a), _ptr(lora_b),
+             R, _ptr(lora_scale), _ptr(offsets), n, max_rank, _ptr(index), _ptr(y), _ptr(workspace),
+             workspace.numel(), _stream(x))
+    return y

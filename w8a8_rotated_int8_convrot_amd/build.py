@@ -14,8 +14,8 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libconvrot.so")
-SOURCES = ("convrot_api.hip", "rotate_quant.hip", "gemm_i8.hip", "gemm_grouped.hip", "default_path.hip", "block_norm.hip",
-           "operators_api.hip", "mfma_probe.hip")
+SOURCES = ("convrot_api.hip", "rotate_quant.hip", "gemm_i8.hip", "gemm_grouped.hip", "gemm_lora.hip", "lora.hip",
+           "default_path.hip", "block_norm.hip", "operators_api.hip", "mfma_probe.hip")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -2,7 +2,8 @@
 // the C ABI).  Kernels live in rotate_quant.hip (rotation + quantization, and
 // the default path's weight unpacking), gemm_core.hpp (the int8 GEMM with its
 // epilogues, and the default path's bf16/fp16 product on the same tiles),
-// launched by gemm_i8.hip and, per expert, by gemm_grouped.hip,
+// launched by gemm_i8.hip, per expert by gemm_grouped.hip and with low-rank
+// adapters by gemm_lora.hip, lora.hip (the adapters' first product),
 // default_path.hip (the guarded layer's check), block_norm.hip (the step
 // between two blocks) and mfma_probe.hip (two measurement aids); argument
 // checking, dispatch and the guard state live in convrot_api.hip, the entry
@@ -81,6 +82,22 @@ hipError_t launch_gemm_grouped(const int8_t* xq, const float* x_scale, int64_t x
                                const float* w_scale, bool row_scale, const uint16_t* bias, uint16_t* y, bool f16,
                                const int32_t* offsets, const int32_t* rows, int64_t experts, int64_t P, int64_t N,
                                int64_t K, hipStream_t stream);
+
+// The first product of low-rank adapters (lora.hip): t [M, t_stride] in the io
+// type, t[m][r] = scale[a] * (row offsets[a] + r of a_rows [ranks, K]) . x[m]
+// with a = index[m]; zero from the adapter's rank on, unset for a token whose
+// index is outside [0, adapters).  t_stride: max_rank rounded up to 32.
+hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, bool f16, const uint16_t* a, int64_t ranks,
+                            const float* scale, const int32_t* offsets, int64_t adapters, const int32_t* index,
+                            int64_t max_rank, uint16_t* t, int64_t t_stride, hipStream_t stream);
+
+// The layer's product with the adapters' second one, t . b (b [ranks, N]),
+// added before the output is rounded (gemm_lora.hip).
+hipError_t launch_gemm_lora(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+                            bool row_scale, const uint16_t* bias, uint16_t* y, bool f16, int64_t M, int64_t N, int64_t K,
+                            const uint16_t* t, int64_t t_stride, const uint16_t* b, int64_t ranks,
+                            const int32_t* offsets, int64_t adapters, const int32_t* index, int64_t max_rank,
+                            hipStream_t stream);
 
 // ---------------------------------------------------------------- guard check
 // (default_path.hip)

@@ -330,6 +330,97 @@ struct Grouped {
   }
 };
 
+// Low-rank adapters beside the product: token m with adapter a = index[m] gets
+//   y[m][n] += sum_r t[m][r] * b[offsets[a] + r][n],    r < rank of a
+// before the output is rounded; t holds the adapter's first product, already
+// scaled (lora.hip).  Both factors are in the io type, the sum in fp32.
+struct Lora {
+  const uint16_t* t;        // [M, t_stride], zero from the token's rank on
+  const uint16_t* b;        // [ranks, N]
+  const int32_t* offsets;   // [adapters + 1]
+  const int32_t* index;     // [M]
+  int adapters, ranks, max_rank, t_stride;
+  // rows [lo, lo + rank) of adapter a, inside [0, ranks)
+  __device__ void range(int a, int& lo, int& rank) const {
+    lo = min(max(offsets[a], 0), ranks);
+    rank = min(min(max(offsets[a + 1], lo), ranks) - lo, max_rank);
+  }
+};
+
+// Adds the adapters' part to a wave's TN x TM result blocks, which hold the
+// layer's fp32 results by their bits.  n_first, m_first: the wave's corner.
+// One pass per adapter met among the wave's tokens (neighbours in a batch
+// mostly share theirs), each on the matrix cores: channels x ranks times ranks
+// x tokens, in the layout of the layer's own blocks.  A lane takes the pass's
+// sum only if its token has that adapter: a product with zero instead would
+// carry one adapter's infinities into the other tokens.
+template <int MF, int TN, int TM, bool F16, class AccT>
+__device__ inline void lora_add(AccT (&acc)[TN][TM], const Lora& lo, int lane, int n_first, int m_first, int M,
+                                int N) {
+  constexpr int kRanks = MF == 16 ? 32 : 16;          // ranks of one MFMA
+  constexpr int OP = F16 ? kOpF16 : kOpBf16;
+  using sum_t = typename Acc<MF, OP>::type;
+  const int r = lane & (MF - 1), k8 = lane / MF * 8;
+  int own[TM];
+  const uint16_t* t_row[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int m = m_first + j * MF + r;
+    const int a = m < M ? lo.index[m] : -1;
+    own[j] = a >= 0 && a < lo.adapters ? a : -1;
+    t_row[j] = lo.t + static_cast<int64_t>(min(m, M - 1)) * lo.t_stride + k8;
+  }
+  int left[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) left[j] = own[j];
+  for (;;) {
+    int a = -1;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const uint64_t some = __ballot(left[j] >= 0);
+      if (a < 0 && some != 0) a = __builtin_amdgcn_readlane(left[j], __builtin_ctzll(some));
+    }
+    if (a < 0) return;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) left[j] = left[j] == a ? -1 : left[j];
+    int row0, rank;
+    lo.range(a, row0, rank);
+    if (rank == 0) continue;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const int n = min(n_first + i * MF + r, N - 1);
+      sum_t d[TM];
+#pragma unroll
+      for (int j = 0; j < TM; ++j) d[j] = sum_t{};
+      for (int k = 0; k < rank; k += kRanks) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t h[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int rr = k + k8 + 2 * q + e;
+            const uint32_t v = lo.b[static_cast<int64_t>(row0 + min(rr, rank - 1)) * N + n];
+            h[e] = rr < rank ? v : 0u;
+          }
+          w[q] = h[0] | (h[1] << 16);
+        }
+        const v4i bf = {static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
+#pragma unroll
+        for (int j = 0; j < TM; ++j) d[j] = mfma<MF, OP>(bf, *reinterpret_cast<const v4i*>(t_row[j] + k), d[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+#pragma unroll
+        for (int e = 0; e < (MF == 16 ? 4 : 16); ++e) {
+          const float y = __int_as_float(acc[i][j][e]);
+          acc[i][j][e] = __float_as_int(own[j] == a ? y + d[j][e] : y);
+        }
+      }
+    }
+  }
+}
+
 // Inclusive sum over the wave's lanes.
 __device__ inline int wave_scan(int v, int lane) {
 #pragma unroll
@@ -407,6 +498,7 @@ __global__ __launch_bounds__(T::kThreads) void gemm_i8_kernel(
   constexpr int OP = EPI == kEpiDefBf16 ? kOpBf16 : EPI == kEpiDefF16 ? kOpF16 : kOpI8;
 
   constexpr bool GROUPED = std::is_same_v<X, Grouped>;
+  constexpr bool LORA = std::is_same_v<X, Lora>;
   int n0, m0;
   if constexpr (GROUPED) {
     // this tile's expert: its weight, scales and bias, and its rows [m0, M)
@@ -715,6 +807,18 @@ __global__ __launch_bounds__(T::kThreads) void gemm_i8_kernel(
     // every wave is done with the stages (and every load has landed) before
     // the output tile overwrites them
     wait_vm_barrier<0>();
+    auto put4 = [&](int i, int j, int g, float (&v)[4]) {
+      if constexpr (kF16) {
+        // the output is fp16_rne of the fp32 result: keep v in fp32 here,
+        // or the compiler fuses the fma (or add) and the conversion into
+        // v_fma_mixlo_f16, which rounds the exact value to fp16 once
+#pragma unroll
+        for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(v[e]));
+      }
+      *reinterpret_cast<uint2*>(lds + out_lds_offset<T>(m_loc + j * T::MF, n_loc + i * T::MF + 8 * g)) =
+          kF16 ? make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]))
+               : make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    };
 #pragma unroll
     for (int i = 0; i < T::TN; ++i) {
       float4 ws4[kRowScale ? kGroups : 1];
@@ -724,7 +828,6 @@ __global__ __launch_bounds__(T::kThreads) void gemm_i8_kernel(
       }
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const int nl = n_loc + i * T::MF + 8 * g;
         float b[4];
         if constexpr (kF16) {
           b[0] = f16_bits_lo(bias4[i][g].x); b[1] = f16_bits_hi(bias4[i][g].x);
@@ -751,18 +854,29 @@ __global__ __launch_bounds__(T::kThreads) void gemm_i8_kernel(
             for (int e = 0; e < 4; ++e)
               v[e] = __builtin_fmaf(static_cast<float>(acc[i][j][4 * g + e]), alpha[j], b[e]);
           }
-          if constexpr (kF16) {
-            // the output is fp16_rne of the fp32 result: keep v in fp32 here,
-            // or the compiler fuses the fma (or add) and the conversion into
-            // v_fma_mixlo_f16, which rounds the exact value to fp16 once
+          if constexpr (LORA) {
+            // kept in place for the adapters' part below
 #pragma unroll
-            for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(v[e]));
+            for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] = __float_as_int(v[e]);
+          } else {
+            put4(i, j, g, v);
           }
-          *reinterpret_cast<uint2*>(lds + out_lds_offset<T>(m_loc + j * T::MF, nl)) =
-              kF16 ? make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]))
-                   : make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         }
       }
+    }
+    if constexpr (LORA) {
+      lora_add<T::MF, T::TN, T::TM, kF16>(acc, extra, lane, n0 + wn * T::kWaveN, m0 + wm * T::kWaveM, M, N);
+#pragma unroll
+      for (int i = 0; i < T::TN; ++i)
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+          for (int j = 0; j < T::TM; ++j) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __int_as_float(acc[i][j][4 * g + e]);
+            put4(i, j, g, v);
+          }
     }
     __syncthreads();
     // full rows out: a row is BN/8 16-byte chunks

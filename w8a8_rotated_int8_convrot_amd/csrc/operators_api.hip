@@ -3,6 +3,7 @@
 // convrot_api.hip.
 #include "../../include/convrot.h"
 
+#include <algorithm>
 #include <cmath>
 
 #include "api_checks.hpp"
@@ -14,6 +15,8 @@ using namespace convrot;
 
 constexpr int kMaxRoutes = 64;
 constexpr int64_t kMaxExperts = 65536;
+constexpr int64_t kMaxAdapters = 65536;
+constexpr int64_t kMaxRank = 512;
 
 int check_norm(int kind, const char* what, const char* who) {
   if (kind != CONVROT_NORM_NONE && kind != CONVROT_NORM_RMS && kind != CONVROT_NORM_LAYER)
@@ -27,6 +30,21 @@ hipError_t rotate_quant(const void* x, bool f16, int64_t M, int64_t K, int group
   const auto* xb = static_cast<const uint16_t*>(x);
   return f16 ? launch_rotate_quant_f16(xb, M, K, group, xq, xs, stream)
              : launch_rotate_quant(xb, M, K, group, xq, xs, stream);
+}
+
+// The parts of convrot_linear_lora's workspace for slices of S tokens.
+struct LoraLayout {
+  int64_t S, t_stride;
+  size_t scales, t, total;
+};
+LoraLayout lora_layout(int64_t M, int64_t K, int64_t N, int64_t max_rank) {
+  LoraLayout l;
+  l.S = M < 2 * N ? M : 2 * N;
+  l.t_stride = (max_rank + 31) / 32 * 32;
+  l.scales = round_up(static_cast<size_t>(l.S) * K, 256);
+  l.t = l.scales + round_up(static_cast<size_t>(l.S) * 4, 256);
+  l.total = l.t + static_cast<size_t>(l.S) * l.t_stride * 2;
+  return l;
 }
 
 }  // namespace
@@ -126,6 +144,61 @@ int convrot_grouped_linear(const void* x, int io_dtype, int64_t M, int64_t K, co
                                         static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), f16, offsets,
                                         rows, n_experts, P, N, K, s),
                     who);
+}
+
+size_t convrot_lora_workspace(int64_t M, int64_t K, int64_t N, int64_t max_rank) {
+  if (M < 0 || K < 1 || N < 1 || max_rank < 1 || max_rank > kMaxRank) return 0;
+  return lora_layout(M, K, N, max_rank).total;
+}
+
+int convrot_linear_lora(const void* x, int io_dtype, int64_t M, int64_t K, const int8_t* wq, const float* w_scale,
+                        int scale_mode, int64_t N, int group, const void* bias, const void* lora_a,
+                        const void* lora_b, int64_t R, const float* lora_scale, const int32_t* offsets,
+                        int64_t n_adapters, int64_t max_rank, const int32_t* index, void* y, void* workspace,
+                        size_t ws_bytes, void* stream) {
+  const char* who = "convrot_linear_lora";
+  if (int rc = check_group(group, K, who)) return rc;
+  if (int rc = check_mn(M, N, who)) return rc;
+  if (int rc = check_io(io_dtype, who)) return rc;
+  if (int rc = check_scale_mode(scale_mode, who)) return rc;
+  if (n_adapters < 1 || n_adapters > kMaxAdapters)
+    return fail(CONVROT_EINVAL, "%s: n_adapters=%lld must be in [1, %lld]", who, static_cast<long long>(n_adapters),
+                static_cast<long long>(kMaxAdapters));
+  if (max_rank < 1 || max_rank > kMaxRank)
+    return fail(CONVROT_EINVAL, "%s: max_rank=%lld must be in [1, %lld]", who, static_cast<long long>(max_rank),
+                static_cast<long long>(kMaxRank));
+  if (R < 0 || R > (int64_t(1) << 30))
+    return fail(CONVROT_EINVAL, "%s: R=%lld must be in [0, 2^30]", who, static_cast<long long>(R));
+  if (M == 0) return ok();
+  if (!x || !wq || !w_scale || !y || !lora_scale || !offsets || !index || (R > 0 && (!lora_a || !lora_b)))
+    return fail(CONVROT_EINVAL, "%s: NULL pointer", who);
+  if (!aligned16(x) || !aligned16(wq) || !aligned16(y) || !aligned16(lora_a) || (workspace && !aligned16(workspace)))
+    return fail(CONVROT_EALIGN, "%s: x, wq, y, lora_a and workspace must be 16-byte aligned", who);
+  const LoraLayout l = lora_layout(M, K, N, max_rank);
+  if (!workspace || ws_bytes < l.total)
+    return fail(CONVROT_EWORKSPACE, "%s: workspace of %zu bytes needed (convrot_lora_workspace)", who, l.total);
+  auto* ws = static_cast<char*>(workspace);
+  auto* xq = reinterpret_cast<int8_t*>(ws);
+  auto* xs = reinterpret_cast<float*>(ws + l.scales);
+  auto* t = reinterpret_cast<uint16_t*>(ws + l.t);
+  const bool f16 = io_dtype == CONVROT_F16;
+  auto s = static_cast<hipStream_t>(stream);
+  for (int64_t r0 = 0; r0 < M; r0 += l.S) {
+    const int64_t rows = std::min(M - r0, l.S);
+    const auto* xr = static_cast<const uint16_t*>(x) + r0 * K;
+    if (hipError_t e = rotate_quant(xr, f16, rows, K, group, xq, xs, s); e != hipSuccess) return hip_status(e, who);
+    if (hipError_t e = launch_lora_down(xr, rows, K, f16, static_cast<const uint16_t*>(lora_a), R, lora_scale, offsets,
+                                        n_adapters, index + r0, max_rank, t, l.t_stride, s);
+        e != hipSuccess)
+      return hip_status(e, who);
+    if (hipError_t e = launch_gemm_lora(xq, xs, wq, w_scale, scale_mode == CONVROT_SCALE_ROW,
+                                        static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y) + r0 * N, f16,
+                                        rows, N, K, t, l.t_stride, static_cast<const uint16_t*>(lora_b), R, offsets,
+                                        n_adapters, index + r0, max_rank, s);
+        e != hipSuccess)
+      return hip_status(e, who);
+  }
+  return ok();
 }
 
 }  // extern "C"
