@@ -56,6 +56,10 @@ hipError_t launch_gemm_dequant(const int8_t* xq, const float* x_scale, const int
                                const float* w_scale, const uint16_t* bias, uint16_t* y,
                                int64_t M, int64_t N, int64_t K, hipStream_t stream);
 
+// The tile the layer's product picks for a shape, by the numbers of
+// gemm_i8.hip's choices.
+int pick_gemm_tile(int64_t M, int64_t N);
+
 // Variants: one weight scale per output channel (row_scale: w_scale [N]) and
 // fp16 in place of bf16 for the bias and the output (out_f16).
 hipError_t launch_gemm_dequant_ex(const int8_t* xq, const float* x_scale, const int8_t* wq,

@@ -347,74 +347,221 @@ struct Lora {
   }
 };
 
-// Adds the adapters' part to a wave's TN x TM result blocks, which hold the
-// layer's fp32 results by their bits.  n_first, m_first: the wave's corner.
-// One pass per adapter met among the wave's tokens (neighbours in a batch
-// mostly share theirs), each on the matrix cores: channels x ranks times ranks
-// x tokens, in the layout of the layer's own blocks.  A lane takes the pass's
-// sum only if its token has that adapter: a product with zero instead would
-// carry one adapter's infinities into the other tokens.
-template <int MF, int TN, int TM, bool F16, class AccT>
-__device__ inline void lora_add(AccT (&acc)[TN][TM], const Lora& lo, int lane, int n_first, int m_first, int M,
-                                int N) {
-  constexpr int kRanks = MF == 16 ? 32 : 16;          // ranks of one MFMA
+// The two ways to add them (lora_add, lora_gather below).
+struct LoraList : Lora { static constexpr bool kGather = false; };
+struct LoraGather : Lora { static constexpr bool kGather = true; };
+
+// Eight 16-bit values as fp32.
+template <bool F16>
+__device__ inline void unpack8(const uint4& w, float (&v)[8]) {
+  const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    v[2 * q] = F16 ? f16_bits_lo(d[q]) : __uint_as_float(d[q] << 16);
+    v[2 * q + 1] = F16 ? f16_bits_hi(d[q]) : __uint_as_float(d[q] & 0xffff0000u);
+  }
+}
+
+// Four channels n.. of a row of b as fp32 (past N: the last channel).
+template <bool F16>
+__device__ inline void lora_b4(const uint16_t* row, int n, int N, bool vec, float (&v)[4]) {
+  uint32_t d[2];
+  if (vec) {
+    const uint2 w = *reinterpret_cast<const uint2*>(row + min(n, N - 4));
+    d[0] = w.x;
+    d[1] = w.y;
+  } else {
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = row[min(n + e, N - 1)];
+    d[0] = h[0] | (h[1] << 16);
+    d[1] = h[2] | (h[3] << 16);
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    v[2 * q] = F16 ? f16_bits_lo(d[q]) : __uint_as_float(d[q] << 16);
+    v[2 * q + 1] = F16 ? f16_bits_hi(d[q]) : __uint_as_float(d[q] & 0xffff0000u);
+  }
+}
+
+// Adds the adapters' part to a tile's results, which the waves' blocks hold as
+// fp32 by their bits.  One step per 32 ranks of each adapter met among the
+// tile's tokens (neighbours in a batch mostly share theirs): channels x ranks
+// times ranks x tokens on the matrix cores, in the layout of the layer's own
+// blocks and summed onto them.  b is stored rank by rank, so a step's panel of
+// BN channels goes through LDS: a thread loads eight channels of one rank and
+// writes them apart, so that a lane finds eight ranks of one channel together.
+// Panels are double-buffered: the next one's loads run while this one's
+// products do, one barrier a step.  Where the tokens of a block have several
+// adapters a lane keeps the sum only if its token has the step's: a product
+// with zero instead would carry one adapter's infinities into other tokens.
+template <class T> struct LoraPanel {
+  static constexpr int kBytes = T::BN * 64;                      // 32 ranks of BN channels
+  static constexpr int kChunks = T::BN * 4;                      // eight channels of one rank each
+  static constexpr int kPerThread = (kChunks + T::kThreads - 1) / T::kThreads;
+  __device__ static int at(int n, int chunk) { return n * 64 + ((chunk ^ swz<T::MF, 64>(n)) << 4); }
+};
+
+template <class T, bool F16, class AccT>
+__device__ inline void lora_add(AccT (&acc)[T::TN][T::TM], const Lora& lo, char* panels, int tid, int wn, int wm,
+                                int n0, int m0, int M, int N) {
+  using P = LoraPanel<T>;
+  constexpr int MF = T::MF, TN = T::TN, TM = T::TM;
   constexpr int OP = F16 ? kOpF16 : kOpBf16;
+  constexpr int kSub = MF == 16 ? 1 : 2;              // products per block and step: 32 or 16 ranks each
+  constexpr int kIdx = (T::BM + 63) / 64;
   using sum_t = typename Acc<MF, OP>::type;
-  const int r = lane & (MF - 1), k8 = lane / MF * 8;
+  const int lane = tid & 63;
+  const int r = lane & (MF - 1), c8 = lane / MF;      // fragment row, 8-rank chunk
+  // the tile's tokens, the same in every wave, for the list of its adapters
+  int idx[kIdx];
+  bool left[kIdx];
+#pragma unroll
+  for (int q = 0; q < kIdx; ++q) {
+    const int m = q * 64 + lane;
+    idx[q] = lo.index[min(m0 + m, M - 1)];
+    left[q] = m < T::BM && m0 + m < M && idx[q] >= 0 && idx[q] < lo.adapters;
+  }
   int own[TM];
   const uint16_t* t_row[TM];
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
-    const int m = m_first + j * MF + r;
-    const int a = m < M ? lo.index[m] : -1;
-    own[j] = a >= 0 && a < lo.adapters ? a : -1;
-    t_row[j] = lo.t + static_cast<int64_t>(min(m, M - 1)) * lo.t_stride + k8;
+    const int m = min(m0 + wm * T::kWaveM + j * MF + r, M - 1);   // past the end: as the last token (discarded)
+    own[j] = lo.index[m];
+    t_row[j] = lo.t + static_cast<int64_t>(m) * lo.t_stride + c8 * 8;
   }
-  int left[TM];
+  int a = -1, row0 = 0, rank = 0, k = 0;
+  auto advance = [&]() -> bool {                      // the next 32 ranks
+    k += 32;
+    while (k >= rank) {
+      int next = -1;
 #pragma unroll
-  for (int j = 0; j < TM; ++j) left[j] = own[j];
-  for (;;) {
-    int a = -1;
+      for (int q = 0; q < kIdx; ++q) {
+        const uint64_t some = __ballot(left[q]);
+        if (next < 0 && some != 0) next = __builtin_amdgcn_readlane(idx[q], __builtin_ctzll(some));
+      }
+      if (next < 0) return false;
+#pragma unroll
+      for (int q = 0; q < kIdx; ++q) left[q] = left[q] && idx[q] != next;
+      a = next;
+      lo.range(a, row0, rank);
+      k = 0;
+    }
+    return true;
+  };
+  const bool vec = (N & 7) == 0 && (reinterpret_cast<uintptr_t>(lo.b) & 15) == 0;
+  uint4 raw[P::kPerThread];
+  auto load = [&]() {
+#pragma unroll
+    for (int p = 0; p < P::kPerThread; ++p) {
+      const int c = tid + p * T::kThreads;
+      if (P::kChunks % T::kThreads != 0 && c >= P::kChunks) continue;
+      const int rr = k + (c & 31), n = n0 + (c >> 5) * 8;
+      const uint16_t* src = lo.b + static_cast<int64_t>(row0 + min(rr, rank - 1)) * N;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (rr < rank) {
+        if (vec && n + 8 <= N) {
+          v = *reinterpret_cast<const uint4*>(src + n);
+        } else {
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] = src[min(n + e, N - 1)];
+          v = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+        }
+      }
+      raw[p] = v;
+    }
+  };
+  if (!advance()) return;
+  load();
+  for (int step = 0;; ++step) {
+    char* panel = panels + (step & 1) * P::kBytes;
+    const int now = a;
+    v4i tf[TM][kSub];
+    bool any = false, whole[TM];
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const uint64_t some = __ballot(left[j] >= 0);
-      if (a < 0 && some != 0) a = __builtin_amdgcn_readlane(left[j], __builtin_ctzll(some));
-    }
-    if (a < 0) return;
+      whole[j] = __all(own[j] == now);
+      any = any || __any(own[j] == now);
 #pragma unroll
-    for (int j = 0; j < TM; ++j) left[j] = left[j] == a ? -1 : left[j];
+      for (int u = 0; u < kSub; ++u) tf[j][u] = *reinterpret_cast<const v4i*>(t_row[j] + k + 16 * u);
+    }
+#pragma unroll
+    for (int p = 0; p < P::kPerThread; ++p) {
+      const int c = tid + p * T::kThreads;
+      if (P::kChunks % T::kThreads != 0 && c >= P::kChunks) continue;
+      const int rr = c & 31, n = (c >> 5) * 8;
+      const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        *reinterpret_cast<uint16_t*>(panel + P::at(n + e, rr >> 3) + 2 * (rr & 7)) =
+            static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+    }
+    const bool more = advance();
+    if (more) load();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (any) {
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        v4i bf[kSub];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+          bf[u] = *reinterpret_cast<const v4i*>(panel + P::at(wn * T::kWaveN + i * MF + r, 2 * u + c8));
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          sum_t d = __builtin_bit_cast(sum_t, acc[i][j]);
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) d = mfma<MF, OP>(bf[u], tf[j][u], d);
+          if (whole[j]) {
+            acc[i][j] = __builtin_bit_cast(AccT, d);
+          } else {
+#pragma unroll
+            for (int e = 0; e < T::kAccRegs; ++e) acc[i][j][e] = own[j] == now ? __float_as_int(d[e]) : acc[i][j][e];
+          }
+        }
+      }
+    }
+    if (!more) return;
+  }
+}
+
+// The same for few tokens, each with an adapter of its own, where the list
+// above would be as long as the tile: every lane adds its own token's ranks
+// one by one, four channels at a time.  Rows of b come in 8-byte pieces, eight
+// ranks in flight.
+template <class T, bool F16, class AccT>
+__device__ inline void lora_gather(AccT (&acc)[T::TN][T::TM], const Lora& lo, int lane, int n_first, int m_first,
+                                   int M, int N) {
+  constexpr int MF = T::MF;
+  const bool vec = (N & 3) == 0 && (reinterpret_cast<uintptr_t>(lo.b) & 7) == 0;
+#pragma unroll
+  for (int j = 0; j < T::TM; ++j) {
+    const int m = m_first + j * MF + (lane & (MF - 1));
+    const int a = m < M ? lo.index[m] : -1;
+    if (a < 0 || a >= lo.adapters) continue;
     int row0, rank;
     lo.range(a, row0, rank);
-    if (rank == 0) continue;
+    const uint16_t* t = lo.t + static_cast<int64_t>(m) * lo.t_stride;
+    const uint16_t* b = lo.b + static_cast<int64_t>(row0) * N;
+    for (int k = 0; k < rank; k += 8) {
+      float tv[8];
+      const uint4 tw = *reinterpret_cast<const uint4*>(t + k);
+      unpack8<F16>(tw, tv);
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int n = min(n_first + i * MF + r, N - 1);
-      sum_t d[TM];
+      for (int i = 0; i < T::TN; ++i) {
 #pragma unroll
-      for (int j = 0; j < TM; ++j) d[j] = sum_t{};
-      for (int k = 0; k < rank; k += kRanks) {
-        uint32_t w[4];
+        for (int g = 0; g < T::kAccRegs / 4; ++g) {
+          const int n = n_first + i * MF + 8 * g + 4 * (lane / MF);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t h[2];
+          for (int q = 0; q < 8; ++q) {
+            const uint16_t* row = b + static_cast<int64_t>(min(k + q, rank - 1)) * N;
+            float v[4];
+            lora_b4<F16>(row, n, N, vec, v);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int rr = k + k8 + 2 * q + e;
-            const uint32_t v = lo.b[static_cast<int64_t>(row0 + min(rr, rank - 1)) * N + n];
-            h[e] = rr < rank ? v : 0u;
+            for (int e = 0; e < 4; ++e)
+              acc[i][j][4 * g + e] =
+                  __float_as_int(__builtin_fmaf(tv[q], v[e], __int_as_float(acc[i][j][4 * g + e])));
           }
-          w[q] = h[0] | (h[1] << 16);
-        }
-        const v4i bf = {static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
-#pragma unroll
-        for (int j = 0; j < TM; ++j) d[j] = mfma<MF, OP>(bf, *reinterpret_cast<const v4i*>(t_row[j] + k), d[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-#pragma unroll
-        for (int e = 0; e < (MF == 16 ? 4 : 16); ++e) {
-          const float y = __int_as_float(acc[i][j][e]);
-          acc[i][j][e] = __float_as_int(own[j] == a ? y + d[j][e] : y);
         }
       }
     }
@@ -498,7 +645,7 @@ __global__ __launch_bounds__(T::kThreads) void gemm_i8_kernel(
   constexpr int OP = EPI == kEpiDefBf16 ? kOpBf16 : EPI == kEpiDefF16 ? kOpF16 : kOpI8;
 
   constexpr bool GROUPED = std::is_same_v<X, Grouped>;
-  constexpr bool LORA = std::is_same_v<X, Lora>;
+  constexpr bool LORA = std::is_base_of_v<Lora, X>;
   int n0, m0;
   if constexpr (GROUPED) {
     // this tile's expert: its weight, scales and bias, and its rows [m0, M)
@@ -865,7 +1012,12 @@ __global__ __launch_bounds__(T::kThreads) void gemm_i8_kernel(
       }
     }
     if constexpr (LORA) {
-      lora_add<T::MF, T::TN, T::TM, kF16>(acc, extra, lane, n0 + wn * T::kWaveN, m0 + wm * T::kWaveM, M, N);
+      if constexpr (X::kGather) {
+        lora_gather<T, kF16>(acc, extra, lane, n0 + wn * T::kWaveN, m0 + wm * T::kWaveM, M, N);
+      } else {
+        lora_add<T, kF16>(acc, extra, lds, tid, wn, wm, n0, m0, M, N);
+        __syncthreads();          // the panels make room for the output tile
+      }
 #pragma unroll
       for (int i = 0; i < T::TN; ++i)
 #pragma unroll
@@ -1190,12 +1342,13 @@ __global__ __launch_bounds__(256) void gemm_ksplit_reg_kernel(
 // per tile (K >= 384).  With 16x16 result blocks a lane holds four channels
 // of one token; v_permlane16_swap between the blocks of two neighbouring
 // channel tiles gives every lane eight consecutive channels.
-template <class T, int EPI>
+template <class T, int EPI, class X = NoExtra>
 __global__ __launch_bounds__(T::kThreads) void gemm_persist_kernel(
     const int8_t* __restrict__ wq, const int8_t* __restrict__ xq, int M, int N, int K,
     int tiles_n, int tiles_m, const float* __restrict__ x_scale,
     const float* __restrict__ w_scale, const uint16_t* __restrict__ bias,
-    void* __restrict__ out) {
+    void* __restrict__ out, X extra = X{}) {
+  constexpr bool LORA = std::is_base_of_v<Lora, X>;
   static_assert(T::kStages == 2 && T::BK == 128 && T::kKSteps % 2 == 0, "two 128-byte stages");
   static_assert(T::MF == 32 || T::TN % 2 == 0, "16x16 result blocks are stored in pairs along n");
   constexpr bool DEQUANT = EPI != kEpiI32;
@@ -1213,7 +1366,8 @@ __global__ __launch_bounds__(T::kThreads) void gemm_persist_kernel(
   // block, one per pair of 16 x 16 blocks
   constexpr int kStores = T::MF == 32 ? T::TN * T::TM * 2 : T::TN * T::TM / 2;
   constexpr int kParamFloats = ((kParams > 0 ? kParams : 1) + 3) / 4 * 4;
-  __shared__ __attribute__((aligned(16))) char lds[T::kLdsBytes + 2 * kParamFloats * 4];
+  constexpr int kPanelAt = T::kLdsBytes + 2 * kParamFloats * 4;
+  __shared__ __attribute__((aligned(16))) char lds[kPanelAt + (LORA ? 2 * LoraPanel<T>::kBytes : 0)];
   float* ptab0 = reinterpret_cast<float*>(lds + T::kLdsBytes);
 
   const int total = tiles_n * tiles_m;
@@ -1488,7 +1642,7 @@ __global__ __launch_bounds__(T::kThreads) void gemm_persist_kernel(
     const bool whole = n0 + T::BN <= N && m0 + T::BM <= M;
     // dequant + bias of four consecutive channels nl.. (tile-relative) of one
     // token, packed in two words
-    auto dq4 = [&](const float* pt, float alpha, int nl, const auto& a, int e0, uint32_t (&w)[2]) {
+    auto dq4f = [&](const float* pt, float alpha, int nl, const auto& a, int e0, float (&v)[4]) {
       const float4 b4 = *reinterpret_cast<const float4*>(pt + kPBias + nl);
       const float b[4] = {b4.x, b4.y, b4.z, b4.w};
       float sc[4] = {1.0f, 1.0f, 1.0f, 1.0f};
@@ -1496,12 +1650,20 @@ __global__ __launch_bounds__(T::kThreads) void gemm_persist_kernel(
         const float4 s4 = *reinterpret_cast<const float4*>(pt + kPWs + nl);
         sc[0] = s4.x; sc[1] = s4.y; sc[2] = s4.z; sc[3] = s4.w;
       }
-      float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if constexpr (kDefault) v[e] = a[e0 + e] + b[e];
         else if constexpr (kRowScale) v[e] = __builtin_fmaf(static_cast<float>(a[e0 + e]), alpha * sc[e], b[e]);
         else v[e] = __builtin_fmaf(static_cast<float>(a[e0 + e]), alpha, b[e]);
+      }
+    };
+    auto dq4 = [&](const float* pt, float alpha, int nl, const auto& a, int e0, uint32_t (&w)[2]) {
+      float v[4];
+      if constexpr (LORA) {       // already fp32 results, with the adapters' part
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __int_as_float(a[e0 + e]);
+      } else {
+        dq4f(pt, alpha, nl, a, e0, v);
       }
       if constexpr (kF16) {
         // fp16_rne of the fp32 result: no fused fma-and-convert
@@ -1584,6 +1746,23 @@ __global__ __launch_bounds__(T::kThreads) void gemm_persist_kernel(
         put8(y, m, n0 + n_loc + 16 * (i + (hi & 1)) + 8 * (hi >> 1), make_uint4(p0[0], p1[0], p0[1], p1[1]), vec);
       }
     };
+    if constexpr (LORA) {
+      constexpr int kGroups = T::kAccRegs / 4;
+#pragma unroll
+      for (int j = 0; j < T::TM; ++j) {
+        const float alpha = pt[kPAlpha + m_loc + j * T::MF];
+#pragma unroll
+        for (int i = 0; i < T::TN; ++i)
+#pragma unroll
+          for (int gg = 0; gg < kGroups; ++gg) {
+            float v[4];
+            dq4f(pt, alpha, n_loc + i * T::MF + 8 * gg + 4 * hi, acc[i][j], 4 * gg, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][4 * gg + e] = __float_as_int(v[e]);
+          }
+      }
+      lora_add<T, kF16>(acc, extra, lds + kPanelAt, tid_e, wn, wm, n0, m0, M, N);
+    }
     constexpr int kIStep = T::MF == 32 ? 1 : 2;
     // A whole tile's dequant epilogue with another tile to follow runs
     // together with that tile's first unit: block by block, the results are

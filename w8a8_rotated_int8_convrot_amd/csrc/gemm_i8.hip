@@ -51,7 +51,7 @@ hipError_t launch_persist(const int8_t* xq, const float* x_scale, const int8_t* 
   if (K < 3 * T::BK) return launch_tile<T, EPI>(xq, x_scale, wq, w_scale, bias, out, M, N, K, stream);
   hipLaunchKernelGGL((gemm_persist_kernel<T, EPI>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreads), 0,
                      stream, wq, xq, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), tiles_n,
-                     tiles_m, x_scale, w_scale, bias, out);
+                     tiles_m, x_scale, w_scale, bias, out, NoExtra{});
   return hipGetLastError();
 }
 
@@ -119,7 +119,9 @@ int64_t wide_cost(int64_t M, int64_t N) {
   return ((main_m * tn + kCUs - 1) / kCUs * 2 + 1) * 384 * 96;
 }
 
-int pick_tile(int64_t M, int64_t N) {
+}  // namespace
+
+int pick_gemm_tile(int64_t M, int64_t N) {
   const int64_t kCUs = num_cus();
   if (M <= 16) return (N + 15) / 16 >= 2 * kCUs ? 19 : 7;
   if (M <= 256) {
@@ -173,13 +175,15 @@ int pick_tile(int64_t M, int64_t N) {
   return wide_cost(M, N) * 100 < tile_cost(M, N, 256, 256) * 115 ? 6 : 1;
 }
 
+namespace {
+
 template <int EPI>
 hipError_t launch_gemm(const int8_t* xq, const float* x_scale, const int8_t* wq,
                        const float* w_scale, const uint16_t* bias, void* out, int64_t M,
                        int64_t N, int64_t K, hipStream_t stream) {
   int t = forced_tile();
   const bool automatic = t == 0;
-  if (automatic) t = pick_tile(M, N);
+  if (automatic) t = pick_gemm_tile(M, N);
   if (t == 1) return launch_tile<TileBig, EPI>(xq, x_scale, wq, w_scale, bias, out, M, N, K, stream);
   if (t == 2) return launch_tile<TileBig8, EPI>(xq, x_scale, wq, w_scale, bias, out, M, N, K, stream);
   if (t == 4) return launch_tile<TileWide, EPI>(xq, x_scale, wq, w_scale, bias, out, M, N, K, stream);

@@ -5,27 +5,63 @@
 namespace convrot {
 namespace {
 
-template <class T, int EPI>
+template <class T, int EPI, class X>
 hipError_t launch_tile(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
-                       const uint16_t* bias, uint16_t* y, const Lora& l, int64_t M, int64_t N, int64_t K,
+                       const uint16_t* bias, uint16_t* y, const X& l, int64_t M, int64_t N, int64_t K,
                        hipStream_t stream) {
   const int tiles_n = static_cast<int>((N + T::BN - 1) / T::BN);
   const int tiles_m = static_cast<int>((M + T::BM - 1) / T::BM);
   const int64_t blocks = static_cast<int64_t>(tiles_n) * tiles_m;
-  hipLaunchKernelGGL((gemm_i8_kernel<T, EPI, Lora>), dim3(static_cast<uint32_t>(blocks)), dim3(T::kThreads), 0, stream,
+  hipLaunchKernelGGL((gemm_i8_kernel<T, EPI, X>), dim3(static_cast<uint32_t>(blocks)), dim3(T::kThreads), 0, stream,
                      wq, xq, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), tiles_n, tiles_m, x_scale,
                      w_scale, bias, y, l);
   return hipGetLastError();
 }
 
+template <class T, int EPI>
+hipError_t launch_persist(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+                          const uint16_t* bias, uint16_t* y, const LoraList& l, int64_t M, int64_t N, int64_t K,
+                          hipStream_t stream) {
+  if (K < 3 * T::BK) return launch_tile<T, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+  const int tiles_n = static_cast<int>((N + T::BN - 1) / T::BN);
+  const int tiles_m = static_cast<int>((M + T::BM - 1) / T::BM);
+  const int64_t tiles = static_cast<int64_t>(tiles_n) * tiles_m;
+  const int64_t grid = tiles < num_cus() ? tiles : num_cus();
+  hipLaunchKernelGGL((gemm_persist_kernel<T, EPI, LoraList>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreads), 0,
+                     stream, wq, xq, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), tiles_n, tiles_m,
+                     x_scale, w_scale, bias, y, l);
+  return hipGetLastError();
+}
+
+// The tiles are the layer's own (pick_gemm_tile), with the persistent 192 x 288
+// kernel for its largest ones and the one-wave 16 x 16 tile for few tokens.
+// Up to 128 tokens with several adapters each lane adds its own token's ranks;
+// larger batches, and batches of at most four adapters, go through the list of
+// the tile's adapters.
 template <int EPI>
 hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
-                      const uint16_t* bias, uint16_t* y, const Lora& l, int64_t M, int64_t N, int64_t K,
+                      const uint16_t* bias, uint16_t* y, const Lora& lora, int64_t M, int64_t N, int64_t K,
                       hipStream_t stream) {
-  if (M <= 16) return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
-  if (M <= 64) return launch_tile<TileM64, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
-  if (M <= 1024) return launch_tile<TileMid, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
-  return launch_tile<TileTall, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+  const int tile = pick_gemm_tile(M, N);
+  if (M <= 16 || (M <= 128 && lora.adapters > 4)) {
+    const LoraGather l{lora};
+    if (M <= 16) return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    if (tile == 10) return launch_tile<TileM32, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    if (tile == 11) return launch_tile<TileM64, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    if (tile == 12) return launch_tile<TileM128, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    return launch_tile<TileSkinny, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+  }
+  const LoraList l{lora};
+  switch (tile) {
+    case 7: return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    case 5: return launch_tile<TileSkinny, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    case 10: return launch_tile<TileM32, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    case 11: return launch_tile<TileM64, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    case 12: return launch_tile<TileM128, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    case 3: return launch_tile<TileMid, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    case 8: return launch_tile<TileWideHalf, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+    default: return launch_persist<TileTall, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+  }
 }
 
 }  // namespace
