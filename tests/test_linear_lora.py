@@ -36,7 +36,7 @@ def call(B, x=A, io=1, M=64, K=512, wq=A, ws=A, mode=0, N=64, g=128, bias=None, 
     (dict(b=None), EINVAL), (dict(sc=None), EINVAL), (dict(off=None), EINVAL), (dict(idx=None), EINVAL),
     (dict(y=None), EINVAL), (dict(x=A + 8), EALIGN), (dict(wq=A + 4), EALIGN), (dict(y=A + 2), EALIGN),
     (dict(a=A + 2), EALIGN), (dict(w=A + 8), EALIGN), (dict(w=None), EWORKSPACE),
-    (dict(wb=64 * 512 + 256 + 64 * 32 * 2 - 1), EWORKSPACE),
+    (dict(wb=64 * 512 + 256 + 64 * 64 + 8 * 64 * 128 - 1), EWORKSPACE),
 ])
 def test_refusals(B, kw, status):
     assert call(B, **kw) == status
@@ -46,9 +46,9 @@ def test_refusals(B, kw, status):
 def test_empty_and_workspace(B):
     assert call(B, M=0, x=None, wq=None, y=None, w=None, wb=0) == OK
     assert B.lib().convrot_last_error() == b""
-    # slices of min(M, 2N) tokens: codes, scales, t rows of 32 (ranks are padded to 32)
-    assert B.convrot_lora_workspace(64, 512, 64, 16) == 64 * 512 + 256 + 64 * 64
-    assert B.convrot_lora_workspace(100, 512, 8, 40) == 16 * 512 + 256 + 16 * 128
+    # slices of min(M, 2N) tokens: codes, scales, t rows (ranks are padded to 32), eight parts of their fp32 sums
+    assert B.convrot_lora_workspace(64, 512, 64, 16) == 64 * 512 + 256 + 64 * 64 + 8 * 64 * 128
+    assert B.convrot_lora_workspace(100, 512, 8, 40) == 16 * 512 + 256 + 16 * 128 + 8 * 16 * 256
     assert B.convrot_lora_workspace(64, 512, 64, 0) == 0 and B.convrot_lora_workspace(-1, 512, 64, 8) == 0
 
 
@@ -96,8 +96,8 @@ def reference(B, p, group):
         s, wa, wb = p["lora_scale"][a].double(), p["lora_a"][lo:hi].double(), p["lora_b"][lo:hi].double()
         t = s * (x[at].double() @ wa.t())
         delta[at] = t @ wb
-        # t: half a step of the io type, and a sum of K / 8 + 8 fp32 terms (eight waves share K)
-        lost = torch.finfo(dt).eps / 2 * t.abs() + (K / 8 + 10) * 2.0 ** -24 * s * (x[at].double().abs() @ wa.abs().t())
+        # t: half a step of the io type, and a sum in fp32 over at most K / 4 terms a wave and 16 parts
+        lost = torch.finfo(dt).eps / 2 * t.abs() + (K / 4 + 20) * 2.0 ** -24 * s * (x[at].double().abs() @ wa.abs().t())
         t_lost[at] = lost @ wb.abs() + (hi - lo + 2) * 2.0 ** -24 * (t.abs() @ wb.abs())
     want = base + delta
     # fp32: the int32 sum, the scales, the multiply-add, the sum with the adapter's part

@@ -87,13 +87,21 @@ hipError_t launch_gemm_grouped(const int8_t* xq, const float* x_scale, int64_t x
                                const int32_t* offsets, const int32_t* rows, int64_t experts, int64_t P, int64_t N,
                                int64_t K, hipStream_t stream);
 
+// Whether a batch's adapters are taken token by token (few tokens, most with an
+// adapter of their own) or as a list per tile.  By sizes alone, so that a
+// token's result does not depend on the other tokens' adapters.
+inline bool lora_by_token(int64_t M, int64_t adapters) { return M <= 16 || (M <= 128 && adapters > 4); }
+
 // The first product of low-rank adapters (lora.hip): t [M, t_stride] in the io
 // type, t[m][r] = scale[a] * (row offsets[a] + r of a_rows [ranks, K]) . x[m]
 // with a = index[m]; zero from the adapter's rank on, unset for a token whose
-// index is outside [0, adapters).  t_stride: max_rank rounded up to 32.
+// index is outside [0, adapters).  t_stride: max_rank rounded up to 32.  sums:
+// lora_parts(M, K) * M * t_stride floats (not used token by token).
+constexpr int kMaxLoraParts = 8;
+int lora_parts(int64_t M, int64_t K);
 hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, bool f16, const uint16_t* a, int64_t ranks,
                             const float* scale, const int32_t* offsets, int64_t adapters, const int32_t* index,
-                            int64_t max_rank, uint16_t* t, int64_t t_stride, hipStream_t stream);
+                            int64_t max_rank, uint16_t* t, int64_t t_stride, float* sums, hipStream_t stream);
 
 // The layer's product with the adapters' second one, t . b (b [ranks, N]),
 // added before the output is rounded (gemm_lora.hip).

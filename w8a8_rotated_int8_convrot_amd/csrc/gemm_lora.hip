@@ -43,7 +43,7 @@ hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, 
                       const uint16_t* bias, uint16_t* y, const Lora& lora, int64_t M, int64_t N, int64_t K,
                       hipStream_t stream) {
   const int tile = pick_gemm_tile(M, N);
-  if (M <= 16 || (M <= 128 && lora.adapters > 4)) {
+  if (lora_by_token(M, lora.adapters)) {
     const LoraGather l{lora};
     if (M <= 16) return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
     if (tile == 10) return launch_tile<TileM32, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);

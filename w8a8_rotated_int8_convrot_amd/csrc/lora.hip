@@ -7,16 +7,21 @@
 // layers rounds there too); it moves the result by at most half a step of the
 // adapter's part.
 //
-// A workgroup takes 16 tokens: its eight waves split K (64 elements at a time,
-// so a row piece is a whole 128-byte line), each keeps the sums of up to four
-// blocks of 16 ranks in registers (v_mfma_*_16x16x32, ranks x tokens) and the
-// waves' sums are joined through LDS in a fixed order.  The tokens' adapters
-// are taken one after another, or, where few token tiles would leave the chip
-// idle, dealt out over gridDim.y workgroups; gridDim.z deals out the ranks in
-// blocks of 64.
-#include <type_traits>
-
+// lora_down_kernel: a workgroup takes 64 tokens and a part of K, which its four
+// waves split again; each wave keeps the sums of 4 x NB blocks (16 tokens x 16
+// ranks, v_mfma_*_16x16x32) in registers, so a loaded piece of x serves 16 NB
+// ranks and a piece of the adapter 64 tokens.  What bounds it is what a CU can
+// draw from its L2 (about 27 bytes a cycle here), and 64 tokens a workgroup
+// with K split over gridDim.z move half of what 16 tokens with all of K do
+// while filling the chip.  The waves' sums are joined through LDS, the parts
+// of K by lora_sum_kernel, both in a fixed order.  The adapters met among the
+// tokens are taken one after another, or, where the tiles would leave the chip
+// idle, dealt out over gridDim.y workgroups.
+//
+// lora_dot_kernel, for few tokens with adapters of their own: a wave per token
+// and two of its ranks, each lane a plain dot product over its part of K.
 #include "convrot_internal.hpp"
+#include "rotate_device.hpp"
 
 namespace convrot {
 namespace {
@@ -26,8 +31,21 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
-constexpr int kWaves = 8;
-constexpr int kBlocks = 4;      // 16-rank blocks of one pass
+constexpr int kTile = 64;       // tokens of a workgroup
+constexpr int kWaves = 4;
+
+struct Down {
+  const uint16_t *x, *a_rows;
+  const float* scale;
+  const int32_t *offsets, *index;
+  uint16_t* t;
+  int M, K, ranks, adapters, max_rank, t_stride;
+  // rows [row0, row0 + rank) of adapter a, inside [0, ranks)
+  __device__ void range(int a, int& row0, int& rank) const {
+    row0 = min(max(offsets[a], 0), ranks);
+    rank = min(min(max(offsets[a + 1], row0), ranks) - row0, max_rank);
+  }
+};
 
 template <bool F16>
 __device__ inline v4f mfma(v4i a, v4i b, v4f c) {
@@ -38,97 +56,198 @@ __device__ inline v4f mfma(v4i a, v4i b, v4f c) {
 }
 
 template <bool F16>
-__device__ inline uint16_t round16(float v) {
+__device__ inline uint32_t round16(float v) {
   if constexpr (F16) return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
   else return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
-template <bool F16>
-__global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(
-    const uint16_t* __restrict__ x, int M, int K, const uint16_t* __restrict__ a_rows, int ranks,
-    const float* __restrict__ scale, const int32_t* __restrict__ offsets, int adapters,
-    const int32_t* __restrict__ index, int max_rank, uint16_t* __restrict__ t, int t_stride) {
-  __shared__ __attribute__((aligned(16))) v4f part[kWaves][kBlocks][64];
+// sums [gridDim.z][M][t_stride] fp32
+template <bool F16, int NB>
+__global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* __restrict__ sums) {
+  __shared__ __attribute__((aligned(16))) v4f part[kWaves][4][NB][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, k8 = lane >> 4 << 3;
-  const int m = blockIdx.x * 16 + r;
-  int own = m < M ? index[m] : -1;
-  if (own >= adapters) own = -1;
-  const uint16_t* x_row = x + static_cast<int64_t>(min(m, M - 1)) * K + k8;
+  const int m0 = blockIdx.x * kTile;
+  const int M = p.M, K = p.K;
+  const int mine = p.index[min(m0 + lane, M - 1)];
+  const uint16_t* x_row[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x_row[j] = p.x + static_cast<int64_t>(min(m0 + 16 * j + r, M - 1)) * K + k8;
+  // 64 elements of K at a time, dealt out to the waves of all parts
+  const int step = gridDim.z * kWaves * 64;
+  const int k0 = (blockIdx.z * kWaves + wave) * 64;
+  // after the sum this wave stores token block `wave`
+  const int m_out = m0 + 16 * wave + r;
+  const int own = m_out < M ? p.index[m_out] : -1;
 
-  // the tile's distinct adapters, every gridDim.y-th one here
-  uint64_t left = __ballot(lane < 16 && own >= 0);
+  uint64_t left = __ballot(m0 + lane < M && mine >= 0 && mine < p.adapters);
   for (int turn = 0; left != 0; ++turn) {
-    const int a = __builtin_amdgcn_readlane(own, __builtin_ctzll(left));
-    left &= ~__ballot(own == a);
+    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+    left &= ~__ballot(mine == a);
     if (turn % gridDim.y != blockIdx.y) continue;
-    const int row0 = min(max(offsets[a], 0), ranks);
-    const int rank = min(min(max(offsets[a + 1], row0), ranks) - row0, max_rank);
-    const float s = scale[a];
-    for (int base = blockIdx.z * 16 * kBlocks; base < t_stride; base += gridDim.z * 16 * kBlocks) {
-      const int blocks = min(kBlocks, (t_stride - base) / 16);       // t_stride is a multiple of 32
-      const int full = min(kBlocks, max(0, (rank - base + 15) / 16));   // blocks that hold ranks
-      v4f acc[kBlocks] = {};
-      if (full > 0) {
-        const uint16_t* w_row[kBlocks];
+    int row0, rank;
+    p.range(a, row0, rank);
+    for (int base = 0; base < rank; base += 16 * NB) {
+      v4f acc[4][NB] = {};
+      // rows past the rank: the last one (its sums are not used)
+      const uint16_t* w_row[NB];
 #pragma unroll
-        for (int q = 0; q < kBlocks; ++q)
-          w_row[q] = a_rows + static_cast<int64_t>(row0 + min(base + 16 * q + r, rank - 1)) * K + k8;
-        for (int k = wave * 64; k < K; k += kWaves * 64) {
+      for (int q = 0; q < NB; ++q)
+        w_row[q] = p.a_rows + static_cast<int64_t>(row0 + min(base + 16 * q + r, rank - 1)) * K + k8;
+      for (int k = k0; k < K; k += step) {
+        v4i xf[2][4], wf[2][NB];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const v4i xf = *reinterpret_cast<const v4i*>(x_row + k + 32 * h);
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int q = 0; q < kBlocks; ++q)
-              if (q < full) acc[q] = mfma<F16>(*reinterpret_cast<const v4i*>(w_row[q] + k + 32 * h), xf, acc[q]);
-          }
+          for (int j = 0; j < 4; ++j) xf[h][j] = *reinterpret_cast<const v4i*>(x_row[j] + k + 32 * h);
+#pragma unroll
+          for (int q = 0; q < NB; ++q) wf[h][q] = *reinterpret_cast<const v4i*>(w_row[q] + k + 32 * h);
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int q = 0; q < NB; ++q) acc[j][q] = mfma<F16>(wf[h][q], xf[h][j], acc[j][q]);
       }
 #pragma unroll
-      for (int q = 0; q < kBlocks; ++q) part[wave][q][lane] = acc[q];
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < NB; ++q) part[wave][j][q][lane] = acc[j][q];
       __syncthreads();
-      // wave q adds block q: lane l holds ranks 4 (l >> 4) + e of token l & 15
-      if (wave < blocks) {
-        v4f sum = part[0][wave][lane];
+      // lane l holds ranks 4 (l >> 4) + e of token l & 15
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) sum += part[w][wave][lane];
-        if (own == a) {
-          const int rank0 = base + 16 * wave + (lane >> 4) * 4;
-          uint32_t h[4];
+      for (int q = 0; q < NB; ++q) {
+        v4f sum = part[0][wave][q][lane];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = rank0 + e < rank ? round16<F16>(s * sum[e]) : 0;
-          *reinterpret_cast<uint2*>(t + static_cast<int64_t>(m) * t_stride + rank0) =
-              make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-        }
+        for (int w = 1; w < kWaves; ++w) sum += part[w][wave][q][lane];
+        const int rank0 = base + 16 * q + (lane >> 4) * 4;
+        if (own == a && rank0 < p.t_stride)
+          *reinterpret_cast<v4f*>(sums + (static_cast<int64_t>(blockIdx.z) * M + m_out) * p.t_stride + rank0) = sum;
       }
       __syncthreads();
     }
   }
 }
 
+// t from the parts of K: a thread per four ranks of a token.
+template <bool F16>
+__global__ __launch_bounds__(256) void lora_sum_kernel(Down p, const float* __restrict__ sums, int parts) {
+  const int quads = p.t_stride / 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t m = i / quads;
+  if (m >= p.M) return;
+  const int a = p.index[m];
+  if (a < 0 || a >= p.adapters) return;
+  int row0, rank;
+  p.range(a, row0, rank);
+  const int rank0 = static_cast<int>(i - m * quads) * 4;
+  v4f sum = {};
+  if (rank0 < rank)
+    for (int z = 0; z < parts; ++z)
+      sum += *reinterpret_cast<const v4f*>(sums + (z * static_cast<int64_t>(p.M) + m) * p.t_stride + rank0);
+  const float s = p.scale[a];
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = rank0 + e < rank ? round16<F16>(s * sum[e]) : 0u;
+  *reinterpret_cast<uint2*>(p.t + m * p.t_stride + rank0) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// Ranks 8 * blockIdx.y + 2 * wave + (0, 1) of token blockIdx.x.
+template <typename In>
+__global__ __launch_bounds__(256) void lora_dot_kernel(Down p) {
+  constexpr bool F16 = !std::is_same_v<In, uint16_t>;
+  const int64_t m = blockIdx.x;
+  const int lane = threadIdx.x & 63;
+  const int rank0 = blockIdx.y * 8 + (threadIdx.x >> 6) * 2;
+  const int a = p.index[m];
+  if (a < 0 || a >= p.adapters) return;
+  int row0, rank;
+  p.range(a, row0, rank);
+  float sum[2] = {0.0f, 0.0f};
+  if (rank0 < rank) {
+    const In* x = reinterpret_cast<const In*>(p.x) + m * p.K;
+    const In* w = reinterpret_cast<const In*>(p.a_rows) + static_cast<int64_t>(row0 + rank0) * p.K;
+    const In* w2 = rank0 + 1 < rank ? w + p.K : w;
+#pragma unroll 4
+    for (int k = lane * 8; k < p.K; k += 512) {
+      float xv[8], wv[8], w2v[8];
+      load8(x + k, xv);
+      load8(w + k, wv);
+      load8(w2 + k, w2v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum[0] = __builtin_fmaf(xv[i], wv[i], sum[0]);
+        sum[1] = __builtin_fmaf(xv[i], w2v[i], sum[1]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float v = sum[e];
+      v += lane_xor<1>(v);
+      v += lane_xor<2>(v);
+      v += lane_xor<4>(v);
+      v += lane_xor<8>(v);
+      v += __shfl_xor(v, 16);
+      v += __shfl_xor(v, 32);
+      sum[e] = v;
+    }
+  }
+  if (lane == 0) {
+    const float s = p.scale[a];
+    const uint32_t lo = rank0 < rank ? round16<F16>(s * sum[0]) : 0u;
+    const uint32_t hi = rank0 + 1 < rank ? round16<F16>(s * sum[1]) : 0u;
+    *reinterpret_cast<uint32_t*>(p.t + m * p.t_stride + rank0) = lo | (hi << 16);
+  }
+}
+
+template <bool F16, int NB>
+hipError_t launch_down(const Down& p, float* sums, int parts, hipStream_t stream) {
+  const int tiles = (p.M + kTile - 1) / kTile;
+  const int most = p.adapters < kTile ? p.adapters : kTile;         // adapters a tile can hold
+  const int want = (2 * num_cus() + tiles * parts - 1) / (tiles * parts);
+  const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(want < most ? want : most),
+                  static_cast<uint32_t>(parts));
+  hipLaunchKernelGGL((lora_down_kernel<F16, NB>), grid, dim3(kWaves * 64), 0, stream, p, sums);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  const int64_t threads = static_cast<int64_t>(p.M) * (p.t_stride / 4);
+  hipLaunchKernelGGL(lora_sum_kernel<F16>, dim3(static_cast<uint32_t>((threads + 255) / 256)), dim3(256), 0, stream, p,
+                     sums, parts);
+  return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t launch(const Down& p, float* sums, int parts, bool dots, hipStream_t stream) {
+  using In = std::conditional_t<F16, _Float16, uint16_t>;
+  if (dots) {
+    hipLaunchKernelGGL(lora_dot_kernel<In>, dim3(static_cast<uint32_t>(p.M), static_cast<uint32_t>(p.t_stride / 8)),
+                       dim3(256), 0, stream, p);
+    return hipGetLastError();
+  }
+  if (p.max_rank <= 16) return launch_down<F16, 1>(p, sums, parts, stream);
+  if (p.max_rank <= 32) return launch_down<F16, 2>(p, sums, parts, stream);
+  return launch_down<F16, 4>(p, sums, parts, stream);
+}
+
 }  // namespace
+
+int lora_parts(int64_t M, int64_t K) {
+  const int64_t tiles = (M + kTile - 1) / kTile;
+  int64_t parts = 2 * num_cus() / tiles;
+  if (parts > K / 256) parts = K / 256;
+  return static_cast<int>(parts < 1 ? 1 : parts > kMaxLoraParts ? kMaxLoraParts : parts);
+}
 
 hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, bool f16, const uint16_t* a, int64_t ranks,
                             const float* scale, const int32_t* offsets, int64_t adapters, const int32_t* index,
-                            int64_t max_rank, uint16_t* t, int64_t t_stride, hipStream_t stream) {
+                            int64_t max_rank, uint16_t* t, int64_t t_stride, float* sums, hipStream_t stream) {
   if (M == 0) return hipSuccess;
-  const int64_t tiles = (M + 15) / 16;
-  const int64_t most = adapters < 16 ? adapters : 16;         // adapters a tile can hold
-  const int64_t want = (2 * num_cus() + tiles - 1) / tiles;
-  const int64_t turns = want < most ? want : most;
-  const int64_t rank_blocks = (t_stride + 16 * kBlocks - 1) / (16 * kBlocks);
-  const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(turns), static_cast<uint32_t>(rank_blocks));
-  const int m = static_cast<int>(M), k = static_cast<int>(K);
-  if (f16)
-    hipLaunchKernelGGL(lora_down_kernel<true>, grid, dim3(kWaves * 64), 0, stream, x, m, k, a, static_cast<int>(ranks),
-                       scale, offsets, static_cast<int>(adapters), index, static_cast<int>(max_rank), t,
-                       static_cast<int>(t_stride));
-  else
-    hipLaunchKernelGGL(lora_down_kernel<false>, grid, dim3(kWaves * 64), 0, stream, x, m, k, a, static_cast<int>(ranks),
-                       scale, offsets, static_cast<int>(adapters), index, static_cast<int>(max_rank), t,
-                       static_cast<int>(t_stride));
-  return hipGetLastError();
+  const Down p{x, a, scale, offsets, index, t, static_cast<int>(M), static_cast<int>(K), static_cast<int>(ranks),
+               static_cast<int>(adapters), static_cast<int>(max_rank), static_cast<int>(t_stride)};
+  const int parts = lora_parts(M, K);
+  const bool dots = lora_by_token(M, adapters);
+  return f16 ? launch<true>(p, sums, parts, dots, stream) : launch<false>(p, sums, parts, dots, stream);
 }
 
 }  // namespace convrot
