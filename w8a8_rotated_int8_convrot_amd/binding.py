@@ -105,7 +105,8 @@ def _ptr(t):
 
 
 def _stream(t: torch.Tensor):
-    return torch.cuda.current_stream(t.device).cuda_stream
+    # the handle alone: building a torch.cuda.Stream for it costs 2 us a call
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _need(t, dtype, name, ndim=None):
@@ -555,17 +556,18 @@ def convrot_guard_inject(device: int, fault: str) -> None:
 
 def _call_on(t, name, *args):
     """``_call`` with t's device current (the library launches on the current one)."""
-    if t.device.index == torch.cuda.current_device():
+    if t.get_device() == torch.cuda.current_device():
         return _call(name, *args)
     with torch.cuda.device(t.device):
         return _call(name, *args)
 
 
 def _need_on(t, dev, dtype, name, shape):
-    """A contiguous CUDA tensor of this type and shape, on dev."""
-    if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+    """A contiguous CUDA tensor of this type and shape, on dev; its address."""
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on {dev}, got {t.dtype} "
                          f"{list(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+    return t.data_ptr()
 
 
 class Block(ctypes.Structure):
@@ -598,50 +600,46 @@ def convrot_block_norm(h, u=None, routes=None, post_norm="none", post_weight=Non
     projection, say), each token's row named by the int32 mod_index [M] (row 0 without it).
     h_out may be h.  want_out=False stops after h_out and returns it alone."""
     io = _io_of(h, "h")
-    _need(h, h.dtype, "h", 2)
     dev, dt = h.device, h.dtype
-    M, K = h.shape
+    _need(h, dt, "h", 2)
+    shape = M, K = h.shape
     b = Block(io, group, _norm_of(post_norm, "post_norm"), _norm_of(pre_norm, "pre_norm"), 0, eps, residual_scale, M, K,
               h.data_ptr())
     if routes is not None:
         if u is None:
             raise ValueError("convrot_block_norm: routes without u")
         row, weight = routes
-        _need(u, dt, "u", 2)
         if row.dim() != 2 or row.shape[1] < 1:
             raise ValueError("convrot_block_norm: route rows are [M, t], t >= 1")
         t = row.shape[1]
-        _need_on(u, dev, dt, "u", (u.shape[0], K))
-        _need_on(row, dev, torch.int32, "route rows", (M, t))
-        _need_on(weight, dev, torch.float32, "route weights", (M, t))
-        b.n_routes, b.u_rows, b.route_row, b.route_weight = t, u.shape[0], row.data_ptr(), weight.data_ptr()
+        b.n_routes, b.u_rows = t, u.shape[0]
         # no rows at all: every route is out of range, but u still has to be there
-        b.u = u.data_ptr() or h.data_ptr()
+        b.u = _need_on(u, dev, dt, "u", (u.shape[0], K)) or h.data_ptr()
+        b.route_row = _need_on(row, dev, torch.int32, "route rows", (M, t))
+        b.route_weight = _need_on(weight, dev, torch.float32, "route weights", (M, t))
     elif u is not None:
-        _need_on(u, dev, dt, "u", (M, K))
-        b.u = u.data_ptr()
+        b.u = _need_on(u, dev, dt, "u", shape)
     if post_weight is not None:
-        _need_on(post_weight, dev, dt, "post_weight", (K,))
-        b.post_weight = post_weight.data_ptr()
+        b.post_weight = _need_on(post_weight, dev, dt, "post_weight", (K,))
     if pre_weight is not None:
-        _need_on(pre_weight, dev, dt, "pre_weight", (K,))
-        b.pre_weight = pre_weight.data_ptr()
-    mods = [(n, m) for n, m in (("gate", gate), ("scale", scale), ("shift", shift)) if m is not None]
-    for n, m in mods:
-        if m.dtype != dt or m.device != dev or m.dim() != 2 or m.shape[1] != K or m.shape[0] < 1 or m.stride(1) != 1:
-            raise ValueError(f"{n}: expected {dt} [n, {K}] on {dev} with contiguous rows, got {m.dtype} "
-                             f"{list(m.shape)} on {m.device}")
-        # one row has no neighbour, whatever stride it carries
-        stride = m.stride(0) if m.shape[0] > 1 else K
-        if b.n_mod and (m.shape[0] != b.n_mod or stride != b.mod_stride):
-            raise ValueError("convrot_block_norm: gate, scale and shift must have the same rows and row stride")
-        b.n_mod, b.mod_stride = m.shape[0], stride
-        setattr(b, n, m.data_ptr())
-    if mod_index is not None:
-        if not mods:
-            raise ValueError("convrot_block_norm: mod_index without gate, scale or shift")
-        _need_on(mod_index, dev, torch.int32, "mod_index", (M,))
-        b.mod_index = mod_index.data_ptr()
+        b.pre_weight = _need_on(pre_weight, dev, dt, "pre_weight", (K,))
+    if gate is not None or scale is not None or shift is not None:
+        for n, m in (("gate", gate), ("scale", scale), ("shift", shift)):
+            if m is None:
+                continue
+            if m.dtype != dt or m.device != dev or m.dim() != 2 or m.shape[1] != K or m.shape[0] < 1 or m.stride(1) != 1:
+                raise ValueError(f"{n}: expected {dt} [n, {K}] on {dev} with contiguous rows, got {m.dtype} "
+                                 f"{list(m.shape)} on {m.device}")
+            # one row has no neighbour, whatever stride it carries
+            stride = m.stride(0) if m.shape[0] > 1 else K
+            if b.n_mod and (m.shape[0] != b.n_mod or stride != b.mod_stride):
+                raise ValueError("convrot_block_norm: gate, scale and shift must have the same rows and row stride")
+            b.n_mod, b.mod_stride = m.shape[0], stride
+            setattr(b, n, m.data_ptr())
+        if mod_index is not None:
+            b.mod_index = _need_on(mod_index, dev, torch.int32, "mod_index", (M,))
+    elif mod_index is not None:
+        raise ValueError("convrot_block_norm: mod_index without gate, scale or shift")
     if u is None:
         if h_out is not None:
             raise ValueError("convrot_block_norm: h_out without u")
@@ -649,21 +647,15 @@ def convrot_block_norm(h, u=None, routes=None, post_norm="none", post_weight=Non
     else:
         if h_out is None:
             h_out = torch.empty_like(h)
-        else:
-            _need_on(h_out, dev, dt, "h_out", (M, K))
-        b.h_out = h_out.data_ptr()
+        b.h_out = _need_on(h_out, dev, dt, "h_out", shape)
     if want_out:
         if out is None:
-            out = torch.empty((M, K), dtype=torch.int8 if group else dt, device=dev)
-        else:
-            _need_on(out, dev, torch.int8 if group else dt, "out", (M, K))
-        b.out = out.data_ptr()
+            out = torch.empty_like(h, dtype=torch.int8) if group else torch.empty_like(h)
+        b.out = _need_on(out, dev, torch.int8 if group else dt, "out", shape)
         if group:
             if out_scale is None:
                 out_scale = torch.empty(M, dtype=torch.float32, device=dev)
-            else:
-                _need_on(out_scale, dev, torch.float32, "out_scale", (M,))
-            b.out_scale = out_scale.data_ptr()
+            b.out_scale = _need_on(out_scale, dev, torch.float32, "out_scale", (M,))
     _call_on(h, "convrot_block_norm", ctypes.byref(b), _stream(h))
     if not want_out:
         return h_out
@@ -685,34 +677,31 @@ def convrot_grouped_linear(x, wq, w_scale, group, offsets, rows=None, bias=None,
     were (unset in an ``out`` allocated here)."""
     who = "convrot_grouped_linear"
     io = _io_of(x, "x")
-    _need(x, x.dtype, "x", 2)
     dev, dt = x.device, x.dtype
+    _need(x, dt, "x", 2)
     M, K = x.shape
     if wq.dim() != 3:
         raise ValueError(f"wq: expected 3 dimensions, got {wq.dim()}")
-    E, N = wq.shape[:2]
-    _need_on(wq, dev, torch.int8, "wq", (E, N, K))
+    E, N, _ = wq.shape
     per_row = w_scale.dim() == 2
-    _need_on(w_scale, dev, torch.float32, "w_scale", (E, N) if per_row else (E,))
-    _need_on(offsets, dev, torch.int32, "offsets", (E + 1,))
     P = M
     if rows is not None:
-        _need(rows, torch.int32, "rows", 1)
+        if rows.dim() != 1:
+            raise ValueError(f"rows: expected 1 dimension, got {rows.dim()}")
         P = rows.shape[0]
-        _need_on(rows, dev, torch.int32, "rows", (P,))
+        rows = _need_on(rows, dev, torch.int32, "rows", (P,))
     if bias is not None:
-        _need_on(bias, dev, dt, "bias", (E, N))
+        bias = _need_on(bias, dev, dt, "bias", (E, N))
     if out is None:
         out = torch.empty((P, N), dtype=dt, device=dev)
-    else:
-        _need_on(out, dev, dt, "out", (P, N))
     if workspace is None:
         workspace = torch.empty(max(convrot_grouped_workspace(M, K), 1), dtype=torch.uint8, device=dev)
-    else:
-        _need_on(workspace, dev, torch.uint8, "workspace", (workspace.numel(),))
-    _call_on(x, who, _ptr(x), io, M, K, _ptr(wq), _ptr(w_scale), CONVROT_SCALE_ROW if per_row else CONVROT_SCALE_TENSOR,
-             E, N, group, _ptr(bias), _ptr(offsets), _ptr(rows), P, _ptr(out), _ptr(workspace), workspace.numel(),
-             _stream(x))
+    ws_bytes = workspace.numel()
+    _call_on(x, who, x.data_ptr(), io, M, K, _need_on(wq, dev, torch.int8, "wq", (E, N, K)),
+             _need_on(w_scale, dev, torch.float32, "w_scale", (E, N) if per_row else (E,)),
+             CONVROT_SCALE_ROW if per_row else CONVROT_SCALE_TENSOR, E, N, group, bias,
+             _need_on(offsets, dev, torch.int32, "offsets", (E + 1,)), rows, P, _need_on(out, dev, dt, "out", (P, N)),
+             _need_on(workspace, dev, torch.uint8, "workspace", (ws_bytes,)), ws_bytes, _stream(x))
     return out
 
 
@@ -731,24 +720,24 @@ def convrot_linear_lora(x, wq, w_scale, group, lora_a, lora_b, lora_scale, offse
     [n + 1], lora_scale fp32 [n] and index int32 [M] (each token's adapter, outside
     [0, n) for none) are on the GPU; max_rank is the largest rank."""
     who = "convrot_linear_lora"
-    io, M, K, N, mode, y = _layer_args(who, x, wq, w_scale, bias, out)
+    io = _io_of(x, "x")
     dev, dt = x.device, x.dtype
-    R = lora_a.shape[0]
-    _need_on(lora_a, dev, dt, "lora_a", (R, K))
-    _need_on(lora_b, dev, dt, "lora_b", (R, N))
-    _need(lora_scale, torch.float32, "lora_scale", 1)
-    n = lora_scale.shape[0]
-    _need_on(lora_scale, dev, torch.float32, "lora_scale", (n,))
-    _need_on(offsets, dev, torch.int32, "offsets", (n + 1,))
-    _need_on(index, dev, torch.int32, "index", (M,))
-    for name, o in (("wq", wq), ("w_scale", w_scale), ("bias", bias), ("out", y)):
-        if o is not None and o.device != dev:
-            raise ValueError(f"{name}: expected a tensor on {dev}, got one on {o.device}")
+    _need(x, dt, "x", 2)
+    M, K = x.shape
+    N, R, n = wq.shape[0], lora_a.shape[0], lora_scale.numel()
+    mode = _scale_mode_of(w_scale, N, who)
+    if bias is not None:
+        bias = _need_on(bias, dev, dt, "bias", (N,))
+    if out is None:
+        out = torch.empty((M, N), dtype=dt, device=dev)
     if workspace is None:
         workspace = torch.empty(max(convrot_lora_workspace(M, K, N, max_rank), 1), dtype=torch.uint8, device=dev)
-    else:
-        _need_on(workspace, dev, torch.uint8, "workspace", (workspace.numel(),))
-    _call_on(x, who, _ptr(x), io, M, K, _ptr(wq), _ptr(w_scale), mode, N, group, _ptr(bias), _ptr(lora_a), _ptr(lora_b),
-             R, _ptr(lora_scale), _ptr(offsets), n, max_rank, _ptr(index), _ptr(y), _ptr(workspace),
-             workspace.numel(), _stream(x))
-    return y
+    ws_bytes = workspace.numel()
+    _call_on(x, who, x.data_ptr(), io, M, K, _need_on(wq, dev, torch.int8, "wq", (N, K)),
+             _need_on(w_scale, dev, torch.float32, "w_scale", (w_scale.numel(),)), mode, N, group, bias,
+             _need_on(lora_a, dev, dt, "lora_a", (R, K)), _need_on(lora_b, dev, dt, "lora_b", (R, N)), R,
+             _need_on(lora_scale, dev, torch.float32, "lora_scale", (n,)),
+             _need_on(offsets, dev, torch.int32, "offsets", (n + 1,)), n, max_rank,
+             _need_on(index, dev, torch.int32, "index", (M,)), _need_on(out, dev, dt, "out", (M, N)),
+             _need_on(workspace, dev, torch.uint8, "workspace", (ws_bytes,)), ws_bytes, _stream(x))
+    return out
