@@ -25,14 +25,27 @@ hipError_t launch_tile(const int8_t* xq, const float* x_scale, const int8_t* wq,
   return hipGetLastError();
 }
 
-// The tile goes by the mean rows of an expert, which is all the host knows.
+// The tile goes by the mean rows of an expert, which is all the host knows
+// (weights from HBM, 64 experts of 1536 x 2048, us):
+//   rows      4     8    16    32    64
+//   16 x 16  40.3  43.8  56.5  80.8   130
+//   64 x 64  37.4  37.4  42.8  53.1  68.5
+//   128x128  39.0  40.2  47.7  53.0  57.9
+//   192x288  45.0  46.6  49.4  54.0  57.4
+// and 32 of 2048 x 4096:  96   128   192   256
+//   128x128              88.3  87.6   108   134
+//   192x288              96.4   102   105   109
+// 64 x 64 up to 24 rows, 128 x 128 up to 160, then 192 x 288; 16 x 16 where
+// 64-channel tiles would not give every CU one.
 template <int EPI>
 hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
                       const uint16_t* bias, uint16_t* y, const Grouped& g, int64_t N, int64_t K, hipStream_t stream) {
   const int64_t mean = (static_cast<int64_t>(g.P) + g.experts - 1) / g.experts;
-  if (mean <= 16) return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
-  if (mean <= 64) return launch_tile<TileM64, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
-  if (mean <= 256) return launch_tile<TileMid, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+  const int64_t met = g.experts < g.P ? g.experts : g.P;
+  if (mean <= 16 && met * ((N + 63) / 64) < num_cus())
+    return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+  if (mean <= 24) return launch_tile<TileM64, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+  if (mean <= 160) return launch_tile<TileMid, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
   return launch_tile<TileTall, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
 }
 
