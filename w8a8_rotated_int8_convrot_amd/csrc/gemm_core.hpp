@@ -347,9 +347,13 @@ struct Lora {
   }
 };
 
-// The two ways to add them (lora_add, lora_gather below).
-struct LoraList : Lora { static constexpr bool kGather = false; };
-struct LoraGather : Lora { static constexpr bool kGather = true; };
+// The two ways to add them: LoraTile and lora_gather below.
+struct LoraList : Lora {};
+struct LoraGather : Lora {};
+
+struct LoraNone {
+  template <class... A> __device__ LoraNone(const A&...) {}
+};
 
 // Eight 16-bit values as fp32.
 template <bool F16>
@@ -385,81 +389,71 @@ __device__ inline void lora_b4(const uint16_t* row, int n, int N, bool vec, floa
 }
 
 // Adds the adapters' part to a tile's results, which the waves' blocks hold as
-// fp32 by their bits.  One step per 32 ranks of each adapter met among the
-// tile's tokens (neighbours in a batch mostly share theirs): channels x ranks
-// times ranks x tokens on the matrix cores, in the layout of the layer's own
-// blocks and summed onto them.  b is stored rank by rank, so a step's panel of
-// BN channels goes through LDS: a thread loads eight channels of one rank and
-// writes them apart, so that a lane finds eight ranks of one channel together.
-// Panels are double-buffered: the next one's loads run while this one's
-// products do, one barrier a step.  Where the tokens of a block have several
-// adapters a lane keeps the sum only if its token has the step's: a product
-// with zero instead would carry one adapter's infinities into other tokens.
-template <class T> struct LoraPanel {
-  static constexpr int kBytes = T::BN * 64;                      // 32 ranks of BN channels
-  static constexpr int kChunks = T::BN * 4;                      // eight channels of one rank each
+// fp32 by their bits.  The work is a list of units, 32 ranks of one adapter met
+// among the tile's tokens (neighbours in a batch mostly share theirs): channels
+// x ranks times ranks x tokens on the matrix cores, in the layout of the
+// layer's own blocks and summed onto them.  b is stored rank by rank, so a
+// unit's panel of BN channels goes through LDS: a thread loads eight channels
+// of one rank and writes them apart, so that a lane finds eight ranks of one
+// channel together.  UNITS panels are taken at a time, because what a unit
+// costs is the latency of its loads; begin() issues the first ones' (the tile
+// kernels call it before their main loop, where the index and the offsets have
+// time to arrive).  Where the tokens of a block have several adapters a lane
+// keeps the sum only if its token has the unit's: a product with zero instead
+// would carry one adapter's infinities into other tokens.
+template <class T, bool F16, int UNITS>
+struct LoraTile {
+  static constexpr int MF = T::MF, TN = T::TN, TM = T::TM;
+  static constexpr int OP = F16 ? kOpF16 : kOpBf16;
+  static constexpr int kSub = MF == 16 ? 1 : 2;              // products per block and unit: 32 or 16 ranks each
+  static constexpr int kIdx = (T::BM + 63) / 64;
+  static constexpr int kPanelBytes = T::BN * 64;             // 32 ranks of BN channels
+  static constexpr int kBytes = UNITS * kPanelBytes;
+  static constexpr int kChunks = T::BN * 4;                  // eight channels of one rank each
   static constexpr int kPerThread = (kChunks + T::kThreads - 1) / T::kThreads;
-  __device__ static int at(int n, int chunk) { return n * 64 + ((chunk ^ swz<T::MF, 64>(n)) << 4); }
-};
-
-template <class T, bool F16, class AccT>
-__device__ inline void lora_add(AccT (&acc)[T::TN][T::TM], const Lora& lo, char* panels, int tid, int wn, int wm,
-                                int n0, int m0, int M, int N) {
-  using P = LoraPanel<T>;
-  constexpr int MF = T::MF, TN = T::TN, TM = T::TM;
-  constexpr int OP = F16 ? kOpF16 : kOpBf16;
-  constexpr int kSub = MF == 16 ? 1 : 2;              // products per block and step: 32 or 16 ranks each
-  constexpr int kIdx = (T::BM + 63) / 64;
   using sum_t = typename Acc<MF, OP>::type;
-  const int lane = tid & 63;
-  const int r = lane & (MF - 1), c8 = lane / MF;      // fragment row, 8-rank chunk
-  // the tile's tokens, the same in every wave, for the list of its adapters
-  int idx[kIdx];
-  bool left[kIdx];
-#pragma unroll
-  for (int q = 0; q < kIdx; ++q) {
-    const int m = q * 64 + lane;
-    idx[q] = lo.index[min(m0 + m, M - 1)];
-    left[q] = m < T::BM && m0 + m < M && idx[q] >= 0 && idx[q] < lo.adapters;
-  }
-  int own[TM];
-  const uint16_t* t_row[TM];
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int m = min(m0 + wm * T::kWaveM + j * MF + r, M - 1);   // past the end: as the last token (discarded)
-    own[j] = lo.index[m];
-    t_row[j] = lo.t + static_cast<int64_t>(m) * lo.t_stride + c8 * 8;
-  }
-  int a = -1, row0 = 0, rank = 0, k = 0;
-  auto advance = [&]() -> bool {                      // the next 32 ranks
+
+  const Lora& lo;
+  const int N, M, n0, m0;
+  // the adapters of the tile's tokens, the same in every wave: index, rows
+  int idx[kIdx], row_of[kIdx], rank_of[kIdx];
+  uint64_t left[kIdx];
+  int a = -1, row0 = 0, rank = 0, k = 0;                     // the current unit
+  bool has[UNITS];
+  int unit_a[UNITS], unit_k[UNITS];
+  uint4 raw[UNITS][kPerThread];
+
+  __device__ LoraTile(const Lora& l, int n0_, int m0_, int M_, int N_) : lo(l), N(N_), M(M_), n0(n0_), m0(m0_) {}
+
+  __device__ bool advance() {
     k += 32;
     while (k >= rank) {
-      int next = -1;
+      a = -1;
 #pragma unroll
       for (int q = 0; q < kIdx; ++q) {
-        const uint64_t some = __ballot(left[q]);
-        if (next < 0 && some != 0) next = __builtin_amdgcn_readlane(idx[q], __builtin_ctzll(some));
+        if (a >= 0 || left[q] == 0) continue;
+        const int l = __builtin_ctzll(left[q]);
+        a = __builtin_amdgcn_readlane(idx[q], l);
+        row0 = __builtin_amdgcn_readlane(row_of[q], l);
+        rank = __builtin_amdgcn_readlane(rank_of[q], l);
       }
-      if (next < 0) return false;
+      if (a < 0) return false;
 #pragma unroll
-      for (int q = 0; q < kIdx; ++q) left[q] = left[q] && idx[q] != next;
-      a = next;
-      lo.range(a, row0, rank);
+      for (int q = 0; q < kIdx; ++q) left[q] &= ~__ballot(idx[q] == a);
       k = 0;
     }
     return true;
-  };
-  const bool vec = (N & 7) == 0 && (reinterpret_cast<uintptr_t>(lo.b) & 15) == 0;
-  uint4 raw[P::kPerThread];
-  auto load = [&]() {
+  }
+
+  __device__ void load(int tid, uint4 (&to)[kPerThread]) const {
+    const bool vec = (N & 7) == 0 && (reinterpret_cast<uintptr_t>(lo.b) & 15) == 0;
 #pragma unroll
-    for (int p = 0; p < P::kPerThread; ++p) {
+    for (int p = 0; p < kPerThread; ++p) {
       const int c = tid + p * T::kThreads;
-      if (P::kChunks % T::kThreads != 0 && c >= P::kChunks) continue;
       const int rr = k + (c & 31), n = n0 + (c >> 5) * 8;
-      const uint16_t* src = lo.b + static_cast<int64_t>(row0 + min(rr, rank - 1)) * N;
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (rr < rank) {
+      if (rr < rank && (kChunks % T::kThreads == 0 || c < kChunks)) {
+        const uint16_t* src = lo.b + static_cast<int64_t>(row0 + rr) * N;
         if (vec && n + 8 <= N) {
           v = *reinterpret_cast<const uint4*>(src + n);
         } else {
@@ -469,73 +463,134 @@ __device__ inline void lora_add(AccT (&acc)[T::TN][T::TM], const Lora& lo, char*
           v = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
         }
       }
-      raw[p] = v;
+      to[p] = v;
     }
-  };
-  if (!advance()) return;
-  load();
-  for (int step = 0;; ++step) {
-    char* panel = panels + (step & 1) * P::kBytes;
-    const int now = a;
-    v4i tf[TM][kSub];
-    bool any = false, whole[TM];
+  }
+
+  // the next units' panels, into registers
+  __device__ void fetch(int tid) {
+    bool more = true;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      more = more && advance();
+      has[u] = more;
+      unit_a[u] = a;
+      unit_k[u] = k;
+      if (more) load(tid, raw[u]);
+    }
+  }
+
+  __device__ void begin(int tid) {
+    const int lane = tid & 63;
+#pragma unroll
+    for (int q = 0; q < kIdx; ++q) {
+      const int m = q * 64 + lane;
+      idx[q] = lo.index[min(m0 + m, M - 1)];
+      const bool mine = m < T::BM && m0 + m < M && idx[q] >= 0 && idx[q] < lo.adapters;
+      lo.range(mine ? idx[q] : 0, row_of[q], rank_of[q]);
+      left[q] = __ballot(mine);
+    }
+    fetch(tid);
+  }
+
+  static __device__ int at(int n, int chunk) { return n * 64 + ((chunk ^ swz<MF, 64>(n)) << 4); }
+
+  // panels: kBytes of LDS that nobody else uses until the next barrier after
+  // this returns
+  template <class AccT>
+  __device__ void finish(AccT (&acc)[TN][TM], char* panels, int tid, int wn, int wm) {
+    const int lane = tid & 63;
+    const int r = lane & (MF - 1), c8 = lane / MF;      // fragment row, 8-rank chunk
+    int own[TM];
+    const uint16_t* t_row[TM];
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      whole[j] = __all(own[j] == now);
-      any = any || __any(own[j] == now);
-#pragma unroll
-      for (int u = 0; u < kSub; ++u) tf[j][u] = *reinterpret_cast<const v4i*>(t_row[j] + k + 16 * u);
+      const int m = min(m0 + wm * T::kWaveM + j * MF + r, M - 1);   // past the end: as the last token (discarded)
+      own[j] = lo.index[m];
+      t_row[j] = lo.t + static_cast<int64_t>(m) * lo.t_stride + c8 * 8;
     }
+    while (has[0]) {
+      v4i tf[UNITS][TM][kSub];
 #pragma unroll
-    for (int p = 0; p < P::kPerThread; ++p) {
-      const int c = tid + p * T::kThreads;
-      if (P::kChunks % T::kThreads != 0 && c >= P::kChunks) continue;
-      const int rr = c & 31, n = (c >> 5) * 8;
-      const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
+      for (int u = 0; u < UNITS; ++u) {
+        if (!has[u]) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        *reinterpret_cast<uint16_t*>(panel + P::at(n + e, rr >> 3) + 2 * (rr & 7)) =
-            static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-    }
-    const bool more = advance();
-    if (more) load();
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (any) {
+        for (int j = 0; j < TM; ++j)
 #pragma unroll
-      for (int i = 0; i < TN; ++i) {
-        v4i bf[kSub];
+          for (int s = 0; s < kSub; ++s) tf[u][j][s] = *reinterpret_cast<const v4i*>(t_row[j] + unit_k[u] + 16 * s);
+      }
 #pragma unroll
-        for (int u = 0; u < kSub; ++u)
-          bf[u] = *reinterpret_cast<const v4i*>(panel + P::at(wn * T::kWaveN + i * MF + r, 2 * u + c8));
+      for (int u = 0; u < UNITS; ++u) {
+        if (!has[u]) continue;
+        char* panel = panels + u * kPanelBytes;
+#pragma unroll
+        for (int p = 0; p < kPerThread; ++p) {
+          const int c = tid + p * T::kThreads;
+          if (kChunks % T::kThreads != 0 && c >= kChunks) continue;
+          const int rr = c & 31, n = (c >> 5) * 8;
+          const uint32_t w[4] = {raw[u][p].x, raw[u][p].y, raw[u][p].z, raw[u][p].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint16_t*>(panel + at(n + e, rr >> 3) + 2 * (rr & 7)) =
+                static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        if (!has[u]) continue;
+        const char* panel = panels + u * kPanelBytes;
+        bool any = false, whole[TM];
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
-          sum_t d = __builtin_bit_cast(sum_t, acc[i][j]);
+          whole[j] = __all(own[j] == unit_a[u]);
+          any = any || __any(own[j] == unit_a[u]);
+        }
+        if (!any) continue;
 #pragma unroll
-          for (int u = 0; u < kSub; ++u) d = mfma<MF, OP>(bf[u], tf[j][u], d);
-          if (whole[j]) {
-            acc[i][j] = __builtin_bit_cast(AccT, d);
-          } else {
+        for (int i = 0; i < TN; ++i) {
+          v4i bf[kSub];
 #pragma unroll
-            for (int e = 0; e < T::kAccRegs; ++e) acc[i][j][e] = own[j] == now ? __float_as_int(d[e]) : acc[i][j][e];
+          for (int s = 0; s < kSub; ++s)
+            bf[s] = *reinterpret_cast<const v4i*>(panel + at(wn * T::kWaveN + i * MF + r, 2 * s + c8));
+#pragma unroll
+          for (int j = 0; j < TM; ++j) {
+            sum_t d = __builtin_bit_cast(sum_t, acc[i][j]);
+#pragma unroll
+            for (int s = 0; s < kSub; ++s) d = mfma<MF, OP>(bf[s], tf[u][j][s], d);
+            if (whole[j]) {
+              acc[i][j] = __builtin_bit_cast(AccT, d);
+            } else {
+#pragma unroll
+              for (int e = 0; e < T::kAccRegs; ++e)
+                acc[i][j][e] = own[j] == unit_a[u] ? __float_as_int(d[e]) : acc[i][j][e];
+            }
           }
         }
       }
+      if (!has[UNITS - 1]) return;
+      fetch(tid);
+      if (!has[0]) return;
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the panels are read: the next may come
     }
-    if (!more) return;
   }
-}
+};
 
 // The same for few tokens, each with an adapter of its own, where the list
-// above would be as long as the tile: every lane adds its own token's ranks
-// one by one, four channels at a time.  Rows of b come in 8-byte pieces, eight
-// ranks in flight.
-template <class T, bool F16, class AccT>
-__device__ inline void lora_gather(AccT (&acc)[T::TN][T::TM], const Lora& lo, int lane, int n_first, int m_first,
-                                   int M, int N) {
+// above would be as long as the tile: every lane sums its own token's ranks one
+// by one, four channels at a time, into `part` (added to the layer's results
+// later).  Rows of b come in 8-byte pieces, eight ranks in flight.
+template <class T, bool F16>
+__device__ inline void lora_gather(float (&part)[T::TN][T::TM][T::kAccRegs], const Lora& lo, int lane, int n_first,
+                                   int m_first, int M, int N) {
   constexpr int MF = T::MF;
   const bool vec = (N & 3) == 0 && (reinterpret_cast<uintptr_t>(lo.b) & 7) == 0;
 #pragma unroll
   for (int j = 0; j < T::TM; ++j) {
+#pragma unroll
+    for (int i = 0; i < T::TN; ++i)
+#pragma unroll
+      for (int e = 0; e < T::kAccRegs; ++e) part[i][j][e] = 0.0f;
     const int m = m_first + j * MF + (lane & (MF - 1));
     const int a = m < M ? lo.index[m] : -1;
     if (a < 0 || a >= lo.adapters) continue;
@@ -558,9 +613,7 @@ __device__ inline void lora_gather(AccT (&acc)[T::TN][T::TM], const Lora& lo, in
             float v[4];
             lora_b4<F16>(row, n, N, vec, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              acc[i][j][4 * g + e] =
-                  __float_as_int(__builtin_fmaf(tv[q], v[e], __int_as_float(acc[i][j][4 * g + e])));
+            for (int e = 0; e < 4; ++e) part[i][j][4 * g + e] = __builtin_fmaf(tv[q], v[e], part[i][j][4 * g + e]);
           }
         }
       }
@@ -631,8 +684,12 @@ __device__ inline bool grouped_tile(const Grouped& g, int tiles_n, int& e, int& 
   }
 }
 
+// Waves per SIMD that registers have to leave room for: two workgroups of a
+// 128 x 128 tile share a CU, with adapters too.
+template <class T, class X> constexpr int kMinWaves = std::is_same_v<X, LoraList> && T::BN == 128 ? 2 : 1;
+
 template <class T, int EPI, class X = NoExtra>
-__global__ __launch_bounds__(T::kThreads) void gemm_i8_kernel(
+__global__ __launch_bounds__(T::kThreads, (kMinWaves<T, X>)) void gemm_i8_kernel(
     const int8_t* __restrict__ wq, const int8_t* __restrict__ xq, int M, int N, int K,
     int tiles_n, int tiles_m, const float* __restrict__ x_scale,
     const float* __restrict__ w_scale, const uint16_t* __restrict__ bias,
@@ -889,6 +946,15 @@ __global__ __launch_bounds__(T::kThreads) void gemm_i8_kernel(
 #pragma unroll
     for (int s = 0; s < T::kStages - 1; ++s) issue_slab(min(s, KT - 1), s);
   }
+  // adapters: the list's first panels, or the tokens' own sums, while the first
+  // slabs are on their way
+  constexpr bool GATHER = std::is_same_v<X, LoraGather>;
+  constexpr int kUnits = 2;       // adapter panels at a time
+  using lora_t = std::conditional_t<std::is_same_v<X, LoraList>, LoraTile<T, kF16, kUnits>, LoraNone>;
+  lora_t lora(extra, n0, m0, M, N);
+  float part[GATHER ? T::TN : 1][GATHER ? T::TM : 1][GATHER ? T::kAccRegs : 1];
+  if constexpr (GATHER) lora_gather<T, kF16>(part, extra, lane, n0 + wn * T::kWaveN, m0 + wm * T::kWaveM, M, N);
+  else if constexpr (LORA) lora.begin(tid);
   KFrag f0, f1;
   if constexpr (kThirdA) {
     // As the two stages below, with the weight of slab kt+3 and the tokens of
@@ -1105,10 +1171,9 @@ __global__ __launch_bounds__(T::kThreads) void gemm_i8_kernel(
       }
     }
     if constexpr (LORA) {
-      if constexpr (X::kGather) {
-        lora_gather<T, kF16>(acc, extra, lane, n0 + wn * T::kWaveN, m0 + wm * T::kWaveM, M, N);
-      } else {
-        lora_add<T, kF16>(acc, extra, lds, tid, wn, wm, n0, m0, M, N);
+      if constexpr (!GATHER) {
+        static_assert(LoraTile<T, kF16, kUnits>::kBytes <= T::kLdsBytes, "panels fit the stages");
+        lora.finish(acc, lds, tid, wn, wm);
         __syncthreads();          // the panels make room for the output tile
       }
 #pragma unroll
@@ -1119,7 +1184,10 @@ __global__ __launch_bounds__(T::kThreads) void gemm_i8_kernel(
           for (int j = 0; j < T::TM; ++j) {
             float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __int_as_float(acc[i][j][4 * g + e]);
+            for (int e = 0; e < 4; ++e) {
+              v[e] = __int_as_float(acc[i][j][4 * g + e]);
+              if constexpr (GATHER) v[e] += part[i][j][4 * g + e];
+            }
             put4(i, j, g, v);
           }
     }
@@ -1460,7 +1528,8 @@ __global__ __launch_bounds__(T::kThreads) void gemm_persist_kernel(
   constexpr int kStores = T::MF == 32 ? T::TN * T::TM * 2 : T::TN * T::TM / 2;
   constexpr int kParamFloats = ((kParams > 0 ? kParams : 1) + 3) / 4 * 4;
   constexpr int kPanelAt = T::kLdsBytes + 2 * kParamFloats * 4;
-  __shared__ __attribute__((aligned(16))) char lds[kPanelAt + (LORA ? 2 * LoraPanel<T>::kBytes : 0)];
+  constexpr int kUnits = 1;       // adapter panels at a time: registers hold no more here
+  __shared__ __attribute__((aligned(16))) char lds[kPanelAt + (LORA ? kUnits * T::BN * 64 : 0)];
   float* ptab0 = reinterpret_cast<float*>(lds + T::kLdsBytes);
 
   const int total = tiles_n * tiles_m;
@@ -1854,7 +1923,9 @@ __global__ __launch_bounds__(T::kThreads) void gemm_persist_kernel(
             for (int e = 0; e < 4; ++e) acc[i][j][4 * gg + e] = __float_as_int(v[e]);
           }
       }
-      lora_add<T, kF16>(acc, extra, lds + kPanelAt, tid_e, wn, wm, n0, m0, M, N);
+      LoraTile<T, kF16, kUnits> lora(extra, n0, m0, M, N);
+      lora.begin(tid_e);
+      lora.finish(acc, lds + kPanelAt, tid_e, wn, wm);
     }
     constexpr int kIStep = T::MF == 32 ? 1 : 2;
     // A whole tile's dequant epilogue with another tile to follow runs
