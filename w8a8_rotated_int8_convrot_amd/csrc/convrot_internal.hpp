@@ -35,6 +35,10 @@ hipError_t launch_rotate_quant(const uint16_t* x, int64_t M, int64_t K, int grou
 hipError_t launch_rotate_quant_f16(const uint16_t* x, int64_t M, int64_t K, int group,
                                    int8_t* q, float* scale, hipStream_t stream);
 
+// Whether an activation of this size takes the row kernel (a workgroup per
+// token, the row in registers) rather than the token-block kernel.
+bool rotate_by_row(int64_t M, int64_t K);
+
 // Weight preparation.  in_dtype: kInF32, kInBf16 or kInF16.  Tensorwise (one
 // scale; `amax_cell` is one 4-byte device word of scratch) or, with
 // row_scale, one scale per output channel (w_scale [N]; no scratch).
@@ -96,12 +100,14 @@ inline bool lora_by_token(int64_t M, int64_t adapters) { return M <= 16 || (M <=
 // type, t[m][r] = scale[a] * (row offsets[a] + r of a_rows [ranks, K]) . x[m]
 // with a = index[m]; zero from the adapter's rank on, unset for a token whose
 // index is outside [0, adapters).  t_stride: max_rank rounded up to 32.  sums:
-// lora_parts(M, K) * M * t_stride floats (not used token by token).
+// kMaxLoraParts * M * t_stride floats (not used token by token).  Rotates and
+// quantizes x too (xq, xs as launch_rotate_quant), in the same launch where the
+// row kernel would do it.
 constexpr int kMaxLoraParts = 8;
-int lora_parts(int64_t M, int64_t K);
-hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, bool f16, const uint16_t* a, int64_t ranks,
-                            const float* scale, const int32_t* offsets, int64_t adapters, const int32_t* index,
-                            int64_t max_rank, uint16_t* t, int64_t t_stride, float* sums, hipStream_t stream);
+hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, int group, bool f16, int8_t* xq, float* xs,
+                            const uint16_t* a, int64_t ranks, const float* scale, const int32_t* offsets,
+                            int64_t adapters, const int32_t* index, int64_t max_rank, uint16_t* t, int64_t t_stride,
+                            float* sums, hipStream_t stream);
 
 // The layer's product with the adapters' second one, t . b (b [ranks, N]),
 // added before the output is rounded (gemm_lora.hip).

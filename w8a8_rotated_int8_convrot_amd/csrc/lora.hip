@@ -12,14 +12,16 @@
 // ranks, v_mfma_*_16x16x32) in registers, so a loaded piece of x serves 16 NB
 // ranks and a piece of the adapter 64 tokens.  What bounds it is what a CU can
 // draw from its L2 (about 27 bytes a cycle here), and 64 tokens a workgroup
-// with K split over gridDim.z move half of what 16 tokens with all of K do
-// while filling the chip.  The waves' sums are joined through LDS, the parts
-// of K by lora_sum_kernel, both in a fixed order.  The adapters met among the
+// with K split over gridDim.y move half of what 16 tokens with all of K do
+// while filling the chip.  A wave loads two pieces of K before it multiplies.  The waves' sums are joined through LDS, the parts
+// of K by lora_sum, both in a fixed order.  The adapters met among the
 // tokens are taken one after another, or, where the tiles would leave the chip
-// idle, dealt out over gridDim.y workgroups.
+// idle, dealt out over gridDim.z workgroups.
 //
-// lora_dot_kernel, for few tokens with adapters of their own: a wave per token
-// and two of its ranks, each lane a plain dot product over its part of K.
+// lora_dot, for few tokens with adapters of their own: a wave per token and two
+// of its ranks, each lane a plain dot product over its part of K.
+#include <type_traits>
+
 #include "convrot_internal.hpp"
 #include "rotate_device.hpp"
 
@@ -61,7 +63,7 @@ __device__ inline uint32_t round16(float v) {
   else return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
-// sums [gridDim.z][M][t_stride] fp32
+// sums [gridDim.y][M][t_stride] fp32
 template <bool F16, int NB>
 __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* __restrict__ sums) {
   __shared__ __attribute__((aligned(16))) v4f part[kWaves][4][NB][64];
@@ -71,12 +73,9 @@ __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* _
   const int m0 = blockIdx.x * kTile;
   const int M = p.M, K = p.K;
   const int mine = p.index[min(m0 + lane, M - 1)];
-  const uint16_t* x_row[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x_row[j] = p.x + static_cast<int64_t>(min(m0 + 16 * j + r, M - 1)) * K + k8;
   // 64 elements of K at a time, dealt out to the waves of all parts
-  const int step = gridDim.z * kWaves * 64;
-  const int k0 = (blockIdx.z * kWaves + wave) * 64;
+  const int step = gridDim.y * kWaves * 64;
+  const int k0 = (blockIdx.y * kWaves + wave) * 64;
   // after the sum this wave stores token block `wave`
   const int m_out = m0 + 16 * wave + r;
   const int own = m_out < M ? p.index[m_out] : -1;
@@ -84,10 +83,19 @@ __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* _
   uint64_t left = __ballot(m0 + lane < M && mine >= 0 && mine < p.adapters);
   for (int turn = 0; left != 0; ++turn) {
     const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-    left &= ~__ballot(mine == a);
-    if (turn % gridDim.y != blockIdx.y) continue;
+    const uint64_t same = __ballot(m0 + lane < M && mine == a);
+    left &= ~same;
+    if (turn % gridDim.z != blockIdx.z) continue;
     int row0, rank;
     p.range(a, row0, rank);
+    // a block of 16 tokens without this adapter reads the rows of one with it
+    // (its sums are not used), so that it draws nothing more from L2
+    const uint16_t* x_row[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int from = (same >> (16 * j) & 0xffff) != 0 ? j : __builtin_ctzll(same) / 16;
+      x_row[j] = p.x + static_cast<int64_t>(min(m0 + 16 * from + r, M - 1)) * K + k8;
+    }
     for (int base = 0; base < rank; base += 16 * NB) {
       v4f acc[4][NB] = {};
       // rows past the rank: the last one (its sums are not used)
@@ -95,21 +103,31 @@ __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* _
 #pragma unroll
       for (int q = 0; q < NB; ++q)
         w_row[q] = p.a_rows + static_cast<int64_t>(row0 + min(base + 16 * q + r, rank - 1)) * K + k8;
-      for (int k = k0; k < K; k += step) {
-        v4i xf[2][4], wf[2][NB];
+      for (int k = k0; k < K; k += 2 * step) {
+        const bool two = k + step < K;
+        v4i xf[2][2][4], wf[2][2][NB];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int d = 0; d < 2; ++d) {
+          const int kd = d == 1 && two ? k + step : k;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) xf[h][j] = *reinterpret_cast<const v4i*>(x_row[j] + k + 32 * h);
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int q = 0; q < NB; ++q) wf[h][q] = *reinterpret_cast<const v4i*>(w_row[q] + k + 32 * h);
+            for (int j = 0; j < 4; ++j) xf[d][h][j] = *reinterpret_cast<const v4i*>(x_row[j] + kd + 32 * h);
+#pragma unroll
+            for (int q = 0; q < NB; ++q) wf[d][h][q] = *reinterpret_cast<const v4i*>(w_row[q] + kd + 32 * h);
+          }
         }
+        __builtin_amdgcn_sched_barrier(0);      // every load before the first product
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int d = 0; d < 2; ++d) {
+          if (d == 1 && !two) break;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int q = 0; q < NB; ++q) acc[j][q] = mfma<F16>(wf[h][q], xf[h][j], acc[j][q]);
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int q = 0; q < NB; ++q) acc[j][q] = mfma<F16>(wf[d][h][q], xf[d][h][j], acc[j][q]);
+        }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -124,29 +142,34 @@ __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* _
         for (int w = 1; w < kWaves; ++w) sum += part[w][wave][q][lane];
         const int rank0 = base + 16 * q + (lane >> 4) * 4;
         if (own == a && rank0 < p.t_stride)
-          *reinterpret_cast<v4f*>(sums + (static_cast<int64_t>(blockIdx.z) * M + m_out) * p.t_stride + rank0) = sum;
+          *reinterpret_cast<v4f*>(sums + (static_cast<int64_t>(blockIdx.y) * M + m_out) * p.t_stride + rank0) = sum;
       }
       __syncthreads();
     }
   }
 }
 
-// t from the parts of K: a thread per four ranks of a token.
+// t from the parts of K: thread i of a thread per four ranks of a token.
 template <bool F16>
-__global__ __launch_bounds__(256) void lora_sum_kernel(Down p, const float* __restrict__ sums, int parts) {
+__device__ inline void lora_sum(const Down& p, const float* __restrict__ sums, int parts, int64_t i) {
   const int quads = p.t_stride / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t m = i / quads;
   if (m >= p.M) return;
+  const int rank0 = static_cast<int>(i - m * quads) * 4;
+  // every part is read before the token's adapter is known (what an unwritten
+  // one holds is not used), so that one latency covers them all
+  v4f v[kMaxLoraParts];
+#pragma unroll
+  for (int z = 0; z < kMaxLoraParts; ++z)
+    v[z] = *reinterpret_cast<const v4f*>(sums + (min(z, parts - 1) * static_cast<int64_t>(p.M) + m) * p.t_stride + rank0);
   const int a = p.index[m];
   if (a < 0 || a >= p.adapters) return;
   int row0, rank;
   p.range(a, row0, rank);
-  const int rank0 = static_cast<int>(i - m * quads) * 4;
-  v4f sum = {};
-  if (rank0 < rank)
-    for (int z = 0; z < parts; ++z)
-      sum += *reinterpret_cast<const v4f*>(sums + (z * static_cast<int64_t>(p.M) + m) * p.t_stride + rank0);
+  v4f sum = v[0];
+#pragma unroll
+  for (int z = 1; z < kMaxLoraParts; ++z)
+    if (z < parts) sum += v[z];
   const float s = p.scale[a];
   uint32_t h[4];
 #pragma unroll
@@ -154,13 +177,12 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(Down p, const float* __re
   *reinterpret_cast<uint2*>(p.t + m * p.t_stride + rank0) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// Ranks 8 * blockIdx.y + 2 * wave + (0, 1) of token blockIdx.x.
+// Ranks 8 * part + 2 * wave + (0, 1) of token m.
 template <typename In>
-__global__ __launch_bounds__(256) void lora_dot_kernel(Down p) {
+__device__ inline void lora_dot(const Down& p, int64_t m, int part) {
   constexpr bool F16 = !std::is_same_v<In, uint16_t>;
-  const int64_t m = blockIdx.x;
   const int lane = threadIdx.x & 63;
-  const int rank0 = blockIdx.y * 8 + (threadIdx.x >> 6) * 2;
+  const int rank0 = part * 8 + (threadIdx.x >> 6) * 2;
   const int a = p.index[m];
   if (a < 0 || a >= p.adapters) return;
   int row0, rank;
@@ -202,52 +224,107 @@ __global__ __launch_bounds__(256) void lora_dot_kernel(Down p) {
   }
 }
 
+// The rest of the first product (DOTS: token by token, else the sum of the
+// parts of K), and beside it, in the first `rows` workgroups, the rotation and
+// the codes of the tokens: two kernels of a few microseconds in the time of
+// one.  G = 0: the tokens are coded elsewhere.
+template <typename In, bool DOTS, int G, int CPT>
+__global__ __launch_bounds__(kThreads) void lora_rows_kernel(Down p, int rows, int8_t* __restrict__ xq,
+                                                             float* __restrict__ xs,
+                                                             const float* __restrict__ sums, int parts) {
+  const int block = static_cast<int>(blockIdx.x) - rows;
+  if constexpr (G != 0) {
+    if (block < 0) {
+      const int64_t m = blockIdx.x;
+      rotate_quant_row<G, CPT>(reinterpret_cast<const In*>(p.x) + m * p.K, p.K, xq + m * p.K, xs + m);
+      return;
+    }
+  }
+  if constexpr (DOTS) {
+    const int per_token = p.t_stride / 8;
+    lora_dot<In>(p, block / per_token, block % per_token);
+  } else {
+    lora_sum<!std::is_same_v<In, uint16_t>>(p, sums, parts, static_cast<int64_t>(block) * kThreads + threadIdx.x);
+  }
+}
+
 template <bool F16, int NB>
 hipError_t launch_down(const Down& p, float* sums, int parts, hipStream_t stream) {
   const int tiles = (p.M + kTile - 1) / kTile;
-  const int most = p.adapters < kTile ? p.adapters : kTile;         // adapters a tile can hold
-  const int want = (2 * num_cus() + tiles * parts - 1) / (tiles * parts);
-  const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(want < most ? want : most),
-                  static_cast<uint32_t>(parts));
+  // Workgroups that share a tile's adapters: one, and one and a half times as
+  // many as the runs of a batch of this many adapters put into a tile (the
+  // tile with the most adapters is what one waits for; the workgroups without
+  // an adapter end at once, and come last in the grid).
+  const int64_t cuts = (int64_t{3} * p.adapters * kTile / 2 + p.M - 1) / p.M;
+  const int64_t most = p.adapters < kTile ? p.adapters : kTile;         // adapters a tile can hold
+  const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(parts),
+                  static_cast<uint32_t>(1 + cuts < most ? 1 + cuts : most));
   hipLaunchKernelGGL((lora_down_kernel<F16, NB>), grid, dim3(kWaves * 64), 0, stream, p, sums);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  const int64_t threads = static_cast<int64_t>(p.M) * (p.t_stride / 4);
-  hipLaunchKernelGGL(lora_sum_kernel<F16>, dim3(static_cast<uint32_t>((threads + 255) / 256)), dim3(256), 0, stream, p,
-                     sums, parts);
   return hipGetLastError();
 }
 
-template <bool F16>
-hipError_t launch(const Down& p, float* sums, int parts, bool dots, hipStream_t stream) {
-  using In = std::conditional_t<F16, _Float16, uint16_t>;
-  if (dots) {
-    hipLaunchKernelGGL(lora_dot_kernel<In>, dim3(static_cast<uint32_t>(p.M), static_cast<uint32_t>(p.t_stride / 8)),
-                       dim3(256), 0, stream, p);
+template <typename In, bool DOTS>
+hipError_t launch_rows(const Down& p, int group, int8_t* xq, float* xs, const float* sums, int parts,
+                       hipStream_t stream) {
+  // group 0: coded elsewhere
+  const int rows = group != 0 ? p.M : 0;
+  const int64_t work = DOTS ? static_cast<int64_t>(p.M) * (p.t_stride / 8)
+                            : (static_cast<int64_t>(p.M) * (p.t_stride / 4) + kThreads - 1) / kThreads;
+  const dim3 grid(static_cast<uint32_t>(rows + work));
+  const int slots = (p.K + kThreads * 8 - 1) / (kThreads * 8);
+  auto go = [&](auto g_c, auto cpt_c) {
+    hipLaunchKernelGGL((lora_rows_kernel<In, DOTS, decltype(g_c)::value, decltype(cpt_c)::value>), grid,
+                       dim3(kThreads), 0, stream, p, rows, xq, xs, sums, parts);
     return hipGetLastError();
+  };
+  auto go_group = [&](auto g_c) {
+    if (slots <= 1) return go(g_c, std::integral_constant<int, 1>{});
+    if (slots <= 2) return go(g_c, std::integral_constant<int, 2>{});
+    return go(g_c, std::integral_constant<int, 4>{});
+  };
+  if (group == 0) return go(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
+  if (group == 128) return go_group(std::integral_constant<int, 128>{});
+  return go_group(std::integral_constant<int, 256>{});
+}
+
+// Parts of K: enough for two workgroups a CU, each with at least one piece of
+// K for every wave.
+int parts_of(int64_t M, int64_t K) {
+  const int64_t tiles = (M + kTile - 1) / kTile;
+  int64_t parts = 2 * num_cus() / tiles;
+  if (parts > K / (64 * kWaves)) parts = K / (64 * kWaves);
+  return static_cast<int>(parts < 1 ? 1 : parts > kMaxLoraParts ? kMaxLoraParts : parts);
+}
+
+template <bool F16>
+hipError_t launch(const Down& p, int group, int8_t* xq, float* xs, float* sums, bool dots, hipStream_t stream) {
+  using In = std::conditional_t<F16, _Float16, uint16_t>;
+  if (!rotate_by_row(p.M, p.K)) {
+    const hipError_t e = F16 ? launch_rotate_quant_f16(p.x, p.M, p.K, group, xq, xs, stream)
+                             : launch_rotate_quant(p.x, p.M, p.K, group, xq, xs, stream);
+    if (e != hipSuccess) return e;
+    group = 0;
   }
-  if (p.max_rank <= 16) return launch_down<F16, 1>(p, sums, parts, stream);
-  if (p.max_rank <= 32) return launch_down<F16, 2>(p, sums, parts, stream);
-  return launch_down<F16, 4>(p, sums, parts, stream);
+  if (dots) return launch_rows<In, true>(p, group, xq, xs, nullptr, 0, stream);
+  const int parts = parts_of(p.M, p.K);
+  const hipError_t e = p.max_rank <= 16   ? launch_down<F16, 1>(p, sums, parts, stream)
+                       : p.max_rank <= 32 ? launch_down<F16, 2>(p, sums, parts, stream)
+                                          : launch_down<F16, 4>(p, sums, parts, stream);
+  if (e != hipSuccess) return e;
+  return launch_rows<In, false>(p, group, xq, xs, sums, parts, stream);
 }
 
 }  // namespace
 
-int lora_parts(int64_t M, int64_t K) {
-  const int64_t tiles = (M + kTile - 1) / kTile;
-  int64_t parts = 2 * num_cus() / tiles;
-  if (parts > K / 256) parts = K / 256;
-  return static_cast<int>(parts < 1 ? 1 : parts > kMaxLoraParts ? kMaxLoraParts : parts);
-}
-
-hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, bool f16, const uint16_t* a, int64_t ranks,
-                            const float* scale, const int32_t* offsets, int64_t adapters, const int32_t* index,
-                            int64_t max_rank, uint16_t* t, int64_t t_stride, float* sums, hipStream_t stream) {
+hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, int group, bool f16, int8_t* xq, float* xs,
+                            const uint16_t* a, int64_t ranks, const float* scale, const int32_t* offsets,
+                            int64_t adapters, const int32_t* index, int64_t max_rank, uint16_t* t, int64_t t_stride,
+                            float* sums, hipStream_t stream) {
   if (M == 0) return hipSuccess;
   const Down p{x, a, scale, offsets, index, t, static_cast<int>(M), static_cast<int>(K), static_cast<int>(ranks),
                static_cast<int>(adapters), static_cast<int>(max_rank), static_cast<int>(t_stride)};
-  const int parts = lora_parts(M, K);
   const bool dots = lora_by_token(M, adapters);
-  return f16 ? launch<true>(p, sums, parts, dots, stream) : launch<false>(p, sums, parts, dots, stream);
+  return f16 ? launch<true>(p, group, xq, xs, sums, dots, stream) : launch<false>(p, group, xq, xs, sums, dots, stream);
 }
 
 }  // namespace convrot

@@ -190,8 +190,7 @@ int convrot_linear_lora(const void* x, int io_dtype, int64_t M, int64_t K, const
   for (int64_t r0 = 0; r0 < M; r0 += l.S) {
     const int64_t rows = std::min(M - r0, l.S);
     const auto* xr = static_cast<const uint16_t*>(x) + r0 * K;
-    if (hipError_t e = rotate_quant(xr, f16, rows, K, group, xq, xs, s); e != hipSuccess) return hip_status(e, who);
-    if (hipError_t e = launch_lora_down(xr, rows, K, f16, static_cast<const uint16_t*>(lora_a), R, lora_scale, offsets,
+    if (hipError_t e = launch_lora_down(xr, rows, K, group, f16, xq, xs, static_cast<const uint16_t*>(lora_a), R, lora_scale, offsets,
                                         n_adapters, index + r0, max_rank, t, l.t_stride, sums, s);
         e != hipSuccess)
       return hip_status(e, who);

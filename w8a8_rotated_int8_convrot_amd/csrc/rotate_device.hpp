@@ -9,6 +9,8 @@
 namespace convrot {
 namespace {
 
+constexpr int kThreads = 256;          // of a workgroup that holds one row
+
 // The float nearest to 1/sqrt(g): 2^-3.5 rounds to 0x3db504f3 for g = 128;
 // 2^-4 is exact for g = 256.
 template <int G> struct RotScale;
@@ -114,6 +116,59 @@ __device__ inline uint2 pack8(const float (&v)[8], float s) {
     for (int i = 0; i < 4; ++i) hi |= (static_cast<uint32_t>(quant_code(v[4 + i], s)) & 0xffu) << (8 * i);
   }
   return make_uint2(lo, hi);
+}
+
+// Maximum over the workgroup (max is exact and order-free): inside each
+// 16-lane row by DPP moves, over the four rows of a wave by lane reads, over
+// the waves through LDS.
+__device__ inline float block_max(float a) {
+  __shared__ float part[kThreads / 64];
+  a = fmaxf(a, lane_xor<1>(a));
+  a = fmaxf(a, lane_xor<2>(a));
+  a = fmaxf(a, lane_xor<4>(a));
+  a = fmaxf(a, lane_xor<8>(a));
+  a = fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 0)),
+                  __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 16))),
+            fmaxf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 32)),
+                  __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 48))));
+  const int wave = threadIdx.x / 64;
+  if ((threadIdx.x & 63) == 0) part[wave] = a;
+  __syncthreads();
+  float r = part[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 64; ++w) r = fmaxf(r, part[w]);
+  return r;
+}
+
+// Rotate + quantize one row of at most kThreads * 8 * CPT values by a workgroup
+// of kThreads: the row kernel of rotate_quant.hip for a row that fits its
+// registers, for kernels that do other work beside it.
+template <int G, int CPT, typename In>
+__device__ inline void rotate_quant_row(const In* __restrict__ x, int K, int8_t* __restrict__ q,
+                                        float* __restrict__ scale) {
+  const int tid = threadIdx.x;
+  float v[CPT][8];
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) {
+    const int e = (j * kThreads + tid) * 8;
+    if (e < K) load8(x + e, v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) {
+    if ((j * kThreads + tid) * 8 < K) {
+      rotate_chunk<G>(v[j], tid % (G / 8));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[j][i]));
+    }
+  }
+  const float s = block_max(amax) / 127.0f;
+  if (tid == 0) *scale = s;
+#pragma unroll
+  for (int j = 0; j < CPT; ++j) {
+    const int e = (j * kThreads + tid) * 8;
+    if (e < K) *reinterpret_cast<uint2*>(q + e) = pack8(v[j], s);
+  }
 }
 
 }  // namespace

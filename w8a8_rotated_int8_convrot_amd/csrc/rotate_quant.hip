@@ -30,32 +30,9 @@
 namespace convrot {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxChunksPerThread = 6;   // rows up to 12288 elements are rotated once
 
 enum Mode { kActQuant = 0, kWeightAbsmax = 1, kWeightQuant = 2 };
-
-// Maximum over the workgroup (max is exact and order-free): inside each
-// 16-lane row by DPP moves, over the four rows of a wave by lane reads, over
-// the waves through LDS.
-__device__ inline float block_max(float a) {
-  __shared__ float part[kThreads / 64];
-  a = fmaxf(a, lane_xor<1>(a));
-  a = fmaxf(a, lane_xor<2>(a));
-  a = fmaxf(a, lane_xor<4>(a));
-  a = fmaxf(a, lane_xor<8>(a));
-  a = fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 0)),
-                  __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 16))),
-            fmaxf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 32)),
-                  __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 48))));
-  const int wave = threadIdx.x / 64;
-  if ((threadIdx.x & 63) == 0) part[wave] = a;
-  __syncthreads();
-  float r = part[0];
-#pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) r = fmaxf(r, part[w]);
-  return r;
-}
 
 template <int G, int CPT, typename In, int MODE>
 __global__ __launch_bounds__(kThreads) void rotate_rows_kernel(
@@ -514,7 +491,7 @@ hipError_t rotate_quant_16(const In16* x, int64_t M, int64_t K, int group, int8_
   // a row kernel lane holds four or more chunks in a serial chain, and the
   // block kernel wins at any batch (16 x 12288: 5.7 us instead of 8.1;
   // 16 x 16384, rotated twice by the row kernel: 5.8 instead of 16.1).
-  if (K <= kMaxBlockK && (M * K > kSmallBatchElems || K >= 8192)) {
+  if (K <= kMaxBlockK && !rotate_by_row(M, K)) {
     // Rows per workgroup: as many as fit (256 blocks, 512 lanes), but no more
     // than an even share of two workgroups per CU, so that every CU gets the
     // same work when the batch is small (M = 4608, K = 3072: 512 workgroups of
@@ -547,6 +524,8 @@ hipError_t rotate_quant_16(const In16* x, int64_t M, int64_t K, int group, int8_
 }
 
 }  // namespace
+
+bool rotate_by_row(int64_t M, int64_t K) { return M * K <= kSmallBatchElems && K < 8192; }
 
 int num_cus() {
   // read once (thread-safe static initialisation), from the device current
