@@ -94,7 +94,7 @@ def lib() -> ctypes.CDLL:
 
 
 def _call(name, *args):
-    rc = getattr(lib(), name)(*args)
+    rc = getattr(_lib or lib(), name)(*args)
     if rc != 0:
         raise ConvrotError(name, rc, last_error())
     return rc

@@ -13,7 +13,8 @@
 // ranks and a piece of the adapter 64 tokens.  What bounds it is what a CU can
 // draw from its L2 (about 27 bytes a cycle here), and 64 tokens a workgroup
 // with K split over gridDim.y move half of what 16 tokens with all of K do
-// while filling the chip.  A wave loads two pieces of K before it multiplies.  The waves' sums are joined through LDS, the parts
+// while filling the chip.  A wave that has several pieces of K loads two before it
+// multiplies.  The waves' sums are joined through LDS, the parts
 // of K by lora_sum, both in a fixed order.  The adapters met among the
 // tokens are taken one after another, or, where the tiles would leave the chip
 // idle, dealt out over gridDim.z workgroups.
@@ -64,7 +65,7 @@ __device__ inline uint32_t round16(float v) {
 }
 
 // sums [gridDim.y][M][t_stride] fp32
-template <bool F16, int NB>
+template <bool F16, int NB, int DEPTH>
 __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* __restrict__ sums) {
   __shared__ __attribute__((aligned(16))) v4f part[kWaves][4][NB][64];
   const int lane = threadIdx.x & 63;
@@ -73,9 +74,10 @@ __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* _
   const int m0 = blockIdx.x * kTile;
   const int M = p.M, K = p.K;
   const int mine = p.index[min(m0 + lane, M - 1)];
-  // 64 elements of K at a time, dealt out to the waves of all parts
-  const int step = gridDim.y * kWaves * 64;
-  const int k0 = (blockIdx.y * kWaves + wave) * 64;
+  // this part's pieces of 64 elements are neighbours, dealt out to the waves
+  constexpr int step = kWaves * 64;
+  const int part_k = (K / 64 + gridDim.y - 1) / gridDim.y * 64;
+  const int k0 = blockIdx.y * part_k + wave * 64, k_end = min(K, static_cast<int>(blockIdx.y + 1) * part_k);
   // after the sum this wave stores token block `wave`
   const int m_out = m0 + 16 * wave + r;
   const int own = m_out < M ? p.index[m_out] : -1;
@@ -103,12 +105,11 @@ __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* _
 #pragma unroll
       for (int q = 0; q < NB; ++q)
         w_row[q] = p.a_rows + static_cast<int64_t>(row0 + min(base + 16 * q + r, rank - 1)) * K + k8;
-      for (int k = k0; k < K; k += 2 * step) {
-        const bool two = k + step < K;
-        v4i xf[2][2][4], wf[2][2][NB];
+      for (int k = k0; k < k_end; k += DEPTH * step) {
+        v4i xf[DEPTH][2][4], wf[DEPTH][2][NB];
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          const int kd = d == 1 && two ? k + step : k;
+        for (int d = 0; d < DEPTH; ++d) {
+          const int kd = k + d * step < k_end ? k + d * step : k;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -119,8 +120,8 @@ __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* _
         }
         __builtin_amdgcn_sched_barrier(0);      // every load before the first product
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          if (d == 1 && !two) break;
+        for (int d = 0; d < DEPTH; ++d) {
+          if (d > 0 && k + d * step >= k_end) break;
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -251,15 +252,19 @@ __global__ __launch_bounds__(kThreads) void lora_rows_kernel(Down p, int rows, i
 template <bool F16, int NB>
 hipError_t launch_down(const Down& p, float* sums, int parts, hipStream_t stream) {
   const int tiles = (p.M + kTile - 1) / kTile;
-  // Workgroups that share a tile's adapters: one, and one and a half times as
-  // many as the runs of a batch of this many adapters put into a tile (the
-  // tile with the most adapters is what one waits for; the workgroups without
-  // an adapter end at once, and come last in the grid).
-  const int64_t cuts = (int64_t{3} * p.adapters * kTile / 2 + p.M - 1) / p.M;
+  // Workgroups that share a tile's adapters: one, and three times as many as
+  // the runs of a batch of this many adapters put into a tile on the mean; the
+  // workgroups without an adapter end at once and come last in the grid.  (Each
+  // adapter more in a tile costs its pass: 2000 tokens, K = 12288, rank 32, one
+  // adapter a tile 13.5 us, two 19.6, four 34.5.)
+  const int64_t cuts = (int64_t{3} * p.adapters * kTile + p.M - 1) / p.M;
   const int64_t most = p.adapters < kTile ? p.adapters : kTile;         // adapters a tile can hold
   const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(parts),
                   static_cast<uint32_t>(1 + cuts < most ? 1 + cuts : most));
-  hipLaunchKernelGGL((lora_down_kernel<F16, NB>), grid, dim3(kWaves * 64), 0, stream, p, sums);
+  if (p.K / 64 > parts * kWaves)
+    hipLaunchKernelGGL((lora_down_kernel<F16, NB, 2>), grid, dim3(kWaves * 64), 0, stream, p, sums);
+  else
+    hipLaunchKernelGGL((lora_down_kernel<F16, NB, 1>), grid, dim3(kWaves * 64), 0, stream, p, sums);
   return hipGetLastError();
 }
 
@@ -287,13 +292,15 @@ hipError_t launch_rows(const Down& p, int group, int8_t* xq, float* xs, const fl
   return go_group(std::integral_constant<int, 256>{});
 }
 
-// Parts of K: enough for two workgroups a CU, each with at least one piece of
-// K for every wave.
+// Parts of K: up to two and a half workgroups a CU, and the fewest with which
+// a wave has as few pieces of K as with that many.
 int parts_of(int64_t M, int64_t K) {
-  const int64_t tiles = (M + kTile - 1) / kTile;
-  int64_t parts = 2 * num_cus() / tiles;
-  if (parts > K / (64 * kWaves)) parts = K / (64 * kWaves);
-  return static_cast<int>(parts < 1 ? 1 : parts > kMaxLoraParts ? kMaxLoraParts : parts);
+  const int64_t tiles = (M + kTile - 1) / kTile, pieces = K / 64;
+  int64_t parts = 5 * num_cus() / (2 * tiles);
+  parts = parts < 1 ? 1 : parts > kMaxLoraParts ? kMaxLoraParts : parts;
+  auto turns = [&](int64_t n) { return ((pieces + n - 1) / n + kWaves - 1) / kWaves; };
+  while (parts > 1 && turns(parts - 1) == turns(parts)) --parts;
+  return static_cast<int>(parts);
 }
 
 template <bool F16>

@@ -118,6 +118,29 @@ __device__ inline uint2 pack8(const float (&v)[8], float s) {
   return make_uint2(lo, hi);
 }
 
+// The same codes with a reciprocal and two fused multiply-adds a value instead
+// of a division (the quotient comes out correctly rounded), the nearest integer
+// by adding 1.5 * 2^23; rows whose scale is too small for a normal reciprocal
+// divide.
+__device__ inline uint2 pack8_fast(const float (&v)[8], float s) {
+  const float r = 1.0f / s;
+  if (!(r < 1e30f)) return pack8(v, s);
+  uint32_t w[2];
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    uint32_t t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = v[4 * d + e];
+      const float q0 = x * r;
+      const float rem = __builtin_fmaf(-q0, s, x);
+      t[e] = __float_as_uint(__builtin_fmaf(rem, r, q0) + 12582912.0f);
+    }
+    w[d] = __builtin_amdgcn_perm(t[1], t[0], 0x0c0c0400u) | (__builtin_amdgcn_perm(t[3], t[2], 0x0c0c0400u) << 16);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
 // Maximum over the workgroup (max is exact and order-free): inside each
 // 16-lane row by DPP moves, over the four rows of a wave by lane reads, over
 // the waves through LDS.
