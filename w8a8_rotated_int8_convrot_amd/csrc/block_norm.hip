@@ -211,7 +211,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNorm p) {
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
       if (live[j]) {
-        rotate_chunk<G>(v[j], lane_in_group);
+        rotate_chunk_fast<G>(v[j], lane_in_group);
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[j][i]));
       }

@@ -101,6 +101,59 @@ __device__ inline void rotate_chunk(float (&v)[8], int lane_in_group) {
   for (int i = 0; i < 8; ++i) v[i] = v[i] * RotScale<G>::value;
 }
 
+// Butterfly stages between lanes 1, 2 and 8 apart as one v_fmac_f32 with a DPP
+// source per value, v <- RN(v + sgn * partner).  With sgn = -1 the upper lane
+// holds b and gets b - a, the negative of what it keeps (rounding to nearest is
+// symmetric): its sign is put right by the constant of the last multiply.  The
+// block opens with the two wait states a DPP read needs after a VALU write of
+// its source; inside it no instruction reads what another one wrote.
+template <int T>
+__device__ inline void lane_stage_dpp(float (&v)[8], float sgn) {
+#define CONVROT_DPP8(PERM)                                                                               \
+  asm volatile("s_nop 1\n\t"                                                                             \
+               "v_fmac_f32_dpp %0, %0, %8 " PERM " row_mask:0xf bank_mask:0xf\n\t"                       \
+               "v_fmac_f32_dpp %1, %1, %8 " PERM " row_mask:0xf bank_mask:0xf\n\t"                       \
+               "v_fmac_f32_dpp %2, %2, %8 " PERM " row_mask:0xf bank_mask:0xf\n\t"                       \
+               "v_fmac_f32_dpp %3, %3, %8 " PERM " row_mask:0xf bank_mask:0xf\n\t"                       \
+               "v_fmac_f32_dpp %4, %4, %8 " PERM " row_mask:0xf bank_mask:0xf\n\t"                       \
+               "v_fmac_f32_dpp %5, %5, %8 " PERM " row_mask:0xf bank_mask:0xf\n\t"                       \
+               "v_fmac_f32_dpp %6, %6, %8 " PERM " row_mask:0xf bank_mask:0xf\n\t"                       \
+               "v_fmac_f32_dpp %7, %7, %8 " PERM " row_mask:0xf bank_mask:0xf"                             \
+               : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]),      \
+                 "+v"(v[7])                                                                               \
+               : "v"(sgn))
+  if constexpr (T == 1) CONVROT_DPP8("quad_perm:[1,0,3,2]");
+  else if constexpr (T == 2) CONVROT_DPP8("quad_perm:[2,3,0,1]");
+  else CONVROT_DPP8("row_ror:8");
+#undef CONVROT_DPP8
+}
+
+// rotate_chunk with those stages: the same values, up to the sign of a zero.
+template <int G>
+__device__ inline void rotate_chunk_fast(float (&v)[8], int lane_in_group) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i & h) == 0) {
+        const float a = v[i], b = v[i + h];
+        v[i] = a + b;
+        v[i + h] = a - b;
+      }
+    }
+  }
+  const float s1 = (lane_in_group & 1) != 0 ? -1.0f : 1.0f, s2 = (lane_in_group & 2) != 0 ? -1.0f : 1.0f;
+  const float s8 = (lane_in_group & 8) != 0 ? -1.0f : 1.0f;
+  lane_stage_dpp<1>(v, s1);
+  lane_stage_dpp<2>(v, s2);
+  lane_stage<4>(v, lane_in_group);
+  lane_stage_dpp<8>(v, s8);
+  if constexpr (G == 256) lane_stage<16>(v, lane_in_group);
+  const float c = RotScale<G>::value * (s1 * s2 * s8);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = v[i] * c;
+}
+
 __device__ inline int quant_code(float v, float s) {
   float r = __builtin_rintf(v / s);
   r = fminf(fmaxf(r, -127.0f), 127.0f);
@@ -180,7 +233,7 @@ __device__ inline void rotate_quant_row(const In* __restrict__ x, int K, int8_t*
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
     if ((j * kThreads + tid) * 8 < K) {
-      rotate_chunk<G>(v[j], tid % (G / 8));
+      rotate_chunk_fast<G>(v[j], tid % (G / 8));
 #pragma unroll
       for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[j][i]));
     }
@@ -190,7 +243,7 @@ __device__ inline void rotate_quant_row(const In* __restrict__ x, int K, int8_t*
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
     const int e = (j * kThreads + tid) * 8;
-    if (e < K) *reinterpret_cast<uint2*>(q + e) = pack8(v[j], s);
+    if (e < K) *reinterpret_cast<uint2*>(q + e) = pack8_fast(v[j], s);
   }
 }
 
