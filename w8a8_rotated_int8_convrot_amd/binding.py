@@ -10,6 +10,7 @@ built library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -570,6 +571,24 @@ def _need_on(t, dev, dtype, name, shape):
     return t.data_ptr()
 
 
+def _out_of(x, out, rows, cols):
+    """``out``, or a new one like x, and its address."""
+    if out is None:
+        out = x.new_empty((rows, cols))
+        return out, out.data_ptr()
+    return out, _need_on(out, x.device, x.dtype, "out", (rows, cols))
+
+
+def _workspace_of(x, workspace, need):
+    """``workspace``, or a new one of ``need`` bytes (to be kept until the call
+    that uses it has been queued), and its address and bytes."""
+    if workspace is None:
+        workspace = x.new_empty(max(need, 1), dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), workspace.numel()
+    n = workspace.numel()
+    return workspace, _need_on(workspace, x.device, torch.uint8, "workspace", (n,)), n
+
+
 class Block(ctypes.Structure):
     """Mirror of ``convrot_block`` (include/convrot.h)."""
     _fields_ = [("io_dtype", _I), ("group", _I), ("post_norm", _I), ("pre_norm", _I), ("n_routes", _I),
@@ -647,11 +666,15 @@ def convrot_block_norm(h, u=None, routes=None, post_norm="none", post_weight=Non
     else:
         if h_out is None:
             h_out = torch.empty_like(h)
-        b.h_out = _need_on(h_out, dev, dt, "h_out", shape)
+            b.h_out = h_out.data_ptr()
+        else:
+            b.h_out = _need_on(h_out, dev, dt, "h_out", shape)
     if want_out:
         if out is None:
             out = torch.empty_like(h, dtype=torch.int8) if group else torch.empty_like(h)
-        b.out = _need_on(out, dev, torch.int8 if group else dt, "out", shape)
+            b.out = out.data_ptr()
+        else:
+            b.out = _need_on(out, dev, torch.int8 if group else dt, "out", shape)
         if group:
             if out_scale is None:
                 out_scale = torch.empty(M, dtype=torch.float32, device=dev)
@@ -664,6 +687,10 @@ def convrot_block_norm(h, u=None, routes=None, post_norm="none", post_weight=Non
 
 def convrot_grouped_workspace(M: int, K: int) -> int:
     return lib().convrot_grouped_workspace(M, K)
+
+
+# the sizes are pure functions of their arguments, and a call's are mostly the last one's
+_grouped_bytes = functools.lru_cache(maxsize=256)(convrot_grouped_workspace)
 
 
 def convrot_grouped_linear(x, wq, w_scale, group, offsets, rows=None, bias=None, out=None,
@@ -692,21 +719,21 @@ def convrot_grouped_linear(x, wq, w_scale, group, offsets, rows=None, bias=None,
         rows = _need_on(rows, dev, torch.int32, "rows", (P,))
     if bias is not None:
         bias = _need_on(bias, dev, dt, "bias", (E, N))
-    if out is None:
-        out = torch.empty((P, N), dtype=dt, device=dev)
-    if workspace is None:
-        workspace = torch.empty(max(convrot_grouped_workspace(M, K), 1), dtype=torch.uint8, device=dev)
-    ws_bytes = workspace.numel()
+    out, out_ptr = _out_of(x, out, P, N)
+    workspace, ws_ptr, ws_bytes = _workspace_of(x, workspace, _grouped_bytes(M, K))
     _call_on(x, who, x.data_ptr(), io, M, K, _need_on(wq, dev, torch.int8, "wq", (E, N, K)),
              _need_on(w_scale, dev, torch.float32, "w_scale", (E, N) if per_row else (E,)),
              CONVROT_SCALE_ROW if per_row else CONVROT_SCALE_TENSOR, E, N, group, bias,
-             _need_on(offsets, dev, torch.int32, "offsets", (E + 1,)), rows, P, _need_on(out, dev, dt, "out", (P, N)),
-             _need_on(workspace, dev, torch.uint8, "workspace", (ws_bytes,)), ws_bytes, _stream(x))
+             _need_on(offsets, dev, torch.int32, "offsets", (E + 1,)), rows, P, out_ptr, ws_ptr, ws_bytes,
+             _stream(x))
     return out
 
 
 def convrot_lora_workspace(M: int, K: int, N: int, max_rank: int) -> int:
     return lib().convrot_lora_workspace(M, K, N, max_rank)
+
+
+_lora_bytes = functools.lru_cache(maxsize=256)(convrot_lora_workspace)
 
 
 def convrot_linear_lora(x, wq, w_scale, group, lora_a, lora_b, lora_scale, offsets, index, max_rank, bias=None,
@@ -728,16 +755,12 @@ def convrot_linear_lora(x, wq, w_scale, group, lora_a, lora_b, lora_scale, offse
     mode = _scale_mode_of(w_scale, N, who)
     if bias is not None:
         bias = _need_on(bias, dev, dt, "bias", (N,))
-    if out is None:
-        out = torch.empty((M, N), dtype=dt, device=dev)
-    if workspace is None:
-        workspace = torch.empty(max(convrot_lora_workspace(M, K, N, max_rank), 1), dtype=torch.uint8, device=dev)
-    ws_bytes = workspace.numel()
+    out, out_ptr = _out_of(x, out, M, N)
+    workspace, ws_ptr, ws_bytes = _workspace_of(x, workspace, _lora_bytes(M, K, N, max_rank))
     _call_on(x, who, x.data_ptr(), io, M, K, _need_on(wq, dev, torch.int8, "wq", (N, K)),
              _need_on(w_scale, dev, torch.float32, "w_scale", (w_scale.numel(),)), mode, N, group, bias,
              _need_on(lora_a, dev, dt, "lora_a", (R, K)), _need_on(lora_b, dev, dt, "lora_b", (R, N)), R,
              _need_on(lora_scale, dev, torch.float32, "lora_scale", (n,)),
              _need_on(offsets, dev, torch.int32, "offsets", (n + 1,)), n, max_rank,
-             _need_on(index, dev, torch.int32, "index", (M,)), _need_on(out, dev, dt, "out", (M, N)),
-             _need_on(workspace, dev, torch.uint8, "workspace", (ws_bytes,)), ws_bytes, _stream(x))
+             _need_on(index, dev, torch.int32, "index", (M,)), out_ptr, ws_ptr, ws_bytes, _stream(x))
     return out
