@@ -37,6 +37,13 @@ hipError_t launch_gemm_grouped(const int8_t*, const float*, int64_t, const int8_
   ++g_launches;
   return hipErrorInvalidConfiguration;      // a failed launch
 }
+bool grouped_is_few(int64_t M, int64_t) { return M <= 2; }
+hipError_t launch_grouped_few(const void*, int64_t, int64_t, int, bool, const int8_t*, const float*, bool,
+                              const uint16_t*, uint16_t*, const int32_t*, const int32_t*, int64_t, int64_t, int64_t,
+                              hipStream_t) {
+  ++g_launches;
+  return hipSuccess;
+}
 hipError_t launch_lora_down(const uint16_t*, int64_t M, int64_t, int, bool, int8_t*, float*, const uint16_t*, int64_t,
                             const float*, const int32_t*, int64_t, const int32_t*, int64_t, uint16_t*, int64_t, float*,
                             hipStream_t) {
@@ -116,6 +123,7 @@ int main() {
   };
   const size_t big = std::numeric_limits<size_t>::max();
   expect(grouped(4, 128, 2, 16, 8, i32, big), CONVROT_EHIP, 2, "grouped: failed launch");
+  expect(grouped(2, 128, 2, 16, 8, i32, big), CONVROT_OK, 1, "grouped: few tokens");
   expect(grouped(4, 128, 2, 16, 8, i32, convrot_grouped_workspace(4, 128) - 1), CONVROT_EWORKSPACE, 0, "grouped: workspace");
   expect(grouped(4, 128, 2, 16, 8, nullptr, big), CONVROT_EINVAL, 0, "grouped: rows missing");
   expect(grouped(4, 128, 65536, int64_t{1} << 30, int64_t{1} << 30, i32, big), CONVROT_EINVAL, 0, "grouped: tiles");

@@ -106,6 +106,48 @@ def test_equals_the_layer_expert_by_expert(B, M, K, N, E, P, group, io, row, bia
     assert torch.equal(got, by_expert(B, x, wq, s, group, offsets, rows, b))
 
 
+# one to four tokens go through a kernel of their own up to K = 8192
+@gpu
+@pytest.mark.parametrize("io,row,bias", [("bf16", True, True), ("fp16", False, False)])
+@pytest.mark.parametrize("M,K,N,E,P,group", [
+    (1, 128, 16, 4, 1, 128), (1, 2048, 1408, 16, 4, 128), (2, 2176, 100, 5, 13, 128), (3, 4096, 264, 130, 40, 256),
+    (4, 4352, 37, 3, 77, 256), (4, 8192, 48, 6, 20, 128), (4, 8448, 48, 6, 20, 256), (2, 256, 9, 70, 300, 256)])
+def test_few_tokens(B, M, K, N, E, P, group, io, row, bias):
+    g, dt, wq, s, b = layer(K, N, E, io, row, bias, M + K + N)
+    x = stream(g, M, K, dt)
+    offsets, rows = route(g, M, P, E)
+    assert torch.equal(B.convrot_grouped_linear(x, wq, s, group, offsets, rows=rows, bias=b),
+                       by_expert(B, x, wq, s, group, offsets, rows, b))
+    # rows of no expert, of no token, and a token of zeros
+    x[M - 1] = 0
+    offsets = offsets.clamp(max=max(1, P - 2))
+    rows[::3] = torch.where(torch.arange(len(rows[::3]), device=DEV) % 2 == 0, -1, M).to(torch.int32)
+    out = torch.full((P, N), 5.0, dtype=dt, device=DEV)
+    B.convrot_grouped_linear(x, wq, s, group, offsets, rows=rows, bias=b, out=out)
+    good = (rows >= 0) & (rows < M) & (torch.arange(P, device=DEV) < offsets[-1])
+    want = by_expert(B, x, wq, s, group, offsets, rows.clamp(0, M - 1), b)
+    assert (out[~good] == 5).all() and torch.equal(out[good], want[good])
+
+
+@gpu
+def test_few_tokens_without_rows_captured(B):
+    g, dt, wq, s, b = layer(1024, 80, 3, "bf16", True, True, 12)
+    x = stream(g, 4, 1024, dt)
+    x[2, 5] = float("nan")
+    offsets = torch.tensor([0, 1, 3, 4], dtype=torch.int32, device=DEV)
+    rows = torch.arange(4, device=DEV, dtype=torch.int32)
+    out, ws = torch.empty(4, 80, dtype=dt, device=DEV), torch.empty(1 << 14, dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.convrot_grouped_linear(x, wq, s, 128, offsets, bias=b, out=out, workspace=ws)
+    for k in range(3):
+        x[:2].mul_(0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        fine = [0, 1, 3]                      # the NaN token's codes are unspecified
+        assert torch.equal(out[fine], by_expert(B, x, wq, s, 128, offsets, rows, b)[fine])
+
+
 @gpu
 @pytest.mark.parametrize("io", ["bf16", "fp16"])
 def test_against_64_bits(B, io):

@@ -91,6 +91,14 @@ hipError_t launch_gemm_grouped(const int8_t* xq, const float* x_scale, int64_t x
                                const int32_t* offsets, const int32_t* rows, int64_t experts, int64_t P, int64_t N,
                                int64_t K, hipStream_t stream);
 
+// The whole call for few tokens (M, K that grouped_is_few takes): x [M, K] in
+// the io type, rotated and coded by the kernel itself.  The same bytes.
+bool grouped_is_few(int64_t M, int64_t K);
+hipError_t launch_grouped_few(const void* x, int64_t M, int64_t K, int group, bool f16, const int8_t* wq,
+                              const float* w_scale, bool row_scale, const uint16_t* bias, uint16_t* y,
+                              const int32_t* offsets, const int32_t* rows, int64_t experts, int64_t P, int64_t N,
+                              hipStream_t stream);
+
 // Whether a batch's adapters are taken token by token (few tokens, most with an
 // adapter of their own) or as a list per tile.  By sizes alone, so that a
 // token's result does not depend on the other tokens' adapters.

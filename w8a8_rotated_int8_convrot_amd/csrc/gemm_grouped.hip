@@ -1,6 +1,8 @@
 // gemm_grouped.hip -- the int8 product grouped by expert: launches of
 // gemm_i8_kernel over a Grouped (gemm_core.hpp) and the choice of its tile.
+// For one to four tokens grouped_few_kernel does the whole call in one launch.
 #include "gemm_core.hpp"
+#include "rotate_device.hpp"
 
 namespace convrot {
 namespace {
@@ -49,7 +51,155 @@ hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, 
   return launch_tile<TileTall, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
 }
 
+// At most kFewTokens tokens of at most kFewK values: a launch costs the host as
+// much as this product's weight takes to read, so one kernel does it all.  A
+// workgroup has 16 channels of one expert and 16 of its rows, its four waves
+// share K.  Each wave first sends for all of its weight (STEPS pieces of 16 rows
+// x 64 bytes in the registers of v_mfma_i32_16x16x64_i8's operand), then the
+// workgroup rotates and codes the tokens into LDS -- every workgroup the same,
+// a few hundred instructions a wave under the weight's latency -- and the
+// products take the tokens from there.  The waves' sums are joined in LDS.
+// One token, 4 of 16 experts of 1408 x 2048: rotate + quant 2.4 us and the
+// product 6.2 us in two launches.
+constexpr int kFewTokens = 4;
+constexpr int kFewK = 8192;
+struct FewTile { static constexpr int BN = 16, BM = 16, kGroupM = 1; };
+
+template <typename In, int G, int STEPS>
+__global__ __launch_bounds__(kThreads) void grouped_few_kernel(
+    const In* __restrict__ x, int K, const int8_t* __restrict__ wq, int N, int tiles_n,
+    const float* __restrict__ w_scale, int row_scale, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y,
+    Grouped g) {
+  constexpr bool F16 = !std::is_same_v<In, uint16_t>;
+  constexpr int kCpt = (STEPS * 256 + kThreads * 8 - 1) / (kThreads * 8);   // K <= 256 STEPS
+  extern __shared__ __attribute__((aligned(16))) char codes[];   // [x_rows][K]
+  __shared__ float amax[kFewTokens][4];
+  __shared__ __attribute__((aligned(16))) v4i red[3][64];
+  int e, n0, m0, m_end;
+  if (!grouped_tile<FewTile>(g, tiles_n, e, n0, m0, m_end)) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, c16 = (lane >> 4) * 16;
+
+  // this wave's pieces of K: wave, wave + 4, ... of 64 bytes
+  const int pieces = K / 64;
+  v4i w[STEPS];
+  const int8_t* w_row = wq + (static_cast<int64_t>(e) * N + min(n0 + r, N - 1)) * K + c16;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i)
+    w[i] = *reinterpret_cast<const v4i*>(w_row + min(4 * i + wave, pieces - 1) * 64);
+
+  // every token's codes, and its absolute maximum per wave
+  for (int t = 0; t < g.x_rows; ++t) {
+    const In* xr = x + static_cast<int64_t>(t) * K;
+    float v[kCpt][8];
+    float a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kCpt; ++j) {
+      const int k = (j * kThreads + tid) * 8;
+      if (k < K) load8(xr + k, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kCpt; ++j) {
+      if ((j * kThreads + tid) * 8 < K) {
+        rotate_chunk_fast<G>(v[j], tid % (G / 8));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[j][i]));
+      }
+    }
+    a = wave_max(a);
+    if (lane == 0) amax[t][wave] = a;
+    __syncthreads();
+    const float s = fmaxf(fmaxf(amax[t][0], amax[t][1]), fmaxf(amax[t][2], amax[t][3])) / 127.0f;
+#pragma unroll
+    for (int j = 0; j < kCpt; ++j) {
+      const int k = (j * kThreads + tid) * 8;
+      if (k < K) *reinterpret_cast<uint2*>(codes + t * K + k) = pack8_fast(v[j], s);
+    }
+  }
+  __syncthreads();
+
+  // rows past the expert's end are its last one (not stored)
+  const int p = m0 + r;
+  const int src = g.source(min(p, m_end - 1));
+  v4i acc = {};
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    if (4 * i + wave < pieces) {
+      const v4i b = *reinterpret_cast<const v4i*>(codes + src * K + (4 * i + wave) * 64 + c16);
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], b, acc, 0, 0, 0);
+    }
+  }
+  if (wave > 0) red[wave - 1][lane] = acc;
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) acc += red[q][lane];
+
+  // lane l: channels n0 + 4 (l >> 4) + (0..3) of row m0 + (l & 15); the layer's
+  // own epilogue, operation by operation
+  if (p >= m_end || !g.has_source(p)) return;
+  const float xs = fmaxf(fmaxf(amax[src][0], amax[src][1]), fmaxf(amax[src][2], amax[src][3])) / 127.0f;
+  const int n = n0 + 4 * (lane >> 4);
+  const float* ws = w_scale + (row_scale ? static_cast<int64_t>(e) * N : e);
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int ne = min(n + i, N - 1);
+    float b = 0.0f;
+    if (bias != nullptr) {
+      const uint16_t h = bias[static_cast<int64_t>(e) * N + ne];
+      b = F16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : __uint_as_float(static_cast<uint32_t>(h) << 16);
+    }
+    v[i] = __builtin_fmaf(static_cast<float>(acc[i]), xs * ws[row_scale ? ne : 0], b);
+    if constexpr (F16) asm volatile("" : "+v"(v[i]));      // no fused multiply-add and conversion
+  }
+  const uint32_t lo = F16 ? pack_f16x2(v[0], v[1]) : pack_bf16x2(v[0], v[1]);
+  const uint32_t hi = F16 ? pack_f16x2(v[2], v[3]) : pack_bf16x2(v[2], v[3]);
+  uint16_t* out = y + static_cast<int64_t>(p) * N + n;
+  if ((N & 3) == 0 && n + 3 < N) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) out[i] = static_cast<uint16_t>((i < 2 ? lo : hi) >> (16 * (i & 1)));
+  }
+}
+
+template <typename In>
+hipError_t launch_few(const void* x, const int8_t* wq, const float* w_scale, bool row_scale, const uint16_t* bias,
+                      uint16_t* y, const Grouped& g, int64_t N, int64_t K, int group, hipStream_t stream) {
+  const int64_t tiles_n = (N + 15) / 16;
+  const int64_t blocks = tiles_n * most_tiles(g.P, g.experts, 16);
+  if (blocks > kMaxGroupedTiles) return hipErrorInvalidConfiguration;
+  auto go = [&](auto g_c, auto steps_c) {
+    hipLaunchKernelGGL((grouped_few_kernel<In, decltype(g_c)::value, decltype(steps_c)::value>),
+                       dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), static_cast<size_t>(g.x_rows) * K, stream,
+                       static_cast<const In*>(x), static_cast<int>(K), wq, static_cast<int>(N),
+                       static_cast<int>(tiles_n), w_scale, row_scale ? 1 : 0, bias, y, g);
+    return hipGetLastError();
+  };
+  auto go_group = [&](auto g_c) {
+    if (K <= 2048) return go(g_c, std::integral_constant<int, 8>{});
+    if (K <= 4096) return go(g_c, std::integral_constant<int, 16>{});
+    return go(g_c, std::integral_constant<int, 32>{});
+  };
+  return group == 128 ? go_group(std::integral_constant<int, 128>{}) : go_group(std::integral_constant<int, 256>{});
+}
+
 }  // namespace
+
+bool grouped_is_few(int64_t M, int64_t K) { return M <= kFewTokens && K <= kFewK; }
+
+hipError_t launch_grouped_few(const void* x, int64_t M, int64_t K, int group, bool f16, const int8_t* wq,
+                              const float* w_scale, bool row_scale, const uint16_t* bias, uint16_t* y,
+                              const int32_t* offsets, const int32_t* rows, int64_t experts, int64_t P, int64_t N,
+                              hipStream_t stream) {
+  if (P == 0) return hipSuccess;
+  const Grouped g{offsets, rows, static_cast<int>(experts), static_cast<int>(P), static_cast<int>(M)};
+  return f16 ? launch_few<_Float16>(x, wq, w_scale, row_scale, bias, y, g, N, K, group, stream)
+             : launch_few<uint16_t>(x, wq, w_scale, row_scale, bias, y, g, N, K, group, stream);
+}
 
 hipError_t launch_gemm_grouped(const int8_t* xq, const float* x_scale, int64_t x_rows, const int8_t* wq,
                                const float* w_scale, bool row_scale, const uint16_t* bias, uint16_t* y, bool f16,

@@ -142,6 +142,11 @@ int convrot_grouped_linear(const void* x, int io_dtype, int64_t M, int64_t K, co
   auto* xs = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(static_cast<size_t>(M) * K, 256));
   const bool f16 = io_dtype == CONVROT_F16;
   auto s = static_cast<hipStream_t>(stream);
+  if (grouped_is_few(M, K))
+    return hip_status(launch_grouped_few(x, M, K, group, f16, wq, w_scale, scale_mode == CONVROT_SCALE_ROW,
+                                         static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), offsets, rows,
+                                         n_experts, P, N, s),
+                      who);
   if (hipError_t e = rotate_quant(x, f16, M, K, group, xq, xs, s); e != hipSuccess) return hip_status(e, who);
   return hip_status(launch_gemm_grouped(xq, xs, M, wq, w_scale, scale_mode == CONVROT_SCALE_ROW,
                                         static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), f16, offsets,

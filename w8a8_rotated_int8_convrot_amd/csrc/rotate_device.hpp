@@ -194,19 +194,23 @@ __device__ inline uint2 pack8_fast(const float (&v)[8], float s) {
   return make_uint2(w[0], w[1]);
 }
 
-// Maximum over the workgroup (max is exact and order-free): inside each
-// 16-lane row by DPP moves, over the four rows of a wave by lane reads, over
-// the waves through LDS.
-__device__ inline float block_max(float a) {
-  __shared__ float part[kThreads / 64];
+// Maximum over the wave (max is exact and order-free): inside each 16-lane row
+// by DPP moves, over the four rows by lane reads.
+__device__ inline float wave_max(float a) {
   a = fmaxf(a, lane_xor<1>(a));
   a = fmaxf(a, lane_xor<2>(a));
   a = fmaxf(a, lane_xor<4>(a));
   a = fmaxf(a, lane_xor<8>(a));
-  a = fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 0)),
-                  __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 16))),
-            fmaxf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 32)),
-                  __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 48))));
+  return fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 0)),
+                     __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 16))),
+               fmaxf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 32)),
+                     __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 48))));
+}
+
+// Maximum over the workgroup: the waves' through LDS.
+__device__ inline float block_max(float a) {
+  __shared__ float part[kThreads / 64];
+  a = wave_max(a);
   const int wave = threadIdx.x / 64;
   if ((threadIdx.x & 63) == 0) part[wave] = a;
   __syncthreads();
