@@ -510,10 +510,15 @@ struct LoraTile {
       t_row[j] = lo.t + static_cast<int64_t>(m) * lo.t_stride + c8 * 8;
     }
     while (has[0]) {
+      // these units; the next ones' panels are on their way while these run
+      bool now[UNITS];
+      int now_a[UNITS];
       v4i tf[UNITS][TM][kSub];
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
-        if (!has[u]) continue;
+        now[u] = has[u];
+        now_a[u] = unit_a[u];
+        if (!now[u]) continue;
 #pragma unroll
         for (int j = 0; j < TM; ++j)
 #pragma unroll
@@ -521,7 +526,7 @@ struct LoraTile {
       }
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
-        if (!has[u]) continue;
+        if (!now[u]) continue;
         char* panel = panels + u * kPanelBytes;
 #pragma unroll
         for (int p = 0; p < kPerThread; ++p) {
@@ -535,16 +540,18 @@ struct LoraTile {
                 static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
         }
       }
+      if (now[UNITS - 1]) fetch(tid);
+      else has[0] = false;
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
-        if (!has[u]) continue;
+        if (!now[u]) continue;
         const char* panel = panels + u * kPanelBytes;
         bool any = false, whole[TM];
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
-          whole[j] = __all(own[j] == unit_a[u]);
-          any = any || __any(own[j] == unit_a[u]);
+          whole[j] = __all(own[j] == now_a[u]);
+          any = any || __any(own[j] == now_a[u]);
         }
         if (!any) continue;
 #pragma unroll
@@ -563,13 +570,11 @@ struct LoraTile {
             } else {
 #pragma unroll
               for (int e = 0; e < T::kAccRegs; ++e)
-                acc[i][j][e] = own[j] == unit_a[u] ? __float_as_int(d[e]) : acc[i][j][e];
+                acc[i][j][e] = own[j] == now_a[u] ? __float_as_int(d[e]) : acc[i][j][e];
             }
           }
         }
       }
-      if (!has[UNITS - 1]) return;
-      fetch(tid);
       if (!has[0]) return;
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the panels are read: the next may come
     }
