@@ -56,7 +56,8 @@ INT8_PEAK_TOPS = 5000.0        # MI355X dense int8 MFMA: 5.0 POP/s
 HBM_PEAK_GBS = 8000.0          # MI355X HBM3E: 8 TB/s
 MAX_GFX_MHZ = 2400.0           # MI355X peak engine clock, at which the 5.0 POP/s holds
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "gemm_traffic_mlp_up.json")
-GEMM_SOURCES = [os.path.join(ROOT, "w8a8_rotated_int8_convrot_amd", "csrc", "gemm_i8.hip")]
+GEMM_SOURCES = [os.path.join(ROOT, "w8a8_rotated_int8_convrot_amd", "csrc", f)
+                for f in ("gemm_core.hpp", "gemm_i8.hip")]
 
 
 def parse():

@@ -452,7 +452,9 @@ size_t convrot_grouped_workspace(int64_t M, int64_t K);
  *            (CONVROT_SCALE_ROW).
  *   bias     [n_experts, N] in io_dtype or NULL.
  *   offsets  DEVICE int32 [n_experts + 1], ascending; an expert may have no
- *            rows.  Values are clamped to [0, P] and to the value before.
+ *            rows.  Values are clamped to [0, P], and one below the value before
+ *            it ends an empty range.  Offsets that fall and rise again give
+ *            rows to several experts: what such rows hold is not specified.
  *   rows     DEVICE int32 [P], the token of each row, any order, a token as
  *            often as wanted; NULL: row p is token p, and P has to be M.
  *   y        [P, N] in io_dtype.  Rows outside [offsets[0], offsets[n_experts])
@@ -461,9 +463,9 @@ size_t convrot_grouped_workspace(int64_t M, int64_t K);
  *   workspace at least convrot_grouped_workspace(M, K) bytes.
  * The offsets are read by the kernel only: the call does not wait for the
  * router's, and one captured into a graph takes whatever they then hold.
- * N >= 1, 1 <= n_experts <= 65536, M and P in [0, 2^30], and at most 2^31
- * workgroups of 16 rows and 16 channels, one more of them for each expert
- * (CONVROT_EINVAL).  P = 0 is a no-op.  x, wq, y and workspace are 16-byte
+ * N >= 1, 1 <= n_experts <= 65536, M and P in [0, 2^30], and fewer than 2^31
+ * tiles of 16 rows and 16 channels, one more of them for each expert
+ * (CONVROT_EINVAL); a grid of 2^32 threads or more is CONVROT_EHIP.  P = 0 is a no-op.  x, wq, y and workspace are 16-byte
  * aligned.  Other errors as convrot_linear_ex.  Two launches, rotate +
  * quant of the M tokens and the product; one for few tokens. */
 int convrot_grouped_linear(const void *x, int io_dtype, int64_t M, int64_t K, const int8_t *wq,

@@ -18,8 +18,8 @@ extern "C" const char* convrot_last_error(void) { return convrot::g_last_error; 
 
 namespace convrot {
 int num_cus() { return 256; }
-hipError_t launch_block_norm(const BlockNorm&, int64_t M, int, bool, hipStream_t) {
-  g_rows += M;
+hipError_t launch_block_norm(const BlockNorm& p, int, bool, hipStream_t) {
+  g_rows += p.M;
   ++g_launches;
   return hipSuccess;
 }

@@ -322,6 +322,17 @@ def test_in_place_strides_streams_and_bounds(B):
 
 
 @gpu
+def test_more_rows_than_one_grid_dimension(B):
+    """2^24 workgroups of 256 threads would be 2^32 threads along x."""
+    M, K = (1 << 24) + 3, 8
+    h = (torch.arange(M, device=DEV, dtype=torch.int32) % 251).to(torch.bfloat16)[:, None].expand(M, K).contiguous()
+    _, z = B.convrot_block_norm(h, pre_norm="rms")
+    few = torch.tensor([0, 1, 250, (1 << 20) - 1, 1 << 20, (1 << 24) - 1, 1 << 24, M - 1], device=DEV)
+    _, want = B.convrot_block_norm(h[few].contiguous(), pre_norm="rms")
+    assert torch.equal(z[few], want) and int((z != 0).sum()) == int((h != 0).sum())
+
+
+@gpu
 def test_captured_and_replayed(B):
     c = case(40, 2048, "bf16", post="rms", pre="layer", mods=2, routes=4)
     h, q, s = B.convrot_block_norm(**c, group=128)

@@ -213,6 +213,31 @@ def test_offsets_outside_the_rows_are_clamped(B):
 
 
 @gpu
+@pytest.mark.parametrize("M", [3, 40, 500])
+def test_offsets_that_jump_back_and_forth(B, M):
+    """Every other expert claims all rows: more tiles than the call can launch.  Each piece of a
+    row is some expert's or untouched, and nothing outside the rows is written."""
+    E = 300
+    g, dt, wq, s, b = layer(128, 48, E, "bf16", False, False, 13)
+    x = stream(g, M, 128, dt)
+    bad = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    bad[1::2] = 1 << 30
+    buf = torch.full((M + 2, 48), 5.0, dtype=dt, device=DEV)
+    B.convrot_grouped_linear(x, wq, s, 128, bad, out=buf[1:M + 1])
+    torch.cuda.synchronize()
+    assert (buf[[0, M + 1]] == 5).all()
+    rows = torch.arange(M, device=DEV, dtype=torch.int32)
+    # experts write a row's tiles in any order, 16 bytes at a time: each piece is some expert's
+    pieces = lambda t: t.reshape(M, 6, 8)  # noqa: E731
+    ok = (pieces(buf[1:M + 1]) == 5).all(2)
+    for e in range(0, E, 2):
+        off = torch.zeros(E + 1, dtype=torch.int32)
+        off[e + 1:] = M
+        ok |= (pieces(by_expert(B, x, wq, s, 128, off, rows, None)) == pieces(buf[1:M + 1])).all(2)
+    assert ok.all()
+
+
+@gpu
 def test_without_rows_row_p_is_token_p(B):
     g, dt, wq, s, b = layer(384, 130, 3, "bf16", True, True, 6)
     x = stream(g, 90, 384, dt)

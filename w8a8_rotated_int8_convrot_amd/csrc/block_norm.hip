@@ -90,7 +90,8 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNorm p) {
   constexpr int kWaves = THREADS / 64;
   __shared__ float part[5][kWaves];
   const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
+  const int64_t row = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+  if (row >= p.M) return;
   const int K = p.K;
   const float inv_k = 1.0f / static_cast<float>(K);
   const In* hr = static_cast<const In*>(p.h) + row * K;
@@ -225,9 +226,13 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNorm p) {
 }
 
 template <int G, int THREADS, int CPT, typename In>
-hipError_t launch(const BlockNorm& p, int64_t M, hipStream_t stream) {
-  hipLaunchKernelGGL((block_norm_kernel<G, THREADS, CPT, In>), dim3(static_cast<uint32_t>(M)), dim3(THREADS), 0,
-                     stream, p);
+hipError_t launch(const BlockNorm& p, hipStream_t stream) {
+  // HIP counts the threads along x in 32 bits: very many rows wrap into y
+  constexpr int64_t kMostX = int64_t{1} << 20;
+  const int64_t x = p.M < kMostX ? p.M : kMostX;
+  hipLaunchKernelGGL((block_norm_kernel<G, THREADS, CPT, In>),
+                     dim3(static_cast<uint32_t>(x), static_cast<uint32_t>((p.M + x - 1) / x)), dim3(THREADS), 0, stream,
+                     p);
   return hipGetLastError();
 }
 
@@ -237,30 +242,30 @@ hipError_t launch(const BlockNorm& p, int64_t M, hipStream_t stream) {
 // 16896 x 6144: 177 us with 256 threads of three, 193 with 512 of two, 204 with
 // 768 of one).
 template <int G, typename In>
-hipError_t launch_k(const BlockNorm& p, int64_t M, hipStream_t stream) {
+hipError_t launch_k(const BlockNorm& p, hipStream_t stream) {
   const int chunks = (p.K + 7) / 8;
-  if (chunks <= 64) return launch<G, 64, 1, In>(p, M, stream);
-  if (chunks <= 128) return launch<G, 128, 1, In>(p, M, stream);
-  if (chunks <= 256) return launch<G, 256, 1, In>(p, M, stream);
-  if (chunks <= 512) return launch<G, 256, 2, In>(p, M, stream);
-  if (chunks <= 768) return launch<G, 256, 3, In>(p, M, stream);
-  if (chunks <= 1024) return launch<G, 512, 2, In>(p, M, stream);
-  if (chunks <= 2048) return launch<G, 1024, 2, In>(p, M, stream);
-  return launch<G, 1024, 4, In>(p, M, stream);
+  if (chunks <= 64) return launch<G, 64, 1, In>(p, stream);
+  if (chunks <= 128) return launch<G, 128, 1, In>(p, stream);
+  if (chunks <= 256) return launch<G, 256, 1, In>(p, stream);
+  if (chunks <= 512) return launch<G, 256, 2, In>(p, stream);
+  if (chunks <= 768) return launch<G, 256, 3, In>(p, stream);
+  if (chunks <= 1024) return launch<G, 512, 2, In>(p, stream);
+  if (chunks <= 2048) return launch<G, 1024, 2, In>(p, stream);
+  return launch<G, 1024, 4, In>(p, stream);
 }
 
 template <typename In>
-hipError_t launch_g(const BlockNorm& p, int64_t M, int group, hipStream_t stream) {
-  if (group == 128) return launch_k<128, In>(p, M, stream);
-  if (group == 256) return launch_k<256, In>(p, M, stream);
-  return launch_k<0, In>(p, M, stream);
+hipError_t launch_g(const BlockNorm& p, int group, hipStream_t stream) {
+  if (group == 128) return launch_k<128, In>(p, stream);
+  if (group == 256) return launch_k<256, In>(p, stream);
+  return launch_k<0, In>(p, stream);
 }
 
 }  // namespace
 
-hipError_t launch_block_norm(const BlockNorm& p, int64_t M, int group, bool f16, hipStream_t stream) {
-  if (M == 0) return hipSuccess;
-  return f16 ? launch_g<_Float16>(p, M, group, stream) : launch_g<uint16_t>(p, M, group, stream);
+hipError_t launch_block_norm(const BlockNorm& p, int group, bool f16, hipStream_t stream) {
+  if (p.M == 0) return hipSuccess;
+  return f16 ? launch_g<_Float16>(p, group, stream) : launch_g<uint16_t>(p, group, stream);
 }
 
 }  // namespace convrot

@@ -84,8 +84,7 @@ hipError_t launch_gemm_default(const uint16_t* x, const uint16_t* wu, const uint
 // of y [P, N] are those of expert e (wq [experts, N, K], w_scale [experts] or
 // with row_scale [experts, N], bias [experts, N] or null), row p made from row
 // rows[p] of xq [x_rows, K] (null: p).  offsets and rows are device memory.
-// hipErrorInvalidConfiguration where the grid could pass kMaxGroupedTiles.
-constexpr int64_t kMaxGroupedTiles = (int64_t{1} << 31) - 1;
+// hipErrorInvalidConfiguration where the grid would be larger than HIP takes.
 hipError_t launch_gemm_grouped(const int8_t* xq, const float* x_scale, int64_t x_rows, const int8_t* wq,
                                const float* w_scale, bool row_scale, const uint16_t* bias, uint16_t* y, bool f16,
                                const int32_t* offsets, const int32_t* rows, int64_t experts, int64_t P, int64_t N,
@@ -108,10 +107,17 @@ inline bool lora_by_token(int64_t M, int64_t adapters) { return M <= 16 || (M <=
 // type, t[m][r] = scale[a] * (row offsets[a] + r of a_rows [ranks, K]) . x[m]
 // with a = index[m]; zero from the adapter's rank on, unset for a token whose
 // index is outside [0, adapters).  t_stride: max_rank rounded up to 32.  sums:
-// kMaxLoraParts * M * t_stride floats (not used token by token).  Rotates and
+// lora_sum_rows(M) * t_stride floats (not used token by token).  Rotates and
 // quantizes x too (xq, xs as launch_rotate_quant), in the same launch where the
 // row kernel would do it.
 constexpr int kMaxLoraParts = 8;
+// Rows of the partial sums: parts of K times tokens, K being split only while
+// they stay within kLoraSumRows.
+constexpr int64_t kLoraSumRows = 40960;
+inline int64_t lora_sum_rows(int64_t M) {
+  if (kMaxLoraParts * M <= kLoraSumRows) return kMaxLoraParts * M;
+  return M > kLoraSumRows ? M : kLoraSumRows;
+}
 hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, int group, bool f16, int8_t* xq, float* xs,
                             const uint16_t* a, int64_t ranks, const float* scale, const int32_t* offsets,
                             int64_t adapters, const int32_t* index, int64_t max_rank, uint16_t* t, int64_t t_stride,
@@ -153,6 +159,7 @@ constexpr int64_t kMaxNormK = 32768;
 // Arguments as in convrot_block_norm (16-bit values behind void pointers); a
 // null u leaves the stream as it is, a null out ends after h_out.
 struct BlockNorm {
+  int64_t M;
   int K, n_routes, post_norm, pre_norm;
   const void *h, *u;
   const int32_t* route_row;
@@ -166,7 +173,7 @@ struct BlockNorm {
   float* out_scale;
 };
 // group: 128 or 256 for codes, 0 for 16-bit values.
-hipError_t launch_block_norm(const BlockNorm& p, int64_t M, int group, bool f16, hipStream_t stream);
+hipError_t launch_block_norm(const BlockNorm& p, int group, bool f16, hipStream_t stream);
 
 // ---------------------------------------------------------------- measurement aid
 

@@ -626,12 +626,14 @@ __device__ inline void lora_gather(float (&part)[T::TN][T::TM][T::kAccRegs], con
   }
 }
 
-// Inclusive sum over the wave's lanes.
+// Inclusive sum over the wave's lanes, at most kMostTiles (ascending offsets
+// make fewer than 2^27 token tiles; others may not overflow either).
+constexpr int kMostTiles = 1 << 29;
 __device__ inline int wave_scan(int v, int lane) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
+    if (lane >= d) v = min(v + o, kMostTiles);
   }
   return v;
 }
@@ -654,27 +656,33 @@ __device__ inline bool grouped_tile(const Grouped& g, int tiles_n, int& e, int& 
   const int first_scan = wave_scan(first, lane);
   int total = __builtin_amdgcn_readlane(first_scan, 63);
   for (int base = 64; base < g.experts; base += 64)
-    total += __builtin_amdgcn_readlane(wave_scan(token_tiles(base + lane), lane), 63);
-  const int nb = total * tiles_n;
+    total = min(total + __builtin_amdgcn_readlane(wave_scan(token_tiles(base + lane), lane), 63), kMostTiles);
   int bid = blockIdx.x;
-  if (bid >= nb) return false;
   {  // contiguous tile runs per XCD
+    const int64_t all = static_cast<int64_t>(total) * tiles_n;
+    if (bid >= all) return false;
+    // the grid holds every tile of ascending offsets; of others' tiles the
+    // first ones only
+    const int nb = static_cast<int>(min(all, static_cast<int64_t>(gridDim.x)));
     const int q = nb >> 3, r = nb & 7;
     const int x = bid & 7, local = bid >> 3;
     bid = x * q + (x < r ? x : r) + local;
   }
   int before = 0;           // token tiles of the experts before base
-  for (int base = 0;; base += 64) {
+  for (int base = 0; base < g.experts; base += 64) {
     const int t = base == 0 ? first : token_tiles(base + lane);
     const int scan = base == 0 ? first_scan : wave_scan(t, lane);
-    const uint64_t past = __ballot(bid < (before + scan) * tiles_n);
+    const uint64_t past = __ballot(bid < (static_cast<int64_t>(before) + scan) * tiles_n);
     if (past == 0) {
-      before += __builtin_amdgcn_readlane(scan, 63);
+      before = min(before + __builtin_amdgcn_readlane(scan, 63), kMostTiles);
       continue;
     }
     const int l = __builtin_ctzll(past);
     const int tiles_m = __builtin_amdgcn_readlane(t, l);
-    const int v = bid - (before + __builtin_amdgcn_readlane(scan, l) - tiles_m) * tiles_n;
+    const int64_t at = bid - (static_cast<int64_t>(before) + __builtin_amdgcn_readlane(scan, l) - tiles_m) * tiles_n;
+    // always inside, with ascending offsets
+    if (at < 0 || at >= static_cast<int64_t>(tiles_m) * tiles_n) return false;
+    const int v = static_cast<int>(at);
     e = base + l;
     const int gid = v / (T::kGroupM * tiles_n);
     const int first_m = gid * T::kGroupM;
@@ -687,6 +695,7 @@ __device__ inline bool grouped_tile(const Grouped& g, int tiles_n, int& e, int& 
     m_end = hi;
     return true;
   }
+  return false;
 }
 
 // Waves per SIMD that registers have to leave room for: two workgroups of a

@@ -7,6 +7,9 @@
 namespace convrot {
 namespace {
 
+// HIP counts a grid's threads along x in 32 bits.
+constexpr int64_t kMaxGridThreads = (int64_t{1} << 32) - 1;
+
 // The most token tiles of bm rows that P rows of `experts` experts can make:
 // every expert with rows may end in one partial tile.
 int64_t most_tiles(int64_t P, int64_t experts, int64_t bm) {
@@ -20,7 +23,7 @@ hipError_t launch_tile(const int8_t* xq, const float* x_scale, const int8_t* wq,
                        hipStream_t stream) {
   const int64_t tiles_n = (N + T::BN - 1) / T::BN;
   const int64_t blocks = tiles_n * most_tiles(g.P, g.experts, T::BM);
-  if (blocks > kMaxGroupedTiles) return hipErrorInvalidConfiguration;
+  if (blocks * T::kThreads > kMaxGridThreads) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((gemm_i8_kernel<T, EPI, Grouped>), dim3(static_cast<uint32_t>(blocks)), dim3(T::kThreads), 0,
                      stream, wq, xq, 0, static_cast<int>(N), static_cast<int>(K), static_cast<int>(tiles_n), 0, x_scale,
                      w_scale, bias, y, g);
@@ -171,7 +174,7 @@ hipError_t launch_few(const void* x, const int8_t* wq, const float* w_scale, boo
                       uint16_t* y, const Grouped& g, int64_t N, int64_t K, int group, hipStream_t stream) {
   const int64_t tiles_n = (N + 15) / 16;
   const int64_t blocks = tiles_n * most_tiles(g.P, g.experts, 16);
-  if (blocks > kMaxGroupedTiles) return hipErrorInvalidConfiguration;
+  if (blocks * kThreads > kMaxGridThreads) return hipErrorInvalidConfiguration;
   auto go = [&](auto g_c, auto steps_c) {
     hipLaunchKernelGGL((grouped_few_kernel<In, decltype(g_c)::value, decltype(steps_c)::value>),
                        dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), static_cast<size_t>(g.x_rows) * K, stream,

@@ -297,6 +297,7 @@ hipError_t launch_rows(const Down& p, int group, int8_t* xq, float* xs, const fl
 int parts_of(int64_t M, int64_t K) {
   const int64_t tiles = (M + kTile - 1) / kTile, pieces = K / 64;
   int64_t parts = 5 * num_cus() / (2 * tiles);
+  if (parts * M > kLoraSumRows) parts = kLoraSumRows / M;
   parts = parts < 1 ? 1 : parts > kMaxLoraParts ? kMaxLoraParts : parts;
   auto turns = [&](int64_t n) { return ((pieces + n - 1) / n + kWaves - 1) / kWaves; };
   while (parts > 1 && turns(parts - 1) == turns(parts)) --parts;

@@ -44,9 +44,7 @@ LoraLayout lora_layout(int64_t M, int64_t K, int64_t N, int64_t max_rank) {
   l.scales = round_up(static_cast<size_t>(l.S) * K, 256);
   l.t = l.scales + round_up(static_cast<size_t>(l.S) * 4, 256);
   l.sums = l.t + round_up(static_cast<size_t>(l.S) * l.t_stride * 2, 256);
-  // the parts of K in which the first product is summed (a part count of the
-  // host's alone: the same for every slice)
-  l.total = l.sums + static_cast<size_t>(kMaxLoraParts) * l.S * l.t_stride * 4;
+  l.total = l.sums + static_cast<size_t>(lora_sum_rows(l.S)) * l.t_stride * 4;
   return l;
 }
 
@@ -97,12 +95,11 @@ int convrot_block_norm(const convrot_block* b, void* stream) {
     if (!aligned16(q))
       return fail(CONVROT_EALIGN, "%s: h, u, the weights, gate, scale, shift, h_out and out must be 16-byte aligned",
                   who);
-  const BlockNorm p{static_cast<int>(b->K), b->n_routes, b->post_norm, b->pre_norm, b->h, b->u, b->route_row,
+  const BlockNorm p{b->M, static_cast<int>(b->K), b->n_routes, b->post_norm, b->pre_norm, b->h, b->u, b->route_row,
                     b->route_weight, b->u_rows, b->post_weight, b->pre_weight, b->gate, b->scale, b->shift,
                     mods ? b->mod_index : nullptr, b->n_mod, b->mod_stride, b->residual_scale, b->eps, b->h_out, b->out,
                     b->out_scale};
-  return hip_status(launch_block_norm(p, b->M, b->group, b->io_dtype == CONVROT_F16, static_cast<hipStream_t>(stream)),
-                    who);
+  return hip_status(launch_block_norm(p, b->group, b->io_dtype == CONVROT_F16, static_cast<hipStream_t>(stream)), who);
 }
 
 size_t convrot_grouped_workspace(int64_t M, int64_t K) {
