@@ -7,17 +7,17 @@
 // layers rounds there too); it moves the result by at most half a step of the
 // adapter's part.
 //
-// lora_down_kernel: a workgroup takes 64 tokens and a part of K, which its four
-// waves split again; each wave keeps the sums of 4 x NB blocks (16 tokens x 16
-// ranks, v_mfma_*_16x16x32) in registers, so a loaded piece of x serves 16 NB
-// ranks and a piece of the adapter 64 tokens.  What bounds it is what a CU can
-// draw from its L2 (about 27 bytes a cycle here), and 64 tokens a workgroup
-// with K split over gridDim.y move half of what 16 tokens with all of K do
-// while filling the chip.  A wave that has several pieces of K loads two before it
-// multiplies.  The waves' sums are joined through LDS, the parts
-// of K by lora_sum, both in a fixed order.  The adapters met among the
-// tokens are taken one after another, or, where the tiles would leave the chip
-// idle, dealt out over gridDim.z workgroups.
+// lora_down_kernel: a workgroup takes 64 tokens, 16 a wave, and a part of K
+// (gridDim.y of them fill the chip).  Pieces of 64 elements of K, 64 token rows
+// and 16 NB rows of the adapter, stream through a ring of LDS stages by
+// direct-to-LDS loads of whole 128-byte lines, several pieces ahead, and each
+// wave multiplies its tokens with the shared adapter rows from there
+// (v_mfma_*_16x16x32, ranks x tokens).  A wave's token rows are its own, so a
+// wave without the adapter loads and multiplies none.  What bounds it is what a
+// CU can draw from L2 and the latency of the draw.  The parts of K are summed by
+// lora_sum in a fixed order.  The adapters met among the tokens are taken one
+// after another, or, where the tiles would leave the chip idle, dealt out over
+// gridDim.z workgroups.
 //
 // lora_dot, for few tokens with adapters of their own: a wave per token and two
 // of its ranks, each lane a plain dot product over its part of K.
@@ -64,21 +64,38 @@ __device__ inline uint32_t round16(float v) {
   else return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
+typedef __attribute__((address_space(3))) void lds_void_t;
+typedef const __attribute__((address_space(1))) void glb_void_t;
+
+// 16-byte chunk `chunk` of LDS row `row` (128 bytes), swizzled so that the rows
+// and chunks one fragment read takes fall into distinct banks
+__device__ inline int chunk_at(int row, int chunk) { return row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4); }
+
 // sums [gridDim.y][M][t_stride] fp32
-template <bool F16, int NB, int DEPTH>
+template <bool F16, int NB, int STAGES>
 __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* __restrict__ sums) {
-  __shared__ __attribute__((aligned(16))) v4f part[kWaves][4][NB][64];
+  constexpr int kXBytes = kTile * 128, kStage = kXBytes + NB * 16 * 128;
+  constexpr int kALoads = NB > 2 ? NB / 2 : 1;      // of a wave (with one block two waves load each row twice)
+  __shared__ __attribute__((aligned(16))) char lds[STAGES * kStage];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, k8 = lane >> 4 << 3;
+  const int r = lane & 15;
   const int m0 = blockIdx.x * kTile;
   const int M = p.M, K = p.K;
   const int mine = p.index[min(m0 + lane, M - 1)];
-  // this part's pieces of 64 elements are neighbours, dealt out to the waves
-  constexpr int step = kWaves * 64;
-  const int part_k = (K / 64 + gridDim.y - 1) / gridDim.y * 64;
-  const int k0 = blockIdx.y * part_k + wave * 64, k_end = min(K, static_cast<int>(blockIdx.y + 1) * part_k);
-  // after the sum this wave stores token block `wave`
+  // this part's pieces
+  const int pieces = K / 64, per_part = (pieces + gridDim.y - 1) / gridDim.y;
+  const int first = blockIdx.y * per_part, n = min(pieces - first, per_part);
+  // a load fills eight LDS rows: lane -> row 8 i + (lane >> 3), stored chunk
+  // lane & 7
+  const char* x_base = reinterpret_cast<const char*>(p.x + static_cast<int64_t>(m0) * K) + static_cast<int64_t>(first) * 128;
+  uint32_t x_off[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row = 16 * wave + 8 * j + (lane >> 3);
+    x_off[j] = static_cast<uint32_t>(min(m0 + row, M - 1) - m0) * (2u * static_cast<uint32_t>(K)) +
+               (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+  }
   const int m_out = m0 + 16 * wave + r;
   const int own = m_out < M ? p.index[m_out] : -1;
 
@@ -88,64 +105,74 @@ __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* _
     const uint64_t same = __ballot(m0 + lane < M && mine == a);
     left &= ~same;
     if (turn % gridDim.z != blockIdx.z) continue;
+    const bool here = (same >> (16 * wave) & 0xffff) != 0;
     int row0, rank;
     p.range(a, row0, rank);
-    // a block of 16 tokens without this adapter reads the rows of one with it
-    // (its sums are not used), so that it draws nothing more from L2
-    const uint16_t* x_row[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int from = (same >> (16 * j) & 0xffff) != 0 ? j : __builtin_ctzll(same) / 16;
-      x_row[j] = p.x + static_cast<int64_t>(min(m0 + 16 * from + r, M - 1)) * K + k8;
-    }
     for (int base = 0; base < rank; base += 16 * NB) {
-      v4f acc[4][NB] = {};
+      const char* w_base = reinterpret_cast<const char*>(p.a_rows + static_cast<int64_t>(row0 + base) * K) +
+                           static_cast<int64_t>(first) * 128;
       // rows past the rank: the last one (its sums are not used)
-      const uint16_t* w_row[NB];
+      uint32_t w_off[kALoads];
+      int w_dst[kALoads];
 #pragma unroll
-      for (int q = 0; q < NB; ++q)
-        w_row[q] = p.a_rows + static_cast<int64_t>(row0 + min(base + 16 * q + r, rank - 1)) * K + k8;
-      for (int k = k0; k < k_end; k += DEPTH * step) {
-        v4i xf[DEPTH][2][4], wf[DEPTH][2][NB];
+      for (int j = 0; j < kALoads; ++j) {
+        const int i = NB == 1 ? (wave & 1) : wave * kALoads + j;
+        const int row = 8 * i + (lane >> 3);
+        w_off[j] = static_cast<uint32_t>(min(row, rank - 1 - base)) * (2u * static_cast<uint32_t>(K)) +
+                   (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+        w_dst[j] = kXBytes + i * 1024;
+      }
+      auto issue = [&](int piece, int stage, auto with_x_c) {
+        const int64_t k0 = static_cast<int64_t>(min(piece, n - 1)) * 128;
+        char* st = lds + stage * kStage;
+        if constexpr (decltype(with_x_c)::value) {
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-          const int kd = k + d * step < k_end ? k + d * step : k;
+          for (int j = 0; j < 2; ++j)
+            __builtin_amdgcn_global_load_lds((glb_void_t*)(x_base + k0 + x_off[j]),
+                                             (lds_void_t*)(st + (2 * wave + j) * 1024), 16, 0, 0);
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+        for (int j = 0; j < kALoads; ++j)
+          __builtin_amdgcn_global_load_lds((glb_void_t*)(w_base + k0 + w_off[j]), (lds_void_t*)(st + w_dst[j]), 16, 0, 0);
+      };
+      v4f acc[NB] = {};
+      // one barrier a piece: it has landed everywhere, and everyone is done with
+      // the stage that is filled next; pieces past the end fill stages that are
+      // not read
+      auto stream = [&](auto with_x_c) {
+        constexpr int kLoads = kALoads + (decltype(with_x_c)::value ? 2 : 0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) xf[d][h][j] = *reinterpret_cast<const v4i*>(x_row[j] + kd + 32 * h);
+        for (int d = 0; d < STAGES - 1; ++d) issue(d, d, with_x_c);
+        for (int i = 0; i < n; ++i) {
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * kLoads) : "memory");
+          issue(i + STAGES - 1, (i + STAGES - 1) % STAGES, with_x_c);
+          if constexpr (decltype(with_x_c)::value) {
+            const char* st = lds + (i % STAGES) * kStage;
 #pragma unroll
-            for (int q = 0; q < NB; ++q) wf[d][h][q] = *reinterpret_cast<const v4i*>(w_row[q] + kd + 32 * h);
+            for (int h = 0; h < 2; ++h) {
+              const v4i xf = *reinterpret_cast<const v4i*>(st + chunk_at(16 * wave + r, 4 * h + (lane >> 4)));
+#pragma unroll
+              for (int q = 0; q < NB; ++q) {
+                const v4i wf = *reinterpret_cast<const v4i*>(st + kXBytes + chunk_at(16 * q + r, 4 * h + (lane >> 4)));
+                acc[q] = mfma<F16>(wf, xf, acc[q]);
+              }
+            }
           }
         }
-        __builtin_amdgcn_sched_barrier(0);      // every load before the first product
+      };
+      if (here) stream(std::true_type{});
+      else stream(std::false_type{});
+      // lane l holds ranks 4 (l >> 4) + e of token l & 15
+      if (own == a) {
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-          if (d > 0 && k + d * step >= k_end) break;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int q = 0; q < NB; ++q) acc[j][q] = mfma<F16>(wf[d][h][q], xf[d][h][j], acc[j][q]);
+        for (int q = 0; q < NB; ++q) {
+          const int rank0 = base + 16 * q + (lane >> 4) * 4;
+          if (rank0 < p.t_stride)
+            *reinterpret_cast<v4f*>(sums + (static_cast<int64_t>(blockIdx.y) * M + m_out) * p.t_stride + rank0) = acc[q];
         }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int q = 0; q < NB; ++q) part[wave][j][q][lane] = acc[j][q];
-      __syncthreads();
-      // lane l holds ranks 4 (l >> 4) + e of token l & 15
-#pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        v4f sum = part[0][wave][q][lane];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) sum += part[w][wave][q][lane];
-        const int rank0 = base + 16 * q + (lane >> 4) * 4;
-        if (own == a && rank0 < p.t_stride)
-          *reinterpret_cast<v4f*>(sums + (static_cast<int64_t>(blockIdx.y) * M + m_out) * p.t_stride + rank0) = sum;
-      }
-      __syncthreads();
+      // the ring is quiet before it starts again
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
   }
 }
@@ -261,10 +288,9 @@ hipError_t launch_down(const Down& p, float* sums, int parts, hipStream_t stream
   const int64_t most = p.adapters < kTile ? p.adapters : kTile;         // adapters a tile can hold
   const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(parts),
                   static_cast<uint32_t>(1 + cuts < most ? 1 + cuts : most));
-  if (p.K / 64 > parts * kWaves)
-    hipLaunchKernelGGL((lora_down_kernel<F16, NB, 2>), grid, dim3(kWaves * 64), 0, stream, p, sums);
-  else
-    hipLaunchKernelGGL((lora_down_kernel<F16, NB, 1>), grid, dim3(kWaves * 64), 0, stream, p, sums);
+  // two workgroups a CU
+  constexpr int kStages = NB == 4 ? 4 : NB == 2 ? 6 : 7;
+  hipLaunchKernelGGL((lora_down_kernel<F16, NB, kStages>), grid, dim3(kWaves * 64), 0, stream, p, sums);
   return hipGetLastError();
 }
 
@@ -293,15 +319,14 @@ hipError_t launch_rows(const Down& p, int group, int8_t* xq, float* xs, const fl
 }
 
 // Parts of K: up to two and a half workgroups a CU, and the fewest with which
-// a wave has as few pieces of K as with that many.
+// a workgroup has as few pieces of K as with that many (every part has some).
 int parts_of(int64_t M, int64_t K) {
   const int64_t tiles = (M + kTile - 1) / kTile, pieces = K / 64;
   int64_t parts = 5 * num_cus() / (2 * tiles);
   if (parts * M > kLoraSumRows) parts = kLoraSumRows / M;
   parts = parts < 1 ? 1 : parts > kMaxLoraParts ? kMaxLoraParts : parts;
-  auto turns = [&](int64_t n) { return ((pieces + n - 1) / n + kWaves - 1) / kWaves; };
-  while (parts > 1 && turns(parts - 1) == turns(parts)) --parts;
-  return static_cast<int>(parts);
+  const int64_t per_part = (pieces + parts - 1) / parts;
+  return static_cast<int>((pieces + per_part - 1) / per_part);
 }
 
 template <bool F16>
