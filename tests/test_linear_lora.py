@@ -150,6 +150,27 @@ def test_a_token_does_not_see_the_others(B, M):
 
 
 @gpu
+@pytest.mark.parametrize("M,ranks", [(3, [5, 20]), (16, [17, 33]), (40, [5, 9, 12, 20, 3, 40]), (90, [5, 40]), (300, [7, 33])])
+def test_infinities_are_the_formulas(B, M, ranks):
+    """An infinite weight in an adapter's last row gives the infinity the sum has, not NaN from
+    the padding behind it."""
+    p = problem(M, 256, 40, "bf16", ranks, False, False, M, 2, none=0.0)
+    last = p["offsets"][1:].long() - 1
+    p["lora_b"][last, 3] = float("inf")
+    got = B.convrot_linear_lora(**p, group=128)
+    fine = torch.ones(40, dtype=torch.bool, device=DEV)
+    fine[3] = False
+    q = dict(p, lora_b=p["lora_b"].clone())
+    q["lora_b"][last, 3] = 0.0
+    assert torch.equal(got[:, fine], B.convrot_linear_lora(**q, group=128)[:, fine])
+    a = p["index"].long()
+    t = (p["lora_a"][last[a]].double() * p["x"].double()).sum(1)
+    sure = t.abs() > 1e-3                    # far from a rounding to zero
+    assert sure.sum() > M // 2
+    assert torch.equal(got[sure, 3].double(), torch.where(t[sure] > 0, float("inf"), float("-inf")))
+
+
+@gpu
 @pytest.mark.parametrize("M", [16, 200])
 def test_no_ranks_at_all_and_max_rank(B, M):
     p = problem(M, 256, 72, "fp16", [0, 0], False, True, 2, 4)
