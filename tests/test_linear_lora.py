@@ -115,6 +115,16 @@ def check(B, p, group):
     return got
 
 
+# one round of 256 x 128 tiles: few K, whole and ragged sides
+@gpu
+@pytest.mark.parametrize("io,row,bias", [("bf16", True, True), ("fp16", False, False)])
+@pytest.mark.parametrize("M,K,N,ranks,run,group", [
+    (257, 128, 14337, [16, 5], 100, 128), (1999, 256, 4095, [40] * 9, 50, 256), (2048, 384, 4096, [8], None, 128),
+    (1301, 640, 4001, [64, 0, 33, 512], 7, 128)])
+def test_one_round(B, M, K, N, ranks, run, group, io, row, bias):
+    check(B, problem(M, K, N, io, ranks, row, bias, M + K + N, run), group)
+
+
 # every tile the call chooses from, ranks from 1 up, odd sizes, slices (M > 2N)
 @gpu
 @pytest.mark.parametrize("io,row,bias", [("bf16", False, True), ("fp16", True, False)])

@@ -1,6 +1,7 @@
 // gemm_core.hpp -- the GEMM kernels of the ConvRot linear layer for gfx950,
 // included by the files that launch them: gemm_i8.hip (the layer's product and
-// the default path's) and gemm_grouped.hip (the product per expert).
+// the default path's), gemm_grouped.hip (the product per expert) and
+// gemm_lora.hip (the product with low-rank adapters).
 //
 // What is computed (page "int8 Compute", InvokeAI docs, opening section: the
 // product of the two code tensors runs on the integer matrix units; "What
@@ -184,6 +185,11 @@ using TileTall = Tile<192, 288, 2, 6, 16, 4, 2, 128>;
 using TileM64 = Tile<64, 64, 2, 2, 32, 1, 8>;
 using TileM128 = Tile<64, 128, 2, 2, 32, 1, 8>;
 using TileM32 = Tile<64, 32, 2, 1, 32, 1, 12>;
+
+// 256 channels x 128 tokens, 8 waves (each 64 x 64 with 32x32x32 MFMAs), for
+// layers with adapters and for experts of some dozen rows: two 128-byte stages
+// and a third one of the weight (kThirdA), which comes from HBM.
+using TileDeep = Tile<256, 128, 4, 2, 32, 4, 2, 128>;
 
 typedef int v16i __attribute__((ext_vector_type(16)));
 
@@ -754,7 +760,9 @@ __global__ __launch_bounds__(T::kThreads, (kMinWaves<T, X>)) void gemm_i8_kernel
   // is stage slab % 3, its B part lies behind all A stages.  With waves past
   // the expert's rows skipping their products (below): 8 experts of 385 rows,
   // 12288 x 4096: 215 us with neither, 208 without the third stage, 190.
-  constexpr bool kThirdA = std::is_same_v<X, Grouped> && T::kStages == 2;
+  // Layers with adapters on one round of 256 x 128 tiles: the same.
+  constexpr bool kThirdA =
+      T::kStages == 2 && (std::is_same_v<X, Grouped> || (std::is_same_v<X, LoraList> && std::is_same_v<T, TileDeep>));
   constexpr int kABytes = T::BN * T::BK, kBBytes = T::BM * T::BK;
   __shared__ __attribute__((aligned(16))) char lds[T::kLdsBytes + (kThirdA ? kABytes : 0)];
   constexpr bool DEQUANT = EPI != kEpiI32;
@@ -980,9 +988,17 @@ __global__ __launch_bounds__(T::kThreads, (kMinWaves<T, X>)) void gemm_i8_kernel
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < T::kBLoads; ++j)
-        __builtin_amdgcn_global_load_lds((glb_void_t*)(b_row[GROUPED ? j : 0] + k0),
-                                         (lds_void_t*)(lds + at + dst[T::kALoads + j] - kABytes), 16, 0, 0);
+      for (int j = 0; j < T::kBLoads; ++j) {
+        const int8_t* src;
+        if constexpr (GROUPED) {
+          src = b_row[j] + k0;
+        } else {
+          asm volatile("" : "+v"(off[T::kALoads + j]));
+          src = b_tile + k0 + off[T::kALoads + j];
+        }
+        __builtin_amdgcn_global_load_lds((glb_void_t*)src, (lds_void_t*)(lds + at + dst[T::kALoads + j] - kABytes), 16,
+                                         0, 0);
+      }
     }
   };
   // the fragments of unit kk from the stages at byte offsets a_at and b_at
@@ -1037,7 +1053,7 @@ __global__ __launch_bounds__(T::kThreads, (kMinWaves<T, X>)) void gemm_i8_kernel
       a_next = a_after;
       a_after = freed;
     };
-    if (m0 + wm * T::kWaveM < M) {
+    if (!GROUPED || m0 + wm * T::kWaveM < M) {
       read_parts(a_at, kB0, 0, f0);
       for (int kt = 0; kt < KT; ++kt) {
         const int b_at = kB0 + (kt & 1) * kBBytes, b_next = kB0 + ((kt + 1) & 1) * kBBytes;

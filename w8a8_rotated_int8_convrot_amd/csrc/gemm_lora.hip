@@ -33,8 +33,25 @@ hipError_t launch_persist(const int8_t* xq, const float* x_scale, const int8_t* 
   return hipGetLastError();
 }
 
-// The tiles are the layer's own (pick_gemm_tile), with the persistent 192 x 288
-// kernel for its largest ones and the one-wave 16 x 16 tile for few tokens.
+// Whether 256 x 128 tiles make one round that gives more than 5/8 of the CUs a
+// tile.  Such a round is as long as one tile, and nothing runs beside a tile's
+// prologue and the adapters' panels, so the smallest tile that still makes one
+// round wins; the layer's own choice (two 128 x 128 tiles a CU, half-empty
+// rounds of 384 x 96 or 192 x 288) gives each CU more.  us a call, weight from
+// HBM, the layer's choice -> this (M x K x N, tiles):
+//   2000 x 12288 x 4096 (256)  219 -> 183     1024 x 8192 x 8192 (256)  118 -> 95
+//   1500 x 4096 x 4096 (192)    62 -> 57      512 x 4096 x 12288 (192)  53 -> 50
+//   1300 x 4096 x 4096 (176)    59 -> 53      777 x 2048 x 6144 (168)   50 -> 50
+// and past those bounds 1024 x 4096 x 4096 (128)  44 -> 52, 3000 x 4096 x 4096
+// (384)  81 -> 94, 4608 x 4096 x 12288 (1728)  279 -> 336.
+bool one_round(int64_t M, int64_t N) {
+  const int64_t tiles = ((M + TileDeep::BM - 1) / TileDeep::BM) * ((N + TileDeep::BN - 1) / TileDeep::BN);
+  return M > 256 && tiles <= num_cus() && 8 * tiles > 5 * num_cus();
+}
+
+// The tiles are the layer's own (pick_gemm_tile) otherwise, with the persistent
+// 192 x 288 kernel for its largest ones and the one-wave 16 x 16 tile for few
+// tokens.
 // Up to 128 tokens with several adapters each lane adds its own token's ranks;
 // larger batches, and batches of at most four adapters, go through the list of
 // the tile's adapters.
@@ -52,6 +69,7 @@ hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, 
     return launch_tile<TileSkinny, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
   }
   const LoraList l{lora};
+  if (one_round(M, N)) return launch_tile<TileDeep, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
   switch (tile) {
     case 7: return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
     case 5: return launch_tile<TileSkinny, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
