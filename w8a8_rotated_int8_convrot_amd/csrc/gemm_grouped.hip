@@ -40,8 +40,17 @@ hipError_t launch_tile(const int8_t* xq, const float* x_scale, const int8_t* wq,
 // and 32 of 2048 x 4096:  96   128   192   256
 //   128x128              88.3  87.6   108   134
 //   192x288              96.4   102   105   109
-// 64 x 64 up to 24 rows, 128 x 128 up to 160, then 192 x 288; 16 x 16 where
-// 64-channel tiles would not give every CU one.
+// and 256 x 128 with three weight stages (TileDeep) against 128 x 128:
+//   64 experts of 1536 x 2048:   32  64.4 -> 56.5   128  85.3 -> 81.0   160  94.8 -> 84.9
+//   32 of 2048 x 4096:          128   112 -> 97
+//   16 of 2048 x 7168:          128   101 -> 83
+//   8 of 14336 x 4096:           75   132 -> 123
+//   32 of 4096 x 4096:           64   153 -> 160    160   216 -> 197
+//   16 of 1408 x 2048:           64  23.6 -> 25.5   (96 tiles)
+//   8 of 2048 x 7168:           128  59.6 -> 70.8   (64 tiles)
+// 64 x 64 up to 24 rows; up to 160 rows 256 x 128 where the experts make tiles
+// for half the CUs, else 128 x 128; then 192 x 288 (200 rows, 64 experts: 98.5
+// against 106); 16 x 16 where 64-channel tiles would not give every CU one.
 template <int EPI>
 hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
                       const uint16_t* bias, uint16_t* y, const Grouped& g, int64_t N, int64_t K, hipStream_t stream) {
@@ -50,6 +59,8 @@ hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, 
   if (mean <= 16 && met * ((N + 63) / 64) < num_cus())
     return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
   if (mean <= 24) return launch_tile<TileM64, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+  if (mean <= 160 && 2 * met * ((N + TileDeep::BN - 1) / TileDeep::BN) >= num_cus())
+    return launch_tile<TileDeep, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
   if (mean <= 160) return launch_tile<TileMid, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
   return launch_tile<TileTall, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
 }
@@ -62,8 +73,8 @@ hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, 
 // workgroup rotates and codes the tokens into LDS -- every workgroup the same,
 // a few hundred instructions a wave under the weight's latency -- and the
 // products take the tokens from there.  The waves' sums are joined in LDS.
-// One token, 4 of 16 experts of 1408 x 2048: rotate + quant 2.4 us and the
-// product 6.2 us in two launches.
+// One token, 4 of 16 experts of 1408 x 2048: 6.9 us; in two launches rotate +
+// quant took 2.4 us and the product 6.2, and the call 13.6 us instead of 9.6.
 constexpr int kFewTokens = 4;
 constexpr int kFewK = 8192;
 struct FewTile { static constexpr int BN = 16, BM = 16, kGroupM = 1; };
