@@ -106,11 +106,12 @@ def test_equals_the_layer_expert_by_expert(B, M, K, N, E, P, group, io, row, bia
     assert torch.equal(got, by_expert(B, x, wq, s, group, offsets, rows, b))
 
 
-# 256 x 128 tiles: experts of some dozen rows with many channels
+# 256 x 128 and 256 x 192 tiles: experts with many channels
 @gpu
 @pytest.mark.parametrize("io,row,bias", [("bf16", True, False), ("fp16", False, True)])
 @pytest.mark.parametrize("M,K,N,E,P,group", [
-    (70, 128, 4095, 16, 500, 128), (300, 256, 8200, 5, 777, 256), (129, 640, 1024, 33, 4100, 128), (64, 384, 33000, 1, 64, 128)])
+    (70, 128, 4095, 16, 500, 128), (300, 256, 8200, 5, 777, 256), (129, 640, 1024, 33, 4100, 128), (64, 384, 33000, 1, 64, 128),
+    (500, 128, 7100, 8, 1024, 128), (411, 384, 2050, 20, 5003, 128), (90, 256, 1030, 32, 9000, 256)])
 def test_wide_experts(B, M, K, N, E, P, group, io, row, bias):
     g, dt, wq, s, b = layer(K, N, E, io, row, bias, M + K + N)
     x = stream(g, M, K, dt)

@@ -115,12 +115,13 @@ def check(B, p, group):
     return got
 
 
-# one round of 256 x 128 tiles: few K, whole and ragged sides
+# one round of 256 x 128 or 256 x 192 tiles: few K, whole and ragged sides
 @gpu
 @pytest.mark.parametrize("io,row,bias", [("bf16", True, True), ("fp16", False, False)])
 @pytest.mark.parametrize("M,K,N,ranks,run,group", [
     (257, 128, 14337, [16, 5], 100, 128), (1999, 256, 4095, [40] * 9, 50, 256), (2048, 384, 4096, [8], None, 128),
-    (1301, 640, 4001, [64, 0, 33, 512], 7, 128)])
+    (1301, 640, 4001, [64, 0, 33, 512], 7, 128), (2999, 128, 4090, [7, 300], 1000, 128), (400, 384, 28600, [16, 40, 9], 90, 128),
+    (2112, 256, 4096, [1, 2, 3, 4, 5] * 20, 1, 256)])
 def test_one_round(B, M, K, N, ranks, run, group, io, row, bias):
     check(B, problem(M, K, N, io, ranks, row, bias, M + K + N, run), group)
 

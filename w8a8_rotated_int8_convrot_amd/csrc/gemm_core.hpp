@@ -186,10 +186,12 @@ using TileM64 = Tile<64, 64, 2, 2, 32, 1, 8>;
 using TileM128 = Tile<64, 128, 2, 2, 32, 1, 8>;
 using TileM32 = Tile<64, 32, 2, 1, 32, 1, 12>;
 
-// 256 channels x 128 tokens, 8 waves (each 64 x 64 with 32x32x32 MFMAs), for
-// layers with adapters and for experts of some dozen rows: two 128-byte stages
-// and a third one of the weight (kThirdA), which comes from HBM.
+// 256 channels x 128 or 192 tokens, 8 waves (each 64 x 64 or 64 x 96 with
+// 32x32x32 MFMAs), for layers with adapters and for experts: two 128-byte
+// stages and a third one of the weight (kThirdA), which comes from HBM.
 using TileDeep = Tile<256, 128, 4, 2, 32, 4, 2, 128>;
+using TileDeep192 = Tile<256, 192, 4, 2, 32, 4, 2, 128>;
+template <class T> constexpr bool kIsDeep = std::is_same_v<T, TileDeep> || std::is_same_v<T, TileDeep192>;
 
 typedef int v16i __attribute__((ext_vector_type(16)));
 
@@ -760,9 +762,9 @@ __global__ __launch_bounds__(T::kThreads, (kMinWaves<T, X>)) void gemm_i8_kernel
   // is stage slab % 3, its B part lies behind all A stages.  With waves past
   // the expert's rows skipping their products (below): 8 experts of 385 rows,
   // 12288 x 4096: 215 us with neither, 208 without the third stage, 190.
-  // Layers with adapters on one round of 256 x 128 tiles: the same.
+  // Layers with adapters on one round of these tiles: the same.
   constexpr bool kThirdA =
-      T::kStages == 2 && (std::is_same_v<X, Grouped> || (std::is_same_v<X, LoraList> && std::is_same_v<T, TileDeep>));
+      T::kStages == 2 && (std::is_same_v<X, Grouped> || (std::is_same_v<X, LoraList> && kIsDeep<T>));
   constexpr int kABytes = T::BN * T::BK, kBBytes = T::BM * T::BK;
   __shared__ __attribute__((aligned(16))) char lds[T::kLdsBytes + (kThirdA ? kABytes : 0)];
   constexpr bool DEQUANT = EPI != kEpiI32;

@@ -30,39 +30,52 @@ hipError_t launch_tile(const int8_t* xq, const float* x_scale, const int8_t* wq,
   return hipGetLastError();
 }
 
-// The tile goes by the mean rows of an expert, which is all the host knows
-// (weights from HBM, 64 experts of 1536 x 2048, us):
-//   rows      4     8    16    32    64
-//   16 x 16  40.3  43.8  56.5  80.8   130
-//   64 x 64  37.4  37.4  42.8  53.1  68.5
-//   128x128  39.0  40.2  47.7  53.0  57.9
-//   192x288  45.0  46.6  49.4  54.0  57.4
-// and 32 of 2048 x 4096:  96   128   192   256
-//   128x128              88.3  87.6   108   134
-//   192x288              96.4   102   105   109
-// and 256 x 128 with three weight stages (TileDeep) against 128 x 128:
-//   64 experts of 1536 x 2048:   32  64.4 -> 56.5   128  85.3 -> 81.0   160  94.8 -> 84.9
-//   32 of 2048 x 4096:          128   112 -> 97
-//   16 of 2048 x 7168:          128   101 -> 83
-//   8 of 14336 x 4096:           75   132 -> 123
-//   32 of 4096 x 4096:           64   153 -> 160    160   216 -> 197
-//   16 of 1408 x 2048:           64  23.6 -> 25.5   (96 tiles)
-//   8 of 2048 x 7168:           128  59.6 -> 70.8   (64 tiles)
-// 64 x 64 up to 24 rows; up to 160 rows 256 x 128 where the experts make tiles
-// for half the CUs, else 128 x 128; then 192 x 288 (200 rows, 64 experts: 98.5
-// against 106); 16 x 16 where 64-channel tiles would not give every CU one.
+// The tile goes by the mean rows of an expert, which is all the host knows.  Up
+// to 24 rows 64 x 64, or 16 x 16 where 64-channel tiles would not give every CU
+// one (weights from HBM, 64 experts of 1536 x 2048, us):
+//   rows      4     8    16    32
+//   16 x 16  40.3  43.8  56.5  80.8
+//   64 x 64  37.4  37.4  42.8  53.1
+//   128x128  39.0  40.2  47.7  53.0
+// Beyond, the larger tiles read less a product but come in fewer, coarser
+// rounds.  A tile costs a round of its own weight: the time of a round of
+// 256 x 128 is 1, and 128 x 128 0.7, 256 x 192 and 192 x 288 1.2 (their longer
+// prologue and their products weigh less than their size says); an expert has
+// half a tile more than its rows fill, and of more than one round the last one
+// counts a third.  On 143 shapes (11 layers, 32 to 1024 rows an expert) this
+// choice is 2.4 % behind the best of the four, thresholds on the mean rows
+// 3.5 %, and any one tile 6 to 15 %:
+//   us                 128x128  256x128  256x192  192x288
+//   16 x 1408 x 2048, 64  23.3    25.7     30.8     29.1
+//   64 x 1536 x 2048, 64  66.6    58.0     64.5     65.1
+//   8 x 7168 x 4096, 128  93.1    92.2     68.2     111
+//   8 x 14336 x 4096, 512  422     359      327      305
+double round_cost(double mean, int64_t experts, int64_t N, int bn, int bm, double weight) {
+  const double filled = mean / bm + 0.5;
+  const double rounds =
+      static_cast<double>(experts) * static_cast<double>((N + bn - 1) / bn) * (filled < 1.0 ? 1.0 : filled) / num_cus();
+  return weight * (rounds > 1.0 ? rounds + 0.3 : 1.0);
+}
+
 template <int EPI>
 hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
                       const uint16_t* bias, uint16_t* y, const Grouped& g, int64_t N, int64_t K, hipStream_t stream) {
-  const int64_t mean = (static_cast<int64_t>(g.P) + g.experts - 1) / g.experts;
   const int64_t met = g.experts < g.P ? g.experts : g.P;
+  const double mean = static_cast<double>(g.P) / static_cast<double>(met);
   if (mean <= 16 && met * ((N + 63) / 64) < num_cus())
     return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
   if (mean <= 24) return launch_tile<TileM64, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
-  if (mean <= 160 && 2 * met * ((N + TileDeep::BN - 1) / TileDeep::BN) >= num_cus())
-    return launch_tile<TileDeep, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
-  if (mean <= 160) return launch_tile<TileMid, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
-  return launch_tile<TileTall, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+  const double cost[4] = {round_cost(mean, met, N, 128, 128, 0.7), round_cost(mean, met, N, 256, 128, 1.0),
+                          round_cost(mean, met, N, 256, 192, 1.2), round_cost(mean, met, N, 192, 288, 1.2)};
+  int best = 0;
+  for (int i = 1; i < 4; ++i)
+    if (cost[i] < cost[best]) best = i;
+  switch (best) {
+    case 0: return launch_tile<TileMid, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+    case 1: return launch_tile<TileDeep, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+    case 2: return launch_tile<TileDeep192, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+    default: return launch_tile<TileTall, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+  }
 }
 
 // At most kFewTokens tokens of at most kFewK values: a launch costs the host as

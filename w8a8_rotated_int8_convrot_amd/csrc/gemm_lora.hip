@@ -33,8 +33,8 @@ hipError_t launch_persist(const int8_t* xq, const float* x_scale, const int8_t* 
   return hipGetLastError();
 }
 
-// Whether 256 x 128 tiles make one round that gives more than 5/8 of the CUs a
-// tile.  Such a round is as long as one tile, and nothing runs beside a tile's
+// Whether these tiles make one round that gives more than 5/8 of the CUs a
+// tile: 256 x 128, else 256 x 192.  Such a round is as long as one tile, and nothing runs beside a tile's
 // prologue and the adapters' panels, so the smallest tile that still makes one
 // round wins; the layer's own choice (two 128 x 128 tiles a CU, half-empty
 // rounds of 384 x 96 or 192 x 288) gives each CU more.  us a call, weight from
@@ -42,10 +42,15 @@ hipError_t launch_persist(const int8_t* xq, const float* x_scale, const int8_t* 
 //   2000 x 12288 x 4096 (256)  219 -> 183     1024 x 8192 x 8192 (256)  118 -> 95
 //   1500 x 4096 x 4096 (192)    62 -> 57      512 x 4096 x 12288 (192)  53 -> 50
 //   1300 x 4096 x 4096 (176)    59 -> 53      777 x 2048 x 6144 (168)   50 -> 50
-// and past those bounds 1024 x 4096 x 4096 (128)  44 -> 52, 3000 x 4096 x 4096
-// (384)  81 -> 94, 4608 x 4096 x 12288 (1728)  279 -> 336.
+// with 256 x 192:
+//   1500 x 2048 x 8192 (256)    76 -> 52      1500 x 4096 x 8192 (256)  126 -> 86
+//   3000 x 4096 x 4096 (256)    87 -> 82      2300 x 4096 x 4096 (192)   90 -> 80
+//   2816 x 12288 x 4096 (240)  188 -> 182     769 x 4096 x 12288 (240)   66 -> 69
+// and past those bounds, 256 x 128: 1024 x 4096 x 4096 (128 tiles)  44 -> 52,
+// 4608 x 4096 x 12288 (1728)  279 -> 336.
+template <class T>
 bool one_round(int64_t M, int64_t N) {
-  const int64_t tiles = ((M + TileDeep::BM - 1) / TileDeep::BM) * ((N + TileDeep::BN - 1) / TileDeep::BN);
+  const int64_t tiles = ((M + T::BM - 1) / T::BM) * ((N + T::BN - 1) / T::BN);
   return M > 256 && tiles <= num_cus() && 8 * tiles > 5 * num_cus();
 }
 
@@ -69,7 +74,10 @@ hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, 
     return launch_tile<TileSkinny, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
   }
   const LoraList l{lora};
-  if (one_round(M, N)) return launch_tile<TileDeep, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+  if (one_round<TileDeep>(M, N))
+    return launch_tile<TileDeep, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
+  if (one_round<TileDeep192>(M, N))
+    return launch_tile<TileDeep192, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
   switch (tile) {
     case 7: return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
     case 5: return launch_tile<TileSkinny, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
