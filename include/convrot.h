@@ -465,8 +465,9 @@ size_t convrot_grouped_workspace(int64_t M, int64_t K);
  * router's, and one captured into a graph takes whatever they then hold.
  * N >= 1, 1 <= n_experts <= 65536, M and P in [0, 2^30], and fewer than 2^31
  * tiles of 16 rows and 16 channels, one more of them for each expert
- * (CONVROT_EINVAL); a grid of 2^32 threads or more is CONVROT_EHIP.  P = 0 is a no-op.  x, wq, y and workspace are 16-byte
- * aligned.  Other errors as convrot_linear_ex.  Two launches, rotate +
+ * (CONVROT_EINVAL); a grid of 2^32 threads or more is CONVROT_EHIP.  P = 0 is
+ * a no-op, rows given or not.  x, wq, y and workspace are 16-byte aligned.
+ * Other errors as convrot_linear_ex.  Two launches, rotate +
  * quant of the M tokens and the product; one for few tokens. */
 int convrot_grouped_linear(const void *x, int io_dtype, int64_t M, int64_t K, const int8_t *wq,
                            const float *w_scale, int scale_mode, int64_t n_experts, int64_t N, int group,

@@ -50,7 +50,20 @@ def test_empty_and_workspace(B):
     assert B.convrot_grouped_workspace(-1, 128) == 0 and B.convrot_grouped_workspace(4, 0) == 0
 
 
+def test_no_rows_routed(B):
+    """An empty tensor of rows has no address."""
+    assert call(B, P=0, rows=None) == OK and call(B, P=0, rows=None, x=None, off=None, y=None, w=None, wb=0) == OK
+
+
 gpu = pytest.mark.gpu
+
+
+@gpu
+def test_no_rows_routed_from_python(B):
+    g, dt, wq, s, b = layer(256, 40, 3, "bf16", False, False, 1)
+    empty = torch.empty(0, dtype=torch.int32, device=DEV)
+    y = B.convrot_grouped_linear(stream(g, 5, 256, dt), wq, s, 128, torch.zeros(4, dtype=torch.int32, device=DEV), rows=empty)
+    assert y.shape == (0, 40)
 
 
 def layer(K, N, E, io, row, bias, seed):

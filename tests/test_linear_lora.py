@@ -161,6 +161,20 @@ def test_a_token_does_not_see_the_others(B, M):
 
 
 @gpu
+@pytest.mark.parametrize("M,N", [(1999, 4095), (3000, 4094)])
+def test_infinities_of_others_in_one_round(B, M, N):
+    """256 x 128 and 256 x 192 tiles: neighbours' infinities and NaN stay theirs."""
+    p = problem(M, 256, N, "fp16", [16, 8, 32, 24], False, True, M, 3, none=0.1)
+    want = B.convrot_linear_lora(**p, group=128)
+    a, b, sc, x = p["lora_a"].clone(), p["lora_b"].clone(), p["lora_scale"].clone(), p["x"].clone()
+    a[:16], b[24:], sc[2], x[7, 3] = float("nan"), float("inf"), float("-inf"), float("nan")
+    got = B.convrot_linear_lora(**dict(p, lora_a=a, lora_b=b, lora_scale=sc, x=x), group=128)
+    mine = (p["index"] != 0) & (p["index"] != 2) & (p["index"] != 3)
+    mine[7] = False
+    assert mine.sum() > M // 5 and torch.equal(got[mine], want[mine])
+
+
+@gpu
 @pytest.mark.parametrize("M,ranks", [(3, [5, 20]), (16, [17, 33]), (40, [5, 9, 12, 20, 3, 40]), (90, [5, 40]), (300, [7, 33])])
 def test_infinities_are_the_formulas(B, M, ranks):
     """An infinite weight in an adapter's last row gives the infinity the sum has, not NaN from

@@ -121,10 +121,10 @@ int convrot_grouped_linear(const void* x, int io_dtype, int64_t M, int64_t K, co
                 static_cast<long long>(kMaxExperts));
   if (P < 0 || P > (int64_t(1) << 30))
     return fail(CONVROT_EINVAL, "%s: P=%lld must be in [0, 2^30]", who, static_cast<long long>(P));
+  if (P == 0) return ok();
   if (!rows && P != M)
     return fail(CONVROT_EINVAL, "%s: without rows P=%lld has to be M=%lld", who, static_cast<long long>(P),
                 static_cast<long long>(M));
-  if (P == 0) return ok();
   if (M == 0) return fail(CONVROT_EINVAL, "%s: P=%lld rows of no tokens", who, static_cast<long long>(P));
   if ((P / 16 + n_experts) * ((N + 15) / 16) >= (int64_t(1) << 31))
     return fail(CONVROT_EINVAL, "%s: P=%lld, n_experts=%lld and N=%lld make too many tiles", who,
@@ -192,8 +192,8 @@ int convrot_linear_lora(const void* x, int io_dtype, int64_t M, int64_t K, const
   for (int64_t r0 = 0; r0 < M; r0 += l.S) {
     const int64_t rows = std::min(M - r0, l.S);
     const auto* xr = static_cast<const uint16_t*>(x) + r0 * K;
-    if (hipError_t e = launch_lora_down(xr, rows, K, group, f16, xq, xs, static_cast<const uint16_t*>(lora_a), R, lora_scale, offsets,
-                                        n_adapters, index + r0, max_rank, t, l.t_stride, sums, s);
+    if (hipError_t e = launch_lora_down(xr, rows, K, group, f16, xq, xs, static_cast<const uint16_t*>(lora_a), R,
+                                        lora_scale, offsets, n_adapters, index + r0, max_rank, t, l.t_stride, sums, s);
         e != hipSuccess)
       return hip_status(e, who);
     if (hipError_t e = launch_gemm_lora(xq, xs, wq, w_scale, scale_mode == CONVROT_SCALE_ROW,
