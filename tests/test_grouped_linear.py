@@ -133,6 +133,26 @@ def test_wide_experts(B, M, K, N, E, P, group, io, row, bias):
     assert torch.equal(got, by_expert(B, x, wq, s, group, offsets, rows, b))
 
 
+# 192 x 288 and 384 x 192 tiles: experts of some hundred rows
+@gpu
+@pytest.mark.parametrize("io,row,bias", [("bf16", True, True), ("fp16", False, False)])
+@pytest.mark.parametrize("M,K,N,E,P,group", [
+    (300, 256, 380, 64, 21000, 128), (700, 512, 4100, 6, 5000, 256), (800, 128, 1400, 16, 8000, 128),
+    (4100, 384, 7601, 9, 4100, 128)])
+def test_large_tiles(B, M, K, N, E, P, group, io, row, bias):
+    g, dt, wq, s, b = layer(K, N, E, io, row, bias, M + K + N)
+    x = stream(g, M, K, dt)
+    offsets, rows = route(g, M, P, E)
+    rows[:7] = torch.tensor([-1, M, 0, M - 1, 2 ** 31 - 1, -2 ** 31, 5], device=DEV)
+    offsets[0], offsets[-1] = 2, P - 3
+    offsets = torch.cummax(offsets, 0).values.clamp(max=P - 3).to(torch.int32)
+    out = torch.full((P, N), 3.0, dtype=dt, device=DEV)
+    B.convrot_grouped_linear(x, wq, s, group, offsets, rows=rows, bias=b, out=out)
+    good = (rows >= 0) & (rows < M) & (torch.arange(P, device=DEV) >= 2) & (torch.arange(P, device=DEV) < P - 3)
+    want = by_expert(B, x, wq, s, group, offsets, rows.clamp(0, M - 1), b)
+    assert (out[~good] == 3).all() and torch.equal(out[good], want[good])
+
+
 # one to four tokens go through a kernel of their own up to K = 8192
 @gpu
 @pytest.mark.parametrize("io,row,bias", [("bf16", True, True), ("fp16", False, False)])

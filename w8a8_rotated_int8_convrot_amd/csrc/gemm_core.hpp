@@ -755,7 +755,8 @@ __global__ __launch_bounds__(T::kThreads, (kMinWaves<T, X>)) void gemm_i8_kernel
     int tiles_n, int tiles_m, const float* __restrict__ x_scale,
     const float* __restrict__ w_scale, const uint16_t* __restrict__ bias,
     void* __restrict__ out, X extra = X{}) {
-  // grouped two-stage tiles: the weight has a third stage.  Each expert's weight
+  // grouped two-stage tiles: the weight has a third stage where LDS (160 KB) has
+  // room for it.  Each expert's weight
   // comes from HBM and meets a few token tiles only, and the tiles at the end
   // of an expert's rows run few products a slab, so one slab in flight covers
   // less than the latency of its loads; tokens come from L2.  A slab's A part
@@ -764,7 +765,8 @@ __global__ __launch_bounds__(T::kThreads, (kMinWaves<T, X>)) void gemm_i8_kernel
   // 12288 x 4096: 215 us with neither, 208 without the third stage, 190.
   // Layers with adapters on one round of these tiles: the same.
   constexpr bool kThirdA =
-      T::kStages == 2 && (std::is_same_v<X, Grouped> || (std::is_same_v<X, LoraList> && kIsDeep<T>));
+      T::kStages == 2 && ((std::is_same_v<X, Grouped> && T::kLdsBytes + T::BN * T::BK <= 160 * 1024) ||
+                          (std::is_same_v<X, LoraList> && kIsDeep<T>));
   constexpr int kABytes = T::BN * T::BK, kBBytes = T::BM * T::BK;
   __shared__ __attribute__((aligned(16))) char lds[T::kLdsBytes + (kThirdA ? kABytes : 0)];
   constexpr bool DEQUANT = EPI != kEpiI32;

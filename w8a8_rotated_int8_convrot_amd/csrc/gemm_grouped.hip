@@ -39,22 +39,25 @@ hipError_t launch_tile(const int8_t* xq, const float* x_scale, const int8_t* wq,
 //   128x128  39.0  40.2  47.7  53.0
 // Beyond, the larger tiles read less a product but come in fewer, coarser
 // rounds.  A tile costs a round of its own weight: the time of a round of
-// 256 x 128 is 1, and 128 x 128 0.7, 256 x 192 and 192 x 288 1.2 (their longer
-// prologue and their products weigh less than their size says); an expert has
-// half a tile more than its rows fill, and of more than one round the last one
-// counts a third.  On 143 shapes (11 layers, 32 to 1024 rows an expert) this
-// choice is 2.4 % behind the best of the four, thresholds on the mean rows
-// 3.5 %, and any one tile 6 to 15 %:
-//   us                 128x128  256x128  256x192  192x288
-//   16 x 1408 x 2048, 64  23.3    25.7     30.8     29.1
-//   64 x 1536 x 2048, 64  66.6    58.0     64.5     65.1
-//   8 x 7168 x 4096, 128  93.1    92.2     68.2     111
-//   8 x 14336 x 4096, 512  422     359      327      305
+// 256 x 128 is 1, and 128 x 128 0.7, 256 x 192 1.2, 192 x 288 1.25, 384 x 192
+// 1.75 (the larger the tile, the less its prologue weighs and the better its
+// loads are used); an expert has half a tile more than its rows fill, and more
+// than one round end 0.4 of one late.  Over 11 layers and 32 to 1500 rows an
+// expert this choice is 2.4 % behind the best of the five on the mean, called
+// back to back, and 2.5 % with everything from HBM; thresholds on the mean rows
+// 3.5 %, any one tile 6 to 16 %:
+//   us                  128x128  256x128  256x192  192x288  384x192
+//   16 x 1408 x 2048, 64   23.3    25.7     30.8     29.1
+//   64 x 1536 x 2048, 64   66.6    58.0     64.5     65.1
+//   8 x 7168 x 4096, 128   93.1    92.2     68.2     111
+//   16 x 1408 x 2048, 512  58.8    52.6     64.4     65.7     46.1
+//   8 x 14336 x 4096, 384                   249      259      234
+//   8 x 14336 x 4096, 512   422     359      322      298      303
 double round_cost(double mean, int64_t experts, int64_t N, int bn, int bm, double weight) {
   const double filled = mean / bm + 0.5;
   const double rounds =
       static_cast<double>(experts) * static_cast<double>((N + bn - 1) / bn) * (filled < 1.0 ? 1.0 : filled) / num_cus();
-  return weight * (rounds > 1.0 ? rounds + 0.3 : 1.0);
+  return weight * (rounds > 1.0 ? rounds + 0.4 : 1.0);
 }
 
 template <int EPI>
@@ -65,16 +68,18 @@ hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, 
   if (mean <= 16 && met * ((N + 63) / 64) < num_cus())
     return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
   if (mean <= 24) return launch_tile<TileM64, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
-  const double cost[4] = {round_cost(mean, met, N, 128, 128, 0.7), round_cost(mean, met, N, 256, 128, 1.0),
-                          round_cost(mean, met, N, 256, 192, 1.2), round_cost(mean, met, N, 192, 288, 1.2)};
+  const double cost[5] = {round_cost(mean, met, N, 128, 128, 0.7), round_cost(mean, met, N, 256, 128, 1.0),
+                          round_cost(mean, met, N, 256, 192, 1.2), round_cost(mean, met, N, 192, 288, 1.25),
+                          round_cost(mean, met, N, 384, 192, 1.75)};
   int best = 0;
-  for (int i = 1; i < 4; ++i)
+  for (int i = 1; i < 5; ++i)
     if (cost[i] < cost[best]) best = i;
   switch (best) {
     case 0: return launch_tile<TileMid, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
     case 1: return launch_tile<TileDeep, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
     case 2: return launch_tile<TileDeep192, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
-    default: return launch_tile<TileTall, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+    case 3: return launch_tile<TileTall, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
+    default: return launch_tile<TileWide128, EPI>(xq, x_scale, wq, w_scale, bias, y, g, N, K, stream);
   }
 }
 
