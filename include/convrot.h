@@ -479,11 +479,13 @@ int convrot_grouped_linear(const void *x, int io_dtype, int64_t M, int64_t K, co
  * Compute": adapters run beside the int8 layer in the compute precision and
  * are never coded).  Token m, with adapter a = index[m] of rank
  * offsets[a+1] - offsets[a]:
- *   t_m  = rnd(lora_scale[a] * A_a x_m)        A_a: rows offsets[a] .. of lora_a [R, K]
+ *   t_m  = lora_scale[a] * A_a x_m             A_a: rows offsets[a] .. of lora_a [R, K]
  *   y[m] = rnd(l_m + t_m B_a)                  B_a: the same rows of lora_b [R, N]
  * with l_m the layer's fp32 result (convrot_linear_ex's before its rounding)
- * and the products summed in fp32; rnd: to io_dtype.  x_m enters A_a x_m as it
- * is, neither rotated nor coded.  A token whose index is outside
+ * and the products summed in fp32; rnd: to io_dtype.  t_m is an fp32 value, or
+ * for the matrix units two 16-bit ones that stand for it within 2^-16 (bf16) or
+ * 2^-22 (fp16, over fp32's whole range) of each of its ranks.  x_m enters A_a x_m
+ * as it is, neither rotated nor coded.  A token whose index is outside
  * [0, n_adapters) has no adapter and gets convrot_linear_ex's bytes, and a
  * token's result does not depend on the other tokens' adapters.  A given shape
  * repeats its bytes from call to call. */

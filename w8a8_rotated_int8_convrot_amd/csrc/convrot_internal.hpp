@@ -14,6 +14,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <type_traits>
 
 namespace convrot {
 
@@ -103,13 +104,17 @@ hipError_t launch_grouped_few(const void* x, int64_t M, int64_t K, int group, bo
 // token's result does not depend on the other tokens' adapters.
 inline bool lora_by_token(int64_t M, int64_t adapters) { return M <= 16 || (M <= 128 && adapters > 4); }
 
-// The first product of low-rank adapters (lora.hip): t [M, t_stride] in the io
-// type, t[m][r] = scale[a] * (row offsets[a] + r of a_rows [ranks, K]) . x[m]
+// The first product of low-rank adapters (lora.hip):
+//   t[m][r] = scale[a] * (row offsets[a] + r of a_rows [ranks, K]) . x[m]
 // with a = index[m]; zero from the adapter's rank on, unset for a token whose
 // index is outside [0, adapters).  t_stride: max_rank rounded up to 32.  sums:
-// lora_sum_rows(M) * t_stride floats (not used token by token).  Rotates and
-// quantizes x too (xq, xs as launch_rotate_quant), in the same launch where the
-// row kernel would do it.
+// lora_sum_rows(M) * t_stride floats, lora_behind_t of t.  Token by token t is
+// left there in fp32, [M, t_stride].  Else the first [M, t_stride] words hold it
+// as two parts in the io type, t = (first + second) * factor, each 32 ranks as
+// 32 values of the first part and then 32 of the second; the factors of each 32
+// ranks are [t_stride / 32, M] floats in t's [M, t_stride] 16-bit words (1, and
+// not written, in bf16).  Rotates and quantizes x too (xq, xs as
+// launch_rotate_quant), in the same launch where the row kernel would do it.
 constexpr int kMaxLoraParts = 8;
 // Rows of the partial sums: parts of K times tokens, K being split only while
 // they stay within kLoraSumRows.
@@ -118,13 +123,20 @@ inline int64_t lora_sum_rows(int64_t M) {
   if (kMaxLoraParts * M <= kLoraSumRows) return kMaxLoraParts * M;
   return M > kLoraSumRows ? M : kLoraSumRows;
 }
+// The first 256-byte boundary behind t [M, t_stride].
+template <class U16>
+inline auto lora_behind_t(U16* t, int64_t M, int64_t t_stride) {
+  constexpr bool kConst = std::is_const_v<U16>;
+  return reinterpret_cast<std::conditional_t<kConst, const float, float>*>(t + (M * t_stride + 127) / 128 * 128);
+}
 hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, int group, bool f16, int8_t* xq, float* xs,
                             const uint16_t* a, int64_t ranks, const float* scale, const int32_t* offsets,
                             int64_t adapters, const int32_t* index, int64_t max_rank, uint16_t* t, int64_t t_stride,
                             float* sums, hipStream_t stream);
 
-// The layer's product with the adapters' second one, t . b (b [ranks, N]),
-// added before the output is rounded (gemm_lora.hip).
+// The layer's product with the adapters' second one, t . b (b [ranks, N], t as
+// launch_lora_down leaves it in t and in the sums behind it), added before the
+// output is rounded (gemm_lora.hip).
 hipError_t launch_gemm_lora(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
                             bool row_scale, const uint16_t* bias, uint16_t* y, bool f16, int64_t M, int64_t N, int64_t K,
                             const uint16_t* t, int64_t t_stride, const uint16_t* b, int64_t ranks,

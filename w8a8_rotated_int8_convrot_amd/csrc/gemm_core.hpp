@@ -340,10 +340,11 @@ struct Grouped {
 
 // Low-rank adapters beside the product: token m with adapter a = index[m] gets
 //   y[m][n] += sum_r t[m][r] * b[offsets[a] + r][n],    r < rank of a
-// before the output is rounded; t holds the adapter's first product, already
-// scaled (lora.hip).  Both factors are in the io type, the sum in fp32.
+// before the output is rounded; t is the adapter's first product, already
+// scaled, as launch_lora_down leaves it, b in the io type, the sum in fp32.
 struct Lora {
-  const uint16_t* t;        // [M, t_stride], zero from the token's rank on
+  const float* t;           // [M, t_stride] values, or words of two parts; zero from the token's rank on
+  const float* factor;      // [t_stride / 32, M] of fp16 parts
   const uint16_t* b;        // [ranks, N]
   const int32_t* offsets;   // [adapters + 1]
   const int32_t* index;     // [M]
@@ -362,17 +363,6 @@ struct LoraGather : Lora {};
 struct LoraNone {
   template <class... A> __device__ LoraNone(const A&...) {}
 };
-
-// Eight 16-bit values as fp32.
-template <bool F16>
-__device__ inline void unpack8(const uint4& w, float (&v)[8]) {
-  const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    v[2 * q] = F16 ? f16_bits_lo(d[q]) : __uint_as_float(d[q] << 16);
-    v[2 * q + 1] = F16 ? f16_bits_hi(d[q]) : __uint_as_float(d[q] & 0xffff0000u);
-  }
-}
 
 // Four channels n.. of a row of b as fp32 (past N: the last channel).
 template <bool F16>
@@ -396,6 +386,25 @@ __device__ inline void lora_b4(const uint16_t* row, int n, int N, bool vec, floa
   }
 }
 
+// Eight 16-bit values with infinities and NaN as a large finite value of their
+// sign, 65504 or 2^64 (bf16 values beyond that too, so that a product with it
+// stays finite).  Positive halves order as signed integers do, where negative
+// ones lie below them all, and negative halves as unsigned ones, above them all.
+template <bool F16>
+__device__ inline v4i finite_halves(v4i v) {
+  typedef short v2s __attribute__((ext_vector_type(2)));
+  typedef unsigned short v2u __attribute__((ext_vector_type(2)));
+  constexpr unsigned short kMost = F16 ? 0x7bff : 0x5f80;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int w = v[q];           // (a bit cast of v[q] itself takes v[0])
+    const v2s a = __builtin_elementwise_min(__builtin_bit_cast(v2s, w), (v2s){kMost, kMost});
+    const v2u c = __builtin_elementwise_min(__builtin_bit_cast(v2u, a), (v2u){kMost | 0x8000, kMost | 0x8000});
+    v[q] = __builtin_bit_cast(int, c);
+  }
+  return v;
+}
+
 // Adds the adapters' part to a tile's results, which the waves' blocks hold as
 // fp32 by their bits.  The work is a list of units, 32 ranks of one adapter met
 // among the tile's tokens (neighbours in a batch mostly share theirs): channels
@@ -409,14 +418,28 @@ __device__ inline void lora_b4(const uint16_t* row, int n, int N, bool vec, floa
 // time to arrive).  Where the tokens of a block have several adapters a lane
 // keeps the sum only if its token has the unit's: a product with zero instead
 // would carry one adapter's infinities into other tokens.
-template <class T, bool F16, int UNITS>
+//
+// t comes in two 16-bit parts, each with a product of its own, so that the sum
+// is that of t in twice the bits; the second product takes b with infinities and
+// NaN as finite values, because the first has already given what they give (and
+// a part that is zero or of the other sign would make NaN of it).  fp16 parts
+// are scaled by unit, and their sum is scaled back onto the results.  With
+// STAGED a unit's t goes through LDS beside its panel, fetched with it: 128
+// bytes a token, the first part's 32 values, then the second's.  Else (the
+// persistent kernel, whose LDS has no room: with units of 16 ranks it has, and
+// the units' latencies make 4608 x 4096 x 12288, rank 64, 298 us instead of 268)
+// every wave loads the fragments of its tokens with the unit's adapter.
+template <class T, bool F16, int UNITS, bool STAGED>
 struct LoraTile {
   static constexpr int MF = T::MF, TN = T::TN, TM = T::TM;
   static constexpr int OP = F16 ? kOpF16 : kOpBf16;
   static constexpr int kSub = MF == 16 ? 1 : 2;              // products per block and unit: 32 or 16 ranks each
   static constexpr int kIdx = (T::BM + 63) / 64;
   static constexpr int kPanelBytes = T::BN * 64;             // 32 ranks of BN channels
-  static constexpr int kBytes = UNITS * kPanelBytes;
+  static constexpr int kTokenBytes = STAGED ? T::BM * 128 : 0;   // the unit's t
+  static constexpr int kBytes = UNITS * (kPanelBytes + kTokenBytes);
+  static constexpr int kTokenLoads = STAGED ? T::BM * 8 / T::kThreads : 1;
+  static_assert(!STAGED || T::BM * 8 % T::kThreads == 0, "16-byte chunks of t");
   static constexpr int kChunks = T::BN * 4;                  // eight channels of one rank each
   static constexpr int kPerThread = (kChunks + T::kThreads - 1) / T::kThreads;
   using sum_t = typename Acc<MF, OP>::type;
@@ -424,12 +447,13 @@ struct LoraTile {
   const Lora& lo;
   const int N, M, n0, m0;
   // the adapters of the tile's tokens, the same in every wave: index, rows
-  int idx[kIdx], row_of[kIdx], rank_of[kIdx];
+  int idx[kIdx], row_of[STAGED ? kIdx : 1], rank_of[STAGED ? kIdx : 1];
   uint64_t left[kIdx];
   int a = -1, row0 = 0, rank = 0, k = 0;                     // the current unit
   bool has[UNITS];
   int unit_a[UNITS], unit_k[UNITS];
   uint4 raw[UNITS][kPerThread];
+  v4i raw_t[UNITS][kTokenLoads];
 
   __device__ LoraTile(const Lora& l, int n0_, int m0_, int M_, int N_) : lo(l), N(N_), M(M_), n0(n0_), m0(m0_) {}
 
@@ -442,10 +466,13 @@ struct LoraTile {
         if (a >= 0 || left[q] == 0) continue;
         const int l = __builtin_ctzll(left[q]);
         a = __builtin_amdgcn_readlane(idx[q], l);
-        row0 = __builtin_amdgcn_readlane(row_of[q], l);
-        rank = __builtin_amdgcn_readlane(rank_of[q], l);
+        if constexpr (STAGED) {
+          row0 = __builtin_amdgcn_readlane(row_of[q], l);
+          rank = __builtin_amdgcn_readlane(rank_of[q], l);
+        }
       }
       if (a < 0) return false;
+      if constexpr (!STAGED) lo.range(a, row0, rank);
 #pragma unroll
       for (int q = 0; q < kIdx; ++q) left[q] &= ~__ballot(idx[q] == a);
       k = 0;
@@ -475,7 +502,16 @@ struct LoraTile {
     }
   }
 
-  // the next units' panels, into registers
+  // the tokens' t of the current unit: chunk tid & 7 of rows tid >> 3 and on
+  __device__ void load_t(int tid, v4i (&to)[kTokenLoads]) const {
+#pragma unroll
+    for (int p = 0; p < kTokenLoads; ++p) {
+      const int m = min(m0 + (tid >> 3) + p * (T::kThreads / 8), M - 1);
+      to[p] = *reinterpret_cast<const v4i*>(lo.t + static_cast<int64_t>(m) * lo.t_stride + k + 4 * (tid & 7));
+    }
+  }
+
+  // the next units' panels and t, into registers
   __device__ void fetch(int tid) {
     bool more = true;
 #pragma unroll
@@ -484,7 +520,10 @@ struct LoraTile {
       has[u] = more;
       unit_a[u] = a;
       unit_k[u] = k;
-      if (more) load(tid, raw[u]);
+      if (more) {
+        load(tid, raw[u]);
+        if constexpr (STAGED) load_t(tid, raw_t[u]);
+      }
     }
   }
 
@@ -495,13 +534,14 @@ struct LoraTile {
       const int m = q * 64 + lane;
       idx[q] = lo.index[min(m0 + m, M - 1)];
       const bool mine = m < T::BM && m0 + m < M && idx[q] >= 0 && idx[q] < lo.adapters;
-      lo.range(mine ? idx[q] : 0, row_of[q], rank_of[q]);
+      if constexpr (STAGED) lo.range(mine ? idx[q] : 0, row_of[q], rank_of[q]);
       left[q] = __ballot(mine);
     }
     fetch(tid);
   }
 
   static __device__ int at(int n, int chunk) { return n * 64 + ((chunk ^ swz<MF, 64>(n)) << 4); }
+  static __device__ int at_t(int m, int chunk) { return m * 128 + ((chunk ^ swz<MF, 128>(m)) << 4); }
 
   // panels: kBytes of LDS that nobody else uses until the next barrier after
   // this returns
@@ -510,27 +550,43 @@ struct LoraTile {
     const int lane = tid & 63;
     const int r = lane & (MF - 1), c8 = lane / MF;      // fragment row, 8-rank chunk
     int own[TM];
-    const uint16_t* t_row[TM];
+    int m_own[TM];
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int m = min(m0 + wm * T::kWaveM + j * MF + r, M - 1);   // past the end: as the last token (discarded)
-      own[j] = lo.index[m];
-      t_row[j] = lo.t + static_cast<int64_t>(m) * lo.t_stride + c8 * 8;
+      m_own[j] = min(m0 + wm * T::kWaveM + j * MF + r, M - 1);   // past the end: as the last token (discarded)
+      own[j] = lo.index[m_own[j]];
     }
+    char* tokens = panels + UNITS * kPanelBytes;
     while (has[0]) {
       // these units; the next ones' panels are on their way while these run
       bool now[UNITS];
       int now_a[UNITS];
-      v4i tf[UNITS][TM][kSub];
+      v4i tf[TM][kSub], tl[TM][kSub];
+      float factor[UNITS][TM];
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
         now[u] = has[u];
         now_a[u] = unit_a[u];
         if (!now[u]) continue;
+        if constexpr (F16) {
 #pragma unroll
-        for (int j = 0; j < TM; ++j)
+          for (int j = 0; j < TM; ++j)
+            factor[u][j] = lo.factor[static_cast<int64_t>(unit_k[u] / 32) * M + m_own[j]];
+        }
+        if constexpr (!STAGED) {
+          static_assert(STAGED || UNITS == 1, "one unit's fragments");
 #pragma unroll
-          for (int s = 0; s < kSub; ++s) tf[u][j][s] = *reinterpret_cast<const v4i*>(t_row[j] + unit_k[u] + 16 * s);
+          for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int s = 0; s < kSub; ++s) {
+              const float* row = lo.t + static_cast<int64_t>(m_own[j]) * lo.t_stride + unit_k[u] + 8 * s + 4 * c8;
+              tf[j][s] = tl[j][s] = v4i{};
+              if (own[j] == unit_a[u]) {
+                tf[j][s] = *reinterpret_cast<const v4i*>(row);
+                tl[j][s] = *reinterpret_cast<const v4i*>(row + 16);
+              }
+            }
+        }
       }
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
@@ -547,6 +603,11 @@ struct LoraTile {
             *reinterpret_cast<uint16_t*>(panel + at(n + e, rr >> 3) + 2 * (rr & 7)) =
                 static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
         }
+        if constexpr (STAGED) {
+#pragma unroll
+          for (int p = 0; p < kTokenLoads; ++p)
+            *reinterpret_cast<v4i*>(tokens + u * kTokenBytes + at_t((tid >> 3) + p * (T::kThreads / 8), tid & 7)) = raw_t[u][p];
+        }
       }
       if (now[UNITS - 1]) fetch(tid);
       else has[0] = false;
@@ -562,17 +623,39 @@ struct LoraTile {
           any = any || __any(own[j] == now_a[u]);
         }
         if (!any) continue;
+        if constexpr (STAGED) {
+#pragma unroll
+          for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int s = 0; s < kSub; ++s) {
+              const char* t = tokens + u * kTokenBytes;
+              const int m = wm * T::kWaveM + j * MF + r;
+              tf[j][s] = *reinterpret_cast<const v4i*>(t + at_t(m, 2 * s + c8));
+              tl[j][s] = *reinterpret_cast<const v4i*>(t + at_t(m, 4 + 2 * s + c8));
+            }
+        }
 #pragma unroll
         for (int i = 0; i < TN; ++i) {
-          v4i bf[kSub];
+          v4i bf[kSub], bl[kSub];
 #pragma unroll
-          for (int s = 0; s < kSub; ++s)
+          for (int s = 0; s < kSub; ++s) {
             bf[s] = *reinterpret_cast<const v4i*>(panel + at(wn * T::kWaveN + i * MF + r, 2 * s + c8));
+            bl[s] = finite_halves<F16>(bf[s]);
+          }
 #pragma unroll
           for (int j = 0; j < TM; ++j) {
-            sum_t d = __builtin_bit_cast(sum_t, acc[i][j]);
+            sum_t d = {};
+            if constexpr (!F16) d = __builtin_bit_cast(sum_t, acc[i][j]);
 #pragma unroll
-            for (int s = 0; s < kSub; ++s) d = mfma<MF, OP>(bf[s], tf[u][j][s], d);
+            for (int s = 0; s < kSub; ++s) {
+              d = mfma<MF, OP>(bf[s], tf[j][s], d);
+              d = mfma<MF, OP>(bl[s], tl[j][s], d);
+            }
+            if constexpr (F16) {
+#pragma unroll
+              for (int e = 0; e < T::kAccRegs; ++e)
+                d[e] = __builtin_fmaf(d[e], factor[u][j], __int_as_float(acc[i][j][e]));
+            }
             if (whole[j]) {
               acc[i][j] = __builtin_bit_cast(AccT, d);
             } else {
@@ -611,7 +694,7 @@ __device__ inline void lora_gather(float (&part)[T::TN][T::TM][T::kAccRegs], con
     if (a < 0 || a >= lo.adapters) continue;
     int row0, rank;
     lo.range(a, row0, rank);
-    const uint16_t* t = lo.t + static_cast<int64_t>(m) * lo.t_stride;
+    const float* t = lo.t + static_cast<int64_t>(m) * lo.t_stride;
     const uint16_t* b = lo.b + static_cast<int64_t>(row0) * N;
     // `count` ranks from k on, all their loads before the first sum (t is zero
     // from the rank on, up to a multiple of 32)
@@ -619,7 +702,10 @@ __device__ inline void lora_gather(float (&part)[T::TN][T::TM][T::kAccRegs], con
       constexpr int kCount = decltype(count_c)::value;
       float tv[kCount / 8][8];
 #pragma unroll
-      for (int c = 0; c < kCount / 8; ++c) unpack8<F16>(*reinterpret_cast<const uint4*>(t + k + 8 * c), tv[c]);
+      for (int c = 0; c < kCount / 8; ++c) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) tv[c][q] = t[k + 8 * c + q];
+      }
 #pragma unroll
       for (int i = 0; i < T::TN; ++i) {
 #pragma unroll
@@ -1022,8 +1108,10 @@ __global__ __launch_bounds__(T::kThreads, (kMinWaves<T, X>)) void gemm_i8_kernel
   // adapters: the list's first panels, or the tokens' own sums, while the first
   // slabs are on their way
   constexpr bool GATHER = std::is_same_v<X, LoraGather>;
-  constexpr int kUnits = 2;       // adapter panels at a time
-  using lora_t = std::conditional_t<std::is_same_v<X, LoraList>, LoraTile<T, kF16, kUnits>, LoraNone>;
+  // adapter panels at a time (registers for one beside 192 tokens: 1500 x 4096 x
+  // 8192, rank 32: 71.2 us with two, which spill, 68.6 with one)
+  constexpr int kUnits = std::is_same_v<T, TileDeep192> ? 1 : 2;
+  using lora_t = std::conditional_t<std::is_same_v<X, LoraList>, LoraTile<T, kF16, kUnits, true>, LoraNone>;
   lora_t lora(extra, n0, m0, M, N);
   float part[GATHER ? T::TN : 1][GATHER ? T::TM : 1][GATHER ? T::kAccRegs : 1];
   if constexpr (GATHER) lora_gather<T, kF16>(part, extra, lane, n0 + wn * T::kWaveN, m0 + wm * T::kWaveM, M, N);
@@ -1245,7 +1333,7 @@ __global__ __launch_bounds__(T::kThreads, (kMinWaves<T, X>)) void gemm_i8_kernel
     }
     if constexpr (LORA) {
       if constexpr (!GATHER) {
-        static_assert(LoraTile<T, kF16, kUnits>::kBytes <= T::kLdsBytes, "panels fit the stages");
+        static_assert(lora_t::kBytes <= T::kLdsBytes, "panels fit the stages");
         lora.finish(acc, lds, tid, wn, wm);
         __syncthreads();          // the panels make room for the output tile
       }
@@ -1996,7 +2084,7 @@ __global__ __launch_bounds__(T::kThreads) void gemm_persist_kernel(
             for (int e = 0; e < 4; ++e) acc[i][j][4 * gg + e] = __float_as_int(v[e]);
           }
       }
-      LoraTile<T, kF16, kUnits> lora(extra, n0, m0, M, N);
+      LoraTile<T, kF16, kUnits, false> lora(extra, n0, m0, M, N);
       lora.begin(tid_e);
       lora.finish(acc, lds + kPanelAt, tid_e, wn, wm);
     }

@@ -98,7 +98,7 @@ hipError_t launch_gemm_lora(const int8_t* xq, const float* x_scale, const int8_t
                             const int32_t* offsets, int64_t adapters, const int32_t* index, int64_t max_rank,
                             hipStream_t stream) {
   if (M == 0) return hipSuccess;
-  const Lora l{t, b, offsets, index, static_cast<int>(adapters), static_cast<int>(ranks), static_cast<int>(max_rank),
+  const Lora l{lora_behind_t(t, M, t_stride), reinterpret_cast<const float*>(t), b, offsets, index, static_cast<int>(adapters), static_cast<int>(ranks), static_cast<int>(max_rank),
                static_cast<int>(t_stride)};
   if (f16)
     return row_scale ? launch_epi<kEpiF16Row>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream)

@@ -1,11 +1,16 @@
 // lora.hip -- the first product of the low-rank adapters beside the layer:
-//   t[m][r] = rnd(scale[a] * sum_k A[offsets[a] + r][k] * x[m][k]),  a = index[m]
+//   t[m][r] = scale[a] * sum_k A[offsets[a] + r][k] * x[m][k],  a = index[m]
 // for r below the rank of a, 0 up to the row's stride; tokens without an
 // adapter are skipped (nobody reads their rows).  x is the layer's own input,
-// neither rotated nor coded.  The sum is held in fp32 and rounded to the io
-// type once, as the second product's matrix operand (an adapter run as two
-// layers rounds there too); it moves the result by at most half a step of the
-// adapter's part.
+// neither rotated nor coded.  The sum is held in fp32.  The second product
+// takes it as it is where it runs on the vector unit (token by token); on the
+// matrix units, whose operands have 16 bits, as two parts, the nearest value of
+// the io type and the nearest to what that leaves: one part alone would move
+// the result by up to half a step of sum_r |t_r b_r|, however much of that
+// cancels.  Two are off by 2^-16 of each t_r in bf16 and 2^-22 in fp16, far
+// below the fp32 sum's own worst case.  fp16 parts are those of t scaled by a
+// power of two that takes the largest of 32 ranks to [2^14, 2^15), so that
+// neither its range nor its smallest step meets a t of fp32.
 //
 // lora_down_kernel: a workgroup takes 64 tokens, 16 a wave, and a part of K
 // (gridDim.y of them fill the chip).  Pieces of 64 elements of K, 64 token rows
@@ -42,7 +47,7 @@ struct Down {
   const uint16_t *x, *a_rows;
   const float* scale;
   const int32_t *offsets, *index;
-  uint16_t* t;
+  float* factor;
   int M, K, ranks, adapters, max_rank, t_stride;
   // rows [row0, row0 + rank) of adapter a, inside [0, ranks)
   __device__ void range(int a, int& row0, int& rank) const {
@@ -59,10 +64,15 @@ __device__ inline v4f mfma(v4i a, v4i b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
+// v as the nearest value of the io type and the nearest to the rest (none of an
+// infinity)
 template <bool F16>
-__device__ inline uint32_t round16(float v) {
-  if constexpr (F16) return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
-  else return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+__device__ inline void split16(float v, uint32_t& first, uint32_t& second) {
+  using H = std::conditional_t<F16, _Float16, __bf16>;
+  const H h = static_cast<H>(v);
+  const float rest = v - static_cast<float>(h);
+  first = __builtin_bit_cast(uint16_t, h);
+  second = __builtin_bit_cast(uint16_t, static_cast<H>(fabsf(rest) <= 0x1.fffffep127f ? rest : 0.0f));
 }
 
 typedef __attribute__((address_space(3))) void lds_void_t;
@@ -178,9 +188,11 @@ __global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(Down p, float* _
   }
 }
 
-// t from the parts of K: thread i of a thread per four ranks of a token.
+// t from the parts of K: thread i of a thread per four ranks of a token.  The
+// eight threads of 32 ranks are neighbours in a wave (t_stride is a multiple of
+// 32), which has read all it needs of their words before it writes there.
 template <bool F16>
-__device__ inline void lora_sum(const Down& p, const float* __restrict__ sums, int parts, int64_t i) {
+__device__ inline void lora_sum(const Down& p, float* sums, int parts, int64_t i) {
   const int quads = p.t_stride / 4;
   const int64_t m = i / quads;
   if (m >= p.M) return;
@@ -200,16 +212,35 @@ __device__ inline void lora_sum(const Down& p, const float* __restrict__ sums, i
   for (int z = 1; z < kMaxLoraParts; ++z)
     if (z < parts) sum += v[z];
   const float s = p.scale[a];
-  uint32_t h[4];
+  float t[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = rank0 + e < rank ? round16<F16>(s * sum[e]) : 0u;
-  *reinterpret_cast<uint2*>(p.t + m * p.t_stride + rank0) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  for (int e = 0; e < 4; ++e) t[e] = rank0 + e < rank ? s * sum[e] : 0.0f;
+  float* words = sums + m * p.t_stride + rank0 / 32 * 32 + (rank0 & 31) / 2;
+  if constexpr (F16) {
+    float most = 0.0f;            // of the finite ones
+#pragma unroll
+    for (int e = 0; e < 4; ++e) most = fabsf(t[e]) <= 0x1.fffffep127f ? fmaxf(most, fabsf(t[e])) : most;
+    most = fmaxf(most, lane_xor<1>(most));
+    most = fmaxf(most, lane_xor<2>(most));
+    most = fmaxf(most, lane_xor<4>(most));
+    // 2^(14 - e) for most in [2^e, 2^(e+1)); below 2^-100 nothing is left that fp16 could show
+    const int e = max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) t[q] *= up;
+    if ((rank0 & 31) == 0)
+      p.factor[static_cast<int64_t>(rank0 / 32) * p.M + m] = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+  }
+  uint32_t first[4], second[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) split16<F16>(t[e], first[e], second[e]);
+  *reinterpret_cast<uint2*>(words) = make_uint2(first[0] | (first[1] << 16), first[2] | (first[3] << 16));
+  *reinterpret_cast<uint2*>(words + 16) = make_uint2(second[0] | (second[1] << 16), second[2] | (second[3] << 16));
 }
 
-// Ranks 8 * part + 2 * wave + (0, 1) of token m.
+// Ranks 8 * part + 2 * wave + (0, 1) of token m, into t [M, t_stride].
 template <typename In>
-__device__ inline void lora_dot(const Down& p, int64_t m, int part) {
-  constexpr bool F16 = !std::is_same_v<In, uint16_t>;
+__device__ inline void lora_dot(const Down& p, float* t, int64_t m, int part) {
   const int lane = threadIdx.x & 63;
   const int rank0 = part * 8 + (threadIdx.x >> 6) * 2;
   const int a = p.index[m];
@@ -247,9 +278,8 @@ __device__ inline void lora_dot(const Down& p, int64_t m, int part) {
   }
   if (lane == 0) {
     const float s = p.scale[a];
-    const uint32_t lo = rank0 < rank ? round16<F16>(s * sum[0]) : 0u;
-    const uint32_t hi = rank0 + 1 < rank ? round16<F16>(s * sum[1]) : 0u;
-    *reinterpret_cast<uint32_t*>(p.t + m * p.t_stride + rank0) = lo | (hi << 16);
+    *reinterpret_cast<float2*>(t + m * p.t_stride + rank0) =
+        make_float2(rank0 < rank ? s * sum[0] : 0.0f, rank0 + 1 < rank ? s * sum[1] : 0.0f);
   }
 }
 
@@ -259,8 +289,7 @@ __device__ inline void lora_dot(const Down& p, int64_t m, int part) {
 // one.  G = 0: the tokens are coded elsewhere.
 template <typename In, bool DOTS, int G, int CPT>
 __global__ __launch_bounds__(kThreads) void lora_rows_kernel(Down p, int rows, int8_t* __restrict__ xq,
-                                                             float* __restrict__ xs,
-                                                             const float* __restrict__ sums, int parts) {
+                                                             float* __restrict__ xs, float* sums, int parts) {
   const int block = static_cast<int>(blockIdx.x) - rows;
   if constexpr (G != 0) {
     if (block < 0) {
@@ -271,7 +300,7 @@ __global__ __launch_bounds__(kThreads) void lora_rows_kernel(Down p, int rows, i
   }
   if constexpr (DOTS) {
     const int per_token = p.t_stride / 8;
-    lora_dot<In>(p, block / per_token, block % per_token);
+    lora_dot<In>(p, sums, block / per_token, block % per_token);
   } else {
     lora_sum<!std::is_same_v<In, uint16_t>>(p, sums, parts, static_cast<int64_t>(block) * kThreads + threadIdx.x);
   }
@@ -283,7 +312,7 @@ __global__ __launch_bounds__(kThreads) void lora_rows_kernel(Down p, int rows, i
 template <bool F16>
 struct SumsBeside {
   Down p;
-  const float* sums;
+  float* sums;
   int parts;
   uint32_t wgs;
   __device__ bool operator()(uint32_t wg) const {
@@ -312,7 +341,7 @@ hipError_t launch_down(const Down& p, float* sums, int parts, hipStream_t stream
 }
 
 template <typename In, bool DOTS>
-hipError_t launch_rows(const Down& p, int group, int8_t* xq, float* xs, const float* sums, int parts,
+hipError_t launch_rows(const Down& p, int group, int8_t* xq, float* xs, float* sums, int parts,
                        hipStream_t stream) {
   // group 0: coded elsewhere
   const int rows = group != 0 ? p.M : 0;
@@ -347,7 +376,7 @@ int parts_of(int64_t M, int64_t K) {
 }
 
 template <typename In, bool F16>
-hipError_t launch_codes(const Down& p, int group, int8_t* xq, float* xs, const float* sums, int parts,
+hipError_t launch_codes(const Down& p, int group, int8_t* xq, float* xs, float* sums, int parts,
                         hipStream_t stream) {
   const BlockGrid g = block_grid(p.M, p.K);
   const int64_t work = static_cast<int64_t>(p.M) * (p.t_stride / 4);
@@ -373,7 +402,7 @@ hipError_t launch(const Down& p, int group, int8_t* xq, float* xs, float* sums, 
     if (e != hipSuccess) return e;
     group = 0;
   }
-  if (dots) return launch_rows<In, true>(p, group, xq, xs, nullptr, 0, stream);
+  if (dots) return launch_rows<In, true>(p, group, xq, xs, sums, 0, stream);
   const int parts = parts_of(p.M, p.K);
   const hipError_t e = p.max_rank <= 16   ? launch_down<F16, 1>(p, sums, parts, stream)
                        : p.max_rank <= 32 ? launch_down<F16, 2>(p, sums, parts, stream)
@@ -390,7 +419,7 @@ hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, int group, 
                             int64_t adapters, const int32_t* index, int64_t max_rank, uint16_t* t, int64_t t_stride,
                             float* sums, hipStream_t stream) {
   if (M == 0) return hipSuccess;
-  const Down p{x, a, scale, offsets, index, t, static_cast<int>(M), static_cast<int>(K), static_cast<int>(ranks),
+  const Down p{x, a, scale, offsets, index, reinterpret_cast<float*>(t), static_cast<int>(M), static_cast<int>(K), static_cast<int>(ranks),
                static_cast<int>(adapters), static_cast<int>(max_rank), static_cast<int>(t_stride)};
   const bool dots = lora_by_token(M, adapters);
   return f16 ? launch<true>(p, group, xq, xs, sums, dots, stream) : launch<false>(p, group, xq, xs, sums, dots, stream);

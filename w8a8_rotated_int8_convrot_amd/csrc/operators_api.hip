@@ -35,7 +35,7 @@ hipError_t rotate_quant(const void* x, bool f16, int64_t M, int64_t K, int group
 // The parts of convrot_linear_lora's workspace for slices of S tokens.
 struct LoraLayout {
   int64_t S, t_stride;
-  size_t scales, t, sums, total;
+  size_t scales, t, total;
 };
 LoraLayout lora_layout(int64_t M, int64_t K, int64_t N, int64_t max_rank) {
   LoraLayout l;
@@ -43,8 +43,8 @@ LoraLayout lora_layout(int64_t M, int64_t K, int64_t N, int64_t max_rank) {
   l.t_stride = (max_rank + 31) / 32 * 32;
   l.scales = round_up(static_cast<size_t>(l.S) * K, 256);
   l.t = l.scales + round_up(static_cast<size_t>(l.S) * 4, 256);
-  l.sums = l.t + round_up(static_cast<size_t>(l.S) * l.t_stride * 2, 256);
-  l.total = l.sums + static_cast<size_t>(lora_sum_rows(l.S)) * l.t_stride * 4;
+  const size_t t_bytes = round_up(static_cast<size_t>(l.S) * l.t_stride * 2, 256);
+  l.total = l.t + t_bytes + static_cast<size_t>(lora_sum_rows(l.S)) * l.t_stride * 4;
   return l;
 }
 
@@ -186,14 +186,14 @@ int convrot_linear_lora(const void* x, int io_dtype, int64_t M, int64_t K, const
   auto* xq = reinterpret_cast<int8_t*>(ws);
   auto* xs = reinterpret_cast<float*>(ws + l.scales);
   auto* t = reinterpret_cast<uint16_t*>(ws + l.t);
-  auto* sums = reinterpret_cast<float*>(ws + l.sums);
   const bool f16 = io_dtype == CONVROT_F16;
   auto s = static_cast<hipStream_t>(stream);
   for (int64_t r0 = 0; r0 < M; r0 += l.S) {
     const int64_t rows = std::min(M - r0, l.S);
     const auto* xr = static_cast<const uint16_t*>(x) + r0 * K;
     if (hipError_t e = launch_lora_down(xr, rows, K, group, f16, xq, xs, static_cast<const uint16_t*>(lora_a), R,
-                                        lora_scale, offsets, n_adapters, index + r0, max_rank, t, l.t_stride, sums, s);
+                                        lora_scale, offsets, n_adapters, index + r0, max_rank, t, l.t_stride,
+                                        lora_behind_t(t, rows, l.t_stride), s);
         e != hipSuccess)
       return hip_status(e, who);
     if (hipError_t e = launch_gemm_lora(xq, xs, wq, w_scale, scale_mode == CONVROT_SCALE_ROW,
