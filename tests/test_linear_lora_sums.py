@@ -109,3 +109,20 @@ def test_the_second_parts_leave_infinities_alone(B, M, N, io):
     t = (p["lora_a"][row].double() * p["x"].double()).sum(1)
     sure = t.abs() > 1e-3
     assert torch.equal(got[sure, 7].double(), torch.where(t[sure] > 0, float("-inf"), float("inf")))
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,ranks", [(7, [8, 16]), (100, [8] * 6), (100, [8, 16]), (300, [8, 16])])
+def test_tokens_without_an_adapter_keep_the_sign_of_a_zero(B, M, ranks, io):
+    """A scale product that underflows to zero and a bias of -0 give zeros of both signs, and a token
+    without an adapter, or with one of no rows, gets the layer's own."""
+    p = problem(M, 256, 72, io, ranks + [0], False, True, M, 1, none=0.5)
+    p["w_scale"] *= 1e-37
+    p["x"] *= 1e-6
+    p["bias"] = torch.full_like(p["bias"], -0.0)
+    got = B.convrot_linear_lora(**p, group=128)
+    plain = B.convrot_linear_ex(p["x"], p["wq"], p["w_scale"], 128, bias=p["bias"])
+    none = (p["index"] < 0) | (p["index"] >= len(ranks))
+    zeros = plain[none]
+    assert (zeros == 0).all() and torch.signbit(zeros).any() and not torch.signbit(zeros).all()
+    assert torch.equal(got[none].view(torch.int16), zeros.view(torch.int16))

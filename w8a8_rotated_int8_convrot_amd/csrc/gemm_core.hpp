@@ -688,7 +688,7 @@ __device__ inline void lora_gather(float (&part)[T::TN][T::TM][T::kAccRegs], con
 #pragma unroll
     for (int i = 0; i < T::TN; ++i)
 #pragma unroll
-      for (int e = 0; e < T::kAccRegs; ++e) part[i][j][e] = 0.0f;
+      for (int e = 0; e < T::kAccRegs; ++e) part[i][j][e] = -0.0f;      // adds nothing to a zero of either sign
     const int m = m_first + j * MF + (lane & (MF - 1));
     const int a = m < M ? lo.index[m] : -1;
     if (a < 0 || a >= lo.adapters) continue;
