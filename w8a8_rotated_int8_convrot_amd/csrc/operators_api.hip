@@ -13,6 +13,7 @@ namespace {
 
 using namespace convrot;
 
+constexpr int64_t kMaxTokens = int64_t{1} << 30;       // and channels, as check_mn
 constexpr int kMaxRoutes = 64;
 constexpr int64_t kMaxExperts = 65536;
 constexpr int64_t kMaxAdapters = 65536;
@@ -103,7 +104,7 @@ int convrot_block_norm(const convrot_block* b, void* stream) {
 }
 
 size_t convrot_grouped_workspace(int64_t M, int64_t K) {
-  if (M < 0 || K < 1) return 0;
+  if (M < 0 || M > kMaxTokens || K < 1 || K > kMaxK) return 0;
   return round_up(static_cast<size_t>(M) * static_cast<size_t>(K), 256) + static_cast<size_t>(M) * 4;
 }
 
@@ -152,7 +153,8 @@ int convrot_grouped_linear(const void* x, int io_dtype, int64_t M, int64_t K, co
 }
 
 size_t convrot_lora_workspace(int64_t M, int64_t K, int64_t N, int64_t max_rank) {
-  if (M < 0 || K < 1 || N < 1 || max_rank < 1 || max_rank > kMaxRank) return 0;
+  if (M < 0 || M > kMaxTokens || K < 1 || K > kMaxK || N < 1 || N > kMaxTokens || max_rank < 1 || max_rank > kMaxRank)
+    return 0;
   return lora_layout(M, K, N, max_rank).total;
 }
 
