@@ -30,7 +30,7 @@ def want_and_tol(B, p, group):
     bias = 0.0 if p["bias"] is None else p["bias"].double()
     want, mag, lost = prod + bias, prod.abs() + abs(bias), torch.zeros_like(prod)
     off = p["offsets"].tolist()
-    by_token = M <= 16 or (M <= 128 and len(off) - 1 > 4)
+    by_token = M <= 16           # and some larger batches, whose bound is the list's here
     for a in range(len(off) - 1):
         at = torch.nonzero(p["index"] == a).flatten()
         lo, hi = off[a], off[a + 1]
@@ -59,9 +59,10 @@ def close(B, p, group):
 
 # token by token and as a list, in every tile the call chooses from; K is short, so that the fp32 sums' bound is
 # far below the roundings'
-SHAPES = [(5, 256, 130, [40, 64], 1), (16, 256, 200, [16] * 16, 1), (90, 256, 72, [64, 33, 5, 8, 16, 40], 7),
-          (37, 256, 5244, [8, 40, 64, 3, 16, 20], 3), (60, 128, 9000, [8, 40, 64, 3, 16, 20], 5),
-          (97, 128, 15790, [8, 40, 64, 3, 16, 20], 9), (40, 256, 136, [64, 33], 9), (100, 384, 2000, [64, 8], 30),
+SHAPES = [(5, 256, 130, [40, 64], 1), (16, 256, 200, [16] * 16, 1), (90, 256, 72, [64, 33, 5, 8, 16, 40] * 3, 7),
+          (37, 256, 5244, [8, 40, 64, 3, 16, 20] * 3, 3), (60, 128, 9000, [8, 40, 64, 3, 16, 20] * 4, 5),
+          (97, 128, 15790, [8, 40, 64, 3, 16, 20] * 3, 9), (97, 128, 9000, [8, 40, 64, 3, 16, 20], 9),
+          (40, 256, 136, [64, 33], 9), (100, 384, 2000, [64, 8], 30),
           (85, 256, 3132, [48, 64], 20), (120, 256, 8200, [48, 64], 50), (226, 128, 20434, [33, 64], 60),
           (300, 256, 520, [64, 40, 128], 11), (1000, 256, 2600, [64, 40, 32], 300), (559, 256, 13260, [40, 64], 100),
           (1999, 256, 4095, [40] * 9, 50), (2999, 128, 4090, [64, 100], 1000), (4700, 256, 3000, [64] * 5, 900),

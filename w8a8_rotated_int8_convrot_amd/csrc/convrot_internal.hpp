@@ -99,10 +99,25 @@ hipError_t launch_grouped_few(const void* x, int64_t M, int64_t K, int group, bo
                               const int32_t* offsets, const int32_t* rows, int64_t experts, int64_t P, int64_t N,
                               hipStream_t stream);
 
-// Whether a batch's adapters are taken token by token (few tokens, most with an
-// adapter of their own) or as a list per tile.  By sizes alone, so that a
-// token's result does not depend on the other tokens' adapters.
-inline bool lora_by_token(int64_t M, int64_t adapters) { return M <= 16 || (M <= 128 && adapters > 4); }
+// Whether a batch's adapters are taken token by token or as a list per tile.  By
+// sizes alone, so that a token's result does not depend on the other tokens'
+// adapters.  A token's own ranks run on the vector unit, each token reading its
+// adapter, so the time goes with the rank; a list costs a latency and a matrix
+// product for each adapter and 32 ranks, whoever shares them.  us a call, weight
+// from HBM, 128 tokens in equal runs of each adapter, list / token by token:
+//                      4096 x 4096               2048 x 8192
+//   rank            16      64     128        16      64     128
+//    5 adapters   23/22   26/35   31/52     19/17   21/31   28/48
+//   12            24/22   27/34   34/52     21/18   26/32   36/51
+//   48            33/24   43/37   62/56     37/20   55/38   90/65
+// Over these, 17, 32 and 64 tokens, two adapters, and the tokens shuffled, the
+// rule is 1.6 % behind the better of the two on the mean and 22 % at worst; more
+// than four adapters at any rank would be 10 % and 114 %, the list alone 19 %,
+// token by token alone 22 %.
+inline bool lora_by_token(int64_t M, int64_t adapters, int64_t max_rank) {
+  const int64_t shared = (max_rank < 64 ? max_rank : 64) * 3 / 16;
+  return M <= 16 || (M <= 128 && adapters > (shared > 4 ? shared : 4));
+}
 
 // The first product of low-rank adapters (lora.hip):
 //   t[m][r] = scale[a] * (row offsets[a] + r of a_rows [ranks, K]) . x[m]

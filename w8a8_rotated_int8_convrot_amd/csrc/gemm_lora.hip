@@ -57,15 +57,14 @@ bool one_round(int64_t M, int64_t N) {
 // The tiles are the layer's own (pick_gemm_tile) otherwise, with the persistent
 // 192 x 288 kernel for its largest ones and the one-wave 16 x 16 tile for few
 // tokens.
-// Up to 128 tokens with several adapters each lane adds its own token's ranks;
-// larger batches, and batches of at most four adapters, go through the list of
-// the tile's adapters.
+// Where lora_by_token says so each lane adds its own token's ranks; other batches
+// go through the list of the tile's adapters.
 template <int EPI>
 hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
                       const uint16_t* bias, uint16_t* y, const Lora& lora, int64_t M, int64_t N, int64_t K,
                       hipStream_t stream) {
   const int tile = pick_gemm_tile(M, N);
-  if (lora_by_token(M, lora.adapters)) {
+  if (lora_by_token(M, lora.adapters, lora.max_rank)) {
     const LoraGather l{lora};
     if (M <= 16) return launch_tile<TileSkinny16, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);
     if (tile == 10) return launch_tile<TileM32, EPI>(xq, x_scale, wq, w_scale, bias, y, l, M, N, K, stream);

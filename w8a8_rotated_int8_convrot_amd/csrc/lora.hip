@@ -421,7 +421,7 @@ hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, int group, 
   if (M == 0) return hipSuccess;
   const Down p{x, a, scale, offsets, index, reinterpret_cast<float*>(t), static_cast<int>(M), static_cast<int>(K), static_cast<int>(ranks),
                static_cast<int>(adapters), static_cast<int>(max_rank), static_cast<int>(t_stride)};
-  const bool dots = lora_by_token(M, adapters);
+  const bool dots = lora_by_token(M, adapters, max_rank);
   return f16 ? launch<true>(p, group, xq, xs, sums, dots, stream) : launch<false>(p, group, xq, xs, sums, dots, stream);
 }
 
