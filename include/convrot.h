@@ -439,7 +439,7 @@ int convrot_block_norm(const convrot_block *b, void *stream);
  * with convrot_linear_ex's definitions (codes and scale of token m, the
  * product, bias and rounding), so y[p] has the bytes convrot_linear_ex gives
  * for that token and that expert's weight.  Each token is coded once, however
- * many experts it goes to. */
+ * many experts it goes to (a few tokens by every workgroup of the one launch). */
 
 /* Workspace bytes convrot_grouped_linear needs: codes and scales of M tokens.
  * 0 for a bad size. */

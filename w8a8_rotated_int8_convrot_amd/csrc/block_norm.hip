@@ -240,7 +240,7 @@ hipError_t launch(const BlockNorm& p, hipStream_t stream) {
 // three chunks a thread where that leaves few lanes idle (4608 x 4096: 36.7 us
 // with 256 threads of two chunks, 35.6 with 512 of one, 45.1 with 128 of four;
 // 16896 x 6144: 177 us with 256 threads of three, 193 with 512 of two, 204 with
-// 768 of one).
+// 768 of one, 16-bit; now 168, and 167 coded).
 template <int G, typename In>
 hipError_t launch_k(const BlockNorm& p, hipStream_t stream) {
   const int chunks = (p.K + 7) / 8;

@@ -413,9 +413,9 @@ __device__ inline v4i finite_halves(v4i v) {
 // unit's panel of BN channels goes through LDS: a thread loads eight channels
 // of one rank and writes them apart, so that a lane finds eight ranks of one
 // channel together.  UNITS panels are taken at a time, because what a unit
-// costs is the latency of its loads; begin() issues the first ones' (the tile
-// kernels call it before their main loop, where the index and the offsets have
-// time to arrive).  Where the tokens of a block have several adapters a lane
+// costs is the latency of its loads; begin() issues the first ones', which wait
+// for the index, the offsets and then the panel (the tile kernels call it before
+// their main loop, the persistent one in its epilogue).  Where the tokens of a block have several adapters a lane
 // keeps the sum only if its token has the unit's: a product with zero instead
 // would carry one adapter's infinities into other tokens.
 //
@@ -676,8 +676,8 @@ struct LoraTile {
 // above would be as long as the tile: every lane sums its own token's ranks one
 // by one, four channels at a time, into `part` (added to the layer's results
 // later).  Rows of b come in 8-byte pieces; with four results a lane 32 ranks
-// are in flight (16 tokens of rank 128, 4096 x 4096, the whole call: 24.2 us
-// with eight, 22.1), with sixteen eight.
+// are in flight (16 tokens of rank 128, 4096 x 4096, the whole call: 24.9 us
+// with eight, 21.4; rank 64 16.8 and 15.4), with sixteen eight.
 template <class T, bool F16>
 __device__ inline void lora_gather(float (&part)[T::TN][T::TM][T::kAccRegs], const Lora& lo, int lane, int n_first,
                                    int m_first, int M, int N) {
@@ -1106,7 +1106,8 @@ __global__ __launch_bounds__(T::kThreads, (kMinWaves<T, X>)) void gemm_i8_kernel
     for (int s = 0; s < T::kStages - 1; ++s) issue_slab(min(s, KT - 1), s);
   }
   // adapters: the list's first panels, or the tokens' own sums, while the first
-  // slabs are on their way
+  // slabs are on their way (with three stages and more; with two the slabs are
+  // issued below, after the index and the offsets have been waited for)
   constexpr bool GATHER = std::is_same_v<X, LoraGather>;
   // adapter panels at a time (registers for one beside 192 tokens: 1500 x 4096 x
   // 8192, rank 32: 71.2 us with two, which spill, 68.6 with one)

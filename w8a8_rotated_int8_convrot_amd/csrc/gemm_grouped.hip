@@ -88,11 +88,14 @@ hipError_t launch_epi(const int8_t* xq, const float* x_scale, const int8_t* wq, 
 // workgroup has 16 channels of one expert and 16 of its rows, its four waves
 // share K.  Each wave first sends for all of its weight (STEPS pieces of 16 rows
 // x 64 bytes in the registers of v_mfma_i32_16x16x64_i8's operand), then the
-// workgroup rotates and codes the tokens into LDS -- every workgroup the same,
-// a few hundred instructions a wave under the weight's latency -- and the
-// products take the tokens from there.  The waves' sums are joined in LDS.
-// One token, 4 of 16 experts of 1408 x 2048: 6.9 us; in two launches rotate +
-// quant took 2.4 us and the product 6.2, and the call 13.6 us instead of 9.6.
+// workgroup rotates and codes all the tokens into LDS, every workgroup the same,
+// and the products take them from there.  Loads return in order, so a token's
+// values arrive behind the weight: one latency covers both, and the coding of a
+// few hundred instructions a wave and token comes after it, as does each further
+// token's own latency.  The waves' sums are joined in LDS.
+// One token, 4 of 16 experts of 1408 x 2048: 7.7 us in the trace, 9.8 a call,
+// 7.9 captured; in two launches rotate + quant took 2.4 us, the product 6.2 and
+// the call 13.6.
 constexpr int kFewTokens = 4;
 constexpr int kFewK = 8192;
 struct FewTile { static constexpr int BN = 16, BM = 16, kGroupM = 1; };

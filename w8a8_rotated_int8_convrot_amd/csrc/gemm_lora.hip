@@ -34,20 +34,21 @@ hipError_t launch_persist(const int8_t* xq, const float* x_scale, const int8_t* 
 }
 
 // Whether these tiles make one round that gives more than 5/8 of the CUs a
-// tile: 256 x 128, else 256 x 192.  Such a round is as long as one tile, and nothing runs beside a tile's
-// prologue and the adapters' panels, so the smallest tile that still makes one
-// round wins; the layer's own choice (two 128 x 128 tiles a CU, half-empty
-// rounds of 384 x 96 or 192 x 288) gives each CU more.  us a call, weight from
-// HBM, the layer's choice -> this (M x K x N, tiles):
-//   2000 x 12288 x 4096 (256)  219 -> 183     1024 x 8192 x 8192 (256)  118 -> 95
-//   1500 x 4096 x 4096 (192)    62 -> 57      512 x 4096 x 12288 (192)  53 -> 50
-//   1300 x 4096 x 4096 (176)    59 -> 53      777 x 2048 x 6144 (168)   50 -> 50
+// tile: 256 x 128, else 256 x 192.  Such a round is as long as one tile, and
+// nothing runs beside a tile's prologue and the adapters' panels, so the smallest
+// tile that still makes one round wins; the layer's own choice (two 128 x 128
+// tiles a CU, half-empty rounds of 384 x 96 or 192 x 288) gives each CU more.  us
+// a call with six adapters of rank 32 in bf16, weight from HBM, the layer's
+// choice -> this (M x K x N, tiles):
+//   2000 x 12288 x 4096 (256)  180 -> 137     1024 x 8192 x 8192 (256)  113 -> 87
+//   1500 x 4096 x 4096 (192)    52 -> 49      512 x 4096 x 12288 (192)  59 -> 50
+//   1300 x 4096 x 4096 (176)    53 -> 47      777 x 2048 x 6144 (168)   33 -> 32
 // with 256 x 192:
-//   1500 x 2048 x 8192 (256)    76 -> 52      1500 x 4096 x 8192 (256)  126 -> 86
-//   3000 x 4096 x 4096 (256)    87 -> 82      2300 x 4096 x 4096 (192)   90 -> 80
-//   2816 x 12288 x 4096 (240)  188 -> 182     769 x 4096 x 12288 (240)   66 -> 69
-// and past those bounds, 256 x 128: 1024 x 4096 x 4096 (128 tiles)  44 -> 52,
-// 4608 x 4096 x 12288 (1728)  279 -> 336.
+//   1500 x 2048 x 8192 (256)    74 -> 47      1500 x 4096 x 8192 (256)  109 -> 72
+//   3000 x 4096 x 4096 (256)    78 -> 77      2300 x 4096 x 4096 (192)   69 -> 65
+//   2816 x 12288 x 4096 (240)  182 -> 175     769 x 4096 x 12288 (240)   72 -> 68
+// and past those bounds, 256 x 128: 1024 x 4096 x 4096 (128 tiles)  37 -> 45,
+// 4608 x 4096 x 12288 (1728)  247 -> 284.
 template <class T>
 bool one_round(int64_t M, int64_t N) {
   const int64_t tiles = ((M + T::BM - 1) / T::BM) * ((N + T::BN - 1) / T::BN);

@@ -308,7 +308,7 @@ __global__ __launch_bounds__(kThreads) void lora_rows_kernel(Down p, int rows, i
 
 // The same for larger batches: behind the wgs workgroups that rotate and code
 // by token blocks, others sum, their latency under the coding (a call of 1000 x
-// 4096 x 4096, rank 16: 41.4 -> 38.3 us; 2000 x 12288 x 4096, rank 32: 160 -> 158).
+// 4096 x 4096, rank 16: 41.4 -> 38.9 us; 2000 x 12288 x 4096, rank 32: 160 -> 158).
 template <bool F16>
 struct SumsBeside {
   Down p;
