@@ -484,7 +484,8 @@ int convrot_grouped_linear(const void *x, int io_dtype, int64_t M, int64_t K, co
  * with l_m the layer's fp32 result (convrot_linear_ex's before its rounding)
  * and the products summed in fp32; rnd: to io_dtype.  t_m is an fp32 value, or
  * for the matrix units two 16-bit ones that stand for it within 2^-16 (bf16) or
- * 2^-22 (fp16, over fp32's whole range) of each of its ranks.  x_m enters A_a x_m
+ * 2^-22 (fp16, beside 2^-39 of the largest of 32 ranks; neither fp16's range nor
+ * its smallest step bounds t_m).  x_m enters A_a x_m
  * as it is, neither rotated nor coded.  A token whose index is outside
  * [0, n_adapters) has no adapter and gets convrot_linear_ex's bytes, and a
  * token's result does not depend on the other tokens' adapters.  A given shape

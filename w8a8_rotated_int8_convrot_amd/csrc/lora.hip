@@ -7,8 +7,8 @@
 // matrix units, whose operands have 16 bits, as two parts, the nearest value of
 // the io type and the nearest to what that leaves: one part alone would move
 // the result by up to half a step of sum_r |t_r b_r|, however much of that
-// cancels.  Two are off by 2^-16 of each t_r in bf16 and 2^-22 in fp16, far
-// below the fp32 sum's own worst case.  fp16 parts are those of t scaled by a
+// cancels.  Two are off by 2^-16 of each t_r in bf16 and 2^-22 in fp16 (there
+// also by 2^-39 of the largest of its 32 ranks).  fp16 parts are those of t scaled by a
 // power of two that takes the largest of 32 ranks to [2^14, 2^15), so that
 // neither its range nor its smallest step meets a t of fp32.
 //
