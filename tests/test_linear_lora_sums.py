@@ -127,3 +127,33 @@ def test_tokens_without_an_adapter_keep_the_sign_of_a_zero(B, M, ranks, io):
     zeros = plain[none]
     assert (zeros == 0).all() and torch.signbit(zeros).any() and not torch.signbit(zeros).all()
     assert torch.equal(got[none].view(torch.int16), zeros.view(torch.int16))
+
+
+@pytest.mark.parametrize("M,N,ranks", [(12, 1030, [16] * 12), (100, 2048, [64] * 14), (700, 4096, [64, 40]),
+                                       (2999, 4090, [64, 100]), (4700, 3001, [64] * 5)])
+def test_two_streams_and_two_graphs(B, M, N, ranks):
+    """t lies in the call's own workspace: two calls at once, and two graphs replayed in turn with
+    eager calls between them, give what each gives alone."""
+    ps = [problem(M, 512, N, "fp16", ranks, False, True, s, 50) for s in (1, 2)]
+    want = [B.convrot_linear_lora(**p, group=128) for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    outs = []
+    for p, s in zip(ps, streams):
+        with torch.cuda.stream(s):
+            outs.append(B.convrot_linear_lora(**p, group=128))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    graphs, outs = [], []
+    for p in ps:
+        outs.append(torch.empty_like(want[0]))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            B.convrot_linear_lora(**p, group=128, out=outs[-1])
+    for _ in range(3):
+        for g, o in zip(graphs, outs):
+            o.fill_(9)
+            g.replay()
+        assert torch.equal(B.convrot_linear_lora(**ps[0], group=128), want[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
