@@ -518,6 +518,168 @@ int convrot_linear_lora(const void *x, int io_dtype, int64_t M, int64_t K, const
                         const int32_t *offsets, int64_t n_adapters, int64_t max_rank, const int32_t *index,
                         void *y, void *workspace, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------- rotary positions
+ * Between the QKV layer and the attention: the heads of queries and keys turned
+ * by their token's position p.  Pair i of the first rot_dim dims of a head, with
+ * the frequency f_i (radians a position, 64 bits):
+ *   phi = p f_i
+ *   (a, b) -> rnd(scale * (a cos phi - b sin phi), scale * (b cos phi + a sin phi))
+ * where (a, b) are dims i and i + rot_dim / 2 (CONVROT_ROPE_HALF) or 2 i and
+ * 2 i + 1 (CONVROT_ROPE_INTERLEAVED); dims from rot_dim on are copied.  With
+ * `inverse` phi is negated: the turn taken back (for scale 1), and for any scale
+ * the transpose of the turn, which is what a gradient goes through.  phi / 2 pi
+ * loses its whole turns in 64 bits; sine, cosine and products are fp32. */
+enum convrot_rope_layout { CONVROT_ROPE_HALF = 0, CONVROT_ROPE_INTERLEAVED = 1 };
+
+/* Frequencies of rot_dim / 2 pairs, into HOST memory, and the factor of sine and
+ * cosine; f_i = base^(-2 i / rot_dim), and for contexts `factor` times as long as
+ * the original_length positions a model was trained on:
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   NTK     base * factor^(rot_dim / (rot_dim - 2)) for base
+ *   YARN    f_i (1 - r_i) + f_i / factor r_i, r_i = (i - lo) / (hi - lo) within [0, 1],
+ *           lo = max(floor(d(high)), 0), hi = min(ceil(d(low)), rot_dim - 1) (at least
+ *           lo + 0.001), d(t) = rot_dim ln(original_length / (2 pi t)) / (2 ln base):
+ *           pairs of more than `high` turns over the original length stay, those of
+ *           fewer than `low` are interpolated; *scale = 0.1 ln(factor) + 1
+ *           (Peng et al. 2023)
+ *   BANDS   f_i k_i + f_i / factor (1 - k_i), k_i = (t_i - low) / (high - low) within
+ *           [0, 1], t_i = original_length f_i / (2 pi) the turns of pair i
+ * *scale is 1 but for YARN.  original_length, low and high are read by YARN and
+ * BANDS only, factor by all but NONE.
+ * Errors: NULL, rot_dim odd or outside [2, 1024], base not finite or <= 1, factor
+ * not finite or < 1, original_length not finite or <= 0, not 0 < low < high <
+ * infinity, NTK with rot_dim 2 -> CONVROT_EINVAL; unknown scaling ->
+ * CONVROT_EUNSUPPORTED. */
+enum convrot_rope_scaling {
+    CONVROT_ROPE_NONE = 0, CONVROT_ROPE_LINEAR = 1, CONVROT_ROPE_NTK = 2, CONVROT_ROPE_YARN = 3, CONVROT_ROPE_BANDS = 4
+};
+int convrot_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_length,
+                             double low, double high, double *freqs, float *scale);
+
+/*   q, k        rows of q_heads and k_heads heads of head_dim in io_dtype (CONVROT_BF16
+ *               or CONVROT_F16), one row a token, rows q_stride and k_stride elements
+ *               apart (at least heads * head_dim, a multiple of 8): parts of one QKV
+ *               row, say.  Either may be left out (0 heads, NULL).
+ *   q_out, k_out the results, rows q_out_stride and k_out_stride apart.  An output may
+ *               be its own input (same pointer and stride); else outputs overlap nothing.
+ *   positions   DEVICE int32 [M], any values.
+ *   freqs       DEVICE double [rot_dim / 2].
+ * head_dim a multiple of 8 up to 1024, rot_dim even, 2 to head_dim, heads together
+ * 1 to 16384, M in [0, 2^30]; M = 0 is a no-op.  q, k and the outputs are 16-byte
+ * aligned (CONVROT_EALIGN).  A head of infinities or NaN gives what the formula
+ * gives.  One launch, no workspace.
+ * Errors: NULL, sizes, strides, scale not finite -> CONVROT_EINVAL; unknown
+ * io_dtype or layout -> CONVROT_EUNSUPPORTED; launch, or a grid of 2^32 threads or
+ * more -> CONVROT_EHIP. */
+int convrot_rope(const void *q, int64_t q_heads, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                 const void *k, int64_t k_heads, int64_t k_stride, void *k_out, int64_t k_out_stride,
+                 int io_dtype, int64_t M, int head_dim, int rot_dim, int layout, const int32_t *positions,
+                 const double *freqs, float scale, int inverse, void *stream);
+
+/* ---------------------------------------------------------------- 4-bit cache
+ * Keys and values of many sequences in 4 bits, in pages: the layer's rotation with
+ * a head as its group, and one scale for each token and head.  Row x (a key or
+ * value head of one token, D = head_dim):
+ *   v = x H_D / sqrt(D)    s = bf16_rne(fp32(max |v| / 7))    c = rne(v / s) in [-7, 7]
+ * v, the division and the codes in 64 bits (s = 0: codes 0).  A row that holds
+ * infinities or NaN is held as scale NaN, and what reads it gets NaN.
+ * A page holds `page` tokens of all heads, [kv_heads][page / 32] units of 32
+ * tokens; a unit is, one after another,
+ *   key codes     [32][D / 2] bytes: dim 2 i in the low half of byte i
+ *   value codes   [4][D] 32-bit words: token 8 o + i of dim d in bits 4 i of word [o][d]
+ *   key scales    [32] bf16, value scales [32] bf16
+ * with a code c held as c + 8: 32 D + 128 bytes.  Token t of sequence b lies in
+ * page table[b][t / page].  The tokens of a call are rows: sequence b has rows
+ * offsets[b] .. offsets[b + 1] - 1, and row i of it stands for its token
+ * starts[b] + i - offsets[b]. */
+typedef struct convrot_cache {
+    void          *pages;           /* [n_pages] of convrot_cache_page_bytes bytes, 16-byte aligned */
+    int64_t        n_pages;         /* 1 to 2^31 - 1 */
+    int            page;            /* tokens a page: 32, 64, 128 or 256 */
+    int            head_dim;        /* 64, 128 or 256 */
+    int64_t        kv_heads;        /* 1 to 1024 */
+    const int32_t *table;           /* DEVICE [n_seqs, max_pages], rows table_stride apart; an entry outside
+                                       [0, n_pages) names no page */
+    int64_t        table_stride;    /* at least max_pages */
+    int64_t        n_seqs;          /* 1 to 2^20 */
+    int64_t        max_pages;       /* columns: a sequence's tokens end at max_pages * page (at most 2^30) */
+    const int32_t *starts;          /* DEVICE [n_seqs] token of each sequence's first row; negative: its rows
+                                       before token 0 stand for none */
+    const int32_t *offsets;         /* DEVICE [n_seqs + 1], ascending; values are clamped to [0, M] and to the
+                                       one before.  Offsets that fall and rise again leave open what the rows
+                                       concerned give.  Rows before offsets[0] and from offsets[n_seqs] on are of
+                                       no sequence: not read, their outputs left as they were */
+} convrot_cache;
+
+/* Bytes of a page, kv_heads * (page / 32) * (32 head_dim + 128); 0 for a bad size. */
+size_t convrot_cache_page_bytes(int page, int64_t kv_heads, int head_dim);
+
+/* The rows' keys and values into the cache, at their tokens.
+ *   k, v   [M, kv_heads, head_dim] in io_dtype, rows k_stride and v_stride elements
+ *          apart (at least kv_heads * head_dim, multiples of 8), 16-byte aligned.
+ * Everything else in the pages stays as it is.  A token past the table's end, before 0
+ * or in no page of the cache is not stored.  Two tokens of one call must not share
+ * eight token places of one page (two sequences that share a page append to copies
+ * of it: convrot_cache_copy).  One launch, no workspace, M in [0, 2^30]; M = 0 is a no-op.
+ * Errors: NULL, sizes, strides -> CONVROT_EINVAL; unknown io_dtype, page or head_dim ->
+ * CONVROT_EUNSUPPORTED; alignment -> CONVROT_EALIGN; launch, or a grid of 2^32 threads
+ * or more -> CONVROT_EHIP. */
+int convrot_cache_append(const convrot_cache *cache, const void *k, int64_t k_stride, const void *v,
+                         int64_t v_stride, int io_dtype, int64_t M, void *stream);
+
+/* The rows' tokens back from the cache: rnd(s c H_D / sqrt(D)).  k and v as in
+ * convrot_cache_append, written; either may be NULL (not wanted).  Tokens that no
+ * page holds read as 0.  Errors as convrot_cache_append. */
+int convrot_cache_read(const convrot_cache *cache, void *k, int64_t k_stride, void *v, int64_t v_stride,
+                       int io_dtype, int64_t M, void *stream);
+
+/* Workspace bytes convrot_cache_attention needs (0 where it needs none, and for a
+ * bad size); max_tokens = max_pages * page. */
+size_t convrot_cache_attention_workspace(int64_t M, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t n_seqs,
+                                         int64_t max_tokens);
+
+/* Attention of the rows' queries over the tokens of their sequences in the cache,
+ * the rows' own among them (append them first).  Row i of sequence b with n rows,
+ * at token p = starts[b] + i, and head h of q_heads reads key head
+ * h / (q_heads / kv_heads), at the tokens j with
+ *   causal:  max(0, p - window + 1) <= j <= p     (window 0: from token 0 on)
+ *   else:    0 <= j < starts[b] + n
+ * that pages hold:
+ *   t_j = scale * (q H / sqrt(D)) . (s_j c_j)      (the keys' scales and codes)
+ *   out = rnd((sum_j softmax(t)_j s'_j c'_j) H / sqrt(D))     (the values')
+ * and 0 where there is no such j.  Scores, softmax and sums are fp32, the rotated
+ * query and each weight times its value's scale enter the products as fp16.
+ *   q    [M, q_heads, head_dim] in io_dtype, rows q_stride elements apart (at least
+ *        q_heads * head_dim, a multiple of 8).
+ *   out  [M, q_heads, head_dim] in io_dtype, contiguous; must not overlap q.
+ *   workspace  at least convrot_cache_attention_workspace bytes.
+ * Long sequences are cut into parts by M, n_seqs and max_pages alone, which a host
+ * knows: a table whose columns reach far past the tokens cuts too coarsely, so give
+ * the columns that are used (max_pages, with the table's own stride).  A row's
+ * result does not depend on what other rows, unread tokens or unused places hold.
+ * q_heads a multiple of kv_heads, M * q_heads at most 2^30, window in [0, 2^31) and 0
+ * unless causal; M = 0 is a no-op.  q, out and workspace are 16-byte aligned.
+ * Errors: as convrot_cache_append, and scale not finite -> CONVROT_EINVAL, workspace
+ * missing or too small -> CONVROT_EWORKSPACE. */
+int convrot_cache_attention(const convrot_cache *cache, const void *q, int64_t q_heads, int64_t q_stride,
+                            int io_dtype, int64_t M, float scale, int causal, int64_t window, void *out,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/* Pages copied inside a cache, in each of `layers` caches layer_bytes apart: the last
+ * page of a sequence that forks, pages moved down into gaps.
+ *   src, dst   HOST int32 [n] pages, read during the call only (a captured call keeps
+ *              them).  All copies happen as if at once: a destination may be named
+ *              once, and must not be a source.
+ * page_bytes a multiple of 16, layer_bytes at least n_pages * page_bytes and a multiple
+ * of 16 (layers = 1: not read), layers 1 to 65535, n in [0, 2^20]; n = 0 is a no-op.
+ * One launch for each 256 pairs, no workspace.
+ * Errors: NULL, sizes, a page outside [0, n_pages), a destination named twice or that is
+ * a source -> CONVROT_EINVAL; pages not 16-byte aligned -> CONVROT_EALIGN; launch, a grid
+ * of 2^32 threads or more, or no host memory for the check -> CONVROT_EHIP. */
+int convrot_cache_copy(void *pages, int64_t layers, int64_t layer_bytes, int64_t n_pages, int64_t page_bytes,
+                       const int32_t *src, const int32_t *dst, int64_t n, void *stream);
+
 /* ---------------------------------------------------------------- measurement aid
  * Not a step of the layer and defined by no page: it exists so that a
  * benchmark can state the rate the matrix cores sustain on this machine,

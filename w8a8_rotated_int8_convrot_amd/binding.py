@@ -28,6 +28,7 @@ STATUS = {0: "CONVROT_OK", -1: "CONVROT_EINVAL", -2: "CONVROT_EUNSUPPORTED",
 
 # Every symbol include/convrot.h declares, with (argtypes, restype).
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_D = ctypes.c_double
 SIGNATURES = {
     "convrot_abi_version": ([], _I),
     "convrot_last_error": ([], ctypes.c_char_p),
@@ -62,6 +63,15 @@ SIGNATURES = {
                              _SZ, _P], _I),
     "convrot_grouped_workspace": ([_I64, _I64], _SZ),
     "convrot_grouped_linear": ([_P, _I, _I64, _I64, _P, _P, _I, _I64, _I64, _I, _P, _P, _P, _I64, _P, _P, _SZ, _P], _I),
+    "convrot_rope_frequencies": ([_I, _D, _I, _D, _D, _D, _D, _P, _P], _I),
+    "convrot_rope": ([_P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _I, _I64, _I, _I, _I, _P, _P, ctypes.c_float,
+                      _I, _P], _I),
+    "convrot_cache_page_bytes": ([_I, _I64, _I], _SZ),
+    "convrot_cache_append": ([_P, _P, _I64, _P, _I64, _I, _I64, _P], _I),
+    "convrot_cache_read": ([_P, _P, _I64, _P, _I64, _I, _I64, _P], _I),
+    "convrot_cache_attention_workspace": ([_I64, _I64, _I64, _I, _I64, _I64], _SZ),
+    "convrot_cache_attention": ([_P, _P, _I64, _I64, _I, _I64, ctypes.c_float, _I, _I64, _P, _P, _SZ, _P], _I),
+    "convrot_cache_copy": ([_P, _I64, _I64, _I64, _I64, _P, _P, _I64, _P], _I),
 }
 
 CONVROT_FAULT_NONE = 0
@@ -764,3 +774,196 @@ def convrot_linear_lora(x, wq, w_scale, group, lora_a, lora_b, lora_scale, offse
              _need_on(offsets, dev, torch.int32, "offsets", (n + 1,)), n, max_rank,
              _need_on(index, dev, torch.int32, "index", (M,)), out_ptr, ws_ptr, ws_bytes, _stream(x))
     return out
+
+
+# ---------------------------------------------------------------- between two layers
+
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+def _heads_of(t, dev, dtype, name, shape=None):
+    """Rows of contiguous heads [M, H, D] on dev, all of one row stride; their address and that stride."""
+    if (t.dim() != 3 or t.dtype != dtype or t.device != dev or (shape is not None and t.shape != shape)
+            or (t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1)):
+        want = list(shape) if shape is not None else "[M, H, D]"
+        raise ValueError(f"{name}: expected {dtype} {want} on {dev} with contiguous heads, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}, strides {list(t.stride())}")
+    # one row has no neighbour, whatever stride it carries
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _writable_heads(t, dev, dtype, name, shape):
+    ptr, stride = _heads_of(t, dev, dtype, name, shape)
+    if stride < shape[1] * shape[2]:
+        raise ValueError(f"{name}: rows overlap")
+    return ptr, stride
+
+
+def convrot_rope_frequencies(rot_dim, base=10000.0, kind="none", factor=1.0, original_length=0.0, low=1.0, high=None,
+                             device=None):
+    """Frequencies of rotary positions (see include/convrot.h): fp64 [rot_dim / 2] on ``device`` and
+    the factor of sine and cosine, both as convrot_rope takes them.
+
+    kind: "none", "linear", "ntk", "yarn" or "bands", for contexts ``factor`` times as long as
+    original_length; low and high (32 for "yarn", 4 for "bands") are turns over that length."""
+    if kind not in _ROPE_SCALINGS:
+        raise ValueError(f"kind: one of {sorted(_ROPE_SCALINGS)}, got {kind!r}")
+    if high is None:
+        high = 32.0 if kind == "yarn" else 4.0
+    freqs, scale = (_D * max(1, rot_dim // 2))(), ctypes.c_float()
+    _call("convrot_rope_frequencies", rot_dim, base, _ROPE_SCALINGS[kind], factor, original_length, low, high, freqs,
+          ctypes.byref(scale))
+    return torch.tensor(list(freqs), dtype=torch.float64, device=device), scale.value
+
+
+def convrot_rope(q, k, positions, freqs, scale=1.0, layout="half", inverse=False, q_out=None, k_out=None):
+    """Rotary positions on bf16 or fp16 heads q [M, Hq, D] and k [M, Hk, D] (see include/convrot.h)
+    -> (q_out, k_out); k may be None, and its result then is.
+
+    q and k may be parts of one row (heads contiguous, any row stride), positions is int32 [M],
+    freqs fp64 [rot / 2] on the GPU, the first rot dims of a head being turned.  q_out and
+    k_out may be q and k."""
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout: 'half' or 'interleaved', got {layout!r}")
+    io = _io_of(q, "q")
+    dev, dt = q.device, q.dtype
+    if not q.is_cuda:
+        raise ValueError(f"q: expected a CUDA tensor, got one on {dev}")
+    qp, qs = _heads_of(q, dev, dt, "q")
+    M, Hq, D = q.shape
+    q_out = torch.empty((M, Hq, D), dtype=dt, device=dev) if q_out is None else q_out
+    qop, qos = _writable_heads(q_out, dev, dt, "q_out", q.shape)
+    Hk, kp, ks, kop, kos = 0, None, 0, None, 0
+    if k is not None:
+        Hk = k.shape[1] if k.dim() == 3 else 0
+        kp, ks = _heads_of(k, dev, dt, "k", (M, Hk, D))
+        k_out = torch.empty((M, Hk, D), dtype=dt, device=dev) if k_out is None else k_out
+        kop, kos = _writable_heads(k_out, dev, dt, "k_out", k.shape)
+    elif k_out is not None:
+        raise ValueError("convrot_rope: k_out without k")
+    if freqs.dim() != 1:
+        raise ValueError(f"freqs: expected 1 dimension, got {freqs.dim()}")
+    _call_on(q, "convrot_rope", qp, Hq, qs, qop, qos, kp, Hk, ks, kop, kos, io, M, D, 2 * freqs.shape[0],
+             _ROPE_LAYOUTS[layout], _need_on(positions, dev, torch.int32, "positions", (M,)),
+             _need_on(freqs, dev, torch.float64, "freqs", (freqs.shape[0],)), scale, 1 if inverse else 0, _stream(q))
+    return q_out, k_out
+
+
+class Cache(ctypes.Structure):
+    """Mirror of ``convrot_cache`` (include/convrot.h)."""
+    _fields_ = [("pages", _P), ("n_pages", _I64), ("page", _I), ("head_dim", _I), ("kv_heads", _I64), ("table", _P),
+                ("table_stride", _I64), ("n_seqs", _I64), ("max_pages", _I64), ("starts", _P), ("offsets", _P)]
+
+
+def convrot_cache_page_bytes(page: int, kv_heads: int, head_dim: int) -> int:
+    return lib().convrot_cache_page_bytes(page, kv_heads, head_dim)
+
+
+_page_bytes = functools.lru_cache(maxsize=256)(convrot_cache_page_bytes)
+
+
+def _cache_of(dev, pages, table, starts, offsets, page, kv_heads, head_dim):
+    """The C view of a cache and of a call's rows (to be kept until the call has been queued)."""
+    need = _page_bytes(page, kv_heads, head_dim)
+    # 0: sizes the call refuses itself
+    if pages.dim() != 2 or (need != 0 and pages.shape[1] != need):
+        raise ValueError(f"pages: expected [n, {need}] (convrot_cache_page_bytes), got {list(pages.shape)}")
+    if table.dim() != 2 or table.dtype != torch.int32 or table.device != dev or (table.stride(1) != 1 and table.shape[1] > 1):
+        raise ValueError(f"table: expected int32 [sequences, pages] on {dev} with contiguous rows, got {table.dtype} "
+                         f"{list(table.shape)} on {table.device}")
+    B, W = table.shape
+    return Cache(_need_on(pages, dev, torch.uint8, "pages", pages.shape), pages.shape[0], page, head_dim, kv_heads,
+                 table.data_ptr(), table.stride(0) if B > 1 else W, B, W,
+                 _need_on(starts, dev, torch.int32, "starts", (B,)),
+                 _need_on(offsets, dev, torch.int32, "offsets", (B + 1,)))
+
+
+def convrot_cache_append(pages, table, starts, offsets, k, v, page) -> None:
+    """New tokens' keys and values into a paged 4-bit cache (see include/convrot.h).
+
+    pages: uint8 [n, convrot_cache_page_bytes(page, H, D)], written; table: int32 [B, W] page of each
+    ``page`` tokens of a sequence; k and v: bf16 or fp16 [M, H, D] (heads contiguous, any row
+    stride), rows offsets[b] to offsets[b + 1] (int32 [B + 1]) being sequence b's tokens from
+    starts[b] (int32 [B]) on.  table, starts and offsets are on the GPU and read by the kernel only."""
+    io = _io_of(k, "k")
+    dev, dt = k.device, k.dtype
+    if not k.is_cuda:
+        raise ValueError(f"k: expected a CUDA tensor, got one on {dev}")
+    kp, ks = _heads_of(k, dev, dt, "k")
+    M, H, D = k.shape
+    vp, vs = _heads_of(v, dev, dt, "v", k.shape)
+    c = _cache_of(dev, pages, table, starts, offsets, page, H, D)
+    _call_on(k, "convrot_cache_append", ctypes.byref(c), kp, ks, vp, vs, io, M, _stream(k))
+
+
+def convrot_cache_read(pages, table, starts, offsets, rows, kv_heads, head_dim, page, dtype=torch.bfloat16, k=None, v=None):
+    """Tokens back from a paged 4-bit cache (see include/convrot.h) -> (k, v) [rows, H, D].
+
+    Arguments as convrot_cache_append; rows not of any sequence are left as they were (unset
+    in a k or v allocated here)."""
+    dev = pages.device
+    if not pages.is_cuda:
+        raise ValueError(f"pages: expected a CUDA tensor, got one on {dev}")
+    shape = (rows, kv_heads, head_dim)
+    k = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
+    io = _io_of(k, "k")
+    kp, ks = _writable_heads(k, dev, k.dtype, "k", shape)
+    vp, vs = _writable_heads(v, dev, k.dtype, "v", shape)
+    c = _cache_of(dev, pages, table, starts, offsets, page, kv_heads, head_dim)
+    _call_on(pages, "convrot_cache_read", ctypes.byref(c), kp, ks, vp, vs, io, rows, _stream(pages))
+    return k, v
+
+
+def convrot_cache_attention_workspace(M: int, q_heads: int, kv_heads: int, head_dim: int, n_seqs: int,
+                                      max_tokens: int) -> int:
+    return lib().convrot_cache_attention_workspace(M, q_heads, kv_heads, head_dim, n_seqs, max_tokens)
+
+
+_attention_bytes = functools.lru_cache(maxsize=256)(convrot_cache_attention_workspace)
+
+
+def convrot_cache_attention(q, pages, table, starts, offsets, kv_heads, page, scale=None, causal=True, window=0, out=None,
+                            workspace=None) -> torch.Tensor:
+    """Attention of new tokens' queries over a paged 4-bit cache (see include/convrot.h): bf16 or
+    fp16 q [M, Hq, D] -> out [M, Hq, D].
+
+    pages, table, starts and offsets as convrot_cache_append takes them, after it: the rows' own
+    tokens are among those read.  scale is 1 / sqrt(D) if not given; window > 0 lets a token
+    see only the last ``window`` tokens, itself among them; causal=False lets each see all of its
+    sequence.  Rows of no sequence are left as they were (unset in an ``out`` allocated here)."""
+    io = _io_of(q, "q")
+    dev, dt = q.device, q.dtype
+    if not q.is_cuda:
+        raise ValueError(f"q: expected a CUDA tensor, got one on {dev}")
+    qp, qs = _heads_of(q, dev, dt, "q")
+    M, Hq, D = q.shape
+    c = _cache_of(dev, pages, table, starts, offsets, page, kv_heads, D)
+    if out is None:
+        out = torch.empty((M, Hq, D), dtype=dt, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _need_on(out, dev, dt, "out", q.shape)
+    need = _attention_bytes(M, Hq, kv_heads, D, c.n_seqs, c.max_pages * page)
+    ws, wp, wn = (None, None, 0) if need == 0 else _workspace_of(q, workspace, need)
+    _call_on(q, "convrot_cache_attention", ctypes.byref(c), qp, Hq, qs, io, M, D ** -0.5 if scale is None else scale,
+             1 if causal else 0, window, op, wp, wn, _stream(q))
+    return out
+
+
+def convrot_cache_copy(pages, pairs) -> None:
+    """Pages copied inside a cache, all as if at once (see include/convrot.h): uint8 pages [n, bytes] or
+    [layers, n, bytes], pairs of (source, destination) page numbers known on the host."""
+    if not pages.is_cuda or pages.dtype != torch.uint8 or pages.dim() not in (2, 3) or not pages.is_contiguous():
+        raise ValueError(f"pages: expected a contiguous uint8 CUDA tensor of 2 or 3 dimensions, got {pages.dtype} "
+                         f"{list(pages.shape)} on {pages.device}")
+    n = len(pairs)
+    src, dst = (ctypes.c_int32 * max(n, 1))(), (ctypes.c_int32 * max(n, 1))()
+    for i, (a, b) in enumerate(pairs):
+        if not (-1 < a < 2 ** 31 and -1 < b < 2 ** 31):
+            raise ValueError(f"pairs: page {a} to {b} is outside [0, {pages.shape[-2]})")
+        src[i], dst[i] = a, b
+    layers = pages.shape[0] if pages.dim() == 3 else 1
+    _call_on(pages, "convrot_cache_copy", pages.data_ptr(), layers, pages.shape[-2] * pages.shape[-1], pages.shape[-2],
+             pages.shape[-1], src, dst, n, _stream(pages))

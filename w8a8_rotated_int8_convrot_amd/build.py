@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libconvrot.so")
 SOURCES = ("convrot_api.hip", "rotate_quant.hip", "gemm_i8.hip", "gemm_grouped.hip", "gemm_lora.hip", "lora.hip",
-           "default_path.hip", "block_norm.hip", "operators_api.hip", "mfma_probe.hip")
+           "default_path.hip", "block_norm.hip", "operators_api.hip", "rope.hip", "kv_cache.hip", "cache_attention.hip",
+           "cache_api.hip", "mfma_probe.hip")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -30,35 +30,6 @@
 namespace convrot {
 namespace {
 
-typedef float v2f __attribute__((ext_vector_type(2)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-
-// two fp32 values rounded to nearest even and packed
-template <typename In> __device__ inline uint32_t pack2(float a, float b);
-template <> __device__ inline uint32_t pack2<uint16_t>(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2bf));
-}
-template <> __device__ inline uint32_t pack2<_Float16>(float a, float b) {
-  // keep the fp32 results: a multiply-add fused with its conversion would
-  // round the exact value to fp16 once
-  asm volatile("" : "+v"(a), "+v"(b));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2h));
-}
-
-template <typename In>
-__device__ inline void widen8(const uint4& w, float (&v)[8]) {
-  v[0] = in_lo<In>(w.x); v[1] = in_hi<In>(w.x);
-  v[2] = in_lo<In>(w.y); v[3] = in_hi<In>(w.y);
-  v[4] = in_lo<In>(w.z); v[5] = in_hi<In>(w.z);
-  v[6] = in_lo<In>(w.w); v[7] = in_hi<In>(w.w);
-}
-
-template <typename In>
-__device__ inline uint4 narrow8(const float (&v)[8]) {
-  return make_uint4(pack2<In>(v[0], v[1]), pack2<In>(v[2], v[3]), pack2<In>(v[4], v[5]), pack2<In>(v[6], v[7]));
-}
-
 template <bool MAX>
 __device__ inline float join(float a, float b) { return MAX ? fmaxf(a, b) : a + b; }
 

@@ -1,0 +1,699 @@
+// cache_attention.hip -- attention over the paged 4-bit cache (cache.hpp).
+//
+// Per query head, with its head vector q and the visible keys j:
+//   t_j = scale * (q H / sqrt(D)) . (ks_j kc_j)     w = softmax(t)
+//   out = rnd((sum_j w_j vs_j vc_j) H / sqrt(D))    no visible key: 0
+// kc, vc the codes of the rotated heads, ks, vs their scales: the rotation
+// leaves q . k as it is, so the cache is read as it lies, the query is rotated
+// once, and the rotation of the values is taken back once at the end.
+//
+// A wave's work is a unit of 32 keys against 16 NT query columns, a column
+// being one query head of one token: the heads that share a key head, and
+// tokens of one sequence, share its unit.  Everything stays in registers:
+//   scores  v_mfma_f32_16x16x32_f16 of codes x queries, so that a lane holds
+//           eight keys of one column: 8 g .. 8 g + 7 for its quarter g of the
+//           wave, by the order in which the rows of codes enter
+//   softmax running reference m, sum l per column, in base 2 and fp32
+//   output  v_mfma of value codes x weights: the eight keys a lane holds are
+//           those its operand has to hold, so the weights go from one product to
+//           the next without leaving their lane
+// Codes become fp16 by putting their four bits under an exponent: bits 0-3
+// under 2^10 read as 1024 + u, bits 4-7 as 1024 + 16 u, and one packed add or
+// multiply-add makes the code of it, without rounding.  Roundings: the rotated
+// query to fp16 (with a power of two of its own for a row whose values fp16
+// does not hold well), and a weight times its value's scale to fp16, both 11
+// bits, more than the 16-bit output of bf16 and as many as that of fp16.
+//
+// The reference m is not the maximum of t but of t + log2 vs, what the rounded
+// weight is made of, so that fp16 holds it whatever the scales are; it is a whole
+// number, moves only where a weight would pass 2^kRise times the last one, and
+// the sums are then rescaled by an exact power of two.
+#include <algorithm>
+
+#include "cache.hpp"
+
+namespace convrot {
+namespace {
+
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+constexpr int kAttnWaves = 4;
+constexpr int kAttnThreads = kAttnWaves * 64;
+// A column's largest rounded weight lies in [2^kTop, 2^(kTop + kRise)], far
+// enough below fp16's 2^16, and one that is 2^-22 of it still has all its bits.
+constexpr float kTop = 8.0f;
+constexpr float kRise = 6.0f;
+// Value scales below 2^-60 count as that in the reference: the sum l, which has
+// no such factor, then stays below 2^(60 + 14) a key.
+constexpr float kLeastScale = -60.0f;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+template <int D> struct RootScale;      // 1 / sqrt(D)
+template <> struct RootScale<64> { static constexpr float value = 0.125f; };
+template <> struct RootScale<128> { static constexpr float value = 0x1.6a09e6p-4f; };
+template <> struct RootScale<256> { static constexpr float value = 0x1p-4f; };
+
+__device__ inline float xor16(float v) { return __shfl_xor(v, 16); }
+__device__ inline float xor32(float v) { return __shfl_xor(v, 32); }
+
+__device__ inline int wave_index() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
+__device__ inline int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Eight codes of a word as fp16, in the order of its nibbles 0 4 1 5 2 6 3 7.
+__device__ inline v8h codes_of(uint32_t w) {
+  const v2h off = {static_cast<_Float16>(-1032), static_cast<_Float16>(-1032)};
+  const v2h sixteenth = {static_cast<_Float16>(0.0625f), static_cast<_Float16>(0.0625f)};
+  const v2h off16 = {static_cast<_Float16>(-72), static_cast<_Float16>(-72)};
+  auto low = [&](uint32_t x) { return __builtin_bit_cast(v2h, (x & 0x000f000fu) | 0x64006400u) + off; };
+  auto high = [&](uint32_t x) {
+    return __builtin_elementwise_fma(__builtin_bit_cast(v2h, (x & 0x00f000f0u) | 0x64006400u), sixteenth, off16);
+  };
+  const uint32_t w8 = w >> 8;
+  const v2h p[4] = {low(w), high(w), low(w8), high(w8)};
+  return __builtin_bit_cast(v8h, p);
+}
+
+// What a lane holds of one unit: the words of two tokens' key codes (dims
+// [D / 4 * g, D / 4 * (g + 1))), of D / 16 dims' value codes (octet g), and the
+// scales of octet g, bf16.
+template <int D> struct UnitWords {
+  uint32_t k[2][D / 32], v[D / 16];
+  uint4 ks, vs;
+};
+
+template <int N>
+__device__ inline void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 2) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    w[0] = r.x, w[1] = r.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 r = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = r.x, w[4 * i + 1] = r.y, w[4 * i + 2] = r.z, w[4 * i + 3] = r.w;
+    }
+  }
+}
+
+__device__ inline void widen_scales(const uint4& r, float (&s)[8]) {
+  s[0] = bf16_lo(r.x), s[1] = bf16_hi(r.x), s[2] = bf16_lo(r.y), s[3] = bf16_hi(r.y);
+  s[4] = bf16_lo(r.z), s[5] = bf16_hi(r.z), s[6] = bf16_lo(r.w), s[7] = bf16_hi(r.w);
+}
+
+// One sequence's units of one key head, in the order they are asked for: the
+// table's entries are held 64 at a time, one a lane, so that a page's place is
+// no load behind a load.
+template <int D>
+struct UnitReader {
+  const Cache& c;
+  const int32_t* table;
+  int head, held;                       // first table column held
+  int32_t entry;
+
+  __device__ UnitReader(const Cache& cache, int b, int h)
+      : c(cache), table(cache.table + b * cache.table_stride), head(h), held(-64), entry(-1) {}
+
+  // False where no page of the cache is named; the words are then another page's.
+  __device__ bool load(int u, UnitWords<D>& w) {
+    const int shift = c.page_shift - 5, lane = threadIdx.x & 63;
+    const int column = u >> shift;
+    if (column < held || column >= held + 64) {
+      held = column;
+      const int at = column + lane;
+      entry = at < (c.max_tokens >> c.page_shift) ? table[at] : -1;
+    }
+    const int64_t page = __builtin_amdgcn_readlane(entry, column - held);
+    const bool there = page >= 0 && page < c.n_pages;
+    const uint8_t* unit = c.pages + (there ? page * c.page_bytes : 0) +
+                          static_cast<int64_t>((head << shift) + (u & ((1 << shift) - 1))) * unit_bytes(D);
+    const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      load_words(unit + (8 * (m >> 2) + 4 * t + (m & 3)) * (D / 2) + g * (D / 8), w.k[t]);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      uint32_t r[4];
+      load_words(unit + value_codes_at(D) + (g * D + 64 * i + 4 * m) * 4, r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w.v[4 * i + j] = r[j];
+    }
+    w.ks = *reinterpret_cast<const uint4*>(unit + key_scales_at(D) + 16 * g);
+    w.vs = *reinterpret_cast<const uint4*>(unit + value_scales_at(D) + 16 * g);
+    return there;
+  }
+};
+
+// 16 NT query columns of a wave: their queries, bounds and running sums.
+template <int D, int NT>
+struct Columns {
+  v8h q[NT][D / 32];
+  float qs[NT];                         // power of two a column's queries were divided by
+  int from[NT], to[NT];                 // visible keys of a column
+  float m[NT], l[NT];                   // reference; sum of this lane's keys
+  v4f o[NT][D / 16];                    // value dims 64 (t / 4) + 16 g + 4 i + t % 4 in o[][t][i]
+  int full_from, full_to;               // keys that every column sees
+  int any_from, any_to;                 // keys that some column sees
+
+  // Columns of tile rows [row0, row0 + 16 NT) of a sequence's n * group rows.
+  template <typename In>
+  __device__ void open(const Attention& a, int group, int kv_head, int off, int n, int64_t start, int length, int row0) {
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    full_from = 0, full_to = 0x7fffffff, any_from = 0x7fffffff, any_to = 0;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int row = row0 + 16 * t + col;
+      const bool live = row < n * group;
+      const int i = live ? row / group : 0;
+      const int head = kv_head * group + (live ? row - i * group : 0);
+      from[t] = 0, to[t] = 0x7fffffff;
+      int any0 = 0x7fffffff, any1 = 0;
+      if (live) {
+        const int64_t pos = start + i;
+        to[t] = a.causal ? static_cast<int>(max(int64_t{0}, min(pos + 1, static_cast<int64_t>(length)))) : length;
+        if (a.window != 0) from[t] = static_cast<int>(max(int64_t{0}, min(pos + 1 - a.window, int64_t{0x7fffffff})));
+        any0 = from[t], any1 = to[t];
+      }
+      full_from = max(full_from, wave_most(from[t]));
+      full_to = min(full_to, -wave_most(-to[t]));
+      any_from = min(any_from, -wave_most(-any0));
+      any_to = max(any_to, wave_most(any1));
+
+      constexpr int E = D / 4;          // dims of a lane
+      const In* p = static_cast<const In*>(a.q) + (static_cast<int64_t>(off) + i) * a.q_stride +
+                    static_cast<int64_t>(head) * D + g * E;
+      float v[E];
+#pragma unroll
+      for (int j = 0; j < E / 8; ++j) {
+        const uint4 r = live ? reinterpret_cast<const uint4*>(p)[j] : make_uint4(0, 0, 0, 0);
+        float f[8];
+        widen8<In>(r, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[8 * j + e] = f[e];
+      }
+#pragma unroll
+      for (int h = 1; h < E; h <<= 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if ((e & h) == 0) {
+            const float x = v[e], y = v[e + h];
+            v[e] = x + y;
+            v[e + h] = x - y;
+          }
+        }
+      }
+      float top = 0.0f;
+      const float c = RootScale<D>::value * (a.scale * kLog2e);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float other = xor16(v[e]);
+        v[e] = (g & 1) != 0 ? other - v[e] : v[e] + other;
+        other = xor32(v[e]);
+        v[e] = ((g & 2) != 0 ? other - v[e] : v[e] + other) * c;
+        top = fmaxf(top, fabsf(v[e]));
+      }
+      top = fmaxf(top, xor16(top));
+      top = fmaxf(top, xor32(top));
+      // within [2^-4, 2^15) the values go to fp16 as they are
+      float down = 1.0f;
+      qs[t] = 1.0f;
+      if (!(top >= 0x1p-4f && top < 0x1p15f) && top > 0.0f && top < __builtin_inff()) {
+        const int e = max(-120, min(120, ilogbf(top)));
+        down = ldexpf(1.0f, -e);
+        qs[t] = ldexpf(1.0f, e);
+      }
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        constexpr int kOrder[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[t][k][e] = static_cast<_Float16>(v[8 * k + kOrder[e]] * down);
+      }
+      m[t] = -__builtin_inff();
+      l[t] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) o[t][d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  }
+
+  static __device__ int wave_most(int v) {
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) v = max(v, __shfl_xor(v, s));
+    return scalar(v);
+  }
+
+  template <bool MASKED>
+  __device__ void step(const UnitWords<D>& w, int u) {
+    const int g = (threadIdx.x & 63) >> 4;
+    float ks[8], vs[8], lv[8];
+    widen_scales(w.ks, ks);
+    widen_scales(w.vs, vs);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lv[i] = fmaxf(__builtin_amdgcn_logf(vs[i]), kLeastScale);
+
+    v4f s[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v8h key = codes_of(w.k[h][k]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) s[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[t][k], s[t][h], 0, 0, 0);
+      }
+    }
+
+    v8h p[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float x[8], kq[8], most = -__builtin_inff();
+      bool seen[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = s[t][i >> 2][i & 3];
+        kq[i] = ks[i] * qs[t];
+        float r = __builtin_fmaf(x[i], kq[i], lv[i]);
+        if constexpr (MASKED) {
+          const int key = kUnit * u + 8 * g + i;
+          seen[i] = key >= from[t] && key < to[t];
+          r = seen[i] ? r : -__builtin_inff();
+        }
+        most = fmaxf(most, r);
+      }
+      // the reference, kTop below what the largest weight is made of
+      if (__any(most - kTop > m[t] + kRise)) {
+        most = fmaxf(most, xor16(most));
+        most = fmaxf(most, xor32(most));
+        const float wanted = __builtin_ceilf(most) - kTop;
+        if (wanted > m[t] + kRise) {
+          const float f = __builtin_amdgcn_exp2f(m[t] - wanted);        // 0 for the first keys
+          m[t] = wanted;
+          l[t] *= f;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) o[t][d] *= f;
+        }
+      }
+      float wgt[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], kq[i], -m[t]));
+        if constexpr (MASKED) e = seen[i] ? e : 0.0f;
+        l[t] += e;
+        wgt[i] = e * vs[i];
+        if constexpr (MASKED) wgt[i] = seen[i] ? wgt[i] : 0.0f;
+      }
+      v2h pairs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{wgt[i], wgt[i + 4]}), v2h);
+      p[t] = __builtin_bit_cast(v8h, pairs);
+    }
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      const v8h value = codes_of(w.v[d]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[t], o[t][d], 0, 0, 0);
+    }
+  }
+
+  // Units first, first + by, ... below last.
+  __device__ void run(UnitReader<D>& reader, int first, int last, int by) {
+    if (first >= last) return;
+    UnitWords<D> now, next;
+    bool there = reader.load(first, now), there_next = false;
+    for (int u = first; u < last; u += by) {
+      if (u + by < last) there_next = reader.load(u + by, next);
+      if (there) {
+        if (kUnit * u >= full_from && kUnit * u + kUnit <= full_to) step<false>(now, u);
+        else step<true>(now, u);
+      }
+      now = next;
+      there = there_next;
+    }
+  }
+};
+
+// The sums of one column, 16 lanes with E = D / 16 dims each: rotated back, divided
+// and rounded.
+template <int D, typename In, int E = D / 16>
+__device__ inline void finish(float (&v)[E], float l, int part, In* out) {
+#pragma unroll
+  for (int h = 1; h < E; h <<= 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if ((e & h) == 0) {
+        const float x = v[e], y = v[e + h];
+        v[e] = x + y;
+        v[e + h] = x - y;
+      }
+    }
+  }
+  const float by = l != 0.0f ? RootScale<D>::value / l : 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    float x = v[e], other;
+    other = lane_xor<1>(x);
+    x = (part & 1) != 0 ? other - x : x + other;
+    other = lane_xor<2>(x);
+    x = (part & 2) != 0 ? other - x : x + other;
+    other = lane_xor<4>(x);
+    x = (part & 4) != 0 ? other - x : x + other;
+    other = lane_xor<8>(x);
+    x = (part & 8) != 0 ? other - x : x + other;
+    v[e] = l != 0.0f ? x * by : 0.0f;
+  }
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) w[e] = pack2<In>(v[2 * e], v[2 * e + 1]);
+  if constexpr (E == 4) {
+    *reinterpret_cast<uint2*>(out + part * E) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < E / 8; ++j)
+      reinterpret_cast<uint4*>(out + part * E)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  }
+}
+
+// The tile a workgroup has: rows [row0, ...) of sequence b.
+struct Tile {
+  int b, off, n, row0;
+};
+
+// Tile `index` of all sequences' tiles of `rows` rows, a sequence's last first
+// (of a causal prompt the longest): offsets are looked at 64 sequences at a time,
+// one a lane.  Sequences of at most `few` or more than `many` rows have none here.
+__device__ inline bool find_tile(const Attention& a, int group, int rows, int few, int many, int index, Tile& tile) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int b0 = 0; b0 < a.cache.n_seqs; b0 += 64) {
+    const int b = b0 + lane;
+    Span s{0, 0};
+    if (b < a.cache.n_seqs) s = span_of(a.offsets, b, a.M);
+    const int64_t all = static_cast<int64_t>(s.end - s.off) * group;
+    const int mine = all > few && all <= many ? static_cast<int>((all + rows - 1) / rows) : 0;
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int other = __shfl_up(sum, d);
+      if (lane >= d) sum += other;
+    }
+    const int total = __builtin_amdgcn_readlane(sum, 63);
+    if (index - before < total) {
+      const uint64_t behind = __ballot(index - before < sum);
+      const int l = __builtin_ctzll(behind);
+      tile.b = b0 + l;
+      tile.off = __builtin_amdgcn_readlane(s.off, l);
+      tile.n = __builtin_amdgcn_readlane(s.end, l) - tile.off;
+      const int at = index - before - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l));
+      tile.row0 = (__builtin_amdgcn_readlane(mine, l) - 1 - at) * rows;
+      return true;
+    }
+    before += total;
+  }
+  return false;
+}
+
+// SHARED: the four waves have the same columns and every fourth unit each, for
+// few rows; else they have columns of their own and the same units.
+template <int D, int NT, bool SHARED, typename In>
+__global__ __launch_bounds__(kAttnThreads) void attention_kernel(Attention a, int few, int many) {
+  constexpr int kRows = SHARED ? 16 * NT : 16 * NT * kAttnWaves;
+  const int kv_heads = a.cache.kv_heads, group = a.q_heads / kv_heads;
+  const int kv_head = static_cast<int>(blockIdx.x % static_cast<unsigned>(kv_heads));
+  const int part = static_cast<int>(blockIdx.y);
+  Tile tile;
+  if (!find_tile(a, group, kRows, few, many, static_cast<int>(blockIdx.x / static_cast<unsigned>(kv_heads)), tile)) return;
+  const int wave = wave_index(), lane = threadIdx.x & 63;
+  const int64_t start = a.starts[tile.b];
+  const int length = static_cast<int>(max(int64_t{0}, min(start + tile.n, static_cast<int64_t>(a.cache.max_tokens))));
+  Columns<D, NT> c;
+  const int row0 = tile.row0 + (SHARED ? 0 : 16 * NT * wave);
+  const int all = tile.n * group;
+  if (!SHARED && row0 >= all) return;
+
+  c.template open<In>(a, group, kv_head, tile.off, tile.n, start, length, row0);
+  // this part's keys
+  const int lo = max(c.any_from, part * a.chunk);
+  const int hi = part == a.splits - 1 ? c.any_to : min(c.any_to, (part + 1) * a.chunk);
+  const int first = lo / kUnit, last = lo < hi ? (hi + kUnit - 1) / kUnit : 0;
+  UnitReader<D> reader(a.cache, tile.b, kv_head);
+  c.run(reader, first + (SHARED ? wave : 0), last, SHARED ? kAttnWaves : 1);
+
+  const int64_t rows = static_cast<int64_t>(a.M) * a.q_heads;
+  // the row of the output (and of a part's sums) that a column is
+  auto row_of = [&](int row) {
+    const int i = row / group;
+    return (static_cast<int64_t>(tile.off) + i) * a.q_heads + kv_head * group + (row - i * group);
+  };
+  const int col = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    c.l[t] += xor16(c.l[t]);
+    c.l[t] += xor32(c.l[t]);
+  }
+
+  if constexpr (SHARED) {
+    constexpr int kStride = D + 4;
+    __shared__ float sums[kAttnWaves][16][kStride];
+    __shared__ float refs[kAttnWaves][16], totals[kAttnWaves][16];
+    const int mine = threadIdx.x >> 4, piece = threadIdx.x & 15;
+    constexpr int E = D / 16;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (t > 0) __syncthreads();
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(&sums[wave][col][64 * d + 16 * g + 4 * i]) =
+              make_float4(c.o[t][4 * d][i], c.o[t][4 * d + 1][i], c.o[t][4 * d + 2][i], c.o[t][4 * d + 3][i]);
+      if (g == 0) {
+        refs[wave][col] = c.m[t];
+        totals[wave][col] = c.l[t];
+      }
+      __syncthreads();
+      const int row = tile.row0 + 16 * t + mine;
+      float m = refs[0][mine];
+#pragma unroll
+      for (int w = 1; w < kAttnWaves; ++w) m = fmaxf(m, refs[w][mine]);
+      float v[E], l = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) {
+        const float r = refs[w][mine];
+        const float f = r == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(r - m);
+        l = __builtin_fmaf(totals[w][mine], f, l);
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(&sums[w][mine][piece * E + e]);
+          v[e] = __builtin_fmaf(x.x, f, v[e]);
+          v[e + 1] = __builtin_fmaf(x.y, f, v[e + 1]);
+          v[e + 2] = __builtin_fmaf(x.z, f, v[e + 2]);
+          v[e + 3] = __builtin_fmaf(x.w, f, v[e + 3]);
+        }
+      }
+      if (row < all) {
+        if (a.splits == 1) {
+          finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row_of(row) * D);
+        } else {
+          const int64_t at = part * rows + row_of(row);
+          float* to = a.part + at * D + piece * E;
+#pragma unroll
+          for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          if (piece == 0)
+            *reinterpret_cast<float2*>(a.part + a.splits * rows * D + 2 * at) = make_float2(m, l);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int row = row0 + 16 * t + col;
+      // dims 64 d + 16 g + e of this column
+      float v[D / 64][16];
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[d][e] = c.o[t][4 * d + (e & 3)][e >> 2];
+      if (a.splits != 1) {
+        if (row < all) {
+          const int64_t at = part * rows + row_of(row);
+#pragma unroll
+          for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(a.part + at * D + 64 * d + 16 * g + e) =
+                  make_float4(v[d][e], v[d][e + 1], v[d][e + 2], v[d][e + 3]);
+          if (g == 0) *reinterpret_cast<float2*>(a.part + a.splits * rows * D + 2 * at) = make_float2(c.m[t], c.l[t]);
+        }
+        continue;
+      }
+      const float by = c.l[t] != 0.0f ? RootScale<D>::value / c.l[t] : 0.0f;
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d) {
+#pragma unroll
+        for (int h = 1; h < 16; h <<= 1) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if ((e & h) == 0) {
+              const float x = v[d][e], y = v[d][e + h];
+              v[d][e] = x + y;
+              v[d][e + h] = x - y;
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float other = xor16(v[d][e]);
+          v[d][e] = (g & 1) != 0 ? other - v[d][e] : v[d][e] + other;
+          other = xor32(v[d][e]);
+          v[d][e] = (g & 2) != 0 ? other - v[d][e] : v[d][e] + other;
+        }
+      }
+#pragma unroll
+      for (int h = 1; h < D / 64; h <<= 1) {
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d) {
+          if ((d & h) == 0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x = v[d][e], y = v[d + h][e];
+              v[d][e] = x + y;
+              v[d + h][e] = x - y;
+            }
+          }
+        }
+      }
+      if (row < all) {
+        In* out = static_cast<In*>(a.out) + row_of(row) * D;
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = c.l[t] != 0.0f ? v[d][8 * j + e] * by : 0.0f;
+            *reinterpret_cast<uint4*>(out + 64 * d + 16 * g + 8 * j) = narrow8<In>(f);
+          }
+        }
+      }
+    }
+  }
+}
+
+// The parts of a row joined: 16 lanes a row.  Those whose keys the row does not
+// see at all may not have been written, and are not read.
+template <int D, typename In>
+__global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
+  constexpr int E = D / 16;
+  const int64_t rows = static_cast<int64_t>(a.M) * a.q_heads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kAttnThreads / 16) + (threadIdx.x >> 4);
+  const int piece = threadIdx.x & 15;
+  if (row >= rows) return;
+  const int token = static_cast<int>(row / a.q_heads);
+  const int b = sequence_of(a.offsets, a.cache.n_seqs, token);
+  if (b >= a.cache.n_seqs) return;
+  const Span s = span_of(a.offsets, b, a.M);
+  if (token < s.off || token >= s.end) return;
+  const int64_t start = a.starts[b], pos = start + token - s.off;
+  const int length = static_cast<int>(max(int64_t{0}, min(start + s.end - s.off, static_cast<int64_t>(a.cache.max_tokens))));
+  const int to = a.causal ? static_cast<int>(max(int64_t{0}, min(pos + 1, static_cast<int64_t>(length)))) : length;
+  const int from = a.window != 0 ? static_cast<int>(max(int64_t{0}, min(pos + 1 - a.window, int64_t{0x7fffffff}))) : 0;
+  float v[E], l = 0.0f, m = -__builtin_inff();
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.0f;
+  if (from < to) {
+    const int p0 = min(from / a.chunk, a.splits - 1), p1 = min((to - 1) / a.chunk, a.splits - 1);
+    const float2* heads = reinterpret_cast<const float2*>(a.part + a.splits * rows * D);
+    for (int p = p0; p <= p1; ++p) m = fmaxf(m, heads[p * rows + row].x);
+    for (int p = p0; p <= p1; ++p) {
+      const float2 h = heads[p * rows + row];
+      const float f = h.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(h.x - m);
+      l = __builtin_fmaf(h.y, f, l);
+      const float* x = a.part + (p * rows + row) * D + piece * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(x + e);
+        v[e] = __builtin_fmaf(y.x, f, v[e]);
+        v[e + 1] = __builtin_fmaf(y.y, f, v[e + 1]);
+        v[e + 2] = __builtin_fmaf(y.z, f, v[e + 2]);
+        v[e + 3] = __builtin_fmaf(y.w, f, v[e + 3]);
+      }
+    }
+  }
+  finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row * D);
+}
+
+// Sequences of at most this many rows (tokens times query heads a key head) take
+// the kernel whose waves share their columns.
+constexpr int kFewRows = 32;
+
+int64_t tiles_bound(int64_t M, int64_t group, int64_t n_seqs, int64_t rows) {
+  // one for every sequence that has rows, and one for every full tile
+  return std::min(M * group / rows + std::min(n_seqs, M), M * ((group + rows - 1) / rows));
+}
+
+template <int D, int NT, bool SHARED, typename In>
+hipError_t launch_tiles(const Attention& a, int few, int many, hipStream_t stream) {
+  constexpr int kRows = SHARED ? 16 * NT : 16 * NT * kAttnWaves;
+  const int64_t tiles = tiles_bound(a.M, a.q_heads / a.cache.kv_heads, a.cache.n_seqs, kRows);
+  const int64_t grid = tiles * a.cache.kv_heads;
+  if (grid * kAttnThreads * a.splits >= (int64_t{1} << 32)) return hipErrorInvalidConfiguration;
+  attention_kernel<D, NT, SHARED, In><<<dim3(static_cast<unsigned>(grid), static_cast<unsigned>(a.splits)),
+                                        dim3(kAttnThreads), 0, stream>>>(a, few, many);
+  return hipGetLastError();
+}
+
+template <int D, typename In>
+hipError_t launch_heads(const Attention& a, hipStream_t stream) {
+  constexpr int kAll = 0x7fffffff;
+  constexpr int kWide = D == 256 ? 2 : 4;
+  const int64_t rows = static_cast<int64_t>(a.M) * (a.q_heads / a.cache.kv_heads);
+  const int64_t mean = rows / a.cache.n_seqs;
+  hipError_t e;
+  if (mean <= 16) e = launch_tiles<D, 1, true, In>(a, 0, kAll, stream);
+  else if (mean <= kFewRows) e = launch_tiles<D, 2, true, In>(a, 0, kAll, stream);
+  else {
+    const int few = a.cache.n_seqs > 1 ? kFewRows : 0;
+    e = few != 0 ? launch_tiles<D, 1, true, In>(a, 0, few, stream) : hipSuccess;
+    if (e == hipSuccess) e = launch_tiles<D, kWide, false, In>(a, few, kAll, stream);
+  }
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t out_rows = static_cast<int64_t>(a.M) * a.q_heads;
+  const int64_t grid = (out_rows + kAttnThreads / 16 - 1) / (kAttnThreads / 16);
+  if (grid * kAttnThreads >= (int64_t{1} << 32)) return hipErrorInvalidConfiguration;
+  join_kernel<D, In><<<dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <typename In>
+hipError_t launch_type(const Attention& a, hipStream_t stream) {
+  if (a.cache.head_dim == 64) return launch_heads<64, In>(a, stream);
+  if (a.cache.head_dim == 128) return launch_heads<128, In>(a, stream);
+  return launch_heads<256, In>(a, stream);
+}
+
+}  // namespace
+
+AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t n_seqs,
+                                   int64_t max_tokens) {
+  const int64_t group = q_heads / kv_heads, rows = M * group, mean = rows / n_seqs;
+  const bool shared = mean <= kFewRows;
+  const int64_t tile = shared ? (mean <= 16 ? 16 : 32) : (head_dim == 256 ? 128 : 256);
+  const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
+  const int64_t wanted = shared ? 2048 : 512;
+  const int64_t least = shared ? 4 * kUnit : 16 * kUnit;         // keys of a part
+  int64_t splits = std::max<int64_t>(1, std::min((wanted + work - 1) / work, max_tokens / least));
+  splits = std::min<int64_t>(splits, 64);
+  AttentionPlan p;
+  p.chunk = static_cast<int>(((max_tokens + splits - 1) / splits + least - 1) / least * least);
+  p.splits = static_cast<int>((max_tokens + p.chunk - 1) / p.chunk);
+  p.workspace = p.splits == 1 ? 0 : static_cast<size_t>(p.splits) * static_cast<size_t>(M * q_heads) * (head_dim + 2) * 4;
+  return p;
+}
+
+hipError_t launch_cache_attention(const Attention& a, bool f16, hipStream_t stream) {
+  return f16 ? launch_type<_Float16>(a, stream) : launch_type<uint16_t>(a, stream);
+}
+
+}  // namespace convrot

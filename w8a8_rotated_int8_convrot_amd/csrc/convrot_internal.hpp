@@ -5,9 +5,11 @@
 // launched by gemm_i8.hip, per expert by gemm_grouped.hip and with low-rank
 // adapters by gemm_lora.hip, lora.hip (the adapters' first product),
 // default_path.hip (the guarded layer's check), block_norm.hip (the step
-// between two blocks) and mfma_probe.hip (two measurement aids); argument
-// checking, dispatch and the guard state live in convrot_api.hip, the entry
-// points of the operators around the layer in operators_api.hip.
+// between two blocks), rope.hip, kv_cache.hip and cache_attention.hip (rotary
+// positions, the 4-bit cache and the attention over it) and mfma_probe.hip (two
+// measurement aids); argument checking, dispatch and the guard state live in
+// convrot_api.hip, the entry points of the operators around the layer in
+// operators_api.hip and those between two layers in cache_api.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -201,6 +203,71 @@ struct BlockNorm {
 };
 // group: 128 or 256 for codes, 0 for 16-bit values.
 hipError_t launch_block_norm(const BlockNorm& p, int group, bool f16, hipStream_t stream);
+
+// ---------------------------------------------------------------- between two layers
+// (rope.hip, kv_cache.hip, cache_attention.hip)
+
+// One tensor of heads: rows of `heads` vectors, `stride` elements apart.
+struct RopePart {
+  const void* in;
+  void* out;
+  int64_t heads, in_stride, out_stride;
+};
+// Arguments as in convrot_rope; a part without heads is left out.
+struct Rope {
+  RopePart part[2];
+  int64_t M;
+  int head_dim, rot_dim;
+  bool interleaved, inverse;
+  const int32_t* positions;
+  const double* freqs;
+  float scale;
+};
+hipError_t launch_rope(const Rope& p, bool f16, hipStream_t stream);
+
+// convrot_cache by value, with the sizes the kernels need.
+struct Cache {
+  uint8_t* pages;
+  int64_t n_pages, page_bytes;
+  int page_shift, kv_heads, head_dim;
+  const int32_t* table;
+  int64_t table_stride;
+  int n_seqs;
+  int max_tokens;                       // columns of the table times the page
+};
+// Rows of keys and values to or from the cache, [M, kv_heads, head_dim], rows
+// k_stride and v_stride elements apart; starts [n_seqs], offsets [n_seqs + 1].
+hipError_t launch_cache_append(const Cache& c, const void* k, int64_t k_stride, const void* v, int64_t v_stride, bool f16,
+                               int64_t M, const int32_t* starts, const int32_t* offsets, hipStream_t stream);
+hipError_t launch_cache_read(const Cache& c, void* k, int64_t k_stride, void* v, int64_t v_stride, bool f16, int64_t M,
+                             const int32_t* starts, const int32_t* offsets, hipStream_t stream);
+
+// Pages src[i] -> dst[i] in each of `layers` caches, layer_bytes apart (host lists).
+hipError_t launch_cache_copy(uint8_t* pages, int64_t layers, int64_t layer_bytes, int64_t page_bytes, const int32_t* src,
+                             const int32_t* dst, int64_t n, hipStream_t stream);
+
+// How convrot_cache_attention cuts its work, from sizes the host knows: the keys
+// of a sequence in `splits` parts of `chunk` (the last takes the rest).
+struct AttentionPlan {
+  int splits, chunk;
+  size_t workspace;                     // bytes
+};
+AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t n_seqs,
+                                   int64_t max_tokens);
+struct Attention {
+  Cache cache;
+  const void* q;
+  int64_t q_stride;
+  int M, q_heads;
+  const int32_t *starts, *offsets;
+  float scale;
+  bool causal;
+  int window;                           // 0: none
+  void* out;                            // [M, q_heads, head_dim]
+  int splits, chunk;
+  float* part;                          // workspace: [splits][M * q_heads][head_dim], then [splits][M * q_heads][2]
+};
+hipError_t launch_cache_attention(const Attention& a, bool f16, hipStream_t stream);
 
 // ---------------------------------------------------------------- measurement aid
 

@@ -1,7 +1,8 @@
 // rotate_device.hpp -- device code shared by the kernels that rotate rows held
-// in registers (rotate_quant.hip, block_norm.hip): 16-bit loads widened to
-// fp32, the butterfly of one 8-element chunk of a g-group spread over g/8
-// lanes, and the int8 code of a value.
+// in registers (rotate_quant.hip, block_norm.hip, and those of the cache of
+// heads): 16-bit loads widened to fp32, two fp32 values rounded to 16 bits, the
+// butterfly of one 8-element chunk of a g-group spread over g/8 lanes, and the
+// int8 code of a value.
 #pragma once
 
 #include "convrot_internal.hpp"
@@ -50,6 +51,35 @@ __device__ inline void load8(const float* p, float (&v)[8]) {
   const float4 b = *reinterpret_cast<const float4*>(p + 4);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+
+// two fp32 values rounded to nearest even and packed
+template <typename In> __device__ inline uint32_t pack2(float a, float b);
+template <> __device__ inline uint32_t pack2<uint16_t>(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2bf));
+}
+template <> __device__ inline uint32_t pack2<_Float16>(float a, float b) {
+  // keep the fp32 results: a multiply-add fused with its conversion would
+  // round the exact value to fp16 once
+  asm volatile("" : "+v"(a), "+v"(b));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2h));
+}
+
+template <typename In>
+__device__ inline void widen8(const uint4& w, float (&v)[8]) {
+  v[0] = in_lo<In>(w.x); v[1] = in_hi<In>(w.x);
+  v[2] = in_lo<In>(w.y); v[3] = in_hi<In>(w.y);
+  v[4] = in_lo<In>(w.z); v[5] = in_hi<In>(w.z);
+  v[6] = in_lo<In>(w.w); v[7] = in_hi<In>(w.w);
+}
+
+template <typename In>
+__device__ inline uint4 narrow8(const float (&v)[8]) {
+  return make_uint4(pack2<In>(v[0], v[1]), pack2<In>(v[2], v[3]), pack2<In>(v[4], v[5]), pack2<In>(v[6], v[7]));
 }
 
 // v of lane (this lane ^ T).  Inside a 16-lane row DPP moves do it: xor 1
