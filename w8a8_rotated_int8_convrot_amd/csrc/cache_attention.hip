@@ -37,6 +37,7 @@ namespace {
 
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * 64;
@@ -47,6 +48,8 @@ constexpr float kRise = 6.0f;
 // Value scales below 2^-60 count as that in the reference: the sum l, which has
 // no such factor, then stays below 2^(60 + 14) a key.
 constexpr float kLeastScale = -60.0f;
+// Before the first key: below every score, and finite.
+constexpr float kNoReference = -0x1p120f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int D> struct RootScale;      // 1 / sqrt(D)
@@ -147,8 +150,9 @@ struct UnitReader {
 // 16 NT query columns of a wave: their queries, bounds and running sums.
 template <int D, int NT>
 struct Columns {
-  v8h q[NT][D / 32];
-  float qs[NT];                         // power of two a column's queries were divided by
+  v4i hi[NT][D / 64], lo[NT][D / 64];   // the queries as 256 hi + lo
+  int eight[NT];                        // -8 times a column's sum of them: codes are held as c + 8
+  float qs[NT];                         // what one step of them stands for, with scale and log2(e)
   int from[NT], to[NT];                 // visible keys of a column
   float m[NT], l[NT];                   // reference; sum of this lane's keys
   v4f o[NT][D / 16];                    // value dims 64 (t / 4) + 16 g + 4 i + t % 4 in o[][t][i]
@@ -203,32 +207,44 @@ struct Columns {
         }
       }
       float top = 0.0f;
-      const float c = RootScale<D>::value * (a.scale * kLog2e);
+      bool finite = true;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         float other = xor16(v[e]);
         v[e] = (g & 1) != 0 ? other - v[e] : v[e] + other;
         other = xor32(v[e]);
-        v[e] = ((g & 2) != 0 ? other - v[e] : v[e] + other) * c;
+        v[e] = (g & 2) != 0 ? other - v[e] : v[e] + other;
         top = fmaxf(top, fabsf(v[e]));
+        finite = finite && fabsf(v[e]) < __builtin_inff();
       }
       top = fmaxf(top, xor16(top));
       top = fmaxf(top, xor32(top));
-      // within [2^-4, 2^15) the values go to fp16 as they are
-      float down = 1.0f;
-      qs[t] = 1.0f;
-      if (!(top >= 0x1p-4f && top < 0x1p15f) && top > 0.0f && top < __builtin_inff()) {
-        const int e = max(-120, min(120, ilogbf(top)));
-        down = ldexpf(1.0f, -e);
-        qs[t] = ldexpf(1.0f, e);
-      }
+      // steps of top / 32512, so that both digits fit; a row that is not finite is so in
+      // all its sums, and its scores are NaN by their factor
+      const float least = fmaxf(top, 0x1p-100f), inverse = finite ? 1.0f / least : 0.0f;
+      qs[t] = finite ? least * (RootScale<D>::value * kLog2e / 32512.0f) * a.scale : __builtin_nanf("");
+      int sum = 0;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        constexpr int kOrder[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+      for (int k = 0; k < D / 64; ++k) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[t][k][e] = static_cast<_Float16>(v[8 * k + kOrder[e]] * down);
+        for (int r = 0; r < 4; ++r) {
+          uint32_t h = 0, l8 = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = finite ? v[16 * k + 8 * (r >> 1) + 2 * e + (r & 1)] * inverse : 0.0f;
+            const int c = static_cast<int>(__builtin_rintf(x * 32512.0f)), high = (c + 128) >> 8;
+            sum += c;
+            h |= static_cast<uint32_t>(high & 0xff) << (8 * e);
+            l8 |= static_cast<uint32_t>(c & 0xff) << (8 * e);
+          }
+          hi[t][k][r] = static_cast<int>(h);
+          lo[t][k][r] = static_cast<int>(l8);
+        }
       }
-      m[t] = -__builtin_inff();
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      eight[t] = -8 * sum;
+      m[t] = kNoReference;
       l[t] = 0.0f;
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) o[t][d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -241,47 +257,51 @@ struct Columns {
     return scalar(v);
   }
 
-  template <bool MASKED>
-  __device__ void step(const UnitWords<D>& w, int u) {
+  // One unit; `masked` where some column does not see all of it.
+  __device__ __forceinline__ void step(const UnitWords<D>& w, int u, bool masked) {
     const int g = (threadIdx.x & 63) >> 4;
     float ks[8], vs[8], lv[8];
     widen_scales(w.ks, ks);
     widen_scales(w.vs, vs);
 #pragma unroll
     for (int i = 0; i < 8; ++i) lv[i] = fmaxf(__builtin_amdgcn_logf(vs[i]), kLeastScale);
-
-    v4f s[NT][2];
+    v4i key[2][D / 64];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v8h key = codes_of(w.k[h][k]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) s[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[t][k], s[t][h], 0, 0, 0);
+      for (int k = 0; k < D / 64; ++k) {
+        const uint32_t w0 = w.k[h][2 * k], w1 = w.k[h][2 * k + 1];
+        key[h][k] = v4i{static_cast<int>(w0 & 0x0f0f0f0fu), static_cast<int>(w0 >> 4 & 0x0f0f0f0fu),
+                        static_cast<int>(w1 & 0x0f0f0f0fu), static_cast<int>(w1 >> 4 & 0x0f0f0f0fu)};
       }
-    }
-
     v8h p[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float x[8], kq[8], most = -__builtin_inff();
-      bool seen[8];
+      float x[8], kq[8], r[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v4i high = {0, 0, 0, 0}, low = {eight[t], eight[t], eight[t], eight[t]};
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          high = __builtin_amdgcn_mfma_i32_16x16x64_i8(key[h][k], hi[t][k], high, 0, 0, 0);
+          low = __builtin_amdgcn_mfma_i32_16x16x64_i8(key[h][k], lo[t][k], low, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * h + i] = static_cast<float>((high[i] << 8) + low[i]);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[i] = s[t][i >> 2][i & 3];
         kq[i] = ks[i] * qs[t];
-        float r = __builtin_fmaf(x[i], kq[i], lv[i]);
-        if constexpr (MASKED) {
-          const int key = kUnit * u + 8 * g + i;
-          seen[i] = key >= from[t] && key < to[t];
-          r = seen[i] ? r : -__builtin_inff();
-        }
-        most = fmaxf(most, r);
+        r[i] = __builtin_fmaf(x[i], kq[i], lv[i]);
       }
+      const int first = kUnit * u + 8 * g;
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = first + i >= from[t] && first + i < to[t] ? r[i] : -__builtin_inff();
+      }
+      float most = fmaxf(fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3])), fmaxf(fmaxf(r[4], r[5]), fmaxf(r[6], r[7])));
       // the reference, kTop below what the largest weight is made of
-      if (__any(most - kTop > m[t] + kRise)) {
+      if (__any(most > m[t] + (kTop + kRise))) {
         most = fmaxf(most, xor16(most));
         most = fmaxf(most, xor32(most));
         const float wanted = __builtin_ceilf(most) - kTop;
@@ -293,15 +313,22 @@ struct Columns {
           for (int d = 0; d < D / 16; ++d) o[t][d] *= f;
         }
       }
-      float wgt[8];
+      float e[8], wgt[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], kq[i], -m[t]));
-        if constexpr (MASKED) e = seen[i] ? e : 0.0f;
-        l[t] += e;
-        wgt[i] = e * vs[i];
-        if constexpr (MASKED) wgt[i] = seen[i] ? wgt[i] : 0.0f;
+        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], kq[i], -m[t]));
+        wgt[i] = e[i] * vs[i];
       }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool seen = first + i >= from[t] && first + i < to[t];
+          e[i] = seen ? e[i] : 0.0f;
+          wgt[i] = seen ? wgt[i] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) l[t] += e[i];
       v2h pairs[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{wgt[i], wgt[i + 4]}), v2h);
@@ -323,8 +350,7 @@ struct Columns {
     for (int u = first; u < last; u += by) {
       if (u + by < last) there_next = reader.load(u + by, next);
       if (there) {
-        if (kUnit * u >= full_from && kUnit * u + kUnit <= full_to) step<false>(now, u);
-        else step<true>(now, u);
+        step(now, u, kUnit * u < full_from || kUnit * u + kUnit > full_to);
       }
       now = next;
       there = there_next;
@@ -412,10 +438,11 @@ __device__ inline bool find_tile(const Attention& a, int group, int rows, int fe
   return false;
 }
 
+constexpr int WPE(int d, int nt, bool shared) { return d * nt <= 64 ? 4 : d * nt <= 128 ? 3 : d * nt <= 256 ? 2 : 1; }
 // SHARED: the four waves have the same columns and every fourth unit each, for
 // few rows; else they have columns of their own and the same units.
 template <int D, int NT, bool SHARED, typename In>
-__global__ __launch_bounds__(kAttnThreads) void attention_kernel(Attention a, int few, int many) {
+__global__ __launch_bounds__(kAttnThreads, WPE(D, NT, SHARED)) void attention_kernel(Attention a, int few, int many) {
   constexpr int kRows = SHARED ? 16 * NT : 16 * NT * kAttnWaves;
   const int kv_heads = a.cache.kv_heads, group = a.q_heads / kv_heads;
   const int kv_head = static_cast<int>(blockIdx.x % static_cast<unsigned>(kv_heads));
@@ -481,7 +508,7 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(Attention a, in
 #pragma unroll
       for (int w = 0; w < kAttnWaves; ++w) {
         const float r = refs[w][mine];
-        const float f = r == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(r - m);
+        const float f = __builtin_amdgcn_exp2f(r - m);
         l = __builtin_fmaf(totals[w][mine], f, l);
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
@@ -599,7 +626,7 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
   const int length = static_cast<int>(max(int64_t{0}, min(start + s.end - s.off, static_cast<int64_t>(a.cache.max_tokens))));
   const int to = a.causal ? static_cast<int>(max(int64_t{0}, min(pos + 1, static_cast<int64_t>(length)))) : length;
   const int from = a.window != 0 ? static_cast<int>(max(int64_t{0}, min(pos + 1 - a.window, int64_t{0x7fffffff}))) : 0;
-  float v[E], l = 0.0f, m = -__builtin_inff();
+  float v[E], l = 0.0f, m = kNoReference;
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.0f;
   if (from < to) {
@@ -608,7 +635,7 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
     for (int p = p0; p <= p1; ++p) m = fmaxf(m, heads[p * rows + row].x);
     for (int p = p0; p <= p1; ++p) {
       const float2 h = heads[p * rows + row];
-      const float f = h.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(h.x - m);
+      const float f = __builtin_amdgcn_exp2f(h.x - m);
       l = __builtin_fmaf(h.y, f, l);
       const float* x = a.part + (p * rows + row) * D + piece * E;
 #pragma unroll
@@ -647,7 +674,7 @@ hipError_t launch_tiles(const Attention& a, int few, int many, hipStream_t strea
 template <int D, typename In>
 hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   constexpr int kAll = 0x7fffffff;
-  constexpr int kWide = D == 256 ? 2 : 4;
+  constexpr int kWide = D == 256 ? 1 : D == 128 ? 2 : 4;
   const int64_t rows = static_cast<int64_t>(a.M) * (a.q_heads / a.cache.kv_heads);
   const int64_t mean = rows / a.cache.n_seqs;
   hipError_t e;
@@ -679,7 +706,7 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
                                    int64_t max_tokens) {
   const int64_t group = q_heads / kv_heads, rows = M * group, mean = rows / n_seqs;
   const bool shared = mean <= kFewRows;
-  const int64_t tile = shared ? (mean <= 16 ? 16 : 32) : (head_dim == 256 ? 128 : 256);
+  const int64_t tile = shared ? (mean <= 16 ? 16 : 32) : (head_dim == 256 ? 64 : head_dim == 128 ? 128 : 256);
   const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
   const int64_t wanted = shared ? 2048 : 512;
   const int64_t least = shared ? 4 * kUnit : 16 * kUnit;         // keys of a part
