@@ -50,5 +50,22 @@ __device__ inline int sequence_of(const int32_t* offsets, int n_seqs, int i) {
   return lo;
 }
 
+// The same for one row of the whole wave: 64 sequences' ends looked at in one
+// latency, so three of them find one of 2^18 sequences.
+__device__ inline int sequence_of_wave(const int32_t* offsets, int n_seqs, int i) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = n_seqs;
+  while (lo < hi) {
+    const int step = (hi - lo + 63) >> 6;
+    const int at = lo + (lane + 1) * step - 1;
+    const uint64_t behind = __ballot(at >= hi || offsets[at + 1] > i);
+    if (behind == 0) return hi;
+    const int l = __builtin_ctzll(behind);
+    hi = min(hi, lo + (l + 1) * step - 1);
+    lo += l * step;
+  }
+  return lo;
+}
+
 }  // namespace
 }  // namespace convrot

@@ -45,6 +45,8 @@ constexpr int kAttnThreads = kAttnWaves * 64;
 // enough below fp16's 2^16, and one that is 2^-22 of it still has all its bits.
 constexpr float kTop = 8.0f;
 constexpr float kRise = 6.0f;
+// A key that a column does not see; no score is as low.
+constexpr float kHidden = -0x1.fffffep127f;
 // Value scales below 2^-60 count as that in the reference: the sum l, which has
 // no such factor, then stays below 2^(60 + 14) a key.
 constexpr float kLeastScale = -60.0f;
@@ -61,16 +63,25 @@ __device__ inline float xor16(float v) { return __shfl_xor(v, 16); }
 __device__ inline float xor32(float v) { return __shfl_xor(v, 32); }
 
 __device__ inline int wave_index() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
-__device__ inline int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The constants of a word's way to fp16, the exponents in a vector register and
+// the masks in scalar ones: one instruction then takes both.
+struct Spread {
+  uint32_t exponent, low, high;
+  __device__ Spread() : exponent(0x64006400u), low(0x000f000fu), high(0x00f000f0u) {
+    asm volatile("" : "+v"(exponent));
+    asm volatile("" : "+s"(low), "+s"(high));
+  }
+};
 
 // Eight codes of a word as fp16, in the order of its nibbles 0 4 1 5 2 6 3 7.
-__device__ inline v8h codes_of(uint32_t w) {
+__device__ inline v8h codes_of(uint32_t w, const Spread& c) {
   const v2h off = {static_cast<_Float16>(-1032), static_cast<_Float16>(-1032)};
   const v2h sixteenth = {static_cast<_Float16>(0.0625f), static_cast<_Float16>(0.0625f)};
   const v2h off16 = {static_cast<_Float16>(-72), static_cast<_Float16>(-72)};
-  auto low = [&](uint32_t x) { return __builtin_bit_cast(v2h, (x & 0x000f000fu) | 0x64006400u) + off; };
+  auto low = [&](uint32_t x) { return __builtin_bit_cast(v2h, (x & c.low) | c.exponent) + off; };
   auto high = [&](uint32_t x) {
-    return __builtin_elementwise_fma(__builtin_bit_cast(v2h, (x & 0x00f000f0u) | 0x64006400u), sixteenth, off16);
+    return __builtin_elementwise_fma(__builtin_bit_cast(v2h, (x & c.high) | c.exponent), sixteenth, off16);
   };
   const uint32_t w8 = w >> 8;
   const v2h p[4] = {low(w), high(w), low(w8), high(w8)};
@@ -152,7 +163,7 @@ template <int D, int NT>
 struct Columns {
   v4i hi[NT][D / 64], lo[NT][D / 64];   // the queries as 256 hi + lo
   int eight[NT];                        // -8 times a column's sum of them: codes are held as c + 8
-  float qs[NT];                         // what one step of them stands for, with scale and log2(e)
+  float qs[NT];                         // what one step of them stands for, with |scale| and log2(e)
   int from[NT], to[NT];                 // visible keys of a column
   float m[NT], l[NT];                   // reference; sum of this lane's keys
   v4f o[NT][D / 16];                    // value dims 64 (t / 4) + 16 g + 4 i + t % 4 in o[][t][i]
@@ -163,25 +174,23 @@ struct Columns {
   template <typename In>
   __device__ void open(const Attention& a, int group, int kv_head, int off, int n, int64_t start, int length, int row0) {
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-    full_from = 0, full_to = 0x7fffffff, any_from = 0x7fffffff, any_to = 0;
+    // bounds grow from token to token
+    auto bounds = [&](int i, int& first, int& end) {
+      const int64_t pos = start + i;
+      end = a.causal ? static_cast<int>(max(int64_t{0}, min(pos + 1, static_cast<int64_t>(length)))) : length;
+      first = a.window != 0 ? static_cast<int>(max(int64_t{0}, min(pos + 1 - a.window, int64_t{0x7fffffff}))) : 0;
+    };
+    const int all = n * group;
+    bounds(row0 / group, any_from, full_to);
+    bounds((min(row0 + 16 * NT, all) - 1) / group, full_from, any_to);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int row = row0 + 16 * t + col;
-      const bool live = row < n * group;
+      const bool live = row < all;
       const int i = live ? row / group : 0;
       const int head = kv_head * group + (live ? row - i * group : 0);
       from[t] = 0, to[t] = 0x7fffffff;
-      int any0 = 0x7fffffff, any1 = 0;
-      if (live) {
-        const int64_t pos = start + i;
-        to[t] = a.causal ? static_cast<int>(max(int64_t{0}, min(pos + 1, static_cast<int64_t>(length)))) : length;
-        if (a.window != 0) from[t] = static_cast<int>(max(int64_t{0}, min(pos + 1 - a.window, int64_t{0x7fffffff})));
-        any0 = from[t], any1 = to[t];
-      }
-      full_from = max(full_from, wave_most(from[t]));
-      full_to = min(full_to, -wave_most(-to[t]));
-      any_from = min(any_from, -wave_most(-any0));
-      any_to = max(any_to, wave_most(any1));
+      if (live) bounds(i, from[t], to[t]);
 
       constexpr int E = D / 4;          // dims of a lane
       const In* p = static_cast<const In*>(a.q) + (static_cast<int64_t>(off) + i) * a.q_stride +
@@ -222,7 +231,8 @@ struct Columns {
       // steps of top / 32512, so that both digits fit; a row that is not finite is so in
       // all its sums, and its scores are NaN by their factor
       const float least = fmaxf(top, 0x1p-100f), inverse = finite ? 1.0f / least : 0.0f;
-      qs[t] = finite ? least * (RootScale<D>::value * kLog2e / 32512.0f) * a.scale : __builtin_nanf("");
+      qs[t] = finite ? least * (RootScale<D>::value * kLog2e / 32512.0f) * fabsf(a.scale) : __builtin_nanf("");
+      const float signed_steps = a.scale < 0.0f ? -32512.0f : 32512.0f;
       int sum = 0;
 #pragma unroll
       for (int k = 0; k < D / 64; ++k) {
@@ -232,7 +242,7 @@ struct Columns {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float x = finite ? v[16 * k + 8 * (r >> 1) + 2 * e + (r & 1)] * inverse : 0.0f;
-            const int c = static_cast<int>(__builtin_rintf(x * 32512.0f)), high = (c + 128) >> 8;
+            const int c = static_cast<int>(__builtin_rintf(x * signed_steps)), high = (c + 128) >> 8;
             sum += c;
             h |= static_cast<uint32_t>(high & 0xff) << (8 * e);
             l8 |= static_cast<uint32_t>(c & 0xff) << (8 * e);
@@ -251,20 +261,13 @@ struct Columns {
     }
   }
 
-  static __device__ int wave_most(int v) {
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) v = max(v, __shfl_xor(v, s));
-    return scalar(v);
-  }
-
   // One unit; `masked` where some column does not see all of it.
-  __device__ __forceinline__ void step(const UnitWords<D>& w, int u, bool masked) {
+  __device__ __forceinline__ void step(const UnitWords<D>& w, const Spread& spread, int u, bool masked) {
     const int g = (threadIdx.x & 63) >> 4;
-    float ks[8], vs[8], lv[8];
+    float ks[8], vs[8];
     widen_scales(w.ks, ks);
     widen_scales(w.vs, vs);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) lv[i] = fmaxf(__builtin_amdgcn_logf(vs[i]), kLeastScale);
+    const float large = log_scale(vs);
     v4i key[2][D / 64];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -277,7 +280,7 @@ struct Columns {
     v8h p[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float x[8], kq[8], r[8];
+      float y[8], v[8], by = large;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         v4i high = {0, 0, 0, 0}, low = {eight[t], eight[t], eight[t], eight[t]};
@@ -287,20 +290,23 @@ struct Columns {
           low = __builtin_amdgcn_mfma_i32_16x16x64_i8(key[h][k], lo[t][k], low, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[4 * h + i] = static_cast<float>((high[i] << 8) + low[i]);
+        for (int i = 0; i < 4; ++i) y[4 * h + i] = static_cast<float>((high[i] << 8) + low[i]) * ks[4 * h + i];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        kq[i] = ks[i] * qs[t];
-        r[i] = __builtin_fmaf(x[i], kq[i], lv[i]);
-      }
-      const int first = kUnit * u + 8 * g;
+      for (int i = 0; i < 8; ++i) v[i] = vs[i];
       if (masked) {
+        const int first = kUnit * u + 8 * g;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = first + i >= from[t] && first + i < to[t] ? r[i] : -__builtin_inff();
+        for (int i = 0; i < 8; ++i) {
+          const bool seen = first + i >= from[t] && first + i < to[t];
+          y[i] = seen ? y[i] : kHidden;
+          v[i] = seen ? v[i] : 0.0f;
+        }
+        by = log_scale(v);
       }
-      float most = fmaxf(fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3])), fmaxf(fmaxf(r[4], r[5]), fmaxf(r[6], r[7])));
-      // the reference, kTop below what the largest weight is made of
+      float most = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+      most = __builtin_fmaf(most, qs[t], by);
+      // the reference, kTop below what the largest weight may be made of
       if (__any(most > m[t] + (kTop + kRise))) {
         most = fmaxf(most, xor16(most));
         most = fmaxf(most, xor32(most));
@@ -313,47 +319,52 @@ struct Columns {
           for (int d = 0; d < D / 16; ++d) o[t][d] *= f;
         }
       }
-      float e[8], wgt[8];
+      float e[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], kq[i], -m[t]));
-        wgt[i] = e[i] * vs[i];
-      }
+      for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[i], qs[t], -m[t]));
       if (masked) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool seen = first + i >= from[t] && first + i < to[t];
-          e[i] = seen ? e[i] : 0.0f;
-          wgt[i] = seen ? wgt[i] : 0.0f;
-        }
+        for (int i = 0; i < 8; ++i) e[i] = y[i] == kHidden ? 0.0f : e[i];
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) l[t] += e[i];
       v2h pairs[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{wgt[i], wgt[i + 4]}), v2h);
+      for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{e[i] * v[i], e[i + 4] * v[i + 4]}), v2h);
       p[t] = __builtin_bit_cast(v8h, pairs);
     }
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
-      const v8h value = codes_of(w.v[d]);
+      const v8h value = codes_of(w.v[d], spread);
 #pragma unroll
       for (int t = 0; t < NT; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[t], o[t][d], 0, 0, 0);
     }
   }
 
-  // Units first, first + by, ... below last.
-  __device__ void run(UnitReader<D>& reader, int first, int last, int by) {
+  // log2 of the largest of a lane's value scales (of a NaN and a number, of the number).
+  static __device__ float log_scale(const float (&v)[8]) {
+    const float most = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+    return fmaxf(__builtin_amdgcn_logf(most), kLeastScale);
+  }
+
+  // Units first, first + by, ... below last, each loaded while the one before is worked on.
+  __device__ __forceinline__ void run(UnitReader<D>& reader, int first, int last, int by) {
     if (first >= last) return;
-    UnitWords<D> now, next;
-    bool there = reader.load(first, now), there_next = false;
-    for (int u = first; u < last; u += by) {
-      if (u + by < last) there_next = reader.load(u + by, next);
-      if (there) {
-        step(now, u, kUnit * u < full_from || kUnit * u + kUnit > full_to);
-      }
-      now = next;
-      there = there_next;
+    const Spread spread;
+    auto take = [&](const UnitWords<D>& w, int u, bool there) {
+      if (there) step(w, spread, u, kUnit * u < full_from || kUnit * u + kUnit > full_to);
+    };
+    UnitWords<D> a, b;
+    bool there_a = reader.load(first, a), there_b = false;
+    for (int u = first;;) {
+      if (u + by < last) there_b = reader.load(u + by, b);
+      take(a, u, there_a);
+      u += by;
+      if (u >= last) break;
+      if (u + by < last) there_a = reader.load(u + by, a);
+      take(b, u, there_b);
+      u += by;
+      if (u >= last) break;
     }
   }
 };
@@ -608,17 +619,18 @@ __global__ __launch_bounds__(kAttnThreads, WPE(D, NT, SHARED)) void attention_ke
   }
 }
 
-// The parts of a row joined: 16 lanes a row.  Those whose keys the row does not
-// see at all may not have been written, and are not read.
+// The parts of a row joined, a wave a row: first every part's reference and sum, a
+// part a lane, then four parts at a time by 16 lanes each.  Parts whose keys the row
+// does not see at all may not have been written, and are not read.
 template <int D, typename In>
 __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
   constexpr int E = D / 16;
   const int64_t rows = static_cast<int64_t>(a.M) * a.q_heads;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kAttnThreads / 16) + (threadIdx.x >> 4);
-  const int piece = threadIdx.x & 15;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kAttnWaves + wave_index();
+  const int lane = threadIdx.x & 63, piece = lane & 15, g = lane >> 4;
   if (row >= rows) return;
   const int token = static_cast<int>(row / a.q_heads);
-  const int b = sequence_of(a.offsets, a.cache.n_seqs, token);
+  const int b = sequence_of_wave(a.offsets, a.cache.n_seqs, token);
   if (b >= a.cache.n_seqs) return;
   const Span s = span_of(a.offsets, b, a.M);
   if (token < s.off || token >= s.end) return;
@@ -626,29 +638,52 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
   const int length = static_cast<int>(max(int64_t{0}, min(start + s.end - s.off, static_cast<int64_t>(a.cache.max_tokens))));
   const int to = a.causal ? static_cast<int>(max(int64_t{0}, min(pos + 1, static_cast<int64_t>(length)))) : length;
   const int from = a.window != 0 ? static_cast<int>(max(int64_t{0}, min(pos + 1 - a.window, int64_t{0x7fffffff}))) : 0;
-  float v[E], l = 0.0f, m = kNoReference;
+  float v[E], l = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.0f;
   if (from < to) {
-    const int p0 = min(from / a.chunk, a.splits - 1), p1 = min((to - 1) / a.chunk, a.splits - 1);
-    const float2* heads = reinterpret_cast<const float2*>(a.part + a.splits * rows * D);
-    for (int p = p0; p <= p1; ++p) m = fmaxf(m, heads[p * rows + row].x);
-    for (int p = p0; p <= p1; ++p) {
-      const float2 h = heads[p * rows + row];
-      const float f = __builtin_amdgcn_exp2f(h.x - m);
-      l = __builtin_fmaf(h.y, f, l);
-      const float* x = a.part + (p * rows + row) * D + piece * E;
+    const int p0 = min(from / a.chunk, a.splits - 1), n = min((to - 1) / a.chunk, a.splits - 1) - p0 + 1;
+    const float2* heads = reinterpret_cast<const float2*>(a.part + a.splits * rows * D) + p0 * rows + row;
+    const float* sums = a.part + (p0 * rows + row) * D + piece * E;
+    const float2 head = lane < n ? heads[lane * rows] : make_float2(kNoReference, 0.0f);
+    float m = head.x;
+    m = fmaxf(m, lane_xor<1>(m));
+    m = fmaxf(m, lane_xor<2>(m));
+    m = fmaxf(m, lane_xor<4>(m));
+    m = fmaxf(m, lane_xor<8>(m));
+    m = fmaxf(m, xor16(m));
+    m = fmaxf(m, xor32(m));
+    const float f = __builtin_amdgcn_exp2f(head.x - m);
+    l = head.y * f;
+    l += lane_xor<1>(l);
+    l += lane_xor<2>(l);
+    l += lane_xor<4>(l);
+    l += lane_xor<8>(l);
+    l += xor16(l);
+    l += xor32(l);
+#pragma unroll 4
+    for (int p = 0; p < n; p += 4) {
+      const int mine = min(p + g, n - 1);
+      const float fp = __shfl(f, mine);
+      const float w = p + g < n ? fp : 0.0f;
+      const float* x = sums + mine * rows * D;
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
         const float4 y = *reinterpret_cast<const float4*>(x + e);
-        v[e] = __builtin_fmaf(y.x, f, v[e]);
-        v[e + 1] = __builtin_fmaf(y.y, f, v[e + 1]);
-        v[e + 2] = __builtin_fmaf(y.z, f, v[e + 2]);
-        v[e + 3] = __builtin_fmaf(y.w, f, v[e + 3]);
+        // a part left out by its lane is not multiplied: it may be NaN
+        v[e] = p + g < n ? __builtin_fmaf(y.x, w, v[e]) : v[e];
+        v[e + 1] = p + g < n ? __builtin_fmaf(y.y, w, v[e + 1]) : v[e + 1];
+        v[e + 2] = p + g < n ? __builtin_fmaf(y.z, w, v[e + 2]) : v[e + 2];
+        v[e + 3] = p + g < n ? __builtin_fmaf(y.w, w, v[e + 3]) : v[e + 3];
       }
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      v[e] += xor16(v[e]);
+      v[e] += xor32(v[e]);
+    }
   }
-  finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row * D);
+  if (g == 0) finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row * D);
 }
 
 // Sequences of at most this many rows (tokens times query heads a key head) take
@@ -687,7 +722,7 @@ hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   }
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t out_rows = static_cast<int64_t>(a.M) * a.q_heads;
-  const int64_t grid = (out_rows + kAttnThreads / 16 - 1) / (kAttnThreads / 16);
+  const int64_t grid = (out_rows + kAttnWaves - 1) / kAttnWaves;
   if (grid * kAttnThreads >= (int64_t{1} << 32)) return hipErrorInvalidConfiguration;
   join_kernel<D, In><<<dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream>>>(a);
   return hipGetLastError();

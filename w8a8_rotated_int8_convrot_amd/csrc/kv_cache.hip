@@ -158,8 +158,11 @@ __device__ inline void for_octets(const Cache& cache, const Rows<In>& rows, int 
   int64_t at = 0;
   const int row = first + lane;
   bool leads = false;
+  if (first >= rows.M) return;
+  const int b0 = sequence_of_wave(rows.offsets, cache.n_seqs, first);
   if (lane < count && row < rows.M) {
-    b = sequence_of(rows.offsets, cache.n_seqs, row);
+    b = b0;
+    if (b < cache.n_seqs && rows.offsets[b + 1] <= row) b = sequence_of(rows.offsets, cache.n_seqs, row);
     if (b < cache.n_seqs) {
       const Span s = span_of(rows.offsets, b, rows.M);
       off = s.off;
