@@ -277,10 +277,9 @@ struct Columns {
         key[h][k] = v4i{static_cast<int>(w0 & 0x0f0f0f0fu), static_cast<int>(w0 >> 4 & 0x0f0f0f0fu),
                         static_cast<int>(w1 & 0x0f0f0f0fu), static_cast<int>(w1 >> 4 & 0x0f0f0f0fu)};
       }
-    v8h p[NT];
+    float y[NT][8];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float y[8], v[8], by = large;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         v4i high = {0, 0, 0, 0}, low = {eight[t], eight[t], eight[t], eight[t]};
@@ -290,27 +289,42 @@ struct Columns {
           low = __builtin_amdgcn_mfma_i32_16x16x64_i8(key[h][k], lo[t][k], low, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[4 * h + i] = static_cast<float>((high[i] << 8) + low[i]) * ks[4 * h + i];
+        for (int i = 0; i < 4; ++i) y[t][4 * h + i] = static_cast<float>((high[i] << 8) + low[i]) * ks[4 * h + i];
       }
+    }
+    float by[NT];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = vs[i];
-      if (masked) {
-        const int first = kUnit * u + 8 * g;
+    for (int t = 0; t < NT; ++t) by[t] = large;
+    const int first = kUnit * u + 8 * g;
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const bool seen = first + i >= from[t] && first + i < to[t];
-          y[i] = seen ? y[i] : kHidden;
-          v[i] = seen ? v[i] : 0.0f;
+          y[t][i] = seen ? y[t][i] : kHidden;
+          v[i] = seen ? vs[i] : 0.0f;
         }
-        by = log_scale(v);
+        by[t] = log_scale(v);
       }
-      float most = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-      most = __builtin_fmaf(most, qs[t], by);
-      // the reference, kTop below what the largest weight may be made of
-      if (__any(most > m[t] + (kTop + kRise))) {
-        most = fmaxf(most, xor16(most));
-        most = fmaxf(most, xor32(most));
-        const float wanted = __builtin_ceilf(most) - kTop;
+    }
+    // the reference, kTop below what the largest weight may be made of
+    float most[NT];
+    bool move = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float* x = y[t];
+      most[t] = __builtin_fmaf(fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))),
+                               qs[t], by[t]);
+      move = move || most[t] > m[t] + (kTop + kRise);
+    }
+    if (__any(move)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        most[t] = fmaxf(most[t], xor16(most[t]));
+        most[t] = fmaxf(most[t], xor32(most[t]));
+        const float wanted = __builtin_ceilf(most[t]) - kTop;
         if (wanted > m[t] + kRise) {
           const float f = __builtin_amdgcn_exp2f(m[t] - wanted);        // 0 for the first keys
           m[t] = wanted;
@@ -319,20 +333,31 @@ struct Columns {
           for (int d = 0; d < D / 16; ++d) o[t][d] *= f;
         }
       }
-      float e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[i], qs[t], -m[t]));
-      if (masked) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = y[i] == kHidden ? 0.0f : e[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) l[t] += e[i];
-      v2h pairs[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{e[i] * v[i], e[i + 4] * v[i + 4]}), v2h);
-      p[t] = __builtin_bit_cast(v8h, pairs);
     }
+    v8h p[NT];
+    auto weights = [&](auto hidden) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float e[8], v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[t][i], qs[t], -m[t]));
+          v[i] = e[i] * vs[i];
+          if constexpr (hidden.value) {
+            // nothing of a key that is not seen, whatever its place holds
+            e[i] = y[t][i] == kHidden ? 0.0f : e[i];
+            v[i] = y[t][i] == kHidden ? 0.0f : v[i];
+          }
+        }
+        l[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+        v2h pairs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{v[i], v[i + 4]}), v2h);
+        p[t] = __builtin_bit_cast(v8h, pairs);
+      }
+    };
+    if (masked) weights(std::true_type{});
+    else weights(std::false_type{});
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
       const v8h value = codes_of(w.v[d], spread);
@@ -661,7 +686,6 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
     l += lane_xor<8>(l);
     l += xor16(l);
     l += xor32(l);
-#pragma unroll 4
     for (int p = 0; p < n; p += 4) {
       const int mine = min(p + g, n - 1);
       const float fp = __shfl(f, mine);
@@ -709,7 +733,7 @@ hipError_t launch_tiles(const Attention& a, int few, int many, hipStream_t strea
 template <int D, typename In>
 hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   constexpr int kAll = 0x7fffffff;
-  constexpr int kWide = D == 256 ? 1 : D == 128 ? 2 : 4;
+  constexpr int kWide = D == 256 ? 1 : 2;
   const int64_t rows = static_cast<int64_t>(a.M) * (a.q_heads / a.cache.kv_heads);
   const int64_t mean = rows / a.cache.n_seqs;
   hipError_t e;
@@ -741,7 +765,7 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
                                    int64_t max_tokens) {
   const int64_t group = q_heads / kv_heads, rows = M * group, mean = rows / n_seqs;
   const bool shared = mean <= kFewRows;
-  const int64_t tile = shared ? (mean <= 16 ? 16 : 32) : (head_dim == 256 ? 64 : head_dim == 128 ? 128 : 256);
+  const int64_t tile = shared ? (mean <= 16 ? 16 : 32) : (head_dim == 256 ? 64 : 128);
   const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
   const int64_t wanted = shared ? 2048 : 512;
   const int64_t least = shared ? 4 * kUnit : 16 * kUnit;         // keys of a part
