@@ -88,6 +88,12 @@ __device__ inline v8h codes_of(uint32_t w, const Spread& c) {
   return __builtin_bit_cast(v8h, p);
 }
 
+// Sixteen codes of two words as the bytes they are held in (code + 8).
+__device__ inline v4i key_codes(uint32_t w0, uint32_t w1) {
+  return v4i{static_cast<int>(w0 & 0x0f0f0f0fu), static_cast<int>(w0 >> 4 & 0x0f0f0f0fu),
+             static_cast<int>(w1 & 0x0f0f0f0fu), static_cast<int>(w1 >> 4 & 0x0f0f0f0fu)};
+}
+
 // What a lane holds of one unit: the words of two tokens' key codes (dims
 // [D / 4 * g, D / 4 * (g + 1))), of D / 16 dims' value codes (octet g), and the
 // scales of octet g, bf16.
@@ -124,9 +130,10 @@ struct UnitReader {
   const int32_t* table;
   int head, held;                       // first table column held
   int32_t entry;
+  uint32_t scale;                       // of the last unit: key lane, or value lane - 32
 
   __device__ UnitReader(const Cache& cache, int b, int h)
-      : c(cache), table(cache.table + b * cache.table_stride), head(h), held(-64), entry(-1) {}
+      : c(cache), table(cache.table + b * cache.table_stride), head(h), held(-64), entry(-1), scale(0) {}
 
   // False where no page of the cache is named; the words are then another page's.
   __device__ bool load(int u, UnitWords<D>& w) {
@@ -154,9 +161,47 @@ struct UnitReader {
     }
     w.ks = *reinterpret_cast<const uint4*>(unit + key_scales_at(D) + 16 * g);
     w.vs = *reinterpret_cast<const uint4*>(unit + value_scales_at(D) + 16 * g);
+    scale = reinterpret_cast<const uint16_t*>(unit + key_scales_at(D))[lane];
     return there;
   }
 };
+
+// The two views of a unit that a step takes: a lane's own words, or the operands of
+// both products as a workgroup has left them in LDS for all its waves.
+template <int D> struct UnitOfWords {
+  const UnitWords<D>& w;
+  const Spread& spread;
+  __device__ v4i key(int h, int k) const { return key_codes(w.k[h][2 * k], w.k[h][2 * k + 1]); }
+  __device__ v8h value(int d) const { return codes_of(w.v[d], spread); }
+  __device__ void scales(float (&ks)[8], float (&vs)[8]) const {
+    widen_scales(w.ks, ks);
+    widen_scales(w.vs, vs);
+  }
+};
+template <int D> struct StagedUnit {
+  static constexpr int kKeys = 2 * (D / 64), kPieces = kKeys + D / 16;
+  const uint4* piece;                   // [kPieces][64]: a lane's 16 bytes of each
+  const float* scale;                   // of 32 keys, then of 32 values
+  __device__ v4i key(int h, int k) const {
+    return __builtin_bit_cast(v4i, piece[(h * (D / 64) + k) * 64 + (threadIdx.x & 63)]);
+  }
+  __device__ v8h value(int d) const { return __builtin_bit_cast(v8h, piece[(kKeys + d) * 64 + (threadIdx.x & 63)]); }
+  __device__ void scales(float (&ks)[8], float (&vs)[8]) const {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ks[i] = scale[8 * g + i];
+      vs[i] = scale[kUnit + 8 * g + i];
+    }
+  }
+};
+
+// The keys [first, end) that token i of a sequence's rows sees.
+__device__ inline void bounds_of(const Attention& a, int64_t start, int length, int i, int& first, int& end) {
+  const int64_t pos = start + i;
+  end = a.causal ? static_cast<int>(max(int64_t{0}, min(pos + 1, static_cast<int64_t>(length)))) : length;
+  first = a.window != 0 ? static_cast<int>(max(int64_t{0}, min(pos + 1 - a.window, int64_t{0x7fffffff}))) : 0;
+}
 
 // 16 NT query columns of a wave: their queries, bounds and running sums.
 template <int D, int NT>
@@ -175,14 +220,9 @@ struct Columns {
   __device__ void open(const Attention& a, int group, int kv_head, int off, int n, int64_t start, int length, int row0) {
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     // bounds grow from token to token
-    auto bounds = [&](int i, int& first, int& end) {
-      const int64_t pos = start + i;
-      end = a.causal ? static_cast<int>(max(int64_t{0}, min(pos + 1, static_cast<int64_t>(length)))) : length;
-      first = a.window != 0 ? static_cast<int>(max(int64_t{0}, min(pos + 1 - a.window, int64_t{0x7fffffff}))) : 0;
-    };
     const int all = n * group;
-    bounds(row0 / group, any_from, full_to);
-    bounds((min(row0 + 16 * NT, all) - 1) / group, full_from, any_to);
+    bounds_of(a, start, length, row0 / group, any_from, full_to);
+    bounds_of(a, start, length, (min(row0 + 16 * NT, all) - 1) / group, full_from, any_to);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int row = row0 + 16 * t + col;
@@ -190,7 +230,7 @@ struct Columns {
       const int i = live ? row / group : 0;
       const int head = kv_head * group + (live ? row - i * group : 0);
       from[t] = 0, to[t] = 0x7fffffff;
-      if (live) bounds(i, from[t], to[t]);
+      if (live) bounds_of(a, start, length, i, from[t], to[t]);
 
       constexpr int E = D / 4;          // dims of a lane
       const In* p = static_cast<const In*>(a.q) + (static_cast<int64_t>(off) + i) * a.q_stride +
@@ -261,22 +301,19 @@ struct Columns {
     }
   }
 
-  // One unit; `masked` where some column does not see all of it.
-  __device__ __forceinline__ void step(const UnitWords<D>& w, const Spread& spread, int u, bool masked) {
+  // One unit; where some column does not see all of it, masked.
+  template <typename Unit>
+  __device__ __forceinline__ void step(const Unit& unit, int u) {
     const int g = (threadIdx.x & 63) >> 4;
+    const bool masked = kUnit * u < full_from || kUnit * u + kUnit > full_to;
     float ks[8], vs[8];
-    widen_scales(w.ks, ks);
-    widen_scales(w.vs, vs);
+    unit.scales(ks, vs);
     const float large = log_scale(vs);
     v4i key[2][D / 64];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int k = 0; k < D / 64; ++k) {
-        const uint32_t w0 = w.k[h][2 * k], w1 = w.k[h][2 * k + 1];
-        key[h][k] = v4i{static_cast<int>(w0 & 0x0f0f0f0fu), static_cast<int>(w0 >> 4 & 0x0f0f0f0fu),
-                        static_cast<int>(w1 & 0x0f0f0f0fu), static_cast<int>(w1 >> 4 & 0x0f0f0f0fu)};
-      }
+      for (int k = 0; k < D / 64; ++k) key[h][k] = unit.key(h, k);
     float y[NT][8];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -360,7 +397,7 @@ struct Columns {
     else weights(std::false_type{});
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
-      const v8h value = codes_of(w.v[d], spread);
+      const v8h value = unit.value(d);
 #pragma unroll
       for (int t = 0; t < NT; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[t], o[t][d], 0, 0, 0);
     }
@@ -377,7 +414,7 @@ struct Columns {
     if (first >= last) return;
     const Spread spread;
     auto take = [&](const UnitWords<D>& w, int u, bool there) {
-      if (there) step(w, spread, u, kUnit * u < full_from || kUnit * u + kUnit > full_to);
+      if (there) step(UnitOfWords<D>{w, spread}, u);
     };
     UnitWords<D> a, b;
     bool there_a = reader.load(first, a), there_b = false;
@@ -474,7 +511,66 @@ __device__ inline bool find_tile(const Attention& a, int group, int rows, int fe
   return false;
 }
 
-constexpr int WPE(int d, int nt, bool shared) { return d * nt <= 64 ? 4 : d * nt <= 128 ? 3 : d * nt <= 256 ? 2 : 1; }
+constexpr int WPE(int d, int nt, bool shared) { if (!shared) return d == 64 ? 3 : 2; return d * nt <= 64 ? 4 : d * nt <= 128 ? 3 : d * nt <= 256 ? 2 : 1; }
+// A workgroup's groups of units for waves with columns of their own: each unit
+// (or half of one) is loaded and its codes are made operands by one wave, for all four.
+// One group is loaded while the one before is worked on.
+template <int D>
+struct Staged {
+  static constexpr int kUnits = D == 256 ? 2 : 4;                // a group
+  static constexpr int kPieces = StagedUnit<D>::kPieces, kKeys = StagedUnit<D>::kKeys;
+  static constexpr int kParts = kAttnWaves / kUnits, kMine = kPieces / kParts;
+  uint4 piece[kUnits][kPieces][64];
+  float scale[kUnits][64];
+  int there[kUnits];
+
+  template <int NT>
+  __device__ void run(Columns<D, NT>& c, UnitReader<D>& reader, int first, int last, bool idle) {
+    const int wave = wave_index(), lane = threadIdx.x & 63;
+    const int mine = wave % kUnits, part = wave / kUnits;
+    const Spread spread;
+    UnitWords<D> w;
+    uint32_t s = 0;
+    bool held = false;
+    auto load = [&](int u) {
+      held = false;
+      if (u < last) {
+        held = reader.load(u, w);
+        // lanes 0-31: of a key, 32-63: of a value
+        s = reader.scale;
+      }
+    };
+    load(first + mine);
+    for (int u0 = first; u0 < last; u0 += kUnits) {
+      if (u0 != first) __syncthreads();
+      const UnitOfWords<D> unit{w, spread};
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) {
+        if (part == q) {
+#pragma unroll
+          for (int i = q * kMine; i < (q + 1) * kMine; ++i)
+            piece[mine][i][lane] = i < kKeys ? __builtin_bit_cast(uint4, unit.key(i / (D / 64), i % (D / 64)))
+                                             : __builtin_bit_cast(uint4, unit.value(i - kKeys));
+        }
+      }
+      if (part == 0) {
+        scale[mine][lane] = __uint_as_float(s << 16);
+        if (lane == 0) there[mine] = held;
+      }
+      load(u0 + kUnits + mine);
+      __syncthreads();
+#pragma unroll 1
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = u0 + i;
+        if (idle || kUnit * u >= c.any_to) break;
+        if (kUnit * u + kUnit > c.any_from && there[i] != 0) c.step(StagedUnit<D>{&piece[i][0][0], scale[i]}, u);
+      }
+    }
+  }
+};
+
+// SHARED: the four waves have the same columns and every fourth unit each, for
+// few rows; else they have columns of their own and the same units.
 // SHARED: the four waves have the same columns and every fourth unit each, for
 // few rows; else they have columns of their own and the same units.
 template <int D, int NT, bool SHARED, typename In>
@@ -491,15 +587,26 @@ __global__ __launch_bounds__(kAttnThreads, WPE(D, NT, SHARED)) void attention_ke
   Columns<D, NT> c;
   const int row0 = tile.row0 + (SHARED ? 0 : 16 * NT * wave);
   const int all = tile.n * group;
-  if (!SHARED && row0 >= all) return;
-
-  c.template open<In>(a, group, kv_head, tile.off, tile.n, start, length, row0);
-  // this part's keys
-  const int lo = max(c.any_from, part * a.chunk);
-  const int hi = part == a.splits - 1 ? c.any_to : min(c.any_to, (part + 1) * a.chunk);
+  const bool idle = row0 >= all;        // a wave behind the tile's rows: it only stages
+  c.template open<In>(a, group, kv_head, tile.off, tile.n, start, length, idle ? tile.row0 : row0);
+  // this part's keys of the whole tile, and of this wave's columns
+  int tile_from = c.any_from, tile_to = c.any_to;
+  if constexpr (!SHARED) {
+    int unused;
+    bounds_of(a, start, length, tile.row0 / group, tile_from, unused);
+    bounds_of(a, start, length, (min(tile.row0 + kRows, all) - 1) / group, unused, tile_to);
+  }
+  const int part_from = part * a.chunk, part_to = part == a.splits - 1 ? 0x7fffffff : (part + 1) * a.chunk;
+  const int lo = max(tile_from, part_from), hi = min(tile_to, part_to);
   const int first = lo / kUnit, last = lo < hi ? (hi + kUnit - 1) / kUnit : 0;
   UnitReader<D> reader(a.cache, tile.b, kv_head);
-  c.run(reader, first + (SHARED ? wave : 0), last, SHARED ? kAttnWaves : 1);
+  if constexpr (SHARED) {
+    c.run(reader, first + wave, last, kAttnWaves);
+  } else {
+    __shared__ Staged<D> staged;
+    staged.run(c, reader, first, last, idle);
+    if (idle) return;
+  }
 
   const int64_t rows = static_cast<int64_t>(a.M) * a.q_heads;
   // the row of the output (and of a part's sums) that a column is
@@ -659,10 +766,10 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
   if (b >= a.cache.n_seqs) return;
   const Span s = span_of(a.offsets, b, a.M);
   if (token < s.off || token >= s.end) return;
-  const int64_t start = a.starts[b], pos = start + token - s.off;
+  const int64_t start = a.starts[b];
   const int length = static_cast<int>(max(int64_t{0}, min(start + s.end - s.off, static_cast<int64_t>(a.cache.max_tokens))));
-  const int to = a.causal ? static_cast<int>(max(int64_t{0}, min(pos + 1, static_cast<int64_t>(length)))) : length;
-  const int from = a.window != 0 ? static_cast<int>(max(int64_t{0}, min(pos + 1 - a.window, int64_t{0x7fffffff}))) : 0;
+  int from, to;
+  bounds_of(a, start, length, token - s.off, from, to);
   float v[E], l = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.0f;
