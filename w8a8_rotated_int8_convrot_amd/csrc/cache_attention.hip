@@ -38,6 +38,7 @@ namespace {
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * 64;
@@ -59,8 +60,36 @@ template <> struct RootScale<64> { static constexpr float value = 0.125f; };
 template <> struct RootScale<128> { static constexpr float value = 0x1.6a09e6p-4f; };
 template <> struct RootScale<256> { static constexpr float value = 0x1p-4f; };
 
-__device__ inline float xor16(float v) { return __shfl_xor(v, 16); }
-__device__ inline float xor32(float v) { return __shfl_xor(v, 32); }
+// Rows (16 lanes) of two registers exchanged: of a the odd ones with the even ones of b,
+// or the upper two with the lower two.
+template <int T>
+__device__ inline void swap_rows(float& a, float& b) {
+  const auto r = T == 16 ? __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false)
+                         : __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+// Maximum and sum over the four lanes that share a column.
+__device__ inline float column_max(float v) {
+  float w = v;
+  swap_rows<16>(v, w);
+  v = w = fmaxf(v, w);
+  swap_rows<32>(v, w);
+  return fmaxf(v, w);
+}
+__device__ inline float column_sum(float v) {
+  float w = v;
+  swap_rows<16>(v, w);
+  v = w = v + w;
+  swap_rows<32>(v, w);
+  return v + w;
+}
+__device__ inline int column_sum(int v) {
+  auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = static_cast<int>(r[0] + r[1]);
+  r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return static_cast<int>(r[0] + r[1]);
+}
 
 __device__ inline int wave_index() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
 
@@ -220,9 +249,19 @@ struct Columns {
   __device__ void open(const Attention& a, int group, int kv_head, int off, int n, int64_t start, int length, int row0) {
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     // bounds grow from token to token
+    constexpr int E = D / 4;            // dims of a lane
     const int all = n * group;
     bounds_of(a, start, length, row0 / group, any_from, full_to);
     bounds_of(a, start, length, (min(row0 + 16 * NT, all) - 1) / group, full_from, any_to);
+    // +-1 of row 4 r + i and dims (bits 0, 1, of quarter g): the parity of the bits both have
+    uint32_t signs[2];
+    {
+      constexpr uint32_t kOne = std::is_same_v<In, _Float16> ? 0x3c003c00u : 0x3f803f80u;
+      const uint32_t quarter = __builtin_popcount((col >> 2) & g) & 1 ? 0x80008000u : 0u;
+      const uint32_t one = (col & 1) != 0 ? 0x80000000u : 0u, two = (col & 2) != 0 ? 0x80008000u : 0u;
+      signs[0] = kOne ^ quarter ^ one;
+      signs[1] = signs[0] ^ two;
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int row = row0 + 16 * t + col;
@@ -232,20 +271,38 @@ struct Columns {
       from[t] = 0, to[t] = 0x7fffffff;
       if (live) bounds_of(a, start, length, i, from[t], to[t]);
 
-      constexpr int E = D / 4;          // dims of a lane
+      // H_D of the query: five bits of the dim by a product with +-1 (exact, sums in
+      // fp32), the others, those of the chunk, by sums inside the lane.  A lane has dims
+      // [E g, E (g + 1)), as of the keys: in chunk k the eight of bits 0, 1 and the
+      // highest of them, and out come rows 4 g + i of two tiles, bits 0, 1 and that one.
       const In* p = static_cast<const In*>(a.q) + (static_cast<int64_t>(off) + i) * a.q_stride +
                     static_cast<int64_t>(head) * D + g * E;
-      float v[E];
+      uint32_t raw[E / 2];
 #pragma unroll
       for (int j = 0; j < E / 8; ++j) {
         const uint4 r = live ? reinterpret_cast<const uint4*>(p)[j] : make_uint4(0, 0, 0, 0);
-        float f[8];
-        widen8<In>(r, f);
+        raw[4 * j] = r.x, raw[4 * j + 1] = r.y, raw[4 * j + 2] = r.z, raw[4 * j + 3] = r.w;
+      }
+      float v[E];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * j + e] = f[e];
+      for (int k = 0; k < E / 8; ++k) {
+        const uint32_t in[4] = {raw[2 * k], raw[2 * k + 1], raw[E / 4 + 2 * k], raw[E / 4 + 2 * k + 1]};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t flip = h != 0 ? 0x80008000u : 0u;
+          const uint32_t sign[4] = {signs[0], signs[1], signs[0] ^ flip, signs[1] ^ flip};
+          const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+          v4f r;
+          if constexpr (std::is_same_v<In, _Float16>)
+            r = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, sign), __builtin_bit_cast(v8h, in), zero, 0, 0, 0);
+          else
+            r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, sign), __builtin_bit_cast(v8bf, in), zero, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[E / 2 * h + 4 * k + e] = r[e];
+        }
       }
 #pragma unroll
-      for (int h = 1; h < E; h <<= 1) {
+      for (int h = 4; h < E / 2; h <<= 1) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           if ((e & h) == 0) {
@@ -256,44 +313,42 @@ struct Columns {
         }
       }
       float top = 0.0f;
-      bool finite = true;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float other = xor16(v[e]);
-        v[e] = (g & 1) != 0 ? other - v[e] : v[e] + other;
-        other = xor32(v[e]);
-        v[e] = (g & 2) != 0 ? other - v[e] : v[e] + other;
-        top = fmaxf(top, fabsf(v[e]));
-        finite = finite && fabsf(v[e]) < __builtin_inff();
-      }
-      top = fmaxf(top, xor16(top));
-      top = fmaxf(top, xor32(top));
-      // steps of top / 32512, so that both digits fit; a row that is not finite is so in
-      // all its sums, and its scores are NaN by their factor
-      const float least = fmaxf(top, 0x1p-100f), inverse = finite ? 1.0f / least : 0.0f;
+      for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(v[e]));
+      top = column_max(top);
+      // an infinity or NaN is in every sum of its row; one that only a sum has is in the
+      // maximum
+      const bool finite = fabsf(v[0]) < __builtin_inff() && top < __builtin_inff();
+      // steps of top / 32512, so that both digits fit; the scores of a row that is not
+      // finite are NaN by their factor
+      const float least = fmaxf(top, 0x1p-100f);
       qs[t] = finite ? least * (RootScale<D>::value * kLog2e / 32512.0f) * fabsf(a.scale) : __builtin_nanf("");
-      const float signed_steps = a.scale < 0.0f ? -32512.0f : 32512.0f;
-      int sum = 0;
+      const float steps = finite ? (a.scale < 0.0f ? -32512.0f : 32512.0f) / least : 0.0f;
+      int sum = 0, ones = 0;            // of the digits
 #pragma unroll
       for (int k = 0; k < D / 64; ++k) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          uint32_t h = 0, l8 = 0;
+          // the nearest whole number is in the low bits behind 1.5 * 2^23, its upper digit
+          // above them once 128 is added
+          uint32_t c[4], c128[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x = finite ? v[16 * k + 8 * (r >> 1) + 2 * e + (r & 1)] * inverse : 0.0f;
-            const int c = static_cast<int>(__builtin_rintf(x * signed_steps)), high = (c + 128) >> 8;
-            sum += c;
-            h |= static_cast<uint32_t>(high & 0xff) << (8 * e);
-            l8 |= static_cast<uint32_t>(c & 0xff) << (8 * e);
+            const float x = finite ? v[16 * k + 8 * (r >> 1) + 2 * e + (r & 1)] : 0.0f;
+            const float at = __builtin_fmaf(x, steps, 12582912.0f);
+            c[e] = __float_as_uint(at);
+            c128[e] = __float_as_uint(at + 128.0f);
           }
-          hi[t][k][r] = static_cast<int>(h);
-          lo[t][k][r] = static_cast<int>(l8);
+          const uint32_t low = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u) | __builtin_amdgcn_perm(c[3], c[2], 0x04000c0cu);
+          const uint32_t high =
+              __builtin_amdgcn_perm(c128[1], c128[0], 0x0c0c0501u) | __builtin_amdgcn_perm(c128[3], c128[2], 0x05010c0cu);
+          hi[t][k][r] = static_cast<int>(high);
+          lo[t][k][r] = static_cast<int>(low);
+          sum = __builtin_amdgcn_sdot4(static_cast<int>(high), 0x01010101, sum, false);
+          ones = __builtin_amdgcn_sdot4(static_cast<int>(low), 0x01010101, ones, false);
         }
       }
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      eight[t] = -8 * sum;
+      eight[t] = -8 * (256 * column_sum(sum) + column_sum(ones));
       m[t] = kNoReference;
       l[t] = 0.0f;
 #pragma unroll
@@ -359,8 +414,7 @@ struct Columns {
     if (__any(move)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        most[t] = fmaxf(most[t], xor16(most[t]));
-        most[t] = fmaxf(most[t], xor32(most[t]));
+        most[t] = column_max(most[t]);
         const float wanted = __builtin_ceilf(most[t]) - kTop;
         if (wanted > m[t] + kRise) {
           const float f = __builtin_amdgcn_exp2f(m[t] - wanted);        // 0 for the first keys
@@ -616,10 +670,7 @@ __global__ __launch_bounds__(kAttnThreads, WPE(D, NT, SHARED)) void attention_ke
   };
   const int col = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    c.l[t] += xor16(c.l[t]);
-    c.l[t] += xor32(c.l[t]);
-  }
+  for (int t = 0; t < NT; ++t) c.l[t] = column_sum(c.l[t]);
 
   if constexpr (SHARED) {
     constexpr int kStride = D + 4;
@@ -698,7 +749,9 @@ __global__ __launch_bounds__(kAttnThreads, WPE(D, NT, SHARED)) void attention_ke
         }
         continue;
       }
-      const float by = c.l[t] != 0.0f ? RootScale<D>::value / c.l[t] : 0.0f;
+      // H_D: bits 0 to 3 of the dim and those from 6 on lie inside a lane; bits 4 and 5
+      // are the lane's quarter, which is exchanged with two others of the lane's own, so
+      // that each sum has both its terms in one lane: bit 3, and bit 6 (D = 64: bit 2)
 #pragma unroll
       for (int d = 0; d < D / 64; ++d) {
 #pragma unroll
@@ -711,13 +764,6 @@ __global__ __launch_bounds__(kAttnThreads, WPE(D, NT, SHARED)) void attention_ke
               v[d][e + h] = x - y;
             }
           }
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float other = xor16(v[d][e]);
-          v[d][e] = (g & 1) != 0 ? other - v[d][e] : v[d][e] + other;
-          other = xor32(v[d][e]);
-          v[d][e] = (g & 2) != 0 ? other - v[d][e] : v[d][e] + other;
         }
       }
 #pragma unroll
@@ -734,8 +780,36 @@ __global__ __launch_bounds__(kAttnThreads, WPE(D, NT, SHARED)) void attention_ke
           }
         }
       }
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          swap_rows<16>(v[d][e], v[d][e + 8]);
+          const float x = v[d][e], y = v[d][e + 8];
+          v[d][e] = x + y;
+          v[d][e + 8] = x - y;
+        }
+      }
+      // now bit 3 of the dim is bit 0 of the quarter, and index 8 of a lane bit 4
+      auto last = [&](float& p, float& q) {
+        swap_rows<32>(p, q);
+        const float x = p, y = q;
+        p = x + y;
+        q = x - y;
+      };
+      if constexpr (D == 64) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if ((e & 4) == 0) last(v[0][e], v[0][e + 4]);
+      } else {
+#pragma unroll
+        for (int d = 0; d < D / 64; d += 2)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) last(v[d][e], v[d + 1][e]);
+      }
+      const float by = c.l[t] != 0.0f ? RootScale<D>::value / c.l[t] : 0.0f;
       if (row < all) {
-        In* out = static_cast<In*>(a.out) + row_of(row) * D;
+        In* out = static_cast<In*>(a.out) + row_of(row) * D + 8 * (g & 1);
 #pragma unroll
         for (int d = 0; d < D / 64; ++d) {
 #pragma unroll
@@ -743,7 +817,15 @@ __global__ __launch_bounds__(kAttnThreads, WPE(D, NT, SHARED)) void attention_ke
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = c.l[t] != 0.0f ? v[d][8 * j + e] * by : 0.0f;
-            *reinterpret_cast<uint4*>(out + 64 * d + 16 * g + 8 * j) = narrow8<In>(f);
+            if constexpr (D == 64) {
+              // index 4 of a lane is bit 5, the quarter's bit 1 is bit 2
+              const uint4 w = narrow8<In>(f);
+              *reinterpret_cast<uint2*>(out + 16 * j + 4 * (g >> 1)) = make_uint2(w.x, w.y);
+              *reinterpret_cast<uint2*>(out + 16 * j + 32 + 4 * (g >> 1)) = make_uint2(w.z, w.w);
+            } else {
+              // d's bit 0 is bit 5, the quarter's bit 1 is bit 6
+              *reinterpret_cast<uint4*>(out + 128 * (d >> 1) + 64 * (g >> 1) + 32 * (d & 1) + 16 * j) = narrow8<In>(f);
+            }
           }
         }
       }
@@ -783,16 +865,14 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
     m = fmaxf(m, lane_xor<2>(m));
     m = fmaxf(m, lane_xor<4>(m));
     m = fmaxf(m, lane_xor<8>(m));
-    m = fmaxf(m, xor16(m));
-    m = fmaxf(m, xor32(m));
+    m = column_max(m);
     const float f = __builtin_amdgcn_exp2f(head.x - m);
     l = head.y * f;
     l += lane_xor<1>(l);
     l += lane_xor<2>(l);
     l += lane_xor<4>(l);
     l += lane_xor<8>(l);
-    l += xor16(l);
-    l += xor32(l);
+    l = column_sum(l);
     for (int p = 0; p < n; p += 4) {
       const int mine = min(p + g, n - 1);
       const float fp = __shfl(f, mine);
@@ -809,10 +889,7 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
       }
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      v[e] += xor16(v[e]);
-      v[e] += xor32(v[e]);
-    }
+    for (int e = 0; e < E; ++e) v[e] = column_sum(v[e]);
   }
   if (g == 0) finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row * D);
 }
