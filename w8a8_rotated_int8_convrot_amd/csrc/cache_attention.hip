@@ -40,6 +40,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
+constexpr bool PREF = true;
+constexpr int W128 = 2, W64 = 3;
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * 64;
 // A column's largest rounded weight lies in [2^kTop, 2^(kTop + kRise)], far
@@ -356,45 +358,58 @@ struct Columns {
     }
   }
 
-  // One unit; where some column does not see all of it, masked.
+  // The steps of a unit, apart, so that the products of one can run beside the
+  // exponentials of another.
+  struct Scores {
+    v4i high[NT][2], low[NT][2];
+  };
+  struct Weights {
+    v8h p[NT];
+  };
   template <typename Unit>
-  __device__ __forceinline__ void step(const Unit& unit, int u) {
-    const int g = (threadIdx.x & 63) >> 4;
-    const bool masked = kUnit * u < full_from || kUnit * u + kUnit > full_to;
-    float ks[8], vs[8];
-    unit.scales(ks, vs);
-    const float large = log_scale(vs);
-    v4i key[2][D / 64];
+  __device__ __forceinline__ void scores(const Unit& unit, Scores& s) const {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      v4i key[D / 64];
 #pragma unroll
-      for (int k = 0; k < D / 64; ++k) key[h][k] = unit.key(h, k);
-    float y[NT][8];
+      for (int k = 0; k < D / 64; ++k) key[k] = unit.key(h, k);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int t = 0; t < NT; ++t) {
         v4i high = {0, 0, 0, 0}, low = {eight[t], eight[t], eight[t], eight[t]};
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {
-          high = __builtin_amdgcn_mfma_i32_16x16x64_i8(key[h][k], hi[t][k], high, 0, 0, 0);
-          low = __builtin_amdgcn_mfma_i32_16x16x64_i8(key[h][k], lo[t][k], low, 0, 0, 0);
+          high = __builtin_amdgcn_mfma_i32_16x16x64_i8(key[k], hi[t][k], high, 0, 0, 0);
+          low = __builtin_amdgcn_mfma_i32_16x16x64_i8(key[k], lo[t][k], low, 0, 0, 0);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[t][4 * h + i] = static_cast<float>((high[i] << 8) + low[i]) * ks[4 * h + i];
+        s.high[t][h] = high;
+        s.low[t][h] = low;
       }
     }
+  }
+  // Scores times the keys' scales.
+  static __device__ __forceinline__ void scale(const Scores& s, const float (&ks)[8], float (&y)[NT][8]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[t][i] = static_cast<float>((s.high[t][i >> 2][i & 3] << 8) + s.low[t][i >> 2][i & 3]) * ks[i];
+  }
+  // Hides what a column does not see (of a unit that no page holds, everything) and
+  // moves the references where that is due; whether anything is hidden.
+  __device__ __forceinline__ bool settle(float (&y)[NT][8], const float (&vs)[8], int u, bool there) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const bool masked = !there || kUnit * u < full_from || kUnit * u + kUnit > full_to;
     float by[NT];
+    const float large = log_scale(vs);
 #pragma unroll
     for (int t = 0; t < NT; ++t) by[t] = large;
-    const int first = kUnit * u + 8 * g;
     if (masked) {
+      const int first = kUnit * u + 8 * g;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const bool seen = first + i >= from[t] && first + i < to[t];
+          const bool seen = there && first + i >= from[t] && first + i < to[t];
           y[t][i] = seen ? y[t][i] : kHidden;
           v[i] = seen ? vs[i] : 0.0f;
         }
@@ -425,35 +440,79 @@ struct Columns {
         }
       }
     }
-    v8h p[NT];
-    auto weights = [&](auto hidden) {
+    return masked;
+  }
+  template <bool HIDDEN>
+  __device__ __forceinline__ void weights(const float (&y)[NT][8], const float (&vs)[8], Weights& w) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float e[8], v[8];
+    for (int t = 0; t < NT; ++t) {
+      float e[8], v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[t][i], qs[t], -m[t]));
-          v[i] = e[i] * vs[i];
-          if constexpr (hidden.value) {
-            // nothing of a key that is not seen, whatever its place holds
-            e[i] = y[t][i] == kHidden ? 0.0f : e[i];
-            v[i] = y[t][i] == kHidden ? 0.0f : v[i];
-          }
+      for (int i = 0; i < 8; ++i) {
+        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[t][i], qs[t], -m[t]));
+        v[i] = e[i] * vs[i];
+        if constexpr (HIDDEN) {
+          // nothing of a key that is not seen, whatever its place holds
+          e[i] = y[t][i] == kHidden ? 0.0f : e[i];
+          v[i] = y[t][i] == kHidden ? 0.0f : v[i];
         }
-        l[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-        v2h pairs[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{v[i], v[i + 4]}), v2h);
-        p[t] = __builtin_bit_cast(v8h, pairs);
       }
-    };
-    if (masked) weights(std::true_type{});
-    else weights(std::false_type{});
+      l[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      v2h pairs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{v[i], v[i + 4]}), v2h);
+      w.p[t] = __builtin_bit_cast(v8h, pairs);
+    }
+  }
+  template <typename Unit>
+  __device__ __forceinline__ void add(const Unit& unit, const Weights& w) {
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
       const v8h value = unit.value(d);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[t], o[t][d], 0, 0, 0);
+      for (int t = 0; t < NT; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, w.p[t], o[t][d], 0, 0, 0);
+    }
+  }
+
+  template <typename Unit>
+  __device__ __forceinline__ void step(const Unit& unit, int u) {
+    float ks[8], vs[8], y[NT][8];
+    unit.scales(ks, vs);
+    Scores s;
+    scores(unit, s);
+    scale(s, ks, y);
+    Weights w;
+    if (settle(y, vs, u, true)) weights<true>(y, vs, w);
+    else weights<false>(y, vs, w);
+    add(unit, w);
+  }
+
+  // Units [i0, i1) of a staged group, unit(i) its i-th, there(i) whether a page holds it:
+  // the scores of each beside the exponentials of the one before, whose product with
+  // the values runs beside the next one's scaling.
+  template <typename Unit, typename There>
+  __device__ __forceinline__ void steps(Unit&& unit, There&& there, int u0, int i0, int i1) {
+    if (i0 >= i1) return;
+    float ks[8], vs[8], y[NT][8];
+    Scores s;
+    unit(i0).scales(ks, vs);
+    scores(unit(i0), s);
+    scale(s, ks, y);
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      const int next = min(i + 1, i1 - 1);
+      const auto after = unit(next);
+      Weights w;
+      if (settle(y, vs, u0 + i, there(i))) {
+        weights<true>(y, vs, w);
+        scores(after, s);
+      } else {
+        scores(after, s);
+        weights<false>(y, vs, w);
+      }
+      after.scales(ks, vs);
+      add(unit(i), w);
+      scale(s, ks, y);
     }
   }
 
@@ -565,7 +624,7 @@ __device__ inline bool find_tile(const Attention& a, int group, int rows, int fe
   return false;
 }
 
-constexpr int WPE(int d, int nt, bool shared) { if (!shared) return d == 64 ? 3 : 2; return d * nt <= 64 ? 4 : d * nt <= 128 ? 3 : d * nt <= 256 ? 2 : 1; }
+constexpr int WPE(int d, int nt, bool shared) { if (!shared) return d == 64 ? W64 : d == 128 ? W128 : 2; return d * nt <= 64 ? 4 : d * nt <= 128 ? 3 : d * nt <= 256 ? 2 : 1; }
 // A workgroup's groups of units for waves with columns of their own: each unit
 // (or half of one) is loaded and its codes are made operands by one wave, for all four.
 // One group is loaded while the one before is worked on.
@@ -594,8 +653,9 @@ struct Staged {
         s = reader.scale;
       }
     };
-    load(first + mine);
+    if (PREF) load(first + mine);
     for (int u0 = first; u0 < last; u0 += kUnits) {
+      if (!PREF) load(u0 + mine);
       if (u0 != first) __syncthreads();
       const UnitOfWords<D> unit{w, spread};
 #pragma unroll
@@ -611,14 +671,10 @@ struct Staged {
         scale[mine][lane] = __uint_as_float(s << 16);
         if (lane == 0) there[mine] = held;
       }
-      load(u0 + kUnits + mine);
+      if (PREF) load(u0 + kUnits + mine);
       __syncthreads();
-#pragma unroll 1
-      for (int i = 0; i < kUnits; ++i) {
-        const int u = u0 + i;
-        if (idle || kUnit * u >= c.any_to) break;
-        if (kUnit * u + kUnit > c.any_from && there[i] != 0) c.step(StagedUnit<D>{&piece[i][0][0], scale[i]}, u);
-      }
+      const int i0 = max(0, c.any_from / kUnit - u0), i1 = idle ? 0 : min(kUnits, (c.any_to + kUnit - 1) / kUnit - u0);
+      c.steps([&](int i) { return StagedUnit<D>{&piece[i][0][0], scale[i]}; }, [&](int i) { return there[i] != 0; }, u0, i0, i1);
     }
   }
 };
