@@ -782,22 +782,54 @@ _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 
-def _heads_of(t, dev, dtype, name, shape=None):
-    """Rows of contiguous heads [M, H, D] on dev, all of one row stride; their address and that stride."""
-    if (t.dim() != 3 or t.dtype != dtype or t.device != dev or (shape is not None and t.shape != shape)
-            or (t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1)):
+def _gpu_of(t, name):
+    """The index of t's GPU (cheaper to compare than torch.device objects)."""
+    gpu = t.get_device()
+    if gpu < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return gpu
+
+
+def _at(t, gpu, dtype, name, shape):
+    """A contiguous tensor of this type and shape on a GPU; its address."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != gpu or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on cuda:{gpu}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+    return t.data_ptr()
+
+
+def _heads_of(t, gpu, dtype, name, shape=None):
+    """Rows of contiguous heads [M, H, D] on a GPU, all of one row stride; their address and that stride."""
+    if t.is_contiguous():
+        good = t.dim() == 3
+    else:
+        good = t.dim() == 3 and (t.stride(2) == 1 or t.shape[2] == 1) and (t.stride(1) == t.shape[2] or t.shape[1] == 1)
+    if not good or t.dtype is not dtype or t.get_device() != gpu or (shape is not None and t.shape != shape):
         want = list(shape) if shape is not None else "[M, H, D]"
-        raise ValueError(f"{name}: expected {dtype} {want} on {dev} with contiguous heads, got {t.dtype} "
+        raise ValueError(f"{name}: expected {dtype} {want} on cuda:{gpu} with contiguous heads, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}, strides {list(t.stride())}")
+    m, h, d = t.shape
     # one row has no neighbour, whatever stride it carries
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return t.data_ptr(), t.stride(0) if m > 1 else h * d
 
 
-def _writable_heads(t, dev, dtype, name, shape):
-    ptr, stride = _heads_of(t, dev, dtype, name, shape)
+def _out_heads(like, out, gpu, name, shape):
+    """``out``, or new contiguous heads like ``like``, with address and row stride."""
+    if out is None:
+        out = like.new_empty(shape)
+        return out, out.data_ptr(), shape[1] * shape[2]
+    ptr, stride = _heads_of(out, gpu, like.dtype, name, shape)
     if stride < shape[1] * shape[2]:
         raise ValueError(f"{name}: rows overlap")
-    return ptr, stride
+    return out, ptr, stride
+
+
+def _call_at(gpu, name, *args):
+    """``_call`` with this GPU current (the library launches on the current one), on its current stream."""
+    if gpu == torch._C._cuda_getDevice():
+        return _call(name, *args, torch._C._cuda_getCurrentRawStream(gpu))
+    with torch.cuda.device(gpu):
+        return _call(name, *args, torch._C._cuda_getCurrentRawStream(gpu))
 
 
 def convrot_rope_frequencies(rot_dim, base=10000.0, kind="none", factor=1.0, original_length=0.0, low=1.0, high=None,
@@ -826,27 +858,23 @@ def convrot_rope(q, k, positions, freqs, scale=1.0, layout="half", inverse=False
     k_out may be q and k."""
     if layout not in _ROPE_LAYOUTS:
         raise ValueError(f"layout: 'half' or 'interleaved', got {layout!r}")
-    io = _io_of(q, "q")
-    dev, dt = q.device, q.dtype
-    if not q.is_cuda:
-        raise ValueError(f"q: expected a CUDA tensor, got one on {dev}")
-    qp, qs = _heads_of(q, dev, dt, "q")
+    io, gpu, dt = _io_of(q, "q"), _gpu_of(q, "q"), q.dtype
+    qp, qs = _heads_of(q, gpu, dt, "q")
     M, Hq, D = q.shape
-    q_out = torch.empty((M, Hq, D), dtype=dt, device=dev) if q_out is None else q_out
-    qop, qos = _writable_heads(q_out, dev, dt, "q_out", q.shape)
+    q_out, qop, qos = _out_heads(q, q_out, gpu, "q_out", (M, Hq, D))
     Hk, kp, ks, kop, kos = 0, None, 0, None, 0
     if k is not None:
         Hk = k.shape[1] if k.dim() == 3 else 0
-        kp, ks = _heads_of(k, dev, dt, "k", (M, Hk, D))
-        k_out = torch.empty((M, Hk, D), dtype=dt, device=dev) if k_out is None else k_out
-        kop, kos = _writable_heads(k_out, dev, dt, "k_out", k.shape)
+        kp, ks = _heads_of(k, gpu, dt, "k", (M, Hk, D))
+        k_out, kop, kos = _out_heads(k, k_out, gpu, "k_out", (M, Hk, D))
     elif k_out is not None:
         raise ValueError("convrot_rope: k_out without k")
     if freqs.dim() != 1:
         raise ValueError(f"freqs: expected 1 dimension, got {freqs.dim()}")
-    _call_on(q, "convrot_rope", qp, Hq, qs, qop, qos, kp, Hk, ks, kop, kos, io, M, D, 2 * freqs.shape[0],
-             _ROPE_LAYOUTS[layout], _need_on(positions, dev, torch.int32, "positions", (M,)),
-             _need_on(freqs, dev, torch.float64, "freqs", (freqs.shape[0],)), scale, 1 if inverse else 0, _stream(q))
+    pairs = freqs.shape[0]
+    _call_at(gpu, "convrot_rope", qp, Hq, qs, qop, qos, kp, Hk, ks, kop, kos, io, M, D, 2 * pairs, _ROPE_LAYOUTS[layout],
+             _at(positions, gpu, torch.int32, "positions", (M,)), _at(freqs, gpu, torch.float64, "freqs", (pairs,)), scale,
+             1 if inverse else 0)
     return q_out, k_out
 
 
@@ -863,20 +891,20 @@ def convrot_cache_page_bytes(page: int, kv_heads: int, head_dim: int) -> int:
 _page_bytes = functools.lru_cache(maxsize=256)(convrot_cache_page_bytes)
 
 
-def _cache_of(dev, pages, table, starts, offsets, page, kv_heads, head_dim):
+def _cache_of(gpu, pages, table, starts, offsets, page, kv_heads, head_dim):
     """The C view of a cache and of a call's rows (to be kept until the call has been queued)."""
     need = _page_bytes(page, kv_heads, head_dim)
     # 0: sizes the call refuses itself
     if pages.dim() != 2 or (need != 0 and pages.shape[1] != need):
         raise ValueError(f"pages: expected [n, {need}] (convrot_cache_page_bytes), got {list(pages.shape)}")
-    if table.dim() != 2 or table.dtype != torch.int32 or table.device != dev or (table.stride(1) != 1 and table.shape[1] > 1):
-        raise ValueError(f"table: expected int32 [sequences, pages] on {dev} with contiguous rows, got {table.dtype} "
+    if (table.dim() != 2 or table.dtype is not torch.int32 or table.get_device() != gpu
+            or (table.stride(1) != 1 and table.shape[1] > 1)):
+        raise ValueError(f"table: expected int32 [sequences, pages] on cuda:{gpu} with contiguous rows, got {table.dtype} "
                          f"{list(table.shape)} on {table.device}")
     B, W = table.shape
-    return Cache(_need_on(pages, dev, torch.uint8, "pages", pages.shape), pages.shape[0], page, head_dim, kv_heads,
-                 table.data_ptr(), table.stride(0) if B > 1 else W, B, W,
-                 _need_on(starts, dev, torch.int32, "starts", (B,)),
-                 _need_on(offsets, dev, torch.int32, "offsets", (B + 1,)))
+    return Cache(_at(pages, gpu, torch.uint8, "pages", pages.shape), pages.shape[0], page, head_dim, kv_heads,
+                 table.data_ptr(), table.stride(0) if B > 1 else W, B, W, _at(starts, gpu, torch.int32, "starts", (B,)),
+                 _at(offsets, gpu, torch.int32, "offsets", (B + 1,)))
 
 
 def convrot_cache_append(pages, table, starts, offsets, k, v, page) -> None:
@@ -886,15 +914,12 @@ def convrot_cache_append(pages, table, starts, offsets, k, v, page) -> None:
     ``page`` tokens of a sequence; k and v: bf16 or fp16 [M, H, D] (heads contiguous, any row
     stride), rows offsets[b] to offsets[b + 1] (int32 [B + 1]) being sequence b's tokens from
     starts[b] (int32 [B]) on.  table, starts and offsets are on the GPU and read by the kernel only."""
-    io = _io_of(k, "k")
-    dev, dt = k.device, k.dtype
-    if not k.is_cuda:
-        raise ValueError(f"k: expected a CUDA tensor, got one on {dev}")
-    kp, ks = _heads_of(k, dev, dt, "k")
+    io, gpu, dt = _io_of(k, "k"), _gpu_of(k, "k"), k.dtype
+    kp, ks = _heads_of(k, gpu, dt, "k")
     M, H, D = k.shape
-    vp, vs = _heads_of(v, dev, dt, "v", k.shape)
-    c = _cache_of(dev, pages, table, starts, offsets, page, H, D)
-    _call_on(k, "convrot_cache_append", ctypes.byref(c), kp, ks, vp, vs, io, M, _stream(k))
+    vp, vs = _heads_of(v, gpu, dt, "v", (M, H, D))
+    c = _cache_of(gpu, pages, table, starts, offsets, page, H, D)
+    _call_at(gpu, "convrot_cache_append", ctypes.byref(c), kp, ks, vp, vs, io, M)
 
 
 def convrot_cache_read(pages, table, starts, offsets, rows, kv_heads, head_dim, page, dtype=torch.bfloat16, k=None, v=None):
@@ -902,17 +927,15 @@ def convrot_cache_read(pages, table, starts, offsets, rows, kv_heads, head_dim, 
 
     Arguments as convrot_cache_append; rows not of any sequence are left as they were (unset
     in a k or v allocated here)."""
-    dev = pages.device
-    if not pages.is_cuda:
-        raise ValueError(f"pages: expected a CUDA tensor, got one on {dev}")
+    gpu = _gpu_of(pages, "pages")
     shape = (rows, kv_heads, head_dim)
-    k = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
+    if k is None:
+        k = pages.new_empty(shape, dtype=dtype if v is None else v.dtype)
     io = _io_of(k, "k")
-    kp, ks = _writable_heads(k, dev, k.dtype, "k", shape)
-    vp, vs = _writable_heads(v, dev, k.dtype, "v", shape)
-    c = _cache_of(dev, pages, table, starts, offsets, page, kv_heads, head_dim)
-    _call_on(pages, "convrot_cache_read", ctypes.byref(c), kp, ks, vp, vs, io, rows, _stream(pages))
+    k, kp, ks = _out_heads(k, k, gpu, "k", shape)
+    v, vp, vs = _out_heads(k, v, gpu, "v", shape)
+    c = _cache_of(gpu, pages, table, starts, offsets, page, kv_heads, head_dim)
+    _call_at(gpu, "convrot_cache_read", ctypes.byref(c), kp, ks, vp, vs, io, rows)
     return k, v
 
 
@@ -933,22 +956,25 @@ def convrot_cache_attention(q, pages, table, starts, offsets, kv_heads, page, sc
     tokens are among those read.  scale is 1 / sqrt(D) if not given; window > 0 lets a token
     see only the last ``window`` tokens, itself among them; causal=False lets each see all of its
     sequence.  Rows of no sequence are left as they were (unset in an ``out`` allocated here)."""
-    io = _io_of(q, "q")
-    dev, dt = q.device, q.dtype
-    if not q.is_cuda:
-        raise ValueError(f"q: expected a CUDA tensor, got one on {dev}")
-    qp, qs = _heads_of(q, dev, dt, "q")
+    io, gpu, dt = _io_of(q, "q"), _gpu_of(q, "q"), q.dtype
+    qp, qs = _heads_of(q, gpu, dt, "q")
     M, Hq, D = q.shape
-    c = _cache_of(dev, pages, table, starts, offsets, page, kv_heads, D)
+    c = _cache_of(gpu, pages, table, starts, offsets, page, kv_heads, D)
     if out is None:
-        out = torch.empty((M, Hq, D), dtype=dt, device=dev)
+        out = q.new_empty((M, Hq, D))
         op = out.data_ptr()
     else:
-        op = _need_on(out, dev, dt, "out", q.shape)
+        op = _at(out, gpu, dt, "out", (M, Hq, D))
     need = _attention_bytes(M, Hq, kv_heads, D, c.n_seqs, c.max_pages * page)
-    ws, wp, wn = (None, None, 0) if need == 0 else _workspace_of(q, workspace, need)
-    _call_on(q, "convrot_cache_attention", ctypes.byref(c), qp, Hq, qs, io, M, D ** -0.5 if scale is None else scale,
-             1 if causal else 0, window, op, wp, wn, _stream(q))
+    wp, wn = None, 0
+    if workspace is not None:
+        wn = workspace.numel()
+        wp = _at(workspace, gpu, torch.uint8, "workspace", (wn,))
+    elif need:
+        workspace = q.new_empty(need, dtype=torch.uint8)
+        wp, wn = workspace.data_ptr(), need
+    _call_at(gpu, "convrot_cache_attention", ctypes.byref(c), qp, Hq, qs, io, M, D ** -0.5 if scale is None else scale,
+             1 if causal else 0, window, op, wp, wn)
     return out
 
 
@@ -965,5 +991,5 @@ def convrot_cache_copy(pages, pairs) -> None:
             raise ValueError(f"pairs: page {a} to {b} is outside [0, {pages.shape[-2]})")
         src[i], dst[i] = a, b
     layers = pages.shape[0] if pages.dim() == 3 else 1
-    _call_on(pages, "convrot_cache_copy", pages.data_ptr(), layers, pages.shape[-2] * pages.shape[-1], pages.shape[-2],
-             pages.shape[-1], src, dst, n, _stream(pages))
+    _call_at(pages.get_device(), "convrot_cache_copy", pages.data_ptr(), layers, pages.shape[-2] * pages.shape[-1],
+             pages.shape[-2], pages.shape[-1], src, dst, n)

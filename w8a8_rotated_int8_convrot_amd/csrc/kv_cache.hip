@@ -34,6 +34,9 @@ __device__ inline float lane_xor8(float v, int t) {
   return t == 1 ? lane_xor<1>(v) : t == 2 ? lane_xor<2>(v) : lane_xor<4>(v);
 }
 
+__device__ inline float fused(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
+__device__ inline double fused(double a, double b, double c) { return __builtin_fma(a, b, c); }
+
 // H_D of a row of D = 8 E values, lane c of eight holding [E c, E c + E).
 template <int E, typename T>
 __device__ inline void rotate_head(T (&v)[E], int c) {
@@ -48,14 +51,12 @@ __device__ inline void rotate_head(T (&v)[E], int c) {
       }
     }
   }
+  // the upper lane of a pair keeps the difference: its own value enters negated
 #pragma unroll
   for (int t = 1; t < 8; t <<= 1) {
-    const bool upper = (c & t) != 0;
+    const T sign = (c & t) != 0 ? T(-1) : T(1);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const T other = lane_xor8(v[i], t);
-      v[i] = upper ? other - v[i] : v[i] + other;
-    }
+    for (int i = 0; i < E; ++i) v[i] = fused(v[i], sign, lane_xor8(v[i], t));
   }
 }
 
@@ -85,26 +86,42 @@ __device__ inline void encode(const uint4 (&raw)[E / 8], int c, uint32_t (&w)[E 
   top = fmax(top, lane_xor8(top, 1));
   top = fmax(top, lane_xor8(top, 2));
   top = fmax(top, lane_xor8(top, 4));
-  // one value that is not finite makes every sum of its row so, and fmax passes
-  // over NaN only beside a number
-  bool finite = true;
-#pragma unroll
-  for (int i = 0; i < E; ++i) finite = finite && fabs(v[i]) < __builtin_inf();
+  // one value that is not finite makes every sum of its row so (fmax passes over NaN)
+  const bool finite = fabs(v[0]) < __builtin_inf();
   const auto s16 = static_cast<__bf16>(static_cast<float>(top / 7.0));
   const float s = static_cast<float>(s16);
   scale = __builtin_bit_cast(uint16_t, s16);
   if (!finite || !(s < __builtin_inff())) scale = 0x7fc0u;
   const bool coded = finite && s > 0.0f && s < __builtin_inff();
-  const double sd = static_cast<double>(s);
+  // the whole number nearest to v / s by a reciprocal of 24 bits (added to 1.5 * 2^52 it
+  // stands in the low bits): right where the remainder, which is exact, is below half a
+  // scale; one that is not, about a code in a million, makes the wave divide
+  const double sd = static_cast<double>(s), inverse = static_cast<double>(__builtin_amdgcn_rcpf(s));
+  constexpr double kWhole = 6755399441055744.0;
+  double worst = 0.0;
 #pragma unroll
   for (int j = 0; j < E / 8; ++j) {
-    w[j] = 0;
+    w[j] = 0x88888888u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const double q = coded ? fmin(fmax(rint(v[8 * j + i] / sd), -7.0), 7.0) : 0.0;
-      w[j] |= static_cast<uint32_t>(static_cast<int>(q) + 8) << (4 * i);
+      const double at = __builtin_fma(v[8 * j + i], inverse, kWhole);
+      worst = fmax(worst, fabs(__builtin_fma(kWhole - at, sd, v[8 * j + i])));
+      w[j] += static_cast<uint32_t>(__builtin_bit_cast(uint64_t, at)) << (4 * i);
     }
   }
+  if (__any(coded && !(worst < 0.5 * sd && s >= 0x1p-120f))) {
+#pragma unroll
+    for (int j = 0; j < E / 8; ++j) {
+      w[j] = 0x88888888u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double q = coded ? fmin(fmax(rint(v[8 * j + i] / sd), -7.0), 7.0) : 0.0;
+        w[j] += static_cast<uint32_t>(static_cast<int>(q)) << (4 * i);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < E / 8; ++j) w[j] = coded ? w[j] : 0x88888888u;
 }
 
 template <int D, typename In, int E = D / 8>
