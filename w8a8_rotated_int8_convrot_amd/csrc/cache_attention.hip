@@ -40,7 +40,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr bool PREF = true;
 constexpr int W128 = 2, W64 = 3;
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * 64;
@@ -163,18 +162,21 @@ struct UnitReader {
   int32_t entry;
   uint32_t scale;                       // of the last unit: key lane, or value lane - 32
 
-  __device__ UnitReader(const Cache& cache, int b, int h)
-      : c(cache), table(cache.table + b * cache.table_stride), head(h), held(-64), entry(-1), scale(0) {}
+  __device__ UnitReader(const Cache& cache, int b, int h, int column)
+      : c(cache), table(cache.table + b * cache.table_stride), head(h), scale(0) {
+    hold(column);
+  }
+  __device__ void hold(int column) {
+    held = column;
+    const int at = column + static_cast<int>(threadIdx.x & 63);
+    entry = at < (c.max_tokens >> c.page_shift) ? table[at] : -1;
+  }
 
   // False where no page of the cache is named; the words are then another page's.
   __device__ bool load(int u, UnitWords<D>& w) {
     const int shift = c.page_shift - 5, lane = threadIdx.x & 63;
     const int column = u >> shift;
-    if (column < held || column >= held + 64) {
-      held = column;
-      const int at = column + lane;
-      entry = at < (c.max_tokens >> c.page_shift) ? table[at] : -1;
-    }
+    if (column < held || column >= held + 64) hold(column);
     const int64_t page = __builtin_amdgcn_readlane(entry, column - held);
     const bool there = page >= 0 && page < c.n_pages;
     const uint8_t* unit = c.pages + (there ? page * c.page_bytes : 0) +
@@ -246,9 +248,11 @@ struct Columns {
   int full_from, full_to;               // keys that every column sees
   int any_from, any_to;                 // keys that some column sees
 
-  // Columns of tile rows [row0, row0 + 16 NT) of a sequence's n * group rows.
-  template <typename In>
-  __device__ void open(const Attention& a, int group, int kv_head, int off, int n, int64_t start, int length, int row0) {
+  // Columns of tile rows [row0, row0 + 16 NT) of a sequence's n * group rows; meanwhile()
+  // is called while their queries are on the way.
+  template <typename In, typename F>
+  __device__ __forceinline__ void open(const Attention& a, int group, int kv_head, int off, int n, int64_t start,
+                                       int length, int row0, F&& meanwhile) {
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     // bounds grow from token to token
     constexpr int E = D / 4;            // dims of a lane
@@ -264,6 +268,7 @@ struct Columns {
       signs[0] = kOne ^ quarter ^ one;
       signs[1] = signs[0] ^ two;
     }
+    uint32_t raw[NT][E / 2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int row = row0 + 16 * t + col;
@@ -272,23 +277,25 @@ struct Columns {
       const int head = kv_head * group + (live ? row - i * group : 0);
       from[t] = 0, to[t] = 0x7fffffff;
       if (live) bounds_of(a, start, length, i, from[t], to[t]);
-
+      const In* p = static_cast<const In*>(a.q) + (static_cast<int64_t>(off) + i) * a.q_stride +
+                    static_cast<int64_t>(head) * D + g * E;
+#pragma unroll
+      for (int j = 0; j < E / 8; ++j) {
+        const uint4 r = live ? reinterpret_cast<const uint4*>(p)[j] : make_uint4(0, 0, 0, 0);
+        raw[t][4 * j] = r.x, raw[t][4 * j + 1] = r.y, raw[t][4 * j + 2] = r.z, raw[t][4 * j + 3] = r.w;
+      }
+    }
+    meanwhile();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
       // H_D of the query: five bits of the dim by a product with +-1 (exact, sums in
       // fp32), the others, those of the chunk, by sums inside the lane.  A lane has dims
       // [E g, E (g + 1)), as of the keys: in chunk k the eight of bits 0, 1 and the
       // highest of them, and out come rows 4 g + i of two tiles, bits 0, 1 and that one.
-      const In* p = static_cast<const In*>(a.q) + (static_cast<int64_t>(off) + i) * a.q_stride +
-                    static_cast<int64_t>(head) * D + g * E;
-      uint32_t raw[E / 2];
-#pragma unroll
-      for (int j = 0; j < E / 8; ++j) {
-        const uint4 r = live ? reinterpret_cast<const uint4*>(p)[j] : make_uint4(0, 0, 0, 0);
-        raw[4 * j] = r.x, raw[4 * j + 1] = r.y, raw[4 * j + 2] = r.z, raw[4 * j + 3] = r.w;
-      }
       float v[E];
 #pragma unroll
       for (int k = 0; k < E / 8; ++k) {
-        const uint32_t in[4] = {raw[2 * k], raw[2 * k + 1], raw[E / 4 + 2 * k], raw[E / 4 + 2 * k + 1]};
+        const uint32_t in[4] = {raw[t][2 * k], raw[t][2 * k + 1], raw[t][E / 4 + 2 * k], raw[t][E / 4 + 2 * k + 1]};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t flip = h != 0 ? 0x80008000u : 0u;
@@ -522,15 +529,16 @@ struct Columns {
     return fmaxf(__builtin_amdgcn_logf(most), kLeastScale);
   }
 
-  // Units first, first + by, ... below last, each loaded while the one before is worked on.
-  __device__ __forceinline__ void run(UnitReader<D>& reader, int first, int last, int by) {
+  // Units first, first + by, ... below last, each loaded while the one before is worked on;
+  // the first is in a already.
+  __device__ __forceinline__ void run(UnitReader<D>& reader, UnitWords<D>& a, bool there_a, int first, int last, int by) {
     if (first >= last) return;
     const Spread spread;
     auto take = [&](const UnitWords<D>& w, int u, bool there) {
       if (there) step(UnitOfWords<D>{w, spread}, u);
     };
-    UnitWords<D> a, b;
-    bool there_a = reader.load(first, a), there_b = false;
+    UnitWords<D> b;
+    bool there_b = false;
     for (int u = first;;) {
       if (u + by < last) there_b = reader.load(u + by, b);
       take(a, u, there_a);
@@ -587,7 +595,7 @@ __device__ inline void finish(float (&v)[E], float l, int part, In* out) {
 
 // The tile a workgroup has: rows [row0, ...) of sequence b.
 struct Tile {
-  int b, off, n, row0;
+  int b, off, n, row0, start;
 };
 
 // Tile `index` of all sequences' tiles of `rows` rows, a sequence's last first
@@ -599,7 +607,11 @@ __device__ inline bool find_tile(const Attention& a, int group, int rows, int fe
   for (int b0 = 0; b0 < a.cache.n_seqs; b0 += 64) {
     const int b = b0 + lane;
     Span s{0, 0};
-    if (b < a.cache.n_seqs) s = span_of(a.offsets, b, a.M);
+    int start = 0;
+    if (b < a.cache.n_seqs) {
+      s = span_of(a.offsets, b, a.M);
+      start = a.starts[b];
+    }
     const int64_t all = static_cast<int64_t>(s.end - s.off) * group;
     const int mine = all > few && all <= many ? static_cast<int>((all + rows - 1) / rows) : 0;
     int sum = mine;
@@ -615,6 +627,7 @@ __device__ inline bool find_tile(const Attention& a, int group, int rows, int fe
       tile.b = b0 + l;
       tile.off = __builtin_amdgcn_readlane(s.off, l);
       tile.n = __builtin_amdgcn_readlane(s.end, l) - tile.off;
+      tile.start = __builtin_amdgcn_readlane(start, l);
       const int at = index - before - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l));
       tile.row0 = (__builtin_amdgcn_readlane(mine, l) - 1 - at) * rows;
       return true;
@@ -637,27 +650,28 @@ struct Staged {
   float scale[kUnits][64];
   int there[kUnits];
 
-  template <int NT>
-  __device__ void run(Columns<D, NT>& c, UnitReader<D>& reader, int first, int last, bool idle) {
-    const int wave = wave_index(), lane = threadIdx.x & 63;
-    const int mine = wave % kUnits, part = wave / kUnits;
-    const Spread spread;
+  // A wave's share of a group on its way: a unit's words, and the scale of key lane, or
+  // of value lane - 32.
+  struct Share {
     UnitWords<D> w;
-    uint32_t s = 0;
+    uint32_t scale = 0;
     bool held = false;
-    auto load = [&](int u) {
-      held = false;
-      if (u < last) {
-        held = reader.load(u, w);
-        // lanes 0-31: of a key, 32-63: of a value
-        s = reader.scale;
-      }
-    };
-    if (PREF) load(first + mine);
+    __device__ void load(UnitReader<D>& reader, int u, int last) {
+      held = u < last && reader.load(u, w);
+      scale = reader.scale;
+    }
+  };
+  static __device__ int mine() { return wave_index() % kUnits; }
+
+  // Units [first, last), this wave's share of the first group on its way.
+  template <int NT>
+  __device__ __forceinline__ void run(Columns<D, NT>& c, UnitReader<D>& reader, Share& next, int first, int last, bool idle) {
+    const int lane = threadIdx.x & 63;
+    const int mine = Staged::mine(), part = wave_index() / kUnits;
+    const Spread spread;
     for (int u0 = first; u0 < last; u0 += kUnits) {
-      if (!PREF) load(u0 + mine);
       if (u0 != first) __syncthreads();
-      const UnitOfWords<D> unit{w, spread};
+      const UnitOfWords<D> unit{next.w, spread};
 #pragma unroll
       for (int q = 0; q < kParts; ++q) {
         if (part == q) {
@@ -668,10 +682,10 @@ struct Staged {
         }
       }
       if (part == 0) {
-        scale[mine][lane] = __uint_as_float(s << 16);
-        if (lane == 0) there[mine] = held;
+        scale[mine][lane] = __uint_as_float(next.scale << 16);
+        if (lane == 0) there[mine] = next.held;
       }
-      if (PREF) load(u0 + kUnits + mine);
+      next.load(reader, u0 + kUnits + mine, last);
       __syncthreads();
       const int i0 = max(0, c.any_from / kUnit - u0), i1 = idle ? 0 : min(kUnits, (c.any_to + kUnit - 1) / kUnit - u0);
       c.steps([&](int i) { return StagedUnit<D>{&piece[i][0][0], scale[i]}; }, [&](int i) { return there[i] != 0; }, u0, i0, i1);
@@ -692,29 +706,32 @@ __global__ __launch_bounds__(kAttnThreads, WPE(D, NT, SHARED)) void attention_ke
   Tile tile;
   if (!find_tile(a, group, kRows, few, many, static_cast<int>(blockIdx.x / static_cast<unsigned>(kv_heads)), tile)) return;
   const int wave = wave_index(), lane = threadIdx.x & 63;
-  const int64_t start = a.starts[tile.b];
+  const int64_t start = tile.start;
   const int length = static_cast<int>(max(int64_t{0}, min(start + tile.n, static_cast<int64_t>(a.cache.max_tokens))));
-  Columns<D, NT> c;
   const int row0 = tile.row0 + (SHARED ? 0 : 16 * NT * wave);
   const int all = tile.n * group;
   const bool idle = row0 >= all;        // a wave behind the tile's rows: it only stages
-  c.template open<In>(a, group, kv_head, tile.off, tile.n, start, length, idle ? tile.row0 : row0);
-  // this part's keys of the whole tile, and of this wave's columns
-  int tile_from = c.any_from, tile_to = c.any_to;
-  if constexpr (!SHARED) {
-    int unused;
-    bounds_of(a, start, length, tile.row0 / group, tile_from, unused);
-    bounds_of(a, start, length, (min(tile.row0 + kRows, all) - 1) / group, unused, tile_to);
-  }
+  // this part's keys of the whole tile
+  int tile_from, tile_to, unused;
+  bounds_of(a, start, length, tile.row0 / group, tile_from, unused);
+  bounds_of(a, start, length, (min(tile.row0 + kRows, all) - 1) / group, unused, tile_to);
   const int part_from = part * a.chunk, part_to = part == a.splits - 1 ? 0x7fffffff : (part + 1) * a.chunk;
   const int lo = max(tile_from, part_from), hi = min(tile_to, part_to);
   const int first = lo / kUnit, last = lo < hi ? (hi + kUnit - 1) / kUnit : 0;
-  UnitReader<D> reader(a.cache, tile.b, kv_head);
+  UnitReader<D> reader(a.cache, tile.b, kv_head, first >> (a.cache.page_shift - 5));
+  Columns<D, NT> c;
   if constexpr (SHARED) {
-    c.run(reader, first + wave, last, kAttnWaves);
+    UnitWords<D> words;
+    bool there = false;
+    c.template open<In>(a, group, kv_head, tile.off, tile.n, start, length, row0,
+                        [&] { there = first + wave < last && reader.load(first + wave, words); });
+    c.run(reader, words, there, first + wave, last, kAttnWaves);
   } else {
     __shared__ Staged<D> staged;
-    staged.run(c, reader, first, last, idle);
+    typename Staged<D>::Share share;
+    c.template open<In>(a, group, kv_head, tile.off, tile.n, start, length, idle ? tile.row0 : row0,
+                        [&] { share.load(reader, first + Staged<D>::mine(), last); });
+    staged.run(c, reader, share, first, last, idle);
     if (idle) return;
   }
 
@@ -916,6 +933,17 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
     const float2* heads = reinterpret_cast<const float2*>(a.part + a.splits * rows * D) + p0 * rows + row;
     const float* sums = a.part + (p0 * rows + row) * D + piece * E;
     const float2 head = lane < n ? heads[lane * rows] : make_float2(kNoReference, 0.0f);
+    // the sums of four parts, one for each 16 lanes, on their way before they are used
+    float next[E];
+    auto fetch = [&](int p) {
+      const float* x = sums + min(p + g, n - 1) * rows * D;
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(x + e);
+        next[e] = y.x, next[e + 1] = y.y, next[e + 2] = y.z, next[e + 3] = y.w;
+      }
+    };
+    fetch(0);
     float m = head.x;
     m = fmaxf(m, lane_xor<1>(m));
     m = fmaxf(m, lane_xor<2>(m));
@@ -930,19 +958,14 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
     l += lane_xor<8>(l);
     l = column_sum(l);
     for (int p = 0; p < n; p += 4) {
-      const int mine = min(p + g, n - 1);
-      const float fp = __shfl(f, mine);
-      const float w = p + g < n ? fp : 0.0f;
-      const float* x = sums + mine * rows * D;
+      float x[E];
 #pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const float4 y = *reinterpret_cast<const float4*>(x + e);
-        // a part left out by its lane is not multiplied: it may be NaN
-        v[e] = p + g < n ? __builtin_fmaf(y.x, w, v[e]) : v[e];
-        v[e + 1] = p + g < n ? __builtin_fmaf(y.y, w, v[e + 1]) : v[e + 1];
-        v[e + 2] = p + g < n ? __builtin_fmaf(y.z, w, v[e + 2]) : v[e + 2];
-        v[e + 3] = p + g < n ? __builtin_fmaf(y.w, w, v[e + 3]) : v[e + 3];
-      }
+      for (int e = 0; e < E; ++e) x[e] = next[e];
+      if (p + 4 < n) fetch(p + 4);
+      const float w = __shfl(f, min(p + g, n - 1));
+      // a part behind the last is not multiplied: what was read for it may be NaN
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = p + g < n ? __builtin_fmaf(x[e], w, v[e]) : v[e];
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = column_sum(v[e]);
