@@ -40,7 +40,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr int W128 = 2, W64 = 3;
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * 64;
 // A column's largest rounded weight lies in [2^kTop, 2^(kTop + kRise)], far
@@ -160,10 +159,9 @@ struct UnitReader {
   const int32_t* table;
   int head, held;                       // first table column held
   int32_t entry;
-  uint32_t scale;                       // of the last unit: key lane, or value lane - 32
 
   __device__ UnitReader(const Cache& cache, int b, int h, int column)
-      : c(cache), table(cache.table + b * cache.table_stride), head(h), scale(0) {
+      : c(cache), table(cache.table + b * cache.table_stride), head(h) {
     hold(column);
   }
   __device__ void hold(int column) {
@@ -172,60 +170,42 @@ struct UnitReader {
     entry = at < (c.max_tokens >> c.page_shift) ? table[at] : -1;
   }
 
-  // False where no page of the cache is named; the words are then another page's.
-  __device__ bool load(int u, UnitWords<D>& w) {
-    const int shift = c.page_shift - 5, lane = threadIdx.x & 63;
+  // A unit; where no page of the cache is named for it another page's, and there = false.
+  __device__ __forceinline__ const uint8_t* place(int u, bool& there) {
+    const int shift = c.page_shift - 5;
     const int column = u >> shift;
     if (column < held || column >= held + 64) hold(column);
     const int64_t page = __builtin_amdgcn_readlane(entry, column - held);
-    const bool there = page >= 0 && page < c.n_pages;
-    const uint8_t* unit = c.pages + (there ? page * c.page_bytes : 0) +
-                          static_cast<int64_t>((head << shift) + (u & ((1 << shift) - 1))) * unit_bytes(D);
-    const int m = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      load_words(unit + (8 * (m >> 2) + 4 * t + (m & 3)) * (D / 2) + g * (D / 8), w.k[t]);
+    there = page >= 0 && page < c.n_pages;
+    return c.pages + (there ? page * c.page_bytes : 0) +
+           static_cast<int64_t>((head << shift) + (u & ((1 << shift) - 1))) * unit_bytes(D);
+  }
+  // The key words of tile h and four of the value words.
+  static __device__ __forceinline__ void load_keys(const uint8_t* unit, int h, uint32_t (&w)[D / 32]) {
+    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    load_words(unit + (8 * (m >> 2) + 4 * h + (m & 3)) * (D / 2) + g * (D / 8), w);
+  }
+  static __device__ __forceinline__ void load_values(const uint8_t* unit, int i, uint32_t (&w)[4]) {
+    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    load_words(unit + value_codes_at(D) + (g * D + 64 * i + 4 * m) * 4, w);
+  }
+
+  __device__ __forceinline__ bool load(int u, UnitWords<D>& w) {
+    const int g = (threadIdx.x & 63) >> 4;
+    bool there;
+    const uint8_t* unit = place(u, there);
+    load_keys(unit, 0, w.k[0]);
+    load_keys(unit, 1, w.k[1]);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
       uint32_t r[4];
-      load_words(unit + value_codes_at(D) + (g * D + 64 * i + 4 * m) * 4, r);
+      load_values(unit, i, r);
 #pragma unroll
       for (int j = 0; j < 4; ++j) w.v[4 * i + j] = r[j];
     }
     w.ks = *reinterpret_cast<const uint4*>(unit + key_scales_at(D) + 16 * g);
     w.vs = *reinterpret_cast<const uint4*>(unit + value_scales_at(D) + 16 * g);
-    scale = reinterpret_cast<const uint16_t*>(unit + key_scales_at(D))[lane];
     return there;
-  }
-};
-
-// The two views of a unit that a step takes: a lane's own words, or the operands of
-// both products as a workgroup has left them in LDS for all its waves.
-template <int D> struct UnitOfWords {
-  const UnitWords<D>& w;
-  const Spread& spread;
-  __device__ v4i key(int h, int k) const { return key_codes(w.k[h][2 * k], w.k[h][2 * k + 1]); }
-  __device__ v8h value(int d) const { return codes_of(w.v[d], spread); }
-  __device__ void scales(float (&ks)[8], float (&vs)[8]) const {
-    widen_scales(w.ks, ks);
-    widen_scales(w.vs, vs);
-  }
-};
-template <int D> struct StagedUnit {
-  static constexpr int kKeys = 2 * (D / 64), kPieces = kKeys + D / 16;
-  const uint4* piece;                   // [kPieces][64]: a lane's 16 bytes of each
-  const float* scale;                   // of 32 keys, then of 32 values
-  __device__ v4i key(int h, int k) const {
-    return __builtin_bit_cast(v4i, piece[(h * (D / 64) + k) * 64 + (threadIdx.x & 63)]);
-  }
-  __device__ v8h value(int d) const { return __builtin_bit_cast(v8h, piece[(kKeys + d) * 64 + (threadIdx.x & 63)]); }
-  __device__ void scales(float (&ks)[8], float (&vs)[8]) const {
-    const int g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ks[i] = scale[8 * g + i];
-      vs[i] = scale[kUnit + 8 * g + i];
-    }
   }
 };
 
@@ -234,6 +214,79 @@ __device__ inline void bounds_of(const Attention& a, int64_t start, int length, 
   const int64_t pos = start + i;
   end = a.causal ? static_cast<int>(max(int64_t{0}, min(pos + 1, static_cast<int64_t>(length)))) : length;
   first = a.window != 0 ? static_cast<int>(max(int64_t{0}, min(pos + 1 - a.window, int64_t{0x7fffffff}))) : 0;
+}
+
+// H_D of a query: five bits of the dim by a product with +-1 (exact, sums in fp32), the
+// others, those of the chunk, by sums inside the lane.  A lane has dims [E g, E (g + 1)),
+// E = D / 4, as of the keys: in chunk k the eight of bits 0, 1 and the highest of them,
+// and out come rows 4 g + i of two tiles, bits 0, 1 and that one.
+// The +-1 of row 4 r + i and dims (bits 0, 1, of quarter g): the parity of the bits that
+// both have.
+template <typename In>
+__device__ inline void query_signs(uint32_t (&signs)[2]) {
+  constexpr uint32_t kOne = std::is_same_v<In, _Float16> ? 0x3c003c00u : 0x3f803f80u;
+  const int col = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  const uint32_t quarter = __builtin_popcount((col >> 2) & g) & 1 ? 0x80008000u : 0u;
+  const uint32_t one = (col & 1) != 0 ? 0x80000000u : 0u, two = (col & 2) != 0 ? 0x80008000u : 0u;
+  signs[0] = kOne ^ quarter ^ one;
+  signs[1] = signs[0] ^ two;
+}
+template <int D, typename In, int E = D / 4>
+__device__ inline void rotate_query(const uint32_t (&raw)[E / 2], const uint32_t (&signs)[2], float (&v)[E]) {
+#pragma unroll
+  for (int k = 0; k < E / 8; ++k) {
+    const uint32_t in[4] = {raw[2 * k], raw[2 * k + 1], raw[E / 4 + 2 * k], raw[E / 4 + 2 * k + 1]};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t flip = h != 0 ? 0x80008000u : 0u;
+      const uint32_t sign[4] = {signs[0], signs[1], signs[0] ^ flip, signs[1] ^ flip};
+      const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      v4f r;
+      if constexpr (std::is_same_v<In, _Float16>)
+        r = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, sign), __builtin_bit_cast(v8h, in), zero, 0, 0, 0);
+      else
+        r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, sign), __builtin_bit_cast(v8bf, in), zero, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[E / 2 * h + 4 * k + e] = r[e];
+    }
+  }
+#pragma unroll
+  for (int h = 4; h < E / 2; h <<= 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if ((e & h) == 0) {
+        const float x = v[e], y = v[e + h];
+        v[e] = x + y;
+        v[e + h] = x - y;
+      }
+    }
+  }
+}
+
+// Rows row0 + 16 t + lane % 16 of a sequence's n * group: their queries' words as they
+// lie, and the keys each sees; padding sees everything, so that it never masks a unit.
+template <int D, int NT, typename In>
+__device__ __forceinline__ void fetch_queries(const Attention& a, int group, int kv_head, int off, int n, int64_t start,
+                                              int length, int row0, uint32_t (&raw)[NT][D / 8], int (&from)[NT],
+                                              int (&to)[NT]) {
+  constexpr int E = D / 4;
+  const int col = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4, all = n * group;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int row = row0 + 16 * t + col;
+    const bool live = row < all;
+    const int i = live ? row / group : 0;
+    const int head = kv_head * group + (live ? row - i * group : 0);
+    from[t] = 0, to[t] = 0x7fffffff;
+    if (live) bounds_of(a, start, length, i, from[t], to[t]);
+    const In* p = static_cast<const In*>(a.q) + (static_cast<int64_t>(off) + i) * a.q_stride +
+                  static_cast<int64_t>(head) * D + g * E;
+#pragma unroll
+    for (int j = 0; j < E / 8; ++j) {
+      const uint4 r = live ? reinterpret_cast<const uint4*>(p)[j] : make_uint4(0, 0, 0, 0);
+      raw[t][4 * j] = r.x, raw[t][4 * j + 1] = r.y, raw[t][4 * j + 2] = r.z, raw[t][4 * j + 3] = r.w;
+    }
+  }
 }
 
 // 16 NT query columns of a wave: their queries, bounds and running sums.
@@ -253,74 +306,20 @@ struct Columns {
   template <typename In, typename F>
   __device__ __forceinline__ void open(const Attention& a, int group, int kv_head, int off, int n, int64_t start,
                                        int length, int row0, F&& meanwhile) {
-    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     // bounds grow from token to token
     constexpr int E = D / 4;            // dims of a lane
     const int all = n * group;
     bounds_of(a, start, length, row0 / group, any_from, full_to);
     bounds_of(a, start, length, (min(row0 + 16 * NT, all) - 1) / group, full_from, any_to);
-    // +-1 of row 4 r + i and dims (bits 0, 1, of quarter g): the parity of the bits both have
     uint32_t signs[2];
-    {
-      constexpr uint32_t kOne = std::is_same_v<In, _Float16> ? 0x3c003c00u : 0x3f803f80u;
-      const uint32_t quarter = __builtin_popcount((col >> 2) & g) & 1 ? 0x80008000u : 0u;
-      const uint32_t one = (col & 1) != 0 ? 0x80000000u : 0u, two = (col & 2) != 0 ? 0x80008000u : 0u;
-      signs[0] = kOne ^ quarter ^ one;
-      signs[1] = signs[0] ^ two;
-    }
+    query_signs<In>(signs);
     uint32_t raw[NT][E / 2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int row = row0 + 16 * t + col;
-      const bool live = row < all;
-      const int i = live ? row / group : 0;
-      const int head = kv_head * group + (live ? row - i * group : 0);
-      from[t] = 0, to[t] = 0x7fffffff;
-      if (live) bounds_of(a, start, length, i, from[t], to[t]);
-      const In* p = static_cast<const In*>(a.q) + (static_cast<int64_t>(off) + i) * a.q_stride +
-                    static_cast<int64_t>(head) * D + g * E;
-#pragma unroll
-      for (int j = 0; j < E / 8; ++j) {
-        const uint4 r = live ? reinterpret_cast<const uint4*>(p)[j] : make_uint4(0, 0, 0, 0);
-        raw[t][4 * j] = r.x, raw[t][4 * j + 1] = r.y, raw[t][4 * j + 2] = r.z, raw[t][4 * j + 3] = r.w;
-      }
-    }
+    fetch_queries<D, NT, In>(a, group, kv_head, off, n, start, length, row0, raw, from, to);
     meanwhile();
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      // H_D of the query: five bits of the dim by a product with +-1 (exact, sums in
-      // fp32), the others, those of the chunk, by sums inside the lane.  A lane has dims
-      // [E g, E (g + 1)), as of the keys: in chunk k the eight of bits 0, 1 and the
-      // highest of them, and out come rows 4 g + i of two tiles, bits 0, 1 and that one.
       float v[E];
-#pragma unroll
-      for (int k = 0; k < E / 8; ++k) {
-        const uint32_t in[4] = {raw[t][2 * k], raw[t][2 * k + 1], raw[t][E / 4 + 2 * k], raw[t][E / 4 + 2 * k + 1]};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t flip = h != 0 ? 0x80008000u : 0u;
-          const uint32_t sign[4] = {signs[0], signs[1], signs[0] ^ flip, signs[1] ^ flip};
-          const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-          v4f r;
-          if constexpr (std::is_same_v<In, _Float16>)
-            r = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, sign), __builtin_bit_cast(v8h, in), zero, 0, 0, 0);
-          else
-            r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, sign), __builtin_bit_cast(v8bf, in), zero, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[E / 2 * h + 4 * k + e] = r[e];
-        }
-      }
-#pragma unroll
-      for (int h = 4; h < E / 2; h <<= 1) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if ((e & h) == 0) {
-            const float x = v[e], y = v[e + h];
-            v[e] = x + y;
-            v[e + h] = x - y;
-          }
-        }
-      }
+      rotate_query<D, In>(raw[t], signs, v);
       float top = 0.0f;
 #pragma unroll
       for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(v[e]));
@@ -365,21 +364,19 @@ struct Columns {
     }
   }
 
-  // The steps of a unit, apart, so that the products of one can run beside the
-  // exponentials of another.
-  struct Scores {
-    v4i high[NT][2], low[NT][2];
-  };
-  struct Weights {
-    v8h p[NT];
-  };
-  template <typename Unit>
-  __device__ __forceinline__ void scores(const Unit& unit, Scores& s) const {
+  // One unit; where some column does not see all of it, masked.
+  __device__ __forceinline__ void step(const UnitWords<D>& w, const Spread& spread, int u) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const bool masked = kUnit * u < full_from || kUnit * u + kUnit > full_to;
+    float ks[8], vs[8];
+    widen_scales(w.ks, ks);
+    widen_scales(w.vs, vs);
+    float y[NT][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       v4i key[D / 64];
 #pragma unroll
-      for (int k = 0; k < D / 64; ++k) key[k] = unit.key(h, k);
+      for (int k = 0; k < D / 64; ++k) key[k] = key_codes(w.k[h][2 * k], w.k[h][2 * k + 1]);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         v4i high = {0, 0, 0, 0}, low = {eight[t], eight[t], eight[t], eight[t]};
@@ -388,23 +385,10 @@ struct Columns {
           high = __builtin_amdgcn_mfma_i32_16x16x64_i8(key[k], hi[t][k], high, 0, 0, 0);
           low = __builtin_amdgcn_mfma_i32_16x16x64_i8(key[k], lo[t][k], low, 0, 0, 0);
         }
-        s.high[t][h] = high;
-        s.low[t][h] = low;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[t][4 * h + i] = static_cast<float>((high[i] << 8) + low[i]) * ks[4 * h + i];
       }
     }
-  }
-  // Scores times the keys' scales.
-  static __device__ __forceinline__ void scale(const Scores& s, const float (&ks)[8], float (&y)[NT][8]) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[t][i] = static_cast<float>((s.high[t][i >> 2][i & 3] << 8) + s.low[t][i >> 2][i & 3]) * ks[i];
-  }
-  // Hides what a column does not see (of a unit that no page holds, everything) and
-  // moves the references where that is due; whether anything is hidden.
-  __device__ __forceinline__ bool settle(float (&y)[NT][8], const float (&vs)[8], int u, bool there) {
-    const int g = (threadIdx.x & 63) >> 4;
-    const bool masked = !there || kUnit * u < full_from || kUnit * u + kUnit > full_to;
     float by[NT];
     const float large = log_scale(vs);
 #pragma unroll
@@ -416,7 +400,7 @@ struct Columns {
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const bool seen = there && first + i >= from[t] && first + i < to[t];
+          const bool seen = first + i >= from[t] && first + i < to[t];
           y[t][i] = seen ? y[t][i] : kHidden;
           v[i] = seen ? vs[i] : 0.0f;
         }
@@ -447,79 +431,35 @@ struct Columns {
         }
       }
     }
-    return masked;
-  }
-  template <bool HIDDEN>
-  __device__ __forceinline__ void weights(const float (&y)[NT][8], const float (&vs)[8], Weights& w) {
+    v8h p[NT];
+    auto weights = [&](auto hidden) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float e[8], v[8];
+      for (int t = 0; t < NT; ++t) {
+        float e[8], v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[t][i], qs[t], -m[t]));
-        v[i] = e[i] * vs[i];
-        if constexpr (HIDDEN) {
-          // nothing of a key that is not seen, whatever its place holds
-          e[i] = y[t][i] == kHidden ? 0.0f : e[i];
-          v[i] = y[t][i] == kHidden ? 0.0f : v[i];
+        for (int i = 0; i < 8; ++i) {
+          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[t][i], qs[t], -m[t]));
+          v[i] = e[i] * vs[i];
+          if constexpr (hidden.value) {
+            // nothing of a key that is not seen, whatever its place holds
+            e[i] = y[t][i] == kHidden ? 0.0f : e[i];
+            v[i] = y[t][i] == kHidden ? 0.0f : v[i];
+          }
         }
-      }
-      l[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-      v2h pairs[4];
+        l[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+        v2h pairs[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{v[i], v[i + 4]}), v2h);
-      w.p[t] = __builtin_bit_cast(v8h, pairs);
-    }
-  }
-  template <typename Unit>
-  __device__ __forceinline__ void add(const Unit& unit, const Weights& w) {
+        for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{v[i], v[i + 4]}), v2h);
+        p[t] = __builtin_bit_cast(v8h, pairs);
+      }
+    };
+    if (masked) weights(std::true_type{});
+    else weights(std::false_type{});
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
-      const v8h value = unit.value(d);
+      const v8h value = codes_of(w.v[d], spread);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, w.p[t], o[t][d], 0, 0, 0);
-    }
-  }
-
-  template <typename Unit>
-  __device__ __forceinline__ void step(const Unit& unit, int u) {
-    float ks[8], vs[8], y[NT][8];
-    unit.scales(ks, vs);
-    Scores s;
-    scores(unit, s);
-    scale(s, ks, y);
-    Weights w;
-    if (settle(y, vs, u, true)) weights<true>(y, vs, w);
-    else weights<false>(y, vs, w);
-    add(unit, w);
-  }
-
-  // Units [i0, i1) of a staged group, unit(i) its i-th, there(i) whether a page holds it:
-  // the scores of each beside the exponentials of the one before, whose product with
-  // the values runs beside the next one's scaling.
-  template <typename Unit, typename There>
-  __device__ __forceinline__ void steps(Unit&& unit, There&& there, int u0, int i0, int i1) {
-    if (i0 >= i1) return;
-    float ks[8], vs[8], y[NT][8];
-    Scores s;
-    unit(i0).scales(ks, vs);
-    scores(unit(i0), s);
-    scale(s, ks, y);
-#pragma unroll 1
-    for (int i = i0; i < i1; ++i) {
-      const int next = min(i + 1, i1 - 1);
-      const auto after = unit(next);
-      Weights w;
-      if (settle(y, vs, u0 + i, there(i))) {
-        weights<true>(y, vs, w);
-        scores(after, s);
-      } else {
-        scores(after, s);
-        weights<false>(y, vs, w);
-      }
-      after.scales(ks, vs);
-      add(unit(i), w);
-      scale(s, ks, y);
+      for (int t = 0; t < NT; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[t], o[t][d], 0, 0, 0);
     }
   }
 
@@ -535,7 +475,7 @@ struct Columns {
     if (first >= last) return;
     const Spread spread;
     auto take = [&](const UnitWords<D>& w, int u, bool there) {
-      if (there) step(UnitOfWords<D>{w, spread}, u);
+      if (there) step(w, spread, u);
     };
     UnitWords<D> b;
     bool there_b = false;
@@ -637,268 +577,637 @@ __device__ inline bool find_tile(const Attention& a, int group, int rows, int fe
   return false;
 }
 
-constexpr int WPE(int d, int nt, bool shared) { if (!shared) return d == 64 ? W64 : d == 128 ? W128 : 2; return d * nt <= 64 ? 4 : d * nt <= 128 ? 3 : d * nt <= 256 ? 2 : 1; }
-// A workgroup's groups of units for waves with columns of their own: each unit
-// (or half of one) is loaded and its codes are made operands by one wave, for all four.
-// One group is loaded while the one before is worked on.
-template <int D>
-struct Staged {
-  static constexpr int kUnits = D == 256 ? 2 : 4;                // a group
-  static constexpr int kPieces = StagedUnit<D>::kPieces, kKeys = StagedUnit<D>::kKeys;
-  static constexpr int kParts = kAttnWaves / kUnits, kMine = kPieces / kParts;
-  uint4 piece[kUnits][kPieces][64];
-  float scale[kUnits][64];
-  int there[kUnits];
+// A staged unit: the operands of both products, and what goes with them.
+template <int D> struct StagedUnit {
+  static constexpr int kKeys = 2 * (D / 32), kPieces = kKeys + D / 16;
+  const uint4* piece;                   // [kPieces][64]: a lane's 16 bytes of each
+  __device__ v8h key(int h, int k) const {
+    return __builtin_bit_cast(v8h, piece[(h * (D / 32) + k) * 64 + (threadIdx.x & 63)]);
+  }
+  __device__ v8h value(int d) const { return __builtin_bit_cast(v8h, piece[(kKeys + d) * 64 + (threadIdx.x & 63)]); }
+};
+constexpr int kNoScale = -1000;
+struct UnitFacts {
+  float key;                            // what a 1 of the key operand stands for
+  int value;                            // and of the value operand, as its logarithm
+  uint32_t bad;                         // tokens whose value is not finite
+  uint32_t held;                        // whether a page holds the unit
+  // The same in scalar registers.
+  __device__ UnitFacts same() const {
+    auto one = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))); };
+    return UnitFacts{__uint_as_float(one(__float_as_uint(key))), static_cast<int>(one(static_cast<uint32_t>(value))), one(bad),
+                     one(held)};
+  }
+};
 
-  // A wave's share of a group on its way: a unit's words, and the scale of key lane, or
-  // of value lane - 32.
-  struct Share {
-    UnitWords<D> w;
-    uint32_t scale = 0;
-    bool held = false;
-    __device__ void load(UnitReader<D>& reader, int u, int last) {
-      held = u < last && reader.load(u, w);
-      scale = reader.scale;
-    }
-  };
-  static __device__ int mine() { return wave_index() % kUnits; }
+// The state of 16 NT query columns of a wave whose keys and values come as operands
+// with their scales in them (Staged): TERMS fp16 values that add up to each of the
+// query's, so that a score is the product itself.
+template <int D, int NT, int TERMS>
+struct PromptColumns {
+  v8h q[NT][TERMS][D / 32];
+  float qs[NT];                         // what one of them stands for, with |scale| and log2(e)
+  int from[NT], to[NT];                 // visible keys of a column
+  float m[NT], l[NT];                   // reference; sum of this lane's keys
+  v4f o[NT][D / 16];                    // value dims 64 (t / 4) + 16 g + 4 i + t % 4 in o[][t][i]
+  int whole;                            // what a 1 of them stands for, as its logarithm
+  int full_from, full_to;               // keys that every column sees
+  int any_from, any_to;                 // keys that some column sees
 
-  // Units [first, last), this wave's share of the first group on its way.
-  template <int NT>
-  __device__ __forceinline__ void run(Columns<D, NT>& c, UnitReader<D>& reader, Share& next, int first, int last, bool idle) {
-    const int lane = threadIdx.x & 63;
-    const int mine = Staged::mine(), part = wave_index() / kUnits;
-    const Spread spread;
-    for (int u0 = first; u0 < last; u0 += kUnits) {
-      if (u0 != first) __syncthreads();
-      const UnitOfWords<D> unit{next.w, spread};
+  template <typename In, typename F>
+  __device__ __forceinline__ void open(const Attention& a, int group, int kv_head, int off, int n, int64_t start,
+                                       int length, int row0, F&& meanwhile) {
+    constexpr int E = D / 4;
+    const int all = n * group;
+    bounds_of(a, start, length, row0 / group, any_from, full_to);
+    bounds_of(a, start, length, (min(row0 + 16 * NT, all) - 1) / group, full_from, any_to);
+    uint32_t raw[NT][E / 2], signs[2];
+    fetch_queries<D, NT, In>(a, group, kv_head, off, n, start, length, row0, raw, from, to);
+    meanwhile();
+    query_signs<In>(signs);
+    whole = kNoScale;
+    const float unit = RootScale<D>::value * kLog2e * fabsf(a.scale);
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) {
-        if (part == q) {
+    for (int t = 0; t < NT; ++t) {
+      float v[E];
+      rotate_query<D, In>(raw[t], signs, v);
+      float top = 0.0f;
 #pragma unroll
-          for (int i = q * kMine; i < (q + 1) * kMine; ++i)
-            piece[mine][i][lane] = i < kKeys ? __builtin_bit_cast(uint4, unit.key(i / (D / 64), i % (D / 64)))
-                                             : __builtin_bit_cast(uint4, unit.value(i - kKeys));
+      for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(v[e]));
+      top = column_max(top);
+      const bool finite = fabsf(v[0]) < __builtin_inff() && top < __builtin_inff();
+      // the row's largest value to [256, 512): what fp16 does not hold in full is then
+      // below 2^-22 of it, in one term or in the second
+      const int down = finite ? ilogbf(fmaxf(top, 0x1p-100f)) - 8 : 0;
+      const float by = finite ? ldexpf(a.scale < 0.0f ? -1.0f : 1.0f, -down) : 0.0f;
+      qs[t] = finite ? ldexpf(unit, down) : __builtin_nanf("");
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        constexpr int kOrder[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = finite ? v[8 * k + kOrder[e]] * by : 0.0f;
+          q[t][0][k][e] = static_cast<_Float16>(x);
+          if constexpr (TERMS == 2) q[t][1][k][e] = static_cast<_Float16>(x - static_cast<float>(q[t][0][k][e]));
         }
       }
-      if (part == 0) {
-        scale[mine][lane] = __uint_as_float(next.scale << 16);
-        if (lane == 0) there[mine] = next.held;
+      m[t] = kNoReference;
+      l[t] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) o[t][d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  }
+
+  // Scores of a staged unit, in units of qs times the unit's key factor.
+  __device__ __forceinline__ void scores(const StagedUnit<D>& unit, v4f (&s)[NT][2]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[t][h] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const v8h key = unit.key(h, k);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int r = 0; r < TERMS; ++r) s[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[t][r][k], s[t][h], 0, 0, 0);
       }
-      next.load(reader, u0 + kUnits + mine, last);
-      __syncthreads();
-      const int i0 = max(0, c.any_from / kUnit - u0), i1 = idle ? 0 : min(kUnits, (c.any_to + kUnit - 1) / kUnit - u0);
-      c.steps([&](int i) { return StagedUnit<D>{&piece[i][0][0], scale[i]}; }, [&](int i) { return there[i] != 0; }, u0, i0, i1);
+    }
+  }
+
+  // Hides what a column does not see, and moves the references and what the sums are in
+  // where that is due.  `up`: what the sums are in, by the unit's values' power of two, as
+  // its logarithm.
+  __device__ __forceinline__ void settle(v4f (&s)[NT][2], const float (&f)[NT], int u, const UnitFacts& facts, float& up) {
+    const int first = kUnit * u + 8 * static_cast<int>((threadIdx.x & 63) >> 4);
+    if (facts.value > whole) {
+      const float down = ldexpf(1.0f, max(whole, -200) - facts.value);  // 0 for the first
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) o[t][d] *= down;
+      whole = facts.value;
+    }
+    // past 2^40 a weight's fp16 is 0 either way
+    up = static_cast<float>(facts.value == kNoScale ? 0 : min(whole - facts.value, 40));
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        s[t][i >> 2][i & 3] = facts.held && first + i >= from[t] && first + i < to[t] ? s[t][i >> 2][i & 3] : kHidden;
+    if (facts.bad != 0) {
+      // a value that is not finite: it is not in the product (there it would reach those
+      // who do not see it), but in the sum of who sees it
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((facts.bad >> ((first + i) & 31) & 1) != 0 && s[t][i >> 2][i & 3] != kHidden) l[t] = __builtin_nanf("");
+    }
+    raise(s, f);
+  }
+
+  // The weights times the values' power of two over what the sums are in.
+  __device__ __forceinline__ void weights(const v4f (&s)[NT][2], const float (&f)[NT], float up, v8h (&p)[NT]) {
+    const float all = __builtin_amdgcn_exp2f(up);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float low = -(m[t] + up);
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = s[t][i >> 2][i & 3];
+        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x, f[t], low));
+        e[i] = x == kHidden ? 0.0f : e[i];
+      }
+      l[t] = __builtin_fmaf(((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])), all, l[t]);
+      v2h pairs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{e[i], e[i + 4]}), v2h);
+      p[t] = __builtin_bit_cast(v8h, pairs);
+    }
+  }
+
+  __device__ __forceinline__ void add(const StagedUnit<D>& unit, const v8h (&p)[NT]) {
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      const v8h value = unit.value(d);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[t], o[t][d], 0, 0, 0);
+    }
+  }
+
+  // Moves the references where a weight would get too large.
+  __device__ __forceinline__ void raise(const v4f (&s)[NT][2], const float (&f)[NT]) {
+    float most[NT];
+    bool move = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const v4f a = s[t][0], b = s[t][1];
+      most[t] = f[t] * max3(max3(max3(a[0], a[1], a[2]), a[3], b[0]), max3(b[1], b[2], b[3]), b[3]);
+      move = move || most[t] > m[t] + (kTop + kRise);
+    }
+    if (__any(move)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        most[t] = column_max(most[t]);
+        const float wanted = __builtin_ceilf(most[t]) - kTop;
+        if (wanted > m[t] + kRise) {
+          const float down = __builtin_amdgcn_exp2f(m[t] - wanted);     // 0 for the first keys
+          m[t] = wanted;
+          l[t] *= down;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) o[t][d] *= down;
+        }
+      }
+    }
+  }
+  // (NaN if one is: no canonical form is made of its operands first)
+  static __device__ __forceinline__ float max3(float a, float b, float c) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+  }
+
+  // A whole group that every column sees all of, in the power of two that the sums are in.
+  template <int UNITS, typename Group>
+  __device__ __forceinline__ void whole_group(const Group& group) {
+    v4f s[NT][2];
+    scores(group.unit(0), s);
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      float f[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) f[t] = qs[t] * group.key(i);
+      raise(s, f);
+      v8h p[NT];
+      v4f next[NT][2];
+      if (i + 1 < UNITS) scores(group.unit(i + 1), next);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][j >> 2][j & 3], f[t], -m[t]));
+        l[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+        v2h pairs[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pairs[j] = __builtin_convertvector((v2f{e[j], e[j + 4]}), v2h);
+        p[t] = __builtin_bit_cast(v8h, pairs);
+      }
+      add(group.unit(i), p);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[t][0] = next[t][0], s[t][1] = next[t][1];
+    }
+  }
+
+  // Units [i0, i1) of a staged group, where something is hidden or not as usual.
+  template <typename Group>
+  __device__ __forceinline__ void steps(const Group& group, int u0, int i0, int i1) {
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      const UnitFacts facts = group.facts(i).same();
+      float f[NT], up;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) f[t] = qs[t] * facts.key;
+      v4f s[NT][2];
+      v8h p[NT];
+      scores(group.unit(i), s);
+      settle(s, f, u0 + i, facts, up);
+      weights(s, f, up, p);
+      add(group.unit(i), p);
     }
   }
 };
 
-// SHARED: the four waves have the same columns and every fourth unit each, for
-// few rows; else they have columns of their own and the same units.
-// SHARED: the four waves have the same columns and every fourth unit each, for
-// few rows; else they have columns of their own and the same units.
-template <int D, int NT, bool SHARED, typename In>
-__global__ __launch_bounds__(kAttnThreads, WPE(D, NT, SHARED)) void attention_kernel(Attention a, int few, int many) {
-  constexpr int kRows = SHARED ? 16 * NT : 16 * NT * kAttnWaves;
+// A prompt's keys and values as the operands of both products, made once for all waves of
+// a workgroup, whose columns are their own.  Each unit is made by kParts waves; one group
+// of units is worked on while the next is made and the one behind it loaded.  A code times
+// its scale is exact in fp16, 3 bits by 8, the scales taken relative to a power of two of
+// their unit (those below 2^-14 of it lose bits).
+template <int D, int WAVES>
+struct Staged {
+  static constexpr int kUnits = D == 256 ? 2 : 4;                // a group
+  static constexpr int kKeys = StagedUnit<D>::kKeys, kPieces = StagedUnit<D>::kPieces;
+  static constexpr int kParts = WAVES / kUnits, kMine = kPieces / kParts;
+  uint4 piece[2][kUnits][kPieces][64];
+  UnitFacts facts[2][kUnits];
+  _Float16 scales[WAVES][64];           // a wave's own, from its lanes to where they are used
+
+  // One group as the columns take it.
+  struct Group {
+    const Staged& s;
+    int which;
+    __device__ StagedUnit<D> unit(int i) const { return StagedUnit<D>{&s.piece[which][i][0][0]}; }
+    __device__ UnitFacts facts(int i) const { return s.facts[which][i]; }
+    __device__ float key(int i) const { return s.facts[which][i].key; }
+  };
+
+  // A wave's share of a group on its way: the words of its pieces, and the scale of key
+  // lane, or of value lane - 32.
+  struct Share {
+    uint32_t w[kMine];
+    uint32_t scale = 0;
+    bool held = false;
+    __device__ __forceinline__ void load(UnitReader<D>& reader, int u, int last) {
+      held = false;
+      if (u >= last) return;
+      const uint8_t* unit = reader.place(u, held);
+      const int part = wave_index() / kUnits;
+      if constexpr (kParts == 1) {
+        uint32_t k[2][D / 32], v[4];
+        reader.load_keys(unit, 0, k[0]);
+        reader.load_keys(unit, 1, k[1]);
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) w[i] = k[i / (D / 32)][i % (D / 32)];
+#pragma unroll
+        for (int i = 0; i < kMine - kKeys; i += 4) {
+          reader.load_values(unit, i / 4, v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[kKeys + i + j] = v[j];
+        }
+      } else if (part < kParts / 2) {
+#pragma unroll
+        for (int h = 0; h < kMine / (D / 32); ++h) {
+          uint32_t k[D / 32];
+          reader.load_keys(unit, part * (kMine / (D / 32)) + h, k);
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) w[h * (D / 32) + j] = k[j];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kMine; i += 4) {
+          uint32_t v[4];
+          reader.load_values(unit, (part - kParts / 2) * (kMine / 4) + i / 4, v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[i + j] = v[j];
+        }
+      }
+      scale = reinterpret_cast<const uint16_t*>(unit + key_scales_at(D))[threadIdx.x & 63];
+    }
+  };
+  static __device__ int mine() { return wave_index() % kUnits; }
+
+  // This wave's share of the group from unit u0 on; of keys from `end` on nothing is used.
+  __device__ __forceinline__ void make(int which, const Share& share, const Spread& spread, int u0, int end) {
+    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+    const int wave = wave_index(), mine = Staged::mine(), part = wave / kUnits;
+    float scale = share.held && kUnit * (u0 + mine) + (lane & 31) < end ? __uint_as_float(share.scale << 16) : 0.0f;
+    const bool finite = fabsf(scale) < __builtin_inff();
+    const uint64_t broken = __ballot(!finite);
+    // the largest of the keys in the lower lanes, of the values in the upper ones
+    float top = finite ? scale : 0.0f;
+    top = fmaxf(top, lane_xor<1>(top));
+    top = fmaxf(top, lane_xor<2>(top));
+    top = fmaxf(top, lane_xor<4>(top));
+    top = fmaxf(top, lane_xor<8>(top));
+    float other = top;
+    swap_rows<16>(top, other);
+    top = power_below(fmaxf(top, other));
+    if (!finite && lane >= 32) scale = 0.0f;
+    scales[wave][lane] = static_cast<_Float16>(top > 0.0f ? scale * (1.0f / top) : scale * 0.0f);
+    const float key = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(top), 0));
+    const int value = static_cast<int>(__builtin_amdgcn_readlane(__float_as_uint(top), 32) >> 23);
+    if (lane == 0 && part == 0) facts[which][mine] = UnitFacts{key, value != 0 ? value - 127 : kNoScale, static_cast<uint32_t>(broken >> 32), share.held};
+    // lanes of this wave only read what it wrote itself
+    __builtin_amdgcn_wave_barrier();
+    uint4* to = &piece[which][mine][part * kMine][lane];
+    auto store = [&](int i, const v2h (&by)[4]) {
+      const v8h v = codes_of(share.w[i], spread);
+      v2h p[4];
+      __builtin_memcpy(p, &v, sizeof v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] *= by[e];
+      to[64 * i] = __builtin_bit_cast(uint4, p);
+    };
+    const int tile = kParts == 1 ? 0 : part * (kMine / (D / 32));
+    if (kParts == 1 || part < kParts / 2) {
+#pragma unroll
+      for (int i = 0; i < (kParts == 1 ? kKeys : kMine); ++i) {
+        const _Float16 by = scales[wave][8 * (m >> 2) + 4 * (tile + i / (D / 32)) + (m & 3)];
+        const v2h all[4] = {{by, by}, {by, by}, {by, by}, {by, by}};
+        store(i, all);
+      }
+    }
+    if (kParts == 1 || part >= kParts / 2) {
+      const uint4 eight = *reinterpret_cast<const uint4*>(&scales[wave][32 + 8 * g]);
+      // the scales of tokens 0 and 4, 1 and 5, 2 and 6, 3 and 7 of the octet
+      const uint32_t by_token[4] = {__builtin_amdgcn_perm(eight.z, eight.x, 0x05040100u),
+                                    __builtin_amdgcn_perm(eight.z, eight.x, 0x07060302u),
+                                    __builtin_amdgcn_perm(eight.w, eight.y, 0x05040100u),
+                                    __builtin_amdgcn_perm(eight.w, eight.y, 0x07060302u)};
+      v2h all[4];
+      __builtin_memcpy(all, by_token, sizeof all);
+#pragma unroll
+      for (int i = kParts == 1 ? kKeys : 0; i < kMine; ++i) store(i, all);
+    }
+  }
+
+  // Units [first, last) of keys below `end`, this wave's share of the first group on its way.
+  template <typename Columns>
+  __device__ __forceinline__ void run(Columns& c, UnitReader<D>& reader, Share& next, int first, int last, int end, bool idle) {
+    if (first >= last) return;
+    const int mine = Staged::mine();
+    const Spread spread;
+    make(0, next, spread, first, end);
+    next.load(reader, first + kUnits + mine, last);
+    __syncthreads();
+    int which = 0;
+    for (int u0 = first; u0 < last; u0 += kUnits, which ^= 1) {
+      // into the group that was done with before the last barrier
+      if (u0 + kUnits < last) make(which ^ 1, next, spread, u0 + kUnits, end);
+      next.load(reader, u0 + 2 * kUnits + mine, last);
+      const int i0 = max(0, c.any_from / kUnit - u0);
+      const int i1 = idle ? 0 : min(min(kUnits, last - u0), (c.any_to + kUnit - 1) / kUnit - u0);
+      bool plain = i0 == 0 && i1 == kUnits && kUnit * u0 >= c.full_from && kUnit * (u0 + kUnits) <= c.full_to;
+      if (plain) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+          const UnitFacts f = facts[which][i].same();
+          plain = plain && f.held != 0 && f.bad == 0 && f.value == c.whole;
+        }
+      }
+      if (plain) c.template whole_group<kUnits>(Group{*this, which});
+      else c.steps(Group{*this, which}, u0, i0, i1);
+      __syncthreads();
+    }
+  }
+  // The power of two at or below a scale; 0 for what has none that is normal.
+  static __device__ float power_below(float v) { return __uint_as_float(__float_as_uint(v) & 0x7f800000u); }
+};
+
+// Sums over a query's parts: what a workgroup knows of where its rows go.
+struct Rows {
+  int off, group, kv_head, q_heads;
+  // the row of the output (and of a part's sums) that row `row` of a sequence's is
+  __device__ int64_t operator()(int row) const {
+    const int i = row / group;
+    return (static_cast<int64_t>(off) + i) * q_heads + kv_head * group + (row - i * group);
+  }
+};
+
+// The units [first, last) of a tile's rows [row0, row0 + rows) that belong to a part.
+__device__ inline void units_of(const Attention& a, const Tile& tile, int group, int rows, int part, int64_t start, int length,
+                                int& first, int& last, int& end) {
+  int from, unused;
+  bounds_of(a, start, length, tile.row0 / group, from, unused);
+  bounds_of(a, start, length, (min(tile.row0 + rows, tile.n * group) - 1) / group, unused, end);
+  const int part_to = part == a.splits - 1 ? 0x7fffffff : (part + 1) * a.chunk;
+  const int lo = max(from, part * a.chunk), hi = min(end, part_to);
+  first = lo / kUnit;
+  last = lo < hi ? (hi + kUnit - 1) / kUnit : 0;
+}
+
+// The keys of a sequence that there are.
+__device__ inline int length_of(const Attention& a, const Tile& tile) {
+  return static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(tile.start) + tile.n, static_cast<int64_t>(a.cache.max_tokens))));
+}
+
+// Few rows: the four waves have the same 16 NT columns and every fourth unit each.
+template <int D, int NT, typename In>
+__global__ __launch_bounds__(kAttnThreads, D * NT <= 64 ? 4 : D * NT <= 128 ? 3 : D * NT <= 256 ? 2 : 1) void attend_few(
+    Attention a, int few, int many) {
+  constexpr int kRows = 16 * NT;
   const int kv_heads = a.cache.kv_heads, group = a.q_heads / kv_heads;
   const int kv_head = static_cast<int>(blockIdx.x % static_cast<unsigned>(kv_heads));
   const int part = static_cast<int>(blockIdx.y);
   Tile tile;
   if (!find_tile(a, group, kRows, few, many, static_cast<int>(blockIdx.x / static_cast<unsigned>(kv_heads)), tile)) return;
-  const int wave = wave_index(), lane = threadIdx.x & 63;
-  const int64_t start = tile.start;
-  const int length = static_cast<int>(max(int64_t{0}, min(start + tile.n, static_cast<int64_t>(a.cache.max_tokens))));
-  const int row0 = tile.row0 + (SHARED ? 0 : 16 * NT * wave);
-  const int all = tile.n * group;
-  const bool idle = row0 >= all;        // a wave behind the tile's rows: it only stages
-  // this part's keys of the whole tile
-  int tile_from, tile_to, unused;
-  bounds_of(a, start, length, tile.row0 / group, tile_from, unused);
-  bounds_of(a, start, length, (min(tile.row0 + kRows, all) - 1) / group, unused, tile_to);
-  const int part_from = part * a.chunk, part_to = part == a.splits - 1 ? 0x7fffffff : (part + 1) * a.chunk;
-  const int lo = max(tile_from, part_from), hi = min(tile_to, part_to);
-  const int first = lo / kUnit, last = lo < hi ? (hi + kUnit - 1) / kUnit : 0;
+  const int wave = wave_index(), lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  const int length = length_of(a, tile), all = tile.n * group;
+  int first, last, end;
+  units_of(a, tile, group, kRows, part, tile.start, length, first, last, end);
   UnitReader<D> reader(a.cache, tile.b, kv_head, first >> (a.cache.page_shift - 5));
   Columns<D, NT> c;
-  if constexpr (SHARED) {
-    UnitWords<D> words;
-    bool there = false;
-    c.template open<In>(a, group, kv_head, tile.off, tile.n, start, length, row0,
-                        [&] { there = first + wave < last && reader.load(first + wave, words); });
-    c.run(reader, words, there, first + wave, last, kAttnWaves);
-  } else {
-    __shared__ Staged<D> staged;
-    typename Staged<D>::Share share;
-    c.template open<In>(a, group, kv_head, tile.off, tile.n, start, length, idle ? tile.row0 : row0,
-                        [&] { share.load(reader, first + Staged<D>::mine(), last); });
-    staged.run(c, reader, share, first, last, idle);
-    if (idle) return;
-  }
+  UnitWords<D> words;
+  bool there = false;
+  c.template open<In>(a, group, kv_head, tile.off, tile.n, tile.start, length, tile.row0,
+                      [&] { there = first + wave < last && reader.load(first + wave, words); });
+  c.run(reader, words, there, first + wave, last, kAttnWaves);
 
+  const Rows row_of{tile.off, group, kv_head, a.q_heads};
   const int64_t rows = static_cast<int64_t>(a.M) * a.q_heads;
-  // the row of the output (and of a part's sums) that a column is
-  auto row_of = [&](int row) {
-    const int i = row / group;
-    return (static_cast<int64_t>(tile.off) + i) * a.q_heads + kv_head * group + (row - i * group);
-  };
-  const int col = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int t = 0; t < NT; ++t) c.l[t] = column_sum(c.l[t]);
+  constexpr int kStride = D + 4;
+  __shared__ float sums[kAttnWaves][16][kStride];
+  __shared__ float refs[kAttnWaves][16], totals[kAttnWaves][16];
+  const int mine = threadIdx.x >> 4, piece = threadIdx.x & 15;
+  constexpr int E = D / 16;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (t > 0) __syncthreads();
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(&sums[wave][col][64 * d + 16 * g + 4 * i]) =
+            make_float4(c.o[t][4 * d][i], c.o[t][4 * d + 1][i], c.o[t][4 * d + 2][i], c.o[t][4 * d + 3][i]);
+    if (g == 0) {
+      refs[wave][col] = c.m[t];
+      totals[wave][col] = c.l[t];
+    }
+    __syncthreads();
+    const int row = tile.row0 + 16 * t + mine;
+    float m = refs[0][mine];
+#pragma unroll
+    for (int w = 1; w < kAttnWaves; ++w) m = fmaxf(m, refs[w][mine]);
+    float v[E], l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+      const float r = refs[w][mine];
+      const float f = __builtin_amdgcn_exp2f(r - m);
+      l = __builtin_fmaf(totals[w][mine], f, l);
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&sums[w][mine][piece * E + e]);
+        v[e] = __builtin_fmaf(x.x, f, v[e]);
+        v[e + 1] = __builtin_fmaf(x.y, f, v[e + 1]);
+        v[e + 2] = __builtin_fmaf(x.z, f, v[e + 2]);
+        v[e + 3] = __builtin_fmaf(x.w, f, v[e + 3]);
+      }
+    }
+    if (row < all) {
+      if (a.splits == 1) {
+        finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row_of(row) * D);
+      } else {
+        const int64_t at = part * rows + row_of(row);
+        float* to = a.part + at * D + piece * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        if (piece == 0)
+          *reinterpret_cast<float2*>(a.part + a.splits * rows * D + 2 * at) = make_float2(m, l);
+      }
+    }
+  }
+}
 
-  if constexpr (SHARED) {
-    constexpr int kStride = D + 4;
-    __shared__ float sums[kAttnWaves][16][kStride];
-    __shared__ float refs[kAttnWaves][16], totals[kAttnWaves][16];
-    const int mine = threadIdx.x >> 4, piece = threadIdx.x & 15;
-    constexpr int E = D / 16;
+// Many rows: the waves have 16 NT columns each and the same units, staged.
+template <int D, int NT, int WAVES, typename In>
+__global__ __launch_bounds__(64 * WAVES, 2) void attend_many(Attention a, int few, int many) {
+  constexpr int kRows = 16 * NT * WAVES;
+  const int kv_heads = a.cache.kv_heads, group = a.q_heads / kv_heads;
+  const int kv_head = static_cast<int>(blockIdx.x % static_cast<unsigned>(kv_heads));
+  const int part = static_cast<int>(blockIdx.y);
+  Tile tile;
+  if (!find_tile(a, group, kRows, few, many, static_cast<int>(blockIdx.x / static_cast<unsigned>(kv_heads)), tile)) return;
+  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  const int length = length_of(a, tile), all = tile.n * group;
+  const int row0 = tile.row0 + 16 * NT * wave_index();
+  const bool idle = row0 >= all;        // a wave behind the tile's rows: it only stages
+  int first, last, end;
+  units_of(a, tile, group, kRows, part, tile.start, length, first, last, end);
+  UnitReader<D> reader(a.cache, tile.b, kv_head, first >> (a.cache.page_shift - 5));
+  __shared__ Staged<D, WAVES> staged;
+  PromptColumns<D, NT, std::is_same_v<In, _Float16> ? 2 : 1> c;
+  typename Staged<D, WAVES>::Share share;
+  c.template open<In>(a, group, kv_head, tile.off, tile.n, tile.start, length, idle ? tile.row0 : row0,
+                      [&] { share.load(reader, first + Staged<D, WAVES>::mine(), last); });
+  staged.run(c, reader, share, first, last, end, idle);
+  if (idle) return;
+  const float whole = c.whole == kNoScale ? 0.0f : ldexpf(1.0f, c.whole);
+
+  const Rows row_of{tile.off, group, kv_head, a.q_heads};
+  const int64_t rows = static_cast<int64_t>(a.M) * a.q_heads;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (t > 0) __syncthreads();
+  for (int t = 0; t < NT; ++t) c.l[t] = column_sum(c.l[t]);
 #pragma unroll
-      for (int d = 0; d < D / 64; ++d)
+  for (int t = 0; t < NT; ++t) {
+    const int row = row0 + 16 * t + col;
+    // dims 64 d + 16 g + e of this column
+    float v[D / 64][16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<float4*>(&sums[wave][col][64 * d + 16 * g + 4 * i]) =
-              make_float4(c.o[t][4 * d][i], c.o[t][4 * d + 1][i], c.o[t][4 * d + 2][i], c.o[t][4 * d + 3][i]);
-      if (g == 0) {
-        refs[wave][col] = c.m[t];
-        totals[wave][col] = c.l[t];
-      }
-      __syncthreads();
-      const int row = tile.row0 + 16 * t + mine;
-      float m = refs[0][mine];
+    for (int d = 0; d < D / 64; ++d)
 #pragma unroll
-      for (int w = 1; w < kAttnWaves; ++w) m = fmaxf(m, refs[w][mine]);
-      float v[E], l = 0.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) {
-        const float r = refs[w][mine];
-        const float f = __builtin_amdgcn_exp2f(r - m);
-        l = __builtin_fmaf(totals[w][mine], f, l);
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(&sums[w][mine][piece * E + e]);
-          v[e] = __builtin_fmaf(x.x, f, v[e]);
-          v[e + 1] = __builtin_fmaf(x.y, f, v[e + 1]);
-          v[e + 2] = __builtin_fmaf(x.z, f, v[e + 2]);
-          v[e + 3] = __builtin_fmaf(x.w, f, v[e + 3]);
-        }
-      }
+      for (int e = 0; e < 16; ++e) v[d][e] = c.o[t][4 * d + (e & 3)][e >> 2] * whole;
+    if (a.splits != 1) {
       if (row < all) {
-        if (a.splits == 1) {
-          finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row_of(row) * D);
-        } else {
-          const int64_t at = part * rows + row_of(row);
-          float* to = a.part + at * D + piece * E;
+        const int64_t at = part * rows + row_of(row);
 #pragma unroll
-          for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-          if (piece == 0)
-            *reinterpret_cast<float2*>(a.part + a.splits * rows * D + 2 * at) = make_float2(m, l);
+        for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(a.part + at * D + 64 * d + 16 * g + e) =
+                make_float4(v[d][e], v[d][e + 1], v[d][e + 2], v[d][e + 3]);
+        if (g == 0) *reinterpret_cast<float2*>(a.part + a.splits * rows * D + 2 * at) = make_float2(c.m[t], c.l[t]);
+      }
+      continue;
+    }
+    // H_D: bits 0 to 3 of the dim and those from 6 on lie inside a lane; bits 4 and 5
+    // are the lane's quarter, which is exchanged with two others of the lane's own, so
+    // that each sum has both its terms in one lane: bit 3, and bit 6 (D = 64: bit 2)
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d) {
+#pragma unroll
+      for (int h = 1; h < 16; h <<= 1) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if ((e & h) == 0) {
+            const float x = v[d][e], y = v[d][e + h];
+            v[d][e] = x + y;
+            v[d][e + h] = x - y;
+          }
         }
       }
     }
-  } else {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int row = row0 + 16 * t + col;
-      // dims 64 d + 16 g + e of this column
-      float v[D / 64][16];
-#pragma unroll
-      for (int d = 0; d < D / 64; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[d][e] = c.o[t][4 * d + (e & 3)][e >> 2];
-      if (a.splits != 1) {
-        if (row < all) {
-          const int64_t at = part * rows + row_of(row);
-#pragma unroll
-          for (int d = 0; d < D / 64; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(a.part + at * D + 64 * d + 16 * g + e) =
-                  make_float4(v[d][e], v[d][e + 1], v[d][e + 2], v[d][e + 3]);
-          if (g == 0) *reinterpret_cast<float2*>(a.part + a.splits * rows * D + 2 * at) = make_float2(c.m[t], c.l[t]);
-        }
-        continue;
-      }
-      // H_D: bits 0 to 3 of the dim and those from 6 on lie inside a lane; bits 4 and 5
-      // are the lane's quarter, which is exchanged with two others of the lane's own, so
-      // that each sum has both its terms in one lane: bit 3, and bit 6 (D = 64: bit 2)
+    for (int h = 1; h < D / 64; h <<= 1) {
 #pragma unroll
       for (int d = 0; d < D / 64; ++d) {
-#pragma unroll
-        for (int h = 1; h < 16; h <<= 1) {
+        if ((d & h) == 0) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            if ((e & h) == 0) {
-              const float x = v[d][e], y = v[d][e + h];
-              v[d][e] = x + y;
-              v[d][e + h] = x - y;
-            }
+            const float x = v[d][e], y = v[d + h][e];
+            v[d][e] = x + y;
+            v[d + h][e] = x - y;
           }
         }
       }
+    }
 #pragma unroll
-      for (int h = 1; h < D / 64; h <<= 1) {
+    for (int d = 0; d < D / 64; ++d) {
 #pragma unroll
-        for (int d = 0; d < D / 64; ++d) {
-          if ((d & h) == 0) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = v[d][e], y = v[d + h][e];
-              v[d][e] = x + y;
-              v[d + h][e] = x - y;
-            }
-          }
-        }
+      for (int e = 0; e < 8; ++e) {
+        swap_rows<16>(v[d][e], v[d][e + 8]);
+        const float x = v[d][e], y = v[d][e + 8];
+        v[d][e] = x + y;
+        v[d][e + 8] = x - y;
       }
+    }
+    // now bit 3 of the dim is bit 0 of the quarter, and index 8 of a lane bit 4
+    auto last = [&](float& p, float& q) {
+      swap_rows<32>(p, q);
+      const float x = p, y = q;
+      p = x + y;
+      q = x - y;
+    };
+    if constexpr (D == 64) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if ((e & 4) == 0) last(v[0][e], v[0][e + 4]);
+    } else {
+#pragma unroll
+      for (int d = 0; d < D / 64; d += 2)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) last(v[d][e], v[d + 1][e]);
+    }
+    const float by = c.l[t] != 0.0f ? RootScale<D>::value / c.l[t] : 0.0f;
+    if (row < all) {
+      In* out = static_cast<In*>(a.out) + row_of(row) * D + 8 * (g & 1);
 #pragma unroll
       for (int d = 0; d < D / 64; ++d) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          swap_rows<16>(v[d][e], v[d][e + 8]);
-          const float x = v[d][e], y = v[d][e + 8];
-          v[d][e] = x + y;
-          v[d][e + 8] = x - y;
-        }
-      }
-      // now bit 3 of the dim is bit 0 of the quarter, and index 8 of a lane bit 4
-      auto last = [&](float& p, float& q) {
-        swap_rows<32>(p, q);
-        const float x = p, y = q;
-        p = x + y;
-        q = x - y;
-      };
-      if constexpr (D == 64) {
+        for (int j = 0; j < 2; ++j) {
+          float f[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if ((e & 4) == 0) last(v[0][e], v[0][e + 4]);
-      } else {
-#pragma unroll
-        for (int d = 0; d < D / 64; d += 2)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) last(v[d][e], v[d + 1][e]);
-      }
-      const float by = c.l[t] != 0.0f ? RootScale<D>::value / c.l[t] : 0.0f;
-      if (row < all) {
-        In* out = static_cast<In*>(a.out) + row_of(row) * D + 8 * (g & 1);
-#pragma unroll
-        for (int d = 0; d < D / 64; ++d) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = c.l[t] != 0.0f ? v[d][8 * j + e] * by : 0.0f;
-            if constexpr (D == 64) {
-              // index 4 of a lane is bit 5, the quarter's bit 1 is bit 2
-              const uint4 w = narrow8<In>(f);
-              *reinterpret_cast<uint2*>(out + 16 * j + 4 * (g >> 1)) = make_uint2(w.x, w.y);
-              *reinterpret_cast<uint2*>(out + 16 * j + 32 + 4 * (g >> 1)) = make_uint2(w.z, w.w);
-            } else {
-              // d's bit 0 is bit 5, the quarter's bit 1 is bit 6
-              *reinterpret_cast<uint4*>(out + 128 * (d >> 1) + 64 * (g >> 1) + 32 * (d & 1) + 16 * j) = narrow8<In>(f);
-            }
+          for (int e = 0; e < 8; ++e) f[e] = c.l[t] != 0.0f ? v[d][8 * j + e] * by : 0.0f;
+          if constexpr (D == 64) {
+            // index 4 of a lane is bit 5, the quarter's bit 1 is bit 2
+            const uint4 w = narrow8<In>(f);
+            *reinterpret_cast<uint2*>(out + 16 * j + 4 * (g >> 1)) = make_uint2(w.x, w.y);
+            *reinterpret_cast<uint2*>(out + 16 * j + 32 + 4 * (g >> 1)) = make_uint2(w.z, w.w);
+          } else {
+            // d's bit 0 is bit 5, the quarter's bit 1 is bit 6
+            *reinterpret_cast<uint4*>(out + 128 * (d >> 1) + 64 * (g >> 1) + 32 * (d & 1) + 16 * j) = narrow8<In>(f);
           }
         }
       }
@@ -976,36 +1285,39 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
 // Sequences of at most this many rows (tokens times query heads a key head) take
 // the kernel whose waves share their columns.
 constexpr int kFewRows = 32;
+// Column tiles of a wave and waves of the other kernel.
+constexpr int wide_tiles(int head_dim) { return head_dim == 256 ? 1 : 2; }
+constexpr int wide_waves(int head_dim) { return head_dim == 64 ? 4 : 8; }
 
 int64_t tiles_bound(int64_t M, int64_t group, int64_t n_seqs, int64_t rows) {
   // one for every sequence that has rows, and one for every full tile
   return std::min(M * group / rows + std::min(n_seqs, M), M * ((group + rows - 1) / rows));
 }
 
-template <int D, int NT, bool SHARED, typename In>
-hipError_t launch_tiles(const Attention& a, int few, int many, hipStream_t stream) {
-  constexpr int kRows = SHARED ? 16 * NT : 16 * NT * kAttnWaves;
-  const int64_t tiles = tiles_bound(a.M, a.q_heads / a.cache.kv_heads, a.cache.n_seqs, kRows);
+// A kernel whose waves have `columns` each, or (own = 0) four waves the same ones.
+template <typename Kernel>
+hipError_t launch_tiles(Kernel kernel, const Attention& a, int columns, int own, int few, int many, hipStream_t stream) {
+  const int waves = own != 0 ? own : kAttnWaves;
+  const int64_t tiles = tiles_bound(a.M, a.q_heads / a.cache.kv_heads, a.cache.n_seqs, own != 0 ? columns * own : columns);
   const int64_t grid = tiles * a.cache.kv_heads;
-  if (grid * kAttnThreads * a.splits >= (int64_t{1} << 32)) return hipErrorInvalidConfiguration;
-  attention_kernel<D, NT, SHARED, In><<<dim3(static_cast<unsigned>(grid), static_cast<unsigned>(a.splits)),
-                                        dim3(kAttnThreads), 0, stream>>>(a, few, many);
+  if (grid * 64 * waves >= (int64_t{1} << 32)) return hipErrorInvalidConfiguration;
+  kernel<<<dim3(static_cast<unsigned>(grid), static_cast<unsigned>(a.splits)), dim3(64 * waves), 0, stream>>>(a, few, many);
   return hipGetLastError();
 }
 
 template <int D, typename In>
 hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   constexpr int kAll = 0x7fffffff;
-  constexpr int kWide = D == 256 ? 1 : 2;
+  constexpr int kWide = wide_tiles(D), kWaves = wide_waves(D);
   const int64_t rows = static_cast<int64_t>(a.M) * (a.q_heads / a.cache.kv_heads);
   const int64_t mean = rows / a.cache.n_seqs;
   hipError_t e;
-  if (mean <= 16) e = launch_tiles<D, 1, true, In>(a, 0, kAll, stream);
-  else if (mean <= kFewRows) e = launch_tiles<D, 2, true, In>(a, 0, kAll, stream);
+  if (mean <= 16) e = launch_tiles(attend_few<D, 1, In>, a, 16, 0, 0, kAll, stream);
+  else if (mean <= kFewRows) e = launch_tiles(attend_few<D, 2, In>, a, 32, 0, 0, kAll, stream);
   else {
     const int few = a.cache.n_seqs > 1 ? kFewRows : 0;
-    e = few != 0 ? launch_tiles<D, 1, true, In>(a, 0, few, stream) : hipSuccess;
-    if (e == hipSuccess) e = launch_tiles<D, kWide, false, In>(a, few, kAll, stream);
+    e = few != 0 ? launch_tiles(attend_few<D, 1, In>, a, 16, 0, 0, few, stream) : hipSuccess;
+    if (e == hipSuccess) e = launch_tiles(attend_many<D, kWide, kWaves, In>, a, 16 * kWide, kWaves, few, kAll, stream);
   }
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t out_rows = static_cast<int64_t>(a.M) * a.q_heads;
@@ -1028,7 +1340,7 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
                                    int64_t max_tokens) {
   const int64_t group = q_heads / kv_heads, rows = M * group, mean = rows / n_seqs;
   const bool shared = mean <= kFewRows;
-  const int64_t tile = shared ? (mean <= 16 ? 16 : 32) : (head_dim == 256 ? 64 : 128);
+  const int64_t tile = shared ? (mean <= 16 ? 16 : 32) : 16 * wide_waves(head_dim) * wide_tiles(head_dim);
   const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
   const int64_t wanted = shared ? 2048 : 512;
   const int64_t least = shared ? 4 * kUnit : 16 * kUnit;         // keys of a part
