@@ -55,8 +55,11 @@ def test_workspace_sizes(B):
                 (1, 8, 2, 128, 1, 0), (1, 8, 2, 128, 1, (1 << 30) + 1), (1 << 29, 8, 2, 128, 1, 64), (1, -8, 2, 128, 1, 64)):
         assert f(*bad) == 0
     # parts cost their sums and no more than 64 of them
-    for args in ((1, 32, 8, 128, 1, 1 << 20), (64, 32, 8, 128, 64, 8192), (2000, 8, 8, 64, 3, 1 << 16)):
+    for args in ((1, 32, 8, 128, 1, 1 << 20), (64, 32, 8, 128, 64, 8192), (100, 8, 8, 64, 3, 1 << 16)):
         assert f(*args) <= 64 * args[0] * args[1] * (args[3] + 2) * 4
+    # a long prompt's keys and values as 16-bit operands, 8 GiB of them at most
+    assert 4096 * 8 * 128 * 4 <= f(4096, 32, 8, 128, 1, 4096) <= 1.02 * 4096 * 8 * 128 * 4 + (1 << 20)
+    assert f(4096, 32, 8, 128, 1, 1 << 24) <= 64 * 4096 * 32 * 130 * 4
 
 
 # ---------------------------------------------------------------- inputs
@@ -141,6 +144,10 @@ MANY = [
     ([(0, 40)], 4, 1, 128, 64), ([(0, 300)], 1, 2, 64, 32), ([(5, 130), (70, 1), (0, 65), (9, 0), (300, 90)], 4, 2, 128, 32),
     ([(0, 257)], 2, 1, 256, 256), ([(1000, 77), (31, 64)], 3, 2, 128, 128), ([(0, 70), (400, 100)], 8, 1, 64, 64),
     ([(17, 150), (3, 33)], 1, 3, 256, 64),
+    # more than 512 rows a key head: their keys and values made operands first
+    ([(0, 700)], 1, 2, 64, 32), ([(100, 300), (50, 1), (0, 200), (7, 2)], 4, 1, 128, 64), ([(1000, 600), (31, 64), (3, 530)], 1, 2, 128, 128),
+    ([(17, 650)], 1, 1, 256, 64), ([(2000, 90)], 8, 1, 64, 64), ([(3, 140), (300, 257), (0, 0), (64, 129)], 4, 2, 256, 256),
+    ([(0, 513)], 1, 1, 128, 32), ([(1, 33), (5, 1025)], 2, 1, 64, 128),
 ]
 
 
@@ -160,7 +167,7 @@ def test_many_tokens(B, lens, G, H, D, page, io):
 @pytest.mark.gpu
 @pytest.mark.parametrize("lens,G,H,D,page,window", [
     ([(20000, 1)], 8, 2, 128, 64, 0), ([(9000, 1), (12, 1), (4000, 1)], 4, 2, 64, 256, 0), ([(7000, 3), (6000, 2)], 4, 1, 256, 32, 3000),
-    ([(8000, 60), (100, 70)], 4, 1, 128, 128, 0), ([(5000, 130)], 2, 1, 64, 64, 2000), ([(30000, 1), (200, 90), (3, 2)], 4, 1, 128, 64, 0)])
+    ([(8000, 60), (100, 70)], 4, 1, 128, 128, 0), ([(8000, 160)], 4, 1, 128, 128, 0), ([(6000, 600)], 1, 1, 64, 128, 700), ([(5000, 130)], 2, 1, 64, 64, 2000), ([(30000, 1), (200, 90), (3, 2)], 4, 1, 128, 64, 0)])
 def test_long_sequences_in_parts(B, lens, G, H, D, page, window):
     g, *c = filled(sum(s for s, _ in lens), lens, H, D, page)
     q = queries(g, c[3], G * H, D, torch.float16)
@@ -211,7 +218,7 @@ def test_tokens_without_a_page_are_left_out(B):
 @pytest.mark.parametrize("many", [False, True])
 def test_what_is_not_finite_stays_with_who_reads_it(B, many):
     H, D, page = 2, 128, 32
-    lens = [(64, 70 if many else 5)]
+    lens = [(64, 200 if many else 5)]
     g, pages, table, starts, offsets = filled(3, lens, H, D, page)
     q = queries(g, offsets, 8, D, torch.bfloat16).clone()
     lo, n = int(offsets[0]), lens[0][1]
@@ -242,7 +249,7 @@ def test_what_is_not_finite_stays_with_who_reads_it(B, many):
     (60.0, (0.3, 0.5), None), (2.0, (1e-15, 1e-12), 1e12), (2.0, (1e4, 1e9), 1e-9), (1.0, (0.0, 0.4), None), (2.0, (0.0, 0.0), None)])
 def test_sizes_of_values(B, size, scales, scale):
     """Queries, keys and values from very small to very large, scores that pick one token of all."""
-    for lens, G in (([(300, 1), (40, 1)], 4), ([(100, 80)], 2)):
+    for lens, G in (([(300, 1), (40, 1)], 4), ([(100, 80)], 2), ([(64, 300)], 2)):
         g, *c = filled(7, lens, 1, 128, 64, scales=scales)
         check(B, queries(g, c[3], G, 128, torch.bfloat16, size), *c, 1, 64, scale=scale)
 

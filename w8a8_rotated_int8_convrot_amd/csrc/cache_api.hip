@@ -234,7 +234,8 @@ int convrot_cache_attention(const convrot_cache* cache, const void* q, int64_t q
                 plan.workspace);
   const Attention a{cache_of(*cache), q, q_stride, static_cast<int>(M), static_cast<int>(q_heads), cache->starts,
                     cache->offsets, scale, causal != 0, static_cast<int>(window), out, plan.splits, plan.chunk,
-                    static_cast<float*>(workspace)};
+                    static_cast<float*>(workspace), static_cast<uint8_t*>(workspace) + plan.parts, plan.slots,
+                    plan.slot_units};
   return hip_status(launch_cache_attention(a, io_dtype == CONVROT_F16, static_cast<hipStream_t>(stream)), who);
 }
 

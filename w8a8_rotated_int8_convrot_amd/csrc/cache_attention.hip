@@ -191,9 +191,12 @@ struct UnitReader {
   }
 
   __device__ __forceinline__ bool load(int u, UnitWords<D>& w) {
-    const int g = (threadIdx.x & 63) >> 4;
     bool there;
-    const uint8_t* unit = place(u, there);
+    words(place(u, there), w);
+    return there;
+  }
+  static __device__ __forceinline__ void words(const uint8_t* unit, UnitWords<D>& w) {
+    const int g = (threadIdx.x & 63) >> 4;
     load_keys(unit, 0, w.k[0]);
     load_keys(unit, 1, w.k[1]);
 #pragma unroll
@@ -205,7 +208,6 @@ struct UnitReader {
     }
     w.ks = *reinterpret_cast<const uint4*>(unit + key_scales_at(D) + 16 * g);
     w.vs = *reinterpret_cast<const uint4*>(unit + value_scales_at(D) + 16 * g);
-    return there;
   }
 };
 
@@ -536,6 +538,7 @@ __device__ inline void finish(float (&v)[E], float l, int part, In* out) {
 // The tile a workgroup has: rows [row0, ...) of sequence b.
 struct Tile {
   int b, off, n, row0, start;
+  int slot;                             // of the sequences that have tiles, this one's number
 };
 
 // Tile `index` of all sequences' tiles of `rows` rows, a sequence's last first
@@ -543,7 +546,7 @@ struct Tile {
 // one a lane.  Sequences of at most `few` or more than `many` rows have none here.
 __device__ inline bool find_tile(const Attention& a, int group, int rows, int few, int many, int index, Tile& tile) {
   const int lane = threadIdx.x & 63;
-  int before = 0;
+  int before = 0, slots = 0;
   for (int b0 = 0; b0 < a.cache.n_seqs; b0 += 64) {
     const int b = b0 + lane;
     Span s{0, 0};
@@ -565,6 +568,7 @@ __device__ inline bool find_tile(const Attention& a, int group, int rows, int fe
       const uint64_t behind = __ballot(index - before < sum);
       const int l = __builtin_ctzll(behind);
       tile.b = b0 + l;
+      tile.slot = slots + __builtin_popcountll(__ballot(mine > 0) & ((uint64_t{1} << l) - 1));
       tile.off = __builtin_amdgcn_readlane(s.off, l);
       tile.n = __builtin_amdgcn_readlane(s.end, l) - tile.off;
       tile.start = __builtin_amdgcn_readlane(start, l);
@@ -573,8 +577,14 @@ __device__ inline bool find_tile(const Attention& a, int group, int rows, int fe
       return true;
     }
     before += total;
+    slots += __builtin_popcountll(__ballot(mine > 0));
   }
   return false;
+}
+
+// The keys of a sequence that there are.
+__device__ inline int length_of(const Attention& a, const Tile& tile) {
+  return static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(tile.start) + tile.n, static_cast<int64_t>(a.cache.max_tokens))));
 }
 
 // A staged unit: the operands of both products, and what goes with them.
@@ -592,12 +602,6 @@ struct UnitFacts {
   int value;                            // and of the value operand, as its logarithm
   uint32_t bad;                         // tokens whose value is not finite
   uint32_t held;                        // whether a page holds the unit
-  // The same in scalar registers.
-  __device__ UnitFacts same() const {
-    auto one = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))); };
-    return UnitFacts{__uint_as_float(one(__float_as_uint(key))), static_cast<int>(one(static_cast<uint32_t>(value))), one(bad),
-                     one(held)};
-  }
 };
 
 // The state of 16 NT query columns of a wave whose keys and values come as operands
@@ -803,7 +807,7 @@ struct PromptColumns {
   __device__ __forceinline__ void steps(const Group& group, int u0, int i0, int i1) {
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-      const UnitFacts facts = group.facts(i).same();
+      const UnitFacts facts = group.facts(i);
       float f[NT], up;
 #pragma unroll
       for (int t = 0; t < NT; ++t) f[t] = qs[t] * facts.key;
@@ -817,160 +821,156 @@ struct PromptColumns {
   }
 };
 
-// A prompt's keys and values as the operands of both products, made once for all waves of
-// a workgroup, whose columns are their own.  Each unit is made by kParts waves; one group
-// of units is worked on while the next is made and the one behind it loaded.  A code times
-// its scale is exact in fp16, 3 bits by 8, the scales taken relative to a power of two of
-// their unit (those below 2^-14 of it lose bits).
+// The power of two at or below a scale; 0 for what has none that is normal.
+__device__ inline float power_below(float v) { return __uint_as_float(__float_as_uint(v) & 0x7f800000u); }
+
+// A long prompt's keys and values as the operands of both products, made once in the
+// workspace for all of its tiles: [slot][key head][unit] of kPieces KB, and the facts of
+// as many units behind them.  A code times its scale is exact in fp16, 3 bits by 8, the
+// scales taken relative to a power of two of their unit (those below 2^-14 of it lose bits).
+template <int D>
+struct Operands {
+  static constexpr int kPieces = StagedUnit<D>::kPieces, kKeys = StagedUnit<D>::kKeys;
+  uint4* piece;
+  UnitFacts* facts;
+  __device__ Operands(const Attention& a, int slot, int head) {
+    const int64_t all = static_cast<int64_t>(a.slots) * a.cache.kv_heads * a.slot_units;
+    const int64_t at = (static_cast<int64_t>(slot) * a.cache.kv_heads + head) * a.slot_units;
+    piece = reinterpret_cast<uint4*>(a.operands) + at * (kPieces * 64);
+    facts = reinterpret_cast<UnitFacts*>(a.operands + all * (kPieces * 1024)) + at;
+  }
+};
+
+// One unit a wave.
+template <int D>
+__global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int few) {
+  using O = Operands<D>;
+  __shared__ _Float16 scales[kAttnWaves][64];
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, wave = wave_index();
+  const int u = static_cast<int>(blockIdx.x) * kAttnWaves + wave, head = static_cast<int>(blockIdx.y);
+  Tile tile;
+  if (!find_tile(a, a.q_heads / a.cache.kv_heads, 0x40000000, few, 0x7fffffff, static_cast<int>(blockIdx.z), tile)) return;
+  const int length = length_of(a, tile);
+  if (kUnit * u >= length) return;
+  const O out(a, tile.slot, head);
+  UnitReader<D> reader(a.cache, tile.b, head, u >> (a.cache.page_shift - 5));
+  bool held;
+  const uint8_t* unit = reader.place(u, held);
+  UnitWords<D> w;
+  reader.words(unit, w);
+  const uint32_t bits = reinterpret_cast<const uint16_t*>(unit + key_scales_at(D))[lane];
+  const Spread spread;
+  // the scale of key lane, or of value lane - 32; of places behind the last token nothing
+  float scale = held && kUnit * u + (lane & 31) < length ? __uint_as_float(bits << 16) : 0.0f;
+  const bool finite = fabsf(scale) < __builtin_inff();
+  const uint64_t broken = __ballot(!finite);
+  float top = finite ? scale : 0.0f;
+  top = fmaxf(top, lane_xor<1>(top));
+  top = fmaxf(top, lane_xor<2>(top));
+  top = fmaxf(top, lane_xor<4>(top));
+  top = fmaxf(top, lane_xor<8>(top));
+  float other = top;
+  swap_rows<16>(top, other);
+  top = power_below(fmaxf(top, other));
+  if (!finite && lane >= 32) scale = 0.0f;
+  scales[wave][lane] = static_cast<_Float16>(top > 0.0f ? scale * (1.0f / top) : scale * 0.0f);
+  const float key = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(top), 0));
+  const int value = static_cast<int>(__builtin_amdgcn_readlane(__float_as_uint(top), 32) >> 23);
+  if (lane == 0) out.facts[u] = UnitFacts{key, value != 0 ? value - 127 : kNoScale, static_cast<uint32_t>(broken >> 32), held};
+  // lanes of this wave only read what it wrote itself
+  __builtin_amdgcn_wave_barrier();
+  uint4* to = out.piece + static_cast<int64_t>(u) * (O::kPieces * 64) + lane;
+  auto store = [&](int i, uint32_t word, const v2h (&by)[4]) {
+    const v8h v = codes_of(word, spread);
+    v2h p[4];
+    __builtin_memcpy(p, &v, sizeof v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] *= by[e];
+    to[64 * i] = __builtin_bit_cast(uint4, p);
+  };
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const _Float16 by = scales[wave][8 * (m >> 2) + 4 * h + (m & 3)];
+    const v2h all[4] = {{by, by}, {by, by}, {by, by}, {by, by}};
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) store(h * (D / 32) + k, w.k[h][k], all);
+  }
+  const uint4 eight = *reinterpret_cast<const uint4*>(&scales[wave][32 + 8 * g]);
+  // the scales of tokens 0 and 4, 1 and 5, 2 and 6, 3 and 7 of the octet
+  const uint32_t by_token[4] = {__builtin_amdgcn_perm(eight.z, eight.x, 0x05040100u),
+                                __builtin_amdgcn_perm(eight.z, eight.x, 0x07060302u),
+                                __builtin_amdgcn_perm(eight.w, eight.y, 0x05040100u),
+                                __builtin_amdgcn_perm(eight.w, eight.y, 0x07060302u)};
+  v2h all[4];
+  __builtin_memcpy(all, by_token, sizeof all);
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d) store(O::kKeys + d, w.v[d], all);
+}
+
+// A group of units in LDS for all waves of a workgroup, whose columns are their own; the
+// next group comes straight into the other half while this one is worked on.
 template <int D, int WAVES>
 struct Staged {
   static constexpr int kUnits = D == 256 ? 2 : 4;                // a group
-  static constexpr int kKeys = StagedUnit<D>::kKeys, kPieces = StagedUnit<D>::kPieces;
-  static constexpr int kParts = WAVES / kUnits, kMine = kPieces / kParts;
+  static constexpr int kPieces = StagedUnit<D>::kPieces, kMine = kUnits * kPieces / WAVES;
   uint4 piece[2][kUnits][kPieces][64];
-  UnitFacts facts[2][kUnits];
-  _Float16 scales[WAVES][64];           // a wave's own, from its lanes to where they are used
 
-  // One group as the columns take it.
   struct Group {
     const Staged& s;
     int which;
+    UnitFacts of;                       // unit lane % kUnits
     __device__ StagedUnit<D> unit(int i) const { return StagedUnit<D>{&s.piece[which][i][0][0]}; }
-    __device__ UnitFacts facts(int i) const { return s.facts[which][i]; }
-    __device__ float key(int i) const { return s.facts[which][i].key; }
-  };
-
-  // A wave's share of a group on its way: the words of its pieces, and the scale of key
-  // lane, or of value lane - 32.
-  struct Share {
-    uint32_t w[kMine];
-    uint32_t scale = 0;
-    bool held = false;
-    __device__ __forceinline__ void load(UnitReader<D>& reader, int u, int last) {
-      held = false;
-      if (u >= last) return;
-      const uint8_t* unit = reader.place(u, held);
-      const int part = wave_index() / kUnits;
-      if constexpr (kParts == 1) {
-        uint32_t k[2][D / 32], v[4];
-        reader.load_keys(unit, 0, k[0]);
-        reader.load_keys(unit, 1, k[1]);
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) w[i] = k[i / (D / 32)][i % (D / 32)];
-#pragma unroll
-        for (int i = 0; i < kMine - kKeys; i += 4) {
-          reader.load_values(unit, i / 4, v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[kKeys + i + j] = v[j];
-        }
-      } else if (part < kParts / 2) {
-#pragma unroll
-        for (int h = 0; h < kMine / (D / 32); ++h) {
-          uint32_t k[D / 32];
-          reader.load_keys(unit, part * (kMine / (D / 32)) + h, k);
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) w[h * (D / 32) + j] = k[j];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kMine; i += 4) {
-          uint32_t v[4];
-          reader.load_values(unit, (part - kParts / 2) * (kMine / 4) + i / 4, v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[i + j] = v[j];
-        }
-      }
-      scale = reinterpret_cast<const uint16_t*>(unit + key_scales_at(D))[threadIdx.x & 63];
+    __device__ float key(int i) const { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(of.key), i)); }
+    __device__ UnitFacts facts(int i) const {
+      auto one = [i](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), i)); };
+      return UnitFacts{__uint_as_float(one(__float_as_uint(of.key))), static_cast<int>(one(static_cast<uint32_t>(of.value))),
+                       one(of.bad), one(of.held)};
     }
   };
-  static __device__ int mine() { return wave_index() % kUnits; }
 
-  // This wave's share of the group from unit u0 on; of keys from `end` on nothing is used.
-  __device__ __forceinline__ void make(int which, const Share& share, const Spread& spread, int u0, int end) {
-    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-    const int wave = wave_index(), mine = Staged::mine(), part = wave / kUnits;
-    float scale = share.held && kUnit * (u0 + mine) + (lane & 31) < end ? __uint_as_float(share.scale << 16) : 0.0f;
-    const bool finite = fabsf(scale) < __builtin_inff();
-    const uint64_t broken = __ballot(!finite);
-    // the largest of the keys in the lower lanes, of the values in the upper ones
-    float top = finite ? scale : 0.0f;
-    top = fmaxf(top, lane_xor<1>(top));
-    top = fmaxf(top, lane_xor<2>(top));
-    top = fmaxf(top, lane_xor<4>(top));
-    top = fmaxf(top, lane_xor<8>(top));
-    float other = top;
-    swap_rows<16>(top, other);
-    top = power_below(fmaxf(top, other));
-    if (!finite && lane >= 32) scale = 0.0f;
-    scales[wave][lane] = static_cast<_Float16>(top > 0.0f ? scale * (1.0f / top) : scale * 0.0f);
-    const float key = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(top), 0));
-    const int value = static_cast<int>(__builtin_amdgcn_readlane(__float_as_uint(top), 32) >> 23);
-    if (lane == 0 && part == 0) facts[which][mine] = UnitFacts{key, value != 0 ? value - 127 : kNoScale, static_cast<uint32_t>(broken >> 32), share.held};
-    // lanes of this wave only read what it wrote itself
-    __builtin_amdgcn_wave_barrier();
-    uint4* to = &piece[which][mine][part * kMine][lane];
-    auto store = [&](int i, const v2h (&by)[4]) {
-      const v8h v = codes_of(share.w[i], spread);
-      v2h p[4];
-      __builtin_memcpy(p, &v, sizeof v);
+  // This wave's pieces of the group from unit u0 on; those behind a slot's last unit are
+  // the slot's own spare ones, or the next slot's first.
+  __device__ __forceinline__ void fetch(const Operands<D>& from, int which, int u0) {
+    const int at = wave_index() * kMine;
+    const uint4* src = from.piece + (static_cast<int64_t>(u0) * kPieces + at) * 64 + (threadIdx.x & 63);
+    uint4* dst = &piece[which][0][0][0] + at * 64;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] *= by[e];
-      to[64 * i] = __builtin_bit_cast(uint4, p);
-    };
-    const int tile = kParts == 1 ? 0 : part * (kMine / (D / 32));
-    if (kParts == 1 || part < kParts / 2) {
-#pragma unroll
-      for (int i = 0; i < (kParts == 1 ? kKeys : kMine); ++i) {
-        const _Float16 by = scales[wave][8 * (m >> 2) + 4 * (tile + i / (D / 32)) + (m & 3)];
-        const v2h all[4] = {{by, by}, {by, by}, {by, by}, {by, by}};
-        store(i, all);
-      }
-    }
-    if (kParts == 1 || part >= kParts / 2) {
-      const uint4 eight = *reinterpret_cast<const uint4*>(&scales[wave][32 + 8 * g]);
-      // the scales of tokens 0 and 4, 1 and 5, 2 and 6, 3 and 7 of the octet
-      const uint32_t by_token[4] = {__builtin_amdgcn_perm(eight.z, eight.x, 0x05040100u),
-                                    __builtin_amdgcn_perm(eight.z, eight.x, 0x07060302u),
-                                    __builtin_amdgcn_perm(eight.w, eight.y, 0x05040100u),
-                                    __builtin_amdgcn_perm(eight.w, eight.y, 0x07060302u)};
-      v2h all[4];
-      __builtin_memcpy(all, by_token, sizeof all);
-#pragma unroll
-      for (int i = kParts == 1 ? kKeys : 0; i < kMine; ++i) store(i, all);
-    }
+    for (int j = 0; j < kMine; ++j)
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src + 64 * j),
+                                       (__attribute__((address_space(3))) void*)(dst + 64 * j), 16, 0, 0);
+  }
+  static __device__ __forceinline__ UnitFacts facts_of(const Operands<D>& from, int u0) {
+    return from.facts[u0 + static_cast<int>(threadIdx.x & (kUnits - 1))];
   }
 
-  // Units [first, last) of keys below `end`, this wave's share of the first group on its way.
   template <typename Columns>
-  __device__ __forceinline__ void run(Columns& c, UnitReader<D>& reader, Share& next, int first, int last, int end, bool idle) {
+  __device__ __forceinline__ void run(Columns& c, const Operands<D>& from, const UnitFacts& first_facts, int first, int last,
+                                      bool idle) {
     if (first >= last) return;
-    const int mine = Staged::mine();
-    const Spread spread;
-    make(0, next, spread, first, end);
-    next.load(reader, first + kUnits + mine, last);
-    __syncthreads();
+    UnitFacts facts = first_facts;
     int which = 0;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
     for (int u0 = first; u0 < last; u0 += kUnits, which ^= 1) {
-      // into the group that was done with before the last barrier
-      if (u0 + kUnits < last) make(which ^ 1, next, spread, u0 + kUnits, end);
-      next.load(reader, u0 + 2 * kUnits + mine, last);
+      // into the half that all waves were done with before the last barrier
+      UnitFacts next = facts;
+      if (u0 + kUnits < last) {
+        fetch(from, which ^ 1, u0 + kUnits);
+        next = facts_of(from, u0 + kUnits);
+      }
       const int i0 = max(0, c.any_from / kUnit - u0);
       const int i1 = idle ? 0 : min(min(kUnits, last - u0), (c.any_to + kUnit - 1) / kUnit - u0);
-      bool plain = i0 == 0 && i1 == kUnits && kUnit * u0 >= c.full_from && kUnit * (u0 + kUnits) <= c.full_to;
-      if (plain) {
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-          const UnitFacts f = facts[which][i].same();
-          plain = plain && f.held != 0 && f.bad == 0 && f.value == c.whole;
-        }
-      }
-      if (plain) c.template whole_group<kUnits>(Group{*this, which});
-      else c.steps(Group{*this, which}, u0, i0, i1);
+      const Group group{*this, which, facts};
+      const bool usual = facts.held != 0 && facts.bad == 0 && facts.value == c.whole;
+      if (i0 == 0 && i1 == kUnits && kUnit * u0 >= c.full_from && kUnit * (u0 + kUnits) <= c.full_to && __all(usual))
+        c.template whole_group<kUnits>(group);
+      else
+        c.steps(group, u0, i0, i1);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
+      facts = next;
     }
   }
-  // The power of two at or below a scale; 0 for what has none that is normal.
-  static __device__ float power_below(float v) { return __uint_as_float(__float_as_uint(v) & 0x7f800000u); }
 };
 
 // Sums over a query's parts: what a workgroup knows of where its rows go.
@@ -985,19 +985,14 @@ struct Rows {
 
 // The units [first, last) of a tile's rows [row0, row0 + rows) that belong to a part.
 __device__ inline void units_of(const Attention& a, const Tile& tile, int group, int rows, int part, int64_t start, int length,
-                                int& first, int& last, int& end) {
-  int from, unused;
+                                int& first, int& last) {
+  int from, end, unused;
   bounds_of(a, start, length, tile.row0 / group, from, unused);
   bounds_of(a, start, length, (min(tile.row0 + rows, tile.n * group) - 1) / group, unused, end);
   const int part_to = part == a.splits - 1 ? 0x7fffffff : (part + 1) * a.chunk;
   const int lo = max(from, part * a.chunk), hi = min(end, part_to);
   first = lo / kUnit;
   last = lo < hi ? (hi + kUnit - 1) / kUnit : 0;
-}
-
-// The keys of a sequence that there are.
-__device__ inline int length_of(const Attention& a, const Tile& tile) {
-  return static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(tile.start) + tile.n, static_cast<int64_t>(a.cache.max_tokens))));
 }
 
 // Few rows: the four waves have the same 16 NT columns and every fourth unit each.
@@ -1012,8 +1007,8 @@ __global__ __launch_bounds__(kAttnThreads, D * NT <= 64 ? 4 : D * NT <= 128 ? 3 
   if (!find_tile(a, group, kRows, few, many, static_cast<int>(blockIdx.x / static_cast<unsigned>(kv_heads)), tile)) return;
   const int wave = wave_index(), lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int length = length_of(a, tile), all = tile.n * group;
-  int first, last, end;
-  units_of(a, tile, group, kRows, part, tile.start, length, first, last, end);
+  int first, last;
+  units_of(a, tile, group, kRows, part, tile.start, length, first, last);
   UnitReader<D> reader(a.cache, tile.b, kv_head, first >> (a.cache.page_shift - 5));
   Columns<D, NT> c;
   UnitWords<D> words;
@@ -1090,19 +1085,24 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_many(Attention a, int fe
   const int part = static_cast<int>(blockIdx.y);
   Tile tile;
   if (!find_tile(a, group, kRows, few, many, static_cast<int>(blockIdx.x / static_cast<unsigned>(kv_heads)), tile)) return;
+  if (tile.slot >= a.slots) return;     // more long prompts than rows: the offsets rise and fall
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int length = length_of(a, tile), all = tile.n * group;
   const int row0 = tile.row0 + 16 * NT * wave_index();
-  const bool idle = row0 >= all;        // a wave behind the tile's rows: it only stages
-  int first, last, end;
-  units_of(a, tile, group, kRows, part, tile.start, length, first, last, end);
-  UnitReader<D> reader(a.cache, tile.b, kv_head, first >> (a.cache.page_shift - 5));
+  const bool idle = row0 >= all;        // a wave behind the tile's rows: it only fetches
+  int first, last;
+  units_of(a, tile, group, kRows, part, tile.start, length, first, last);
+  const Operands<D> from(a, tile.slot, kv_head);
   __shared__ Staged<D, WAVES> staged;
   PromptColumns<D, NT, std::is_same_v<In, _Float16> ? 2 : 1> c;
-  typename Staged<D, WAVES>::Share share;
-  c.template open<In>(a, group, kv_head, tile.off, tile.n, tile.start, length, idle ? tile.row0 : row0,
-                      [&] { share.load(reader, first + Staged<D, WAVES>::mine(), last); });
-  staged.run(c, reader, share, first, last, end, idle);
+  UnitFacts facts{};
+  c.template open<In>(a, group, kv_head, tile.off, tile.n, tile.start, length, idle ? tile.row0 : row0, [&] {
+    if (first < last) {
+      staged.fetch(from, 0, first);
+      facts = staged.facts_of(from, first);
+    }
+  });
+  staged.run(c, from, facts, first, last, idle);
   if (idle) return;
   const float whole = c.whole == kNoScale ? 0.0f : ldexpf(1.0f, c.whole);
 
@@ -1282,23 +1282,23 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
   if (g == 0) finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row * D);
 }
 
-// Sequences of at most this many rows (tokens times query heads a key head) take
-// the kernel whose waves share their columns.
-constexpr int kFewRows = 32;
-// Column tiles of a wave and waves of the other kernel.
+// Rows (tokens times query heads a key head) from which on a sequence's keys and values
+// are made operands first; tiles of the kernel for few rows are 16 rows where that is
+// most sequences' number, else 32.
+constexpr int kFewRows = 512;
+// Column tiles of a wave and waves of the kernel for many rows.
 constexpr int wide_tiles(int head_dim) { return head_dim == 256 ? 1 : 2; }
-constexpr int wide_waves(int head_dim) { return head_dim == 64 ? 4 : 8; }
+constexpr int kWideWaves = 8;
+constexpr int64_t kMostOperands = int64_t{8} << 30;             // bytes
 
 int64_t tiles_bound(int64_t M, int64_t group, int64_t n_seqs, int64_t rows) {
   // one for every sequence that has rows, and one for every full tile
   return std::min(M * group / rows + std::min(n_seqs, M), M * ((group + rows - 1) / rows));
 }
 
-// A kernel whose waves have `columns` each, or (own = 0) four waves the same ones.
 template <typename Kernel>
-hipError_t launch_tiles(Kernel kernel, const Attention& a, int columns, int own, int few, int many, hipStream_t stream) {
-  const int waves = own != 0 ? own : kAttnWaves;
-  const int64_t tiles = tiles_bound(a.M, a.q_heads / a.cache.kv_heads, a.cache.n_seqs, own != 0 ? columns * own : columns);
+hipError_t launch_tiles(Kernel kernel, const Attention& a, int rows, int waves, int few, int many, hipStream_t stream) {
+  const int64_t tiles = tiles_bound(a.M, a.q_heads / a.cache.kv_heads, a.cache.n_seqs, rows);
   const int64_t grid = tiles * a.cache.kv_heads;
   if (grid * 64 * waves >= (int64_t{1} << 32)) return hipErrorInvalidConfiguration;
   kernel<<<dim3(static_cast<unsigned>(grid), static_cast<unsigned>(a.splits)), dim3(64 * waves), 0, stream>>>(a, few, many);
@@ -1308,16 +1308,25 @@ hipError_t launch_tiles(Kernel kernel, const Attention& a, int columns, int own,
 template <int D, typename In>
 hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   constexpr int kAll = 0x7fffffff;
-  constexpr int kWide = wide_tiles(D), kWaves = wide_waves(D);
+  constexpr int kTiles = wide_tiles(D);
   const int64_t rows = static_cast<int64_t>(a.M) * (a.q_heads / a.cache.kv_heads);
-  const int64_t mean = rows / a.cache.n_seqs;
-  hipError_t e;
-  if (mean <= 16) e = launch_tiles(attend_few<D, 1, In>, a, 16, 0, 0, kAll, stream);
-  else if (mean <= kFewRows) e = launch_tiles(attend_few<D, 2, In>, a, 32, 0, 0, kAll, stream);
-  else {
+  hipError_t e = hipSuccess;
+  const int many = a.slots > 0 ? kFewRows : kAll;
+  if (a.slots == 0 || a.cache.n_seqs > 1) {
+    e = rows / a.cache.n_seqs <= 16 ? launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream)
+                                    : launch_tiles(attend_few<D, 2, In>, a, 32, kAttnWaves, 0, many, stream);
+  }
+  if (a.slots > 0) {
     const int few = a.cache.n_seqs > 1 ? kFewRows : 0;
-    e = few != 0 ? launch_tiles(attend_few<D, 1, In>, a, 16, 0, 0, few, stream) : hipSuccess;
-    if (e == hipSuccess) e = launch_tiles(attend_many<D, kWide, kWaves, In>, a, 16 * kWide, kWaves, few, kAll, stream);
+    if (e == hipSuccess) {
+      const int64_t units = (a.cache.max_tokens + kUnit - 1) / kUnit;
+      make_operands<D><<<dim3(static_cast<unsigned>((units + kAttnWaves - 1) / kAttnWaves),
+                              static_cast<unsigned>(a.cache.kv_heads), static_cast<unsigned>(a.slots)),
+                         dim3(kAttnThreads), 0, stream>>>(a, few);
+      e = hipGetLastError();
+    }
+    if (e == hipSuccess)
+      e = launch_tiles(attend_many<D, kTiles, kWideWaves, In>, a, 16 * kTiles * kWideWaves, kWideWaves, few, kAll, stream);
   }
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t out_rows = static_cast<int64_t>(a.M) * a.q_heads;
@@ -1339,17 +1348,24 @@ hipError_t launch_type(const Attention& a, hipStream_t stream) {
 AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t n_seqs,
                                    int64_t max_tokens) {
   const int64_t group = q_heads / kv_heads, rows = M * group, mean = rows / n_seqs;
-  const bool shared = mean <= kFewRows;
-  const int64_t tile = shared ? (mean <= 16 ? 16 : 32) : 16 * wide_waves(head_dim) * wide_tiles(head_dim);
+  AttentionPlan p;
+  // long prompts: as many as there can be of more than kFewRows rows
+  const int64_t unit_bytes_ = static_cast<int64_t>(head_dim / 8) * 1024 + 16;
+  p.slot_units = (max_tokens + kUnit - 1) / kUnit + 4;          // and spare ones
+  p.slots = n_seqs == 1 ? (rows > kFewRows ? 1 : 0) : std::min({n_seqs, rows / (kFewRows + 1), int64_t{65535}});
+  if (mean <= 16 || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_) p.slots = 0;
+  const size_t operands = static_cast<size_t>(p.slots) * kv_heads * p.slot_units * unit_bytes_;
+  const bool wide = p.slots > 0;
+  const int64_t tile = wide ? 16 * kWideWaves * wide_tiles(head_dim) : mean <= 16 ? 16 : 32;
   const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
-  const int64_t wanted = shared ? 2048 : 512;
-  const int64_t least = shared ? 4 * kUnit : 16 * kUnit;         // keys of a part
+  const int64_t wanted = wide ? 256 : 2048;
+  const int64_t least = wide ? 16 * kUnit : 4 * kUnit;          // keys of a part
   int64_t splits = std::max<int64_t>(1, std::min((wanted + work - 1) / work, max_tokens / least));
   splits = std::min<int64_t>(splits, 64);
-  AttentionPlan p;
   p.chunk = static_cast<int>(((max_tokens + splits - 1) / splits + least - 1) / least * least);
   p.splits = static_cast<int>((max_tokens + p.chunk - 1) / p.chunk);
-  p.workspace = p.splits == 1 ? 0 : static_cast<size_t>(p.splits) * static_cast<size_t>(M * q_heads) * (head_dim + 2) * 4;
+  p.parts = p.splits == 1 ? 0 : (static_cast<size_t>(p.splits) * static_cast<size_t>(M * q_heads) * (head_dim + 2) * 4 + 255) / 256 * 256;
+  p.workspace = p.parts + operands;
   return p;
 }
 

@@ -250,7 +250,8 @@ hipError_t launch_cache_copy(uint8_t* pages, int64_t layers, int64_t layer_bytes
 // of a sequence in `splits` parts of `chunk` (the last takes the rest).
 struct AttentionPlan {
   int splits, chunk;
-  size_t workspace;                     // bytes
+  int64_t slots, slot_units;            // long prompts whose keys and values are made operands, units of each
+  size_t parts, workspace;              // bytes, of the parts' sums and of all
 };
 AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t n_seqs,
                                    int64_t max_tokens);
@@ -266,6 +267,8 @@ struct Attention {
   void* out;                            // [M, q_heads, head_dim]
   int splits, chunk;
   float* part;                          // workspace: [splits][M * q_heads][head_dim], then [splits][M * q_heads][2]
+  uint8_t* operands;                    // behind it, for `slots` prompts
+  int64_t slots, slot_units;
 };
 hipError_t launch_cache_attention(const Attention& a, bool f16, hipStream_t stream);
 
