@@ -851,7 +851,9 @@ __global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int f
   Tile tile;
   if (!find_tile(a, a.q_heads / a.cache.kv_heads, 0x40000000, few, 0x7fffffff, static_cast<int>(blockIdx.z), tile)) return;
   const int length = length_of(a, tile);
-  if (kUnit * u >= length) return;
+  int seen, unused;                     // from the first row's first key on
+  bounds_of(a, tile.start, length, 0, seen, unused);
+  if (kUnit * u >= length || kUnit * (u + 1) <= seen) return;
   const O out(a, tile.slot, head);
   UnitReader<D> reader(a.cache, tile.b, head, u >> (a.cache.page_shift - 5));
   bool held;
@@ -983,16 +985,18 @@ struct Rows {
   }
 };
 
-// The units [first, last) of a tile's rows [row0, row0 + rows) that belong to a part.
+// The units [first, last) of a tile's rows [row0, row0 + rows) that belong to a part; the
+// parts begin at the first unit that the tile sees.
 __device__ inline void units_of(const Attention& a, const Tile& tile, int group, int rows, int part, int64_t start, int length,
                                 int& first, int& last) {
   int from, end, unused;
   bounds_of(a, start, length, tile.row0 / group, from, unused);
   bounds_of(a, start, length, (min(tile.row0 + rows, tile.n * group) - 1) / group, unused, end);
-  const int part_to = part == a.splits - 1 ? 0x7fffffff : (part + 1) * a.chunk;
-  const int lo = max(from, part * a.chunk), hi = min(end, part_to);
-  first = lo / kUnit;
-  last = lo < hi ? (hi + kUnit - 1) / kUnit : 0;
+  const int64_t base = from / kUnit * kUnit + static_cast<int64_t>(part) * a.chunk;
+  const int64_t lo = max(static_cast<int64_t>(from), base);
+  const int64_t hi = part == a.splits - 1 ? end : min(static_cast<int64_t>(end), base + a.chunk);
+  first = static_cast<int>(min(lo, int64_t{0x7fffffff}) / kUnit);
+  last = lo < hi ? static_cast<int>((hi + kUnit - 1) / kUnit) : 0;
 }
 
 // Few rows: the four waves have the same 16 NT columns and every fourth unit each.
@@ -1219,7 +1223,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_many(Attention a, int fe
 // part a lane, then four parts at a time by 16 lanes each.  Parts whose keys the row
 // does not see at all may not have been written, and are not read.
 template <int D, typename In>
-__global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
+__global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a, int few_rows, int many, int many_rows) {
   constexpr int E = D / 16;
   const int64_t rows = static_cast<int64_t>(a.M) * a.q_heads;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kAttnWaves + wave_index();
@@ -1238,7 +1242,13 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a) {
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.0f;
   if (from < to) {
-    const int p0 = min(from / a.chunk, a.splits - 1), n = min((to - 1) / a.chunk, a.splits - 1) - p0 + 1;
+    // the parts begin where the row's tile does
+    const int group = a.q_heads / a.cache.kv_heads, rows_of = static_cast<int64_t>(s.end - s.off) * group > many ? many_rows : few_rows;
+    const int r = (token - s.off) * group + static_cast<int>(row % a.q_heads) % group;
+    int base, unused;
+    bounds_of(a, start, length, r / rows_of * rows_of / group, base, unused);
+    base = base / kUnit * kUnit;
+    const int p0 = min((from - base) / a.chunk, a.splits - 1), n = min((to - 1 - base) / a.chunk, a.splits - 1) - p0 + 1;
     const float2* heads = reinterpret_cast<const float2*>(a.part + a.splits * rows * D) + p0 * rows + row;
     const float* sums = a.part + (p0 * rows + row) * D + piece * E;
     const float2 head = lane < n ? heads[lane * rows] : make_float2(kNoReference, 0.0f);
@@ -1311,13 +1321,13 @@ hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   constexpr int kTiles = wide_tiles(D);
   const int64_t rows = static_cast<int64_t>(a.M) * (a.q_heads / a.cache.kv_heads);
   hipError_t e = hipSuccess;
-  const int many = a.slots > 0 ? kFewRows : kAll;
+  const int many = a.slots > 0 ? kFewRows : kAll, few = a.cache.n_seqs > 1 ? kFewRows : 0;
+  const int few_rows = rows / a.cache.n_seqs <= 16 ? 16 : 32;
   if (a.slots == 0 || a.cache.n_seqs > 1) {
-    e = rows / a.cache.n_seqs <= 16 ? launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream)
+    e = few_rows == 16 ? launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream)
                                     : launch_tiles(attend_few<D, 2, In>, a, 32, kAttnWaves, 0, many, stream);
   }
   if (a.slots > 0) {
-    const int few = a.cache.n_seqs > 1 ? kFewRows : 0;
     if (e == hipSuccess) {
       const int64_t units = (a.cache.max_tokens + kUnit - 1) / kUnit;
       make_operands<D><<<dim3(static_cast<unsigned>((units + kAttnWaves - 1) / kAttnWaves),
@@ -1332,7 +1342,8 @@ hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   const int64_t out_rows = static_cast<int64_t>(a.M) * a.q_heads;
   const int64_t grid = (out_rows + kAttnWaves - 1) / kAttnWaves;
   if (grid * kAttnThreads >= (int64_t{1} << 32)) return hipErrorInvalidConfiguration;
-  join_kernel<D, In><<<dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream>>>(a);
+  join_kernel<D, In><<<dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream>>>(a, few_rows, a.slots == 0 ? kAll : few,
+                                                                                           16 * kTiles * kWideWaves);
   return hipGetLastError();
 }
 
@@ -1346,7 +1357,7 @@ hipError_t launch_type(const Attention& a, hipStream_t stream) {
 }  // namespace
 
 AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t n_seqs,
-                                   int64_t max_tokens) {
+                                   int64_t max_tokens, int64_t window) {
   const int64_t group = q_heads / kv_heads, rows = M * group, mean = rows / n_seqs;
   AttentionPlan p;
   // long prompts: as many as there can be of more than kFewRows rows
@@ -1358,14 +1369,25 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
   const bool wide = p.slots > 0;
   const int64_t tile = wide ? 16 * kWideWaves * wide_tiles(head_dim) : mean <= 16 ? 16 : 32;
   const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
-  const int64_t wanted = wide ? 256 : 2048;
-  const int64_t least = wide ? 16 * kUnit : 4 * kUnit;          // keys of a part
-  int64_t splits = std::max<int64_t>(1, std::min((wanted + work - 1) / work, max_tokens / least));
-  splits = std::min<int64_t>(splits, 64);
-  p.chunk = static_cast<int>(((max_tokens + splits - 1) / splits + least - 1) / least * least);
-  p.splits = static_cast<int>((max_tokens + p.chunk - 1) / p.chunk);
+  // Workgroups: few rows 1024, four a CU (64 chats of up to 8192 tokens, 8 key heads: 72 us;
+  // 512 86, 2048 76), and no part under 1024 keys, eight units a wave, since joining parts
+  // costs a launch (16 chats that see 1024: one part 20 us, of 512 keys 23, of 256 21; one
+  // chat of 1000 tokens 11 and 14).  Prompts one for every CU, which has room for one.
+  const int64_t wanted = wide ? 256 : 1024;
+  const int64_t least = wide ? 16 * kUnit : 32 * kUnit;         // keys of a part
+  const int64_t most = std::min<int64_t>((wanted + work - 1) / work, 64);
+  // of all the keys, as the workspace is for a call with any window, and then of those a
+  // tile sees: no more parts
+  auto cut = [&](int64_t span, int64_t parts) {
+    parts = std::max<int64_t>(1, std::min(parts, span / least));
+    p.chunk = static_cast<int>(((span + parts - 1) / parts + least - 1) / least * least);
+    p.splits = static_cast<int>((span + p.chunk - 1) / p.chunk);
+  };
+  cut(max_tokens, most);
   p.parts = p.splits == 1 ? 0 : (static_cast<size_t>(p.splits) * static_cast<size_t>(M * q_heads) * (head_dim + 2) * 4 + 255) / 256 * 256;
   p.workspace = p.parts + operands;
+  const int64_t seen = window + (tile + group - 1) / group + kUnit;
+  if (window != 0 && seen < max_tokens) cut(seen, p.splits);
   return p;
 }
 

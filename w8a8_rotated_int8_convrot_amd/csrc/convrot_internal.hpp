@@ -247,14 +247,14 @@ hipError_t launch_cache_copy(uint8_t* pages, int64_t layers, int64_t layer_bytes
                              const int32_t* dst, int64_t n, hipStream_t stream);
 
 // How convrot_cache_attention cuts its work, from sizes the host knows: the keys
-// of a sequence in `splits` parts of `chunk` (the last takes the rest).
+// that a tile of rows sees in `splits` parts of `chunk` (the last takes the rest).
 struct AttentionPlan {
   int splits, chunk;
   int64_t slots, slot_units;            // long prompts whose keys and values are made operands, units of each
   size_t parts, workspace;              // bytes, of the parts' sums and of all
 };
 AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t n_seqs,
-                                   int64_t max_tokens);
+                                   int64_t max_tokens, int64_t window);
 struct Attention {
   Cache cache;
   const void* q;
