@@ -144,10 +144,14 @@ MANY = [
     ([(0, 40)], 4, 1, 128, 64), ([(0, 300)], 1, 2, 64, 32), ([(5, 130), (70, 1), (0, 65), (9, 0), (300, 90)], 4, 2, 128, 32),
     ([(0, 257)], 2, 1, 256, 256), ([(1000, 77), (31, 64)], 3, 2, 128, 128), ([(0, 70), (400, 100)], 8, 1, 64, 64),
     ([(17, 150), (3, 33)], 1, 3, 256, 64),
-    # more than 512 rows a key head: their keys and values made operands first
+    # around 512 rows a key head
     ([(0, 700)], 1, 2, 64, 32), ([(100, 300), (50, 1), (0, 200), (7, 2)], 4, 1, 128, 64), ([(1000, 600), (31, 64), (3, 530)], 1, 2, 128, 128),
     ([(17, 650)], 1, 1, 256, 64), ([(2000, 90)], 8, 1, 64, 64), ([(3, 140), (300, 257), (0, 0), (64, 129)], 4, 2, 256, 256),
     ([(0, 513)], 1, 1, 128, 32), ([(1, 33), (5, 1025)], 2, 1, 64, 128),
+    # 897 rows of one sequence, more than 768 on average of several, more than 2048: their keys and values made operands first
+    ([(0, 897)], 1, 1, 128, 32), ([(0, 910)], 1, 2, 64, 32), ([(17, 1000)], 1, 1, 256, 64), ([(3, 240), (300, 300), (0, 0), (64, 225)], 4, 2, 256, 256),
+    ([(1000, 950), (31, 64), (3, 930)], 1, 2, 128, 128), ([(2000, 130)], 8, 1, 64, 64), ([(100, 1), (9, 2100), (0, 1), (50, 3)], 1, 1, 128, 64),
+    ([(100, 300), (50, 1), (0, 200), (7, 250)], 4, 1, 128, 64),
 ]
 
 
@@ -167,7 +171,7 @@ def test_many_tokens(B, lens, G, H, D, page, io):
 @pytest.mark.gpu
 @pytest.mark.parametrize("lens,G,H,D,page,window", [
     ([(20000, 1)], 8, 2, 128, 64, 0), ([(9000, 1), (12, 1), (4000, 1)], 4, 2, 64, 256, 0), ([(7000, 3), (6000, 2)], 4, 1, 256, 32, 3000),
-    ([(8000, 60), (100, 70)], 4, 1, 128, 128, 0), ([(8000, 160)], 4, 1, 128, 128, 0), ([(6000, 600)], 1, 1, 64, 128, 700), ([(5000, 130)], 2, 1, 64, 64, 2000), ([(30000, 1), (200, 90), (3, 2)], 4, 1, 128, 64, 0)])
+    ([(8000, 60), (100, 70)], 4, 1, 128, 128, 0), ([(8000, 160)], 4, 1, 128, 128, 0), ([(6000, 600)], 1, 1, 64, 128, 700), ([(9000, 1000)], 1, 1, 128, 64, 700), ([(5000, 500)], 2, 1, 256, 128, 0), ([(5000, 130)], 2, 1, 64, 64, 2000), ([(30000, 1), (200, 90), (3, 2)], 4, 1, 128, 64, 0)])
 def test_long_sequences_in_parts(B, lens, G, H, D, page, window):
     g, *c = filled(sum(s for s, _ in lens), lens, H, D, page)
     q = queries(g, c[3], G * H, D, torch.float16)

@@ -913,7 +913,7 @@ __global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int f
 // next group comes straight into the other half while this one is worked on.
 template <int D, int WAVES>
 struct Staged {
-  static constexpr int kUnits = D == 256 ? 2 : 4;                // a group
+  static constexpr int kUnits = 64 * WAVES / D;                  // a group: a half has 8 KB for each wave
   static constexpr int kPieces = StagedUnit<D>::kPieces, kMine = kUnits * kPieces / WAVES;
   uint4 piece[2][kUnits][kPieces][64];
 
@@ -1292,13 +1292,25 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a, int few
   if (g == 0) finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row * D);
 }
 
-// Rows (tokens times query heads a key head) from which on a sequence's keys and values
-// are made operands first; tiles of the kernel for few rows are 16 rows where that is
-// most sequences' number, else 32.
-constexpr int kFewRows = 512;
+// Rows (tokens times query heads a key head) above which a sequence's keys and values are
+// made operands first.  One sequence: with 900 rows it does not pay yet (a fresh prompt 43
+// us and 15; 32 heads of 128 on 8, behind 8000 tokens 85 and 73), with 1001 behind 16000 it
+// does.  Of more only the mean is known here, and the two kernels run one after the other,
+// so that a batch should go by one of them: by this one if the mean is long (1001, 834 and
+// 667 rows: 363 us, 387 by the other, 496 by both), else by the other but for prompts that
+// are much longer than the rest (900 rows and seven of 844 to 506, behind 8000 to 1000
+// tokens: 231 us, 247 by this one, 346 by both).
+constexpr int few_rows(int64_t n_seqs, int64_t mean) { return n_seqs == 1 ? 896 : mean > 768 ? 256 : 2048; }
 // Column tiles of a wave and waves of the kernel for many rows.
 constexpr int wide_tiles(int head_dim) { return head_dim == 256 ? 1 : 2; }
-constexpr int kWideWaves = 8;
+// A workgroup of four waves has 64 KB of LDS and a CU two of them, out of step: better
+// wherever tiles are uneven and a wave's work on a unit is long (D 64: 361 us against 435
+// for three pieces behind 16000 tokens, 143 against 164 for a prompt of 4608; 256: 346
+// against 391; 128 with fp16 queries in two terms: 282 against 320).  128 with one term has
+// the shortest and is held back by the fetches of the units, which eight waves share
+// (four pieces behind 7000 tokens 354 us against 389, a prompt of 4608 as fast).
+template <int D, typename In> constexpr int wide_waves() { return D == 128 && !std::is_same_v<In, _Float16> ? 8 : 4; }
+constexpr int kWidest = 8;              // waves a CU
 constexpr int64_t kMostOperands = int64_t{8} << 30;             // bytes
 
 int64_t tiles_bound(int64_t M, int64_t group, int64_t n_seqs, int64_t rows) {
@@ -1318,13 +1330,15 @@ hipError_t launch_tiles(Kernel kernel, const Attention& a, int rows, int waves, 
 template <int D, typename In>
 hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   constexpr int kAll = 0x7fffffff;
-  constexpr int kTiles = wide_tiles(D);
+  constexpr int kTiles = wide_tiles(D), kWaves = wide_waves<D, In>();
   const int64_t rows = static_cast<int64_t>(a.M) * (a.q_heads / a.cache.kv_heads);
   hipError_t e = hipSuccess;
-  const int many = a.slots > 0 ? kFewRows : kAll, few = a.cache.n_seqs > 1 ? kFewRows : 0;
-  const int few_rows = rows / a.cache.n_seqs <= 16 ? 16 : 32;
+  const int64_t mean = rows / a.cache.n_seqs;
+  // tiles of 16 rows where that is most sequences' number
+  const int limit = few_rows(a.cache.n_seqs, mean), few_tile = mean <= 16 ? 16 : 32;
+  const int many = a.slots > 0 ? limit : kAll, few = a.cache.n_seqs > 1 ? limit : 0;
   if (a.slots == 0 || a.cache.n_seqs > 1) {
-    e = few_rows == 16 ? launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream)
+    e = few_tile == 16 ? launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream)
                                     : launch_tiles(attend_few<D, 2, In>, a, 32, kAttnWaves, 0, many, stream);
   }
   if (a.slots > 0) {
@@ -1336,14 +1350,14 @@ hipError_t launch_heads(const Attention& a, hipStream_t stream) {
       e = hipGetLastError();
     }
     if (e == hipSuccess)
-      e = launch_tiles(attend_many<D, kTiles, kWideWaves, In>, a, 16 * kTiles * kWideWaves, kWideWaves, few, kAll, stream);
+      e = launch_tiles(attend_many<D, kTiles, kWaves, In>, a, 16 * kTiles * kWaves, kWaves, few, kAll, stream);
   }
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t out_rows = static_cast<int64_t>(a.M) * a.q_heads;
   const int64_t grid = (out_rows + kAttnWaves - 1) / kAttnWaves;
   if (grid * kAttnThreads >= (int64_t{1} << 32)) return hipErrorInvalidConfiguration;
-  join_kernel<D, In><<<dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream>>>(a, few_rows, a.slots == 0 ? kAll : few,
-                                                                                           16 * kTiles * kWideWaves);
+  join_kernel<D, In><<<dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream>>>(a, few_tile, a.slots == 0 ? kAll : few,
+                                                                                           16 * kTiles * kWaves);
   return hipGetLastError();
 }
 
@@ -1360,19 +1374,20 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
                                    int64_t max_tokens, int64_t window) {
   const int64_t group = q_heads / kv_heads, rows = M * group, mean = rows / n_seqs;
   AttentionPlan p;
-  // long prompts: as many as there can be of more than kFewRows rows
+  // long prompts: as many as there can be
+  const int limit = few_rows(n_seqs, mean);
   const int64_t unit_bytes_ = static_cast<int64_t>(head_dim / 8) * 1024 + 16;
   p.slot_units = (max_tokens + kUnit - 1) / kUnit + 4;          // and spare ones
-  p.slots = n_seqs == 1 ? (rows > kFewRows ? 1 : 0) : std::min({n_seqs, rows / (kFewRows + 1), int64_t{65535}});
+  p.slots = n_seqs == 1 ? (rows > limit ? 1 : 0) : std::min({n_seqs, rows / (limit + 1), int64_t{65535}});
   if (mean <= 16 || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_) p.slots = 0;
   const size_t operands = static_cast<size_t>(p.slots) * kv_heads * p.slot_units * unit_bytes_;
   const bool wide = p.slots > 0;
-  const int64_t tile = wide ? 16 * kWideWaves * wide_tiles(head_dim) : mean <= 16 ? 16 : 32;
+  const int64_t tile = wide ? 16 * kWidest * wide_tiles(head_dim) : mean <= 16 ? 16 : 32;
   const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
   // Workgroups: few rows 1024, four a CU (64 chats of up to 8192 tokens, 8 key heads: 72 us;
   // 512 86, 2048 76), and no part under 1024 keys, eight units a wave, since joining parts
   // costs a launch (16 chats that see 1024: one part 20 us, of 512 keys 23, of 256 21; one
-  // chat of 1000 tokens 11 and 14).  Prompts one for every CU, which has room for one.
+  // chat of 1000 tokens 11 and 14).  Prompts a CU's full of rows for every CU.
   const int64_t wanted = wide ? 256 : 1024;
   const int64_t least = wide ? 16 * kUnit : 32 * kUnit;         // keys of a part
   const int64_t most = std::min<int64_t>((wanted + work - 1) / work, 64);
