@@ -88,7 +88,10 @@ __device__ inline void encode(const uint4 (&raw)[E / 8], int c, uint32_t (&w)[E 
   top = fmax(top, lane_xor8(top, 4));
   // one value that is not finite makes every sum of its row so (fmax passes over NaN)
   const bool finite = fabs(v[0]) < __builtin_inf();
-  const auto s16 = static_cast<__bf16>(static_cast<float>(top / 7.0));
+  // top / 7, rounded once: by the nearest to 1 / 7 and the remainder, which is exact
+  constexpr double kSeventh = 1.0 / 7.0;
+  const double near = top * kSeventh;
+  const auto s16 = static_cast<__bf16>(static_cast<float>(__builtin_fma(__builtin_fma(-7.0, near, top), kSeventh, near)));
   const float s = static_cast<float>(s16);
   scale = __builtin_bit_cast(uint16_t, s16);
   if (!finite || !(s < __builtin_inff())) scale = 0x7fc0u;

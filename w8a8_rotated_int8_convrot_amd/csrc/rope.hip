@@ -11,7 +11,10 @@
 //
 // Bound by memory: 4 bytes an element.  A workgroup takes a few tokens, makes
 // their sines and cosines once in LDS for all heads, and then moves vectors of
-// up to 16 bytes; a thread has up to four of them in flight.
+// up to 16 bytes; a thread has up to three of them in flight (4608 tokens of 48 heads of 128, half of
+// each turned: 18.9 us, 6.0 TB/s; four 19.7, two 19.0).  An item behind the last is the
+// last again, not stored: with the loads under a condition they went through scratch
+// memory (29 us).
 #include "convrot_internal.hpp"
 #include "rotate_device.hpp"
 
@@ -20,14 +23,14 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxTokens = 4;       // a workgroup
-constexpr int kRopeInFlight = 4;        // vectors a thread has loaded at a time
+constexpr int kRopeInFlight = 3;        // vectors a thread has loaded at a time
 
 // N 16-bit values as one memory access.
 template <int N> struct Raw;
 template <> struct Raw<1> { using type = uint16_t; };
 template <> struct Raw<2> { using type = uint32_t; };
-template <> struct Raw<4> { using type = uint2; };
-template <> struct Raw<8> { using type = uint4; };
+template <> struct Raw<4> { using type = uint32_t __attribute__((ext_vector_type(2))); };
+template <> struct Raw<8> { using type = uint32_t __attribute__((ext_vector_type(4))); };
 
 template <typename In, int N>
 __device__ inline void widen(const typename Raw<N>::type& r, float (&v)[N]) {
@@ -53,9 +56,30 @@ __device__ inline typename Raw<N>::type narrow(const float (&v)[N]) {
   return r;
 }
 
+// The dims behind the turned ones of so many heads, N values an item.
+template <typename In, int N, typename Place>
+__device__ inline void copy_rest(int heads, const Rope& p, int tid, Place&& place) {
+  using R = typename Raw<N>::type;
+  const int each = (p.head_dim - p.rot_dim) / N, items = heads * each;
+  for (int i0 = tid; i0 < items; i0 += kRopeThreads * kRopeInFlight) {
+    R v[kRopeInFlight];
+    In* to[kRopeInFlight];
+#pragma unroll
+    for (int j = 0; j < kRopeInFlight; ++j) {
+      int t, e;                         // behind the last item the last again, not stored
+      const In* from;
+      place(min(i0 + j * kRopeThreads, items - 1), each, t, e, from, to[j]);
+      to[j] += p.rot_dim + N * e;
+      v[j] = *reinterpret_cast<const R*>(from + p.rot_dim + N * e);
+    }
+#pragma unroll
+    for (int j = 0; j < kRopeInFlight; ++j)
+      if (i0 + j * kRopeThreads < items) *reinterpret_cast<R*>(to[j]) = v[j];
+  }
+}
+
 // V pairs are one item: in the half layout two vectors of V values rot / 2
-// apart, interleaved one vector of 2 V.  Behind the turned items of a head come
-// those of its copied rest, two values each.
+// apart, interleaved one vector of 2 V.
 template <typename In, int V, bool INTERLEAVED>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(Rope p, int tokens) {
   extern __shared__ float2 turn[];      // [tokens][rot / 2]: cosine, sine
@@ -63,6 +87,32 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(Rope p, int tokens) 
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * tokens;
   const int here = static_cast<int>(min(static_cast<int64_t>(tokens), p.M - m0));
   const int half = p.rot_dim / 2;
+  const int heads = static_cast<int>(p.part[0].heads + p.part[1].heads);
+
+  // item i of so many a head: its token and place in the head, and the head's
+  // first value in the input and the output
+  const int first = static_cast<int>(p.part[0].heads);
+  const auto* q_in = static_cast<const In*>(p.part[0].in) + m0 * p.part[0].in_stride;
+  const auto* k_in = static_cast<const In*>(p.part[1].in) + m0 * p.part[1].in_stride;
+  auto* q_out = static_cast<In*>(p.part[0].out) + m0 * p.part[0].out_stride;
+  auto* k_out = static_cast<In*>(p.part[1].out) + m0 * p.part[1].out_stride;
+  const int64_t q_in_stride = p.part[0].in_stride, k_in_stride = p.part[1].in_stride;
+  const int64_t q_out_stride = p.part[0].out_stride, k_out_stride = p.part[1].out_stride;
+  auto place = [&](int i, int per_head, int& t, int& e, const In*& from, In*& to) {
+    const int th = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(per_head));
+    e = i - th * per_head;
+    t = static_cast<int>(static_cast<unsigned>(th) / static_cast<unsigned>(heads));
+    const int h = th - t * heads;
+    const bool second = h >= first;
+    const int at = (second ? h - first : h) * p.head_dim;
+    from = (second ? k_in : q_in) + (t * (second ? k_in_stride : q_in_stride) + at);
+    to = (second ? k_out : q_out) + (t * (second ? k_out_stride : q_out_stride) + at);
+  };
+  // what is not turned first: its loads are under way while the sines are made
+  if (p.rot_dim != p.head_dim) {
+    if (p.rot_dim % 8 == 0) copy_rest<In, 8>(here * heads, p, tid, place);
+    else copy_rest<In, 2>(here * heads, p, tid, place);
+  }
   for (int i = tid; i < here * half; i += kRopeThreads) {
     const int t = i / half;
     const double turns = static_cast<double>(p.positions[m0 + t]) * (p.freqs[i - t * half] * 0.15915494309189533577);
@@ -75,41 +125,21 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(Rope p, int tokens) 
   constexpr int kV = INTERLEAVED ? 2 * V : V;
   using R = typename Raw<kV>::type;
   const int turned = half / V;
-  const int heads = static_cast<int>(p.part[0].heads + p.part[1].heads);
-  const int rest = (p.head_dim - p.rot_dim) / 2;
-  const int items = here * heads * turned;
 
-  // item i of so many a head: its token and place in the head, and the head's
-  // first value in the input and the output
-  const int first = static_cast<int>(p.part[0].heads);
-  auto place = [&](int i, int per_head, int& t, int& e, const In*& from, In*& to) {
-    const int th = i / per_head;
-    e = i - th * per_head;
-    t = th / heads;
-    const int h = th - t * heads;
-    const bool second = h >= first;
-    const int64_t m = m0 + t, at = static_cast<int64_t>(second ? h - first : h) * p.head_dim;
-    from = static_cast<const In*>(second ? p.part[1].in : p.part[0].in) +
-           m * (second ? p.part[1].in_stride : p.part[0].in_stride) + at;
-    to = static_cast<In*>(second ? p.part[1].out : p.part[0].out) +
-         m * (second ? p.part[1].out_stride : p.part[0].out_stride) + at;
-  };
+  const int items = here * heads * turned;
   for (int i0 = tid; i0 < items; i0 += kRopeThreads * kRopeInFlight) {
     R a[kRopeInFlight], b[kRopeInFlight];
     In* to[kRopeInFlight];
     const float2* cs[kRopeInFlight];
 #pragma unroll
     for (int j = 0; j < kRopeInFlight; ++j) {
-      const int i = i0 + j * kRopeThreads;
-      if (i < items) {
-        int t, e;
-        const In* from;
-        place(i, turned, t, e, from, to[j]);
-        to[j] += e * kV;
-        cs[j] = turn + t * half + e * V;
-        a[j] = *reinterpret_cast<const R*>(from + e * kV);
-        if constexpr (!INTERLEAVED) b[j] = *reinterpret_cast<const R*>(from + e * kV + half);
-      }
+      int t, e;
+      const In* from;
+      place(min(i0 + j * kRopeThreads, items - 1), turned, t, e, from, to[j]);
+      to[j] += e * kV;
+      cs[j] = turn + t * half + e * V;
+      a[j] = *reinterpret_cast<const R*>(from + e * kV);
+      if constexpr (!INTERLEAVED) b[j] = *reinterpret_cast<const R*>(from + e * kV + half);
     }
 #pragma unroll
     for (int j = 0; j < kRopeInFlight; ++j) {
@@ -136,14 +166,6 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(Rope p, int tokens) 
         *reinterpret_cast<R*>(to[j]) = narrow<In, kV>(u);
       }
     }
-  }
-  for (int i = tid; i < here * heads * rest; i += kRopeThreads) {
-    int t, e;
-    const In* from;
-    In* to;
-    place(i, rest, t, e, from, to);
-    const int at = p.rot_dim + 2 * e;
-    *reinterpret_cast<uint32_t*>(to + at) = *reinterpret_cast<const uint32_t*>(from + at);
   }
 }
 
