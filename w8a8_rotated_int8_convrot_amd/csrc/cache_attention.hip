@@ -9,25 +9,50 @@
 //
 // A wave's work is a unit of 32 keys against 16 NT query columns, a column
 // being one query head of one token: the heads that share a key head, and
-// tokens of one sequence, share its unit.  Everything stays in registers:
-//   scores  v_mfma_f32_16x16x32_f16 of codes x queries, so that a lane holds
-//           eight keys of one column: 8 g .. 8 g + 7 for its quarter g of the
-//           wave, by the order in which the rows of codes enter
-//   softmax running reference m, sum l per column, in base 2 and fp32
-//   output  v_mfma of value codes x weights: the eight keys a lane holds are
-//           those its operand has to hold, so the weights go from one product to
-//           the next without leaving their lane
-// Codes become fp16 by putting their four bits under an exponent: bits 0-3
-// under 2^10 read as 1024 + u, bits 4-7 as 1024 + 16 u, and one packed add or
-// multiply-add makes the code of it, without rounding.  Roundings: the rotated
-// query to fp16 (with a power of two of its own for a row whose values fp16
-// does not hold well), and a weight times its value's scale to fp16, both 11
-// bits, more than the 16-bit output of bf16 and as many as that of fp16.
+// tokens of one sequence, share its unit.  Both products are 16 x 16 matrix
+// instructions whose rows are keys, or the values' dims, and whose columns are
+// the queries.  The order in which the rows of codes enter gives quarter g of
+// the wave the scores of keys 8 g .. 8 g + 7 of its column, which are those that
+// the weights' operand has to hold: they go from one product to the next without
+// leaving their lane.  The softmax keeps a running reference m and sum l a
+// column, in base 2 and fp32.
 //
-// The reference m is not the maximum of t but of t + log2 vs, what the rounded
-// weight is made of, so that fp16 holds it whatever the scales are; it is a whole
-// number, moves only where a weight would pass 2^kRise times the last one, and
-// the sums are then rescaled by an exact power of two.
+// m is not the maximum of t but of t + log2 vs, what the rounded weight is made
+// of, so that fp16 holds it whatever the scales are; it is a whole number, moves
+// only where a weight would pass 2^kRise times the last one, and the sums are
+// then rescaled by an exact power of two.  A weight times its value's scale is
+// rounded to fp16, 11 bits: more than an output of bf16 has and as many as one
+// of fp16.
+//
+// Few rows (attend_few).  The units come from HBM once and bound the kernel, so
+// the codes enter as they lie: scores are int8 products of the codes and of the
+// rotated query in two digits of 8 bits, 15 bits together (one fp16, 11 bits,
+// was fewer than an fp16 output needs: 4.7e-4 off where 3.0e-4 is reached), with
+// the 8 that a code is held with taken off through the sum's first value.  The
+// weights' product takes the value codes as fp16: four bits under an exponent
+// read as 1024 + u or 1024 + 16 u, and one packed operation makes the code of it,
+// without rounding.  A workgroup's four waves take every fourth unit, each with
+// its loads one unit ahead, and join their sums in LDS; long sequences are cut
+// into parts, joined by a launch of their own.  64 tokens of 64 sequences of up
+// to 8192, 32 heads of 128 on 8: 72 us, 3.9 TB/s; 4 of up to 131000, 64 heads on
+// 8: 104 us, 3.3 TB/s, where eight columns a key head make it the vector unit's;
+// 1 of 1000: 10.8 us, latencies one behind the other: table, unit, products, the
+// waves' sums.
+//
+// Many rows (make_operands, attend_many).  A unit then serves hundreds of columns
+// and the products and exponentials bound the kernel.  Turning codes into operands
+// and scaling scores in every tile cost as much as the products (240 us where it is
+// 231 now), so one launch before writes keys and values as fp16 operands with
+// their scales in them, and the tiles fetch those straight into LDS, two groups of
+// units in turn, one worked on while the next is on its way.  A query of bf16 enters
+// as one fp16, 11 bits for an output of 8; one of fp16 as the sum of two.  The scores
+// of the next unit are started beside the exponentials of this one.  A causal
+// prompt of 4608, 32 heads of 128 on 8: 231 us, 753 TFLOP/s counting visible keys
+// (9 of it for the operands); three pieces of 667 to 1001 behind up to 16000, 24
+// heads of 64, fp16, two terms: 359 us, 505 TFLOP/s (44 for the operands, which is
+// their bytes at 6 TB/s).  Matrix and vector unit are busy 31 and 46 %, 35 and 52 %:
+// a wave's products and exponentials follow each other, and two waves a SIMD, all
+// that the registers hold, cover little of that for each other.
 #include <algorithm>
 
 #include "cache.hpp"
@@ -841,7 +866,8 @@ struct Operands {
   }
 };
 
-// One unit a wave.
+// One unit a wave: what it reads comes once, and what it writes bounds it (24 heads of 64,
+// 34000 tokens: 44 us, 6.1 TB/s).
 template <int D>
 __global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int few) {
   using O = Operands<D>;
@@ -1221,7 +1247,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_many(Attention a, int fe
 
 // The parts of a row joined, a wave a row: first every part's reference and sum, a
 // part a lane, then four parts at a time by 16 lanes each.  Parts whose keys the row
-// does not see at all may not have been written, and are not read.
+// does not see at all may not have been written, and are not read.  64 rows of 32 heads in
+// two parts: 4.9 us, a launch's length; 4 of 64 in 32 parts: 6.9.
 template <int D, typename In>
 __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a, int few_rows, int many, int many_rows) {
   constexpr int E = D / 16;
@@ -1301,7 +1328,17 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a, int few
 // are much longer than the rest (900 rows and seven of 844 to 506, behind 8000 to 1000
 // tokens: 231 us, 247 by this one, 346 by both).
 constexpr int few_rows(int64_t n_seqs, int64_t mean) { return n_seqs == 1 ? 896 : mean > 768 ? 256 : 2048; }
-// Column tiles of a wave and waves of the kernel for many rows.
+// Rows of a tile of the kernel for few: 16 where that is most sequences' number, else 32,
+// which share what a unit costs (128 wide: with 8 rows of each of 16 sequences behind 4000
+// tokens 20.4 us and 25.5, with 30 31.8 and 29.7, with 150 80.6 and 78.5; 64 wide: with 30
+// 34.7 and 41.7, with 150 79 and 74).  Sums of 256 wide heads leave no registers for 32 (30
+// rows: 31 us, 48 with 32; 150: 78 and 111).
+constexpr int few_tile(int head_dim, int64_t mean) {
+  return head_dim == 256 || mean <= (head_dim == 64 ? 32 : 16) ? 16 : 32;
+}
+// Column tiles of a wave of the kernel for many rows: two are what its registers hold of
+// 128 wide heads (256 and 40 bytes of scratch), and of 64 wide ones four spill (685 us
+// where two take 359).
 constexpr int wide_tiles(int head_dim) { return head_dim == 256 ? 1 : 2; }
 // A workgroup of four waves has 64 KB of LDS and a CU two of them, out of step: better
 // wherever tiles are uneven and a wave's work on a unit is long (D 64: 361 us against 435
@@ -1334,12 +1371,12 @@ hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.M) * (a.q_heads / a.cache.kv_heads);
   hipError_t e = hipSuccess;
   const int64_t mean = rows / a.cache.n_seqs;
-  // tiles of 16 rows where that is most sequences' number
-  const int limit = few_rows(a.cache.n_seqs, mean), few_tile = mean <= 16 ? 16 : 32;
+  const int limit = few_rows(a.cache.n_seqs, mean), tile = few_tile(D, mean);
   const int many = a.slots > 0 ? limit : kAll, few = a.cache.n_seqs > 1 ? limit : 0;
   if (a.slots == 0 || a.cache.n_seqs > 1) {
-    e = few_tile == 16 ? launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream)
-                                    : launch_tiles(attend_few<D, 2, In>, a, 32, kAttnWaves, 0, many, stream);
+    if constexpr (D == 256) e = launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream);
+    else e = tile == 16 ? launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream)
+                        : launch_tiles(attend_few<D, 2, In>, a, 32, kAttnWaves, 0, many, stream);
   }
   if (a.slots > 0) {
     if (e == hipSuccess) {
@@ -1356,7 +1393,7 @@ hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   const int64_t out_rows = static_cast<int64_t>(a.M) * a.q_heads;
   const int64_t grid = (out_rows + kAttnWaves - 1) / kAttnWaves;
   if (grid * kAttnThreads >= (int64_t{1} << 32)) return hipErrorInvalidConfiguration;
-  join_kernel<D, In><<<dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream>>>(a, few_tile, a.slots == 0 ? kAll : few,
+  join_kernel<D, In><<<dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream>>>(a, tile, a.slots == 0 ? kAll : few,
                                                                                            16 * kTiles * kWaves);
   return hipGetLastError();
 }
@@ -1382,7 +1419,7 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
   if (mean <= 16 || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_) p.slots = 0;
   const size_t operands = static_cast<size_t>(p.slots) * kv_heads * p.slot_units * unit_bytes_;
   const bool wide = p.slots > 0;
-  const int64_t tile = wide ? 16 * kWidest * wide_tiles(head_dim) : mean <= 16 ? 16 : 32;
+  const int64_t tile = wide ? 16 * kWidest * wide_tiles(head_dim) : few_tile(head_dim, mean);
   const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
   // Workgroups: few rows 1024, four a CU (64 chats of up to 8192 tokens, 8 key heads: 72 us;
   // 512 86, 2048 76), and no part under 1024 keys, eight units a wave, since joining parts
@@ -1390,7 +1427,7 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
   // chat of 1000 tokens 11 and 14).  Prompts a CU's full of rows for every CU.
   const int64_t wanted = wide ? 256 : 1024;
   const int64_t least = wide ? 16 * kUnit : 32 * kUnit;         // keys of a part
-  const int64_t most = std::min<int64_t>((wanted + work - 1) / work, 64);
+  const int64_t most = std::min<int64_t>((wanted + work - 1) / work, 64);   // one a lane where they are joined
   // of all the keys, as the workspace is for a call with any window, and then of those a
   // tile sees: no more parts
   auto cut = [&](int64_t span, int64_t parts) {

@@ -15,6 +15,14 @@
 // they are one wave's work: eight lanes a token, D / 8 dims a lane.  The wave that
 // has the first new token of such an octet takes all of its new ones, and keeps
 // the other tokens' bits of the words it writes.
+//
+// Bound by the vector unit where there are many tokens: six to eight stages of
+// 64-bit sums, three of them across lanes, then scale, code and check, some 37
+// instructions a value (10246 tokens of 16 heads of 64: append 26.5 us, 2.0 TB/s,
+// vector unit 64 % busy; read, without the check, 17.0, 3.2 TB/s, 54 %).  A
+// division instead of the reciprocal: 38.  Several heads a wave, with the octet
+// found once: no faster (26), for more registers.  64 tokens of 8 heads: 6.1 and
+// 4.9 us, a launch and a chain of latencies (offsets, table, rows).
 #include "cache.hpp"
 
 namespace convrot {
@@ -305,9 +313,13 @@ __global__ __launch_bounds__(kWaves * 64) void read_kernel(Cache cache, Rows<In>
   });
 }
 
-// Rows a wave: the octets of long runs begin every eight rows; where a sequence
-// brings a row or two, each row begins one of its own.
-int rows_a_wave(int64_t M, int n_seqs) { return M >= int64_t{4} * n_seqs ? 8 : 1; }
+// Rows a wave: the octets of long runs begin every eight rows, so that eight rows are one
+// or two octets' work (append and read of 10246 tokens of 16 heads 43 us, 91 with a wave
+// for each row); where a sequence brings few, each row begins an octet of its own, or most
+// waves end at once, and a wave's octets would follow one another (64 sequences of one
+// row 18 us, 43 with eight rows a wave; of up to eight 16.7 and 24.5; 512 of up to eight
+// 44.9 and 44.6).
+int rows_a_wave(int64_t M, int n_seqs) { return M >= int64_t{16} * n_seqs ? 8 : 1; }
 
 template <typename Launch>
 hipError_t by_rows(const Cache& c, int64_t M, Launch&& launch) {
@@ -320,9 +332,10 @@ hipError_t by_rows(const Cache& c, int64_t M, Launch&& launch) {
 
 // ---------------------------------------------------------------- pages
 
-constexpr int kPairsALaunch = 256;      // 2 KB of the launch's arguments
+constexpr int kPairsALaunch = 256;      // 2 KB of the launch's arguments, which need no copy before it
 constexpr int kCopyThreads = 256;
-constexpr int kCopyLoads = 4;           // 16-byte pieces of a thread
+constexpr int kCopyLoads = 4;           // 16-byte pieces of a thread: at the copy rate (200 pages
+                                        // of 68 KB in 32 layers: 165 us, 5.3 TB/s)
 struct Pairs {
   int32_t src[kPairsALaunch], dst[kPairsALaunch];
 };

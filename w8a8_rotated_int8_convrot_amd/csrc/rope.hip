@@ -11,10 +11,11 @@
 //
 // Bound by memory: 4 bytes an element.  A workgroup takes a few tokens, makes
 // their sines and cosines once in LDS for all heads, and then moves vectors of
-// up to 16 bytes; a thread has up to three of them in flight (4608 tokens of 48 heads of 128, half of
-// each turned: 18.9 us, 6.0 TB/s; four 19.7, two 19.0).  An item behind the last is the
-// last again, not stored: with the loads under a condition they went through scratch
-// memory (29 us).
+// up to 16 bytes; a thread has up to three of them in flight (4608 tokens of 48
+// heads of 128, half of each turned: 18.8 us, 6.0 TB/s; four 19.7, two 19.0).  An
+// item behind the last is the last again, not stored: with the loads under a
+// condition they went through scratch memory (29 us).  One token: 2.5 us, the
+// launch.
 #include "convrot_internal.hpp"
 #include "rotate_device.hpp"
 
@@ -172,7 +173,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(Rope p, int tokens) 
 template <typename In, int V, bool INTERLEAVED>
 hipError_t launch_width(const Rope& p, hipStream_t stream) {
   // the more tokens, the more of their vectors a thread has in flight, as long as
-  // every CU still has two workgroups
+  // every CU still has two workgroups (4608 tokens: four a workgroup 18.9 us, two 19.2, one
+  // 22.6)
   int tokens = 1;
   while (tokens < kRopeMaxTokens && p.M >= int64_t{4} * tokens * num_cus()) tokens *= 2;
   const int64_t grid = (p.M + tokens - 1) / tokens;
