@@ -635,7 +635,7 @@ int convrot_cache_read(const convrot_cache *cache, void *k, int64_t k_stride, vo
                        int io_dtype, int64_t M, void *stream);
 
 /* Workspace bytes convrot_cache_attention needs (0 where it needs none, and for a
- * bad size); max_tokens = max_pages * page. */
+ * bad size), whatever its window; max_tokens = max_pages * page. */
 size_t convrot_cache_attention_workspace(int64_t M, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t n_seqs,
                                          int64_t max_tokens);
 
@@ -648,16 +648,25 @@ size_t convrot_cache_attention_workspace(int64_t M, int64_t q_heads, int64_t kv_
  * that pages hold:
  *   t_j = scale * (q H / sqrt(D)) . (s_j c_j)      (the keys' scales and codes)
  *   out = rnd((sum_j softmax(t)_j s'_j c'_j) H / sqrt(D))     (the values')
- * and 0 where there is no such j.  Scores, softmax and sums are fp32, the rotated
- * query and each weight times its value's scale enter the products as fp16.
+ * and 0 where there is no such j.  Softmax statistics and sums are fp32.  Rounded to
+ * fewer bits are a weight times its value's scale (fp16, 11 bits) and the rotated query
+ * (15 bits of its row's largest value in one integer product; for long prompts fp16, the
+ * sum of two for fp16 rows).  For long prompts the cached scales enter as fp16 relative
+ * to the largest of 32 tokens: those below 2^-14 of it lose bits.
  *   q    [M, q_heads, head_dim] in io_dtype, rows q_stride elements apart (at least
  *        q_heads * head_dim, a multiple of 8).
  *   out  [M, q_heads, head_dim] in io_dtype, contiguous; must not overlap q.
- *   workspace  at least convrot_cache_attention_workspace bytes.
- * Long sequences are cut into parts by M, n_seqs and max_pages alone, which a host
- * knows: a table whose columns reach far past the tokens cuts too coarsely, so give
- * the columns that are used (max_pages, with the table's own stride).  A row's
- * result does not depend on what other rows, unread tokens or unused places hold.
+ *   workspace  at least convrot_cache_attention_workspace bytes: the parts' sums, and
+ *        for prompts of several hundred rows a key head their sequences' keys and values as
+ *        16-bit operands (4 head_dim bytes a token and key head, 8 GiB at most; past that
+ *        they are read as they lie).  It must not be shared with a call that may run at
+ *        the same time.
+ * The work is cut by M, n_seqs, max_pages and the window alone, which a host knows: a
+ * table whose columns reach far past the tokens cuts too coarsely and asks for more
+ * workspace than is used, so give the columns that are used (max_pages, with the table's
+ * own stride).  What other rows, other sequences and unused places hold changes no
+ * result; what tokens hold that a row does not see changes it within the roundings above
+ * at most (a call with other sizes may round differently).
  * q_heads a multiple of kv_heads, M * q_heads at most 2^30, window in [0, 2^31) and 0
  * unless causal; M = 0 is a no-op.  q, out and workspace are 16-byte aligned.
  * Errors: as convrot_cache_append, and scale not finite -> CONVROT_EINVAL, workspace

@@ -34,10 +34,11 @@
 // without rounding.  A workgroup's four waves take every fourth unit, each with
 // its loads one unit ahead, and join their sums in LDS; long sequences are cut
 // into parts, joined by a launch of their own.  64 tokens of 64 sequences of up
-// to 8192, 32 heads of 128 on 8: 72 us, 3.9 TB/s; 4 of up to 131000, 64 heads on
-// 8: 104 us, 3.3 TB/s, where eight columns a key head make it the vector unit's;
-// 1 of 1000: 10.8 us, latencies one behind the other: table, unit, products, the
-// waves' sums.
+// to 8192, 32 heads of 128 on 8: 70 us, 4.0 TB/s (5 of it the join); 4 of up to
+// 131000, 64 heads on 8: 104 us, 3.3 TB/s (7 the join; vector unit 36 %, matrix unit
+// 9 % busy: what is missing is bytes on their way, a unit a wave, 12 waves a CU, with
+// no registers for two); 1 of 1000: 10.8 us, latencies one behind the other: table,
+// unit, products, the waves' sums.
 //
 // Many rows (make_operands, attend_many).  A unit then serves hundreds of columns
 // and the products and exponentials bound the kernel.  Turning codes into operands
@@ -1421,11 +1422,13 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
   const bool wide = p.slots > 0;
   const int64_t tile = wide ? 16 * kWidest * wide_tiles(head_dim) : few_tile(head_dim, mean);
   const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
-  // Workgroups: few rows 1024, four a CU (64 chats of up to 8192 tokens, 8 key heads: 72 us;
-  // 512 86, 2048 76), and no part under 1024 keys, eight units a wave, since joining parts
-  // costs a launch (16 chats that see 1024: one part 20 us, of 512 keys 23, of 256 21; one
-  // chat of 1000 tokens 11 and 14).  Prompts a CU's full of rows for every CU.
-  const int64_t wanted = wide ? 256 : 1024;
+  // Workgroups: few rows 1536, six a CU, which has room for three or four and finds many of
+  // them short (64 chats of up to 8192 tokens, 8 key heads of 128: 70 us; 1024 72, 2048 76,
+  // 512 86; 32 of up to 8000, 16 of 64: 45, 1024 53; 8 of up to 32000: 49, 1024 49, 768 54),
+  // and no part under 1024 keys, eight units a wave, since joining parts costs a launch (16
+  // chats that see 1024: one part 20 us, of 512 keys 23, of 256 21; one chat of 1000 tokens
+  // 11 and 14).  Prompts a CU's full of rows for every CU.
+  const int64_t wanted = wide ? 256 : 1536;
   const int64_t least = wide ? 16 * kUnit : 32 * kUnit;         // keys of a part
   const int64_t most = std::min<int64_t>((wanted + work - 1) / work, 64);   // one a lane where they are joined
   // of all the keys, as the workspace is for a call with any window, and then of those a
