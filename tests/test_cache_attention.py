@@ -222,7 +222,7 @@ def test_tokens_without_a_page_are_left_out(B):
 @pytest.mark.parametrize("many", [False, True])
 def test_what_is_not_finite_stays_with_who_reads_it(B, many):
     H, D, page = 2, 128, 32
-    lens = [(64, 200 if many else 5)]
+    lens = [(64, 260 if many else 5)]
     g, pages, table, starts, offsets = filled(3, lens, H, D, page)
     q = queries(g, offsets, 8, D, torch.bfloat16).clone()
     lo, n = int(offsets[0]), lens[0][1]
@@ -253,7 +253,7 @@ def test_what_is_not_finite_stays_with_who_reads_it(B, many):
     (60.0, (0.3, 0.5), None), (2.0, (1e-15, 1e-12), 1e12), (2.0, (1e4, 1e9), 1e-9), (1.0, (0.0, 0.4), None), (2.0, (0.0, 0.0), None)])
 def test_sizes_of_values(B, size, scales, scale):
     """Queries, keys and values from very small to very large, scores that pick one token of all."""
-    for lens, G in (([(300, 1), (40, 1)], 4), ([(100, 80)], 2), ([(64, 300)], 2)):
+    for lens, G in (([(300, 1), (40, 1)], 4), ([(100, 80)], 2), ([(64, 300)], 2), ([(64, 460)], 2)):
         g, *c = filled(7, lens, 1, 128, 64, scales=scales)
         check(B, queries(g, c[3], G, 128, torch.bfloat16, size), *c, 1, 64, scale=scale)
 
@@ -284,6 +284,77 @@ def test_the_same_pages_twice(B):
     table[1, :4] = table[0, :4]
     q = queries(g, offsets, 8, D, torch.float16)
     check(B, q, pages, table, starts, offsets, H, page)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,io", [(64, "bf16"), (128, "bf16"), (128, "fp16"), (256, "fp16")])
+def test_long_prompts_with_gaps(B, D, io):
+    """Prompts long enough for operands of their own: tokens before the first, pages that no cache
+    has, sequences past their table, one of them alone and beside others."""
+    H, G, page = 2, 4, 64
+    dt = torch.bfloat16 if io == "bf16" else torch.float16
+    for lens in ([(-40, 300)], [(200, 300), (100, 400), (-500, 300), (-9, 260)]):
+        g, pages, table, starts, offsets = filled(len(lens) + D, lens, H, D, page)
+        table[0, 1], table[-1, 2] = -1, pages.shape[0]
+        q = queries(g, offsets, H * G, D, dt)
+        for kw in (dict(), dict(window=70), dict(causal=False)):
+            check(B, q, pages, table, starts, offsets, H, page, **kw)
+        check(B, q, pages, table[:, :3], starts, offsets, H, page)
+
+
+@pytest.mark.gpu
+def test_many_sequences(B):
+    """More sequences than a wave has lanes, of none to thousands of rows, with and without a window."""
+    lens = [(7 * i, i % 4) for i in range(150)]
+    lens[3], lens[66], lens[140] = (5, 2100), (0, 2300), (300, 2049)
+    g, *c = filled(21, lens, 1, 64, 32)
+    q = queries(g, c[3], 1, 64, torch.bfloat16)
+    check(B, q, *c, 1, 32)
+    check(B, q, *c, 1, 32, window=45)
+
+
+@pytest.mark.gpu
+def test_offsets_outside_the_rows_of_long_prompts_reach_nothing(B):
+    D, page, M = 64, 32, 1000
+    for seqs, offs in ((1, ([-5, 2 ** 31 - 1], [3, 3], [900, 2], [-2 ** 31, 990])),
+                       (4, ([0, M, 0, M, 0], [0, 2 ** 31 - 1, -1, M, 7], [M, 0, M, 0, M], [300, 200, 999, 1000, 2000]))):
+        g, pages, table, _, _ = filled(4, [(64, 1000)] * seqs, 1, D, page)
+        q = torch.randn(M, 4, D, device=DEV).half()
+        for off in offs:
+            for st in (0, 2 ** 31 - 1, -2 ** 31, -70, 1000):
+                B.convrot_cache_attention(q, pages, table, torch.full((seqs,), st, dtype=torch.int32, device=DEV),
+                                          torch.tensor(off, dtype=torch.int32, device=DEV), 1, page)
+                torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_long_prompts_captured_with_others(B):
+    """A long prompt and single tokens in one captured call: starts move between the replays."""
+    H, G, D, page = 1, 2, 128, 64
+    lens = [(2000, 1), (300, 1200), (64, 1), (0, 3)]
+    g, pages, table, starts, offsets = filled(13, lens, H, D, page)
+    q = queries(g, offsets, H * G, D, torch.bfloat16).clone()
+    out = torch.empty_like(q)
+    need = B.convrot_cache_attention_workspace(q.shape[0], H * G, H, D, 4, table.shape[1] * page)
+    guarded = torch.full((need + 4096,), 165, dtype=torch.uint8, device=DEV)
+    ws = guarded[:need]
+    run = lambda: B.convrot_cache_attention(q, pages, table, starts, offsets, H, page, out=out, workspace=ws)  # noqa: E731
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    lo, hi = int(offsets[0]), int(offsets[-1])
+    for i in range(3):
+        q.normal_()
+        starts.copy_(torch.tensor([2000 - i, 300 - 70 * i, 64, 0], dtype=torch.int32))
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, tol = ref.attention(q, pages, page, H, table, starts, offsets, D ** -0.5, True, 0)
+        assert ((out[lo:hi].double() - want[lo:hi]).abs() <= tol[lo:hi]).all()
+        assert torch.equal(B.convrot_cache_attention(q, pages, table, starts, offsets, H, page)[lo:hi], out[lo:hi])
+    assert (guarded[need:] == 165).all()
 
 
 @pytest.mark.gpu

@@ -198,6 +198,27 @@ def test_rows_at_the_borders(B, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io,sizes", [("fp16", [2.0 ** e for e in (-22, -18, -14, -7, 0, 7, 13)]),
+                                      ("bf16", [2.0 ** e for e in (-130, -126, -122, -118, -60, 60, 100, 120)])])
+def test_rows_of_every_size(B, io, sizes):
+    """Ordinary rows from subnormal values to the type's largest: bytes as in 64 bits."""
+    dt = torch.bfloat16 if io == "bf16" else torch.float16
+    for D in (64, 128, 256):
+        g = torch.Generator().manual_seed(D)
+        x = torch.randn(8 * len(sizes), 2, D, generator=g, dtype=torch.float64)
+        x *= torch.tensor(sizes, dtype=torch.float64).repeat(8)[:, None, None]
+        x = x.to(dt)
+        n = (x.shape[0] + 31) // 32
+        pages = torch.zeros(n, ref.page_bytes(32, 2, D), dtype=torch.uint8)
+        table, starts = torch.arange(n, dtype=torch.int32)[None], torch.zeros(1, dtype=torch.int32)
+        offsets = torch.tensor([0, x.shape[0]], dtype=torch.int32)
+        dev = [t.to(DEV) for t in (pages, table, starts, offsets, x)]
+        B.convrot_cache_append(dev[0], dev[1], dev[2], dev[3], dev[4], dev[4], 32)
+        ref.write(pages, 32, 2, D, table, starts, offsets, x, x)
+        assert torch.equal(dev[0].cpu(), pages)
+
+
+@pytest.mark.gpu
 def test_what_no_page_holds_is_not_stored(B):
     H, D, page = 2, 64, 32
     pages, _, starts, offsets, kv = batch(4, [(0, 70), (20, 70), (90, 10)], H, D, page, torch.float16)
