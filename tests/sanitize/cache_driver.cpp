@@ -41,7 +41,7 @@ hipError_t launch_cache_copy(uint8_t*, int64_t, int64_t, int64_t, const int32_t*
   for (int64_t i = 0; i < n; ++i) g_tokens += src[i] + dst[i];
   return hipSuccess;
 }
-AttentionPlan plan_cache_attention(int64_t M, int64_t, int64_t, int, int64_t, int64_t, int64_t) {
+AttentionPlan plan_cache_attention(int64_t M, int64_t, int64_t, int, int64_t, int64_t, int64_t, bool) {
   AttentionPlan p{};
   p.splits = 1;
   p.workspace = static_cast<size_t>(M) * 16;

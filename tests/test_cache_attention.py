@@ -96,6 +96,12 @@ def filled(seed, lens, H, D, page, spare=2, W=None, scales=(0.25, 0.55)):
     return g, pages, table, starts, offsets
 
 
+def wide_table(lens, G, page):
+    """Columns with which a sequence alone is long enough for operands of its own."""
+    rows = lens[0][1] * G
+    return 2 ** 23 // rows // page + 2 if len(lens) == 1 and rows > 896 else None
+
+
 def queries(g, offsets, Hq, D, dt, size=2.0):
     """A part of a wider row, as the projection gives it; two rows behind the last sequence."""
     M = int(offsets[-1]) + 2
@@ -148,10 +154,11 @@ MANY = [
     ([(0, 700)], 1, 2, 64, 32), ([(100, 300), (50, 1), (0, 200), (7, 2)], 4, 1, 128, 64), ([(1000, 600), (31, 64), (3, 530)], 1, 2, 128, 128),
     ([(17, 650)], 1, 1, 256, 64), ([(2000, 90)], 8, 1, 64, 64), ([(3, 140), (300, 257), (0, 0), (64, 129)], 4, 2, 256, 256),
     ([(0, 513)], 1, 1, 128, 32), ([(1, 33), (5, 1025)], 2, 1, 64, 128),
-    # 897 rows of one sequence, more than 768 on average of several, more than 2048: their keys and values made operands first
+    # of several more than 2048, and more than 896 alone in a wide table: their keys and values made operands first
     ([(0, 897)], 1, 1, 128, 32), ([(0, 910)], 1, 2, 64, 32), ([(17, 1000)], 1, 1, 256, 64), ([(3, 240), (300, 300), (0, 0), (64, 225)], 4, 2, 256, 256),
     ([(1000, 950), (31, 64), (3, 930)], 1, 2, 128, 128), ([(2000, 130)], 8, 1, 64, 64), ([(100, 1), (9, 2100), (0, 1), (50, 3)], 1, 1, 128, 64),
-    ([(100, 300), (50, 1), (0, 200), (7, 250)], 4, 1, 128, 64),
+    ([(100, 300), (50, 1), (0, 200), (7, 250)], 4, 1, 128, 64), ([(100, 300), (50, 1), (0, 3), (7, 25)], 8, 1, 128, 64),
+    ([(40, 33), (50, 1), (500, 1100), (0, 0), (31, 2)], 2, 2, 64, 128), ([(0, 300), (20, 350)], 3, 30, 64, 32),
 ]
 
 
@@ -160,7 +167,7 @@ MANY = [
 @pytest.mark.parametrize("lens,G,H,D,page", MANY)
 def test_many_tokens(B, lens, G, H, D, page, io):
     dt = torch.bfloat16 if io == "bf16" else torch.float16
-    g, *c = filled(len(lens) + D + 1, lens, H, D, page)
+    g, *c = filled(len(lens) + D + 1, lens, H, D, page, W=wide_table(lens, G, page))
     q = queries(g, c[3], G * H, D, dt)
     check(B, q, *c, H, page)
     check(B, q, *c, H, page, window=1)
@@ -223,7 +230,7 @@ def test_tokens_without_a_page_are_left_out(B):
 def test_what_is_not_finite_stays_with_who_reads_it(B, many):
     H, D, page = 2, 128, 32
     lens = [(64, 260 if many else 5)]
-    g, pages, table, starts, offsets = filled(3, lens, H, D, page)
+    g, pages, table, starts, offsets = filled(3, lens, H, D, page, W=wide_table(lens, 4, page))
     q = queries(g, offsets, 8, D, torch.bfloat16).clone()
     lo, n = int(offsets[0]), lens[0][1]
     clean = B.convrot_cache_attention(q, pages, table, starts, offsets, H, page)
@@ -254,7 +261,7 @@ def test_what_is_not_finite_stays_with_who_reads_it(B, many):
 def test_sizes_of_values(B, size, scales, scale):
     """Queries, keys and values from very small to very large, scores that pick one token of all."""
     for lens, G in (([(300, 1), (40, 1)], 4), ([(100, 80)], 2), ([(64, 300)], 2), ([(64, 460)], 2)):
-        g, *c = filled(7, lens, 1, 128, 64, scales=scales)
+        g, *c = filled(7, lens, 1, 128, 64, scales=scales, W=wide_table(lens, G, 64))
         check(B, queries(g, c[3], G, 128, torch.bfloat16, size), *c, 1, 64, scale=scale)
 
 
@@ -293,9 +300,9 @@ def test_long_prompts_with_gaps(B, D, io):
     has, sequences past their table, one of them alone and beside others."""
     H, G, page = 2, 4, 64
     dt = torch.bfloat16 if io == "bf16" else torch.float16
-    for lens in ([(-40, 300)], [(200, 300), (100, 400), (-500, 300), (-9, 260)]):
-        g, pages, table, starts, offsets = filled(len(lens) + D, lens, H, D, page)
-        table[0, 1], table[-1, 2] = -1, pages.shape[0]
+    for lens in ([(-40, 300)], [(200, 600), (10, 1), (-500, 300), (3, 1), (0, 2), (105, 1)]):
+        g, pages, table, starts, offsets = filled(len(lens) + D, lens, H, D, page, W=wide_table(lens, G, page))
+        table[0, 1], table[-1, 1] = -1, pages.shape[0]
         q = queries(g, offsets, H * G, D, dt)
         for kw in (dict(), dict(window=70), dict(causal=False)):
             check(B, q, pages, table, starts, offsets, H, page, **kw)
@@ -317,8 +324,8 @@ def test_many_sequences(B):
 def test_offsets_outside_the_rows_of_long_prompts_reach_nothing(B):
     D, page, M = 64, 32, 1000
     for seqs, offs in ((1, ([-5, 2 ** 31 - 1], [3, 3], [900, 2], [-2 ** 31, 990])),
-                       (4, ([0, M, 0, M, 0], [0, 2 ** 31 - 1, -1, M, 7], [M, 0, M, 0, M], [300, 200, 999, 1000, 2000]))):
-        g, pages, table, _, _ = filled(4, [(64, 1000)] * seqs, 1, D, page)
+                       (6, ([0, M, 0, M, 0, M, M], [0, 2 ** 31 - 1, -1, M, 7, 8, M - 1], [M, 0, M, 0, M, 0, M], [300, 200, 999, 1000, 2000, 0, 0]))):
+        g, pages, table, _, _ = filled(4, [(64, 1000)] * seqs, 1, D, page, W=wide_table([(64, 1000)] * seqs, 4, page))
         q = torch.randn(M, 4, D, device=DEV).half()
         for off in offs:
             for st in (0, 2 ** 31 - 1, -2 ** 31, -70, 1000):

@@ -202,7 +202,8 @@ size_t convrot_cache_attention_workspace(int64_t M, int64_t q_heads, int64_t kv_
       q_heads % kv_heads != 0 || !head_known(head_dim) || n_seqs < 1 || n_seqs > kMaxSeqs || max_tokens < 1 ||
       max_tokens > kMaxCacheTokens)
     return 0;
-  return plan_cache_attention(M, q_heads, kv_heads, head_dim, n_seqs, max_tokens, 0).workspace;
+  return std::max(plan_cache_attention(M, q_heads, kv_heads, head_dim, n_seqs, max_tokens, 0, false).workspace,
+                  plan_cache_attention(M, q_heads, kv_heads, head_dim, n_seqs, max_tokens, 0, true).workspace);
 }
 
 int convrot_cache_attention(const convrot_cache* cache, const void* q, int64_t q_heads, int64_t q_stride, int io_dtype,
@@ -228,14 +229,14 @@ int convrot_cache_attention(const convrot_cache* cache, const void* q, int64_t q
   if (!aligned16(out) || (workspace && !aligned16(workspace)))
     return fail(CONVROT_EALIGN, "%s: out and workspace must be 16-byte aligned", who);
   const AttentionPlan plan = plan_cache_attention(M, q_heads, cache->kv_heads, cache->head_dim, cache->n_seqs,
-                                                  cache->max_pages * cache->page, window);
+                                                  cache->max_pages * cache->page, window, io_dtype == CONVROT_F16);
   if (plan.workspace != 0 && (!workspace || ws_bytes < plan.workspace))
     return fail(CONVROT_EWORKSPACE, "%s: workspace of %zu bytes needed (convrot_cache_attention_workspace)", who,
                 plan.workspace);
   const Attention a{cache_of(*cache), q, q_stride, static_cast<int>(M), static_cast<int>(q_heads), cache->starts,
                     cache->offsets, scale, causal != 0, static_cast<int>(window), out, plan.splits, plan.chunk,
                     static_cast<float*>(workspace), static_cast<uint8_t*>(workspace) + plan.parts, plan.slots,
-                    plan.slot_units};
+                    plan.slot_units, plan.limit};
   return hip_status(launch_cache_attention(a, io_dtype == CONVROT_F16, static_cast<hipStream_t>(stream)), who);
 }
 

@@ -940,7 +940,7 @@ __global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int f
 // next group comes straight into the other half while this one is worked on.
 template <int D, int WAVES>
 struct Staged {
-  static constexpr int kUnits = 64 * WAVES / D;                  // a group: a half has 8 KB for each wave
+  static constexpr int kUnits = 4;      // a group
   static constexpr int kPieces = StagedUnit<D>::kPieces, kMine = kUnits * kPieces / WAVES;
   uint4 piece[2][kUnits][kPieces][64];
 
@@ -1320,15 +1320,28 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a, int few
   if (g == 0) finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row * D);
 }
 
-// Rows (tokens times query heads a key head) above which a sequence's keys and values are
-// made operands first.  One sequence: with 900 rows it does not pay yet (a fresh prompt 43
-// us and 15; 32 heads of 128 on 8, behind 8000 tokens 85 and 73), with 1001 behind 16000 it
-// does.  Of more only the mean is known here, and the two kernels run one after the other,
-// so that a batch should go by one of them: by this one if the mean is long (1001, 834 and
-// 667 rows: 363 us, 387 by the other, 496 by both), else by the other but for prompts that
-// are much longer than the rest (900 rows and seven of 844 to 506, behind 8000 to 1000
-// tokens: 231 us, 247 by this one, 346 by both).
-constexpr int few_rows(int64_t n_seqs, int64_t mean) { return n_seqs == 1 ? 896 : mean > 768 ? 256 : 2048; }
+// Which types and widths have the way by operands.  256 wide heads and fp16 queries of 128
+// wide ones are better off without: the one has no registers for more than a column tile a
+// wave (a prompt of 4608, 16 heads on 4: 346 us, 316 by the kernel for few; fp16 8 heads
+// 4440 and 2107), the other twice the products for its scores (four pieces of 250 behind
+// 16000 418 and 248, of 600 behind 8000 344 and 278; a prompt of 4608 alone 272 and 293).
+constexpr bool by_operands(int head_dim, bool f16) { return head_dim == 64 || (head_dim == 128 && !f16); }
+// Rows (tokens times query heads a key head) above which a sequence goes that way, which
+// pays where many rows read the same keys.  One sequence: by what its tiles read in all (32
+// heads of 128 on 8: 1000 rows behind 16000 tokens 112 us, 120 by the other; 4000 alone 62
+// and 30, behind 8000 191 and 239).  Of more only the mean is known here, and the two kernels
+// run one after the other, so that a batch should go by one of them: by this one if the
+// mean is long and the tiles are more than the CUs, as their lengths differ (24 heads of 64:
+// 1001, 834 and 667 rows, 288 tiles, 362 us, 387 by the other, 496 by both; 8 heads of 128:
+// four of 4000 to 2500 rows, 440 tiles, 77 and 85, of 2400 to 1500, 280 tiles, 298 and 278, of
+// 1000 to 625, 128 tiles, 325 and 248), else by the other but for prompts that are much
+// longer than the rest.
+constexpr int kNever = 0x7fffffff;
+int few_rows(int64_t n_seqs, int64_t rows, int64_t tiles, int64_t max_tokens) {
+  if (n_seqs == 1) return rows > 896 && rows * max_tokens >= int64_t{1} << 23 ? 896 : kNever;
+  if (rows / n_seqs <= 768) return 2048;
+  return tiles > 256 ? 256 : kNever;
+}
 // Rows of a tile of the kernel for few: 16 where that is most sequences' number, else 32,
 // which share what a unit costs (128 wide: with 8 rows of each of 16 sequences behind 4000
 // tokens 20.4 us and 25.5, with 30 31.8 and 29.7, with 150 80.6 and 78.5; 64 wide: with 30
@@ -1340,14 +1353,14 @@ constexpr int few_tile(int head_dim, int64_t mean) {
 // Column tiles of a wave of the kernel for many rows: two are what its registers hold of
 // 128 wide heads (256 and 40 bytes of scratch), and of 64 wide ones four spill (685 us
 // where two take 359).
-constexpr int wide_tiles(int head_dim) { return head_dim == 256 ? 1 : 2; }
-// A workgroup of four waves has 64 KB of LDS and a CU two of them, out of step: better
-// wherever tiles are uneven and a wave's work on a unit is long (D 64: 361 us against 435
-// for three pieces behind 16000 tokens, 143 against 164 for a prompt of 4608; 256: 346
-// against 391; 128 with fp16 queries in two terms: 282 against 320).  128 with one term has
-// the shortest and is held back by the fetches of the units, which eight waves share
-// (four pieces behind 7000 tokens 354 us against 389, a prompt of 4608 as fast).
-template <int D, typename In> constexpr int wide_waves() { return D == 128 && !std::is_same_v<In, _Float16> ? 8 : 4; }
+constexpr int kWideTiles = 2;
+// A workgroup of four waves has 64 KB of LDS at D = 64 and a CU two of them, out of step:
+// better where tiles are uneven and a wave's work on a unit is long (361 us against 435 with
+// eight for three pieces behind 16000 tokens, 143 against 164 for a prompt of 4608).  128 wide
+// heads have half the columns for as many bytes and are held back by the fetches of the
+// units, which eight waves share (four pieces behind 7000 tokens 354 us against 389, a
+// prompt of 4608 as fast).
+constexpr int wide_waves(int head_dim) { return head_dim == 128 ? 8 : 4; }
 constexpr int kWidest = 8;              // waves a CU
 constexpr int64_t kMostOperands = int64_t{8} << 30;             // bytes
 
@@ -1368,34 +1381,34 @@ hipError_t launch_tiles(Kernel kernel, const Attention& a, int rows, int waves, 
 template <int D, typename In>
 hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   constexpr int kAll = 0x7fffffff;
-  constexpr int kTiles = wide_tiles(D), kWaves = wide_waves<D, In>();
   const int64_t rows = static_cast<int64_t>(a.M) * (a.q_heads / a.cache.kv_heads);
   hipError_t e = hipSuccess;
-  const int64_t mean = rows / a.cache.n_seqs;
-  const int limit = few_rows(a.cache.n_seqs, mean), tile = few_tile(D, mean);
-  const int many = a.slots > 0 ? limit : kAll, few = a.cache.n_seqs > 1 ? limit : 0;
+  const int tile = few_tile(D, rows / a.cache.n_seqs);
+  const int many = a.slots > 0 ? a.limit : kAll, few = a.cache.n_seqs > 1 ? a.limit : 0;
   if (a.slots == 0 || a.cache.n_seqs > 1) {
     if constexpr (D == 256) e = launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream);
     else e = tile == 16 ? launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream)
                         : launch_tiles(attend_few<D, 2, In>, a, 32, kAttnWaves, 0, many, stream);
   }
-  if (a.slots > 0) {
-    if (e == hipSuccess) {
+  int many_tile = tile;
+  if constexpr (by_operands(D, std::is_same_v<In, _Float16>)) {
+    constexpr int kWaves = wide_waves(D);
+    many_tile = 16 * kWideTiles * kWaves;
+    if (a.slots > 0 && e == hipSuccess) {
       const int64_t units = (a.cache.max_tokens + kUnit - 1) / kUnit;
       make_operands<D><<<dim3(static_cast<unsigned>((units + kAttnWaves - 1) / kAttnWaves),
                               static_cast<unsigned>(a.cache.kv_heads), static_cast<unsigned>(a.slots)),
                          dim3(kAttnThreads), 0, stream>>>(a, few);
       e = hipGetLastError();
     }
-    if (e == hipSuccess)
-      e = launch_tiles(attend_many<D, kTiles, kWaves, In>, a, 16 * kTiles * kWaves, kWaves, few, kAll, stream);
+    if (a.slots > 0 && e == hipSuccess)
+      e = launch_tiles(attend_many<D, kWideTiles, kWaves, In>, a, many_tile, kWaves, few, kAll, stream);
   }
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t out_rows = static_cast<int64_t>(a.M) * a.q_heads;
   const int64_t grid = (out_rows + kAttnWaves - 1) / kAttnWaves;
   if (grid * kAttnThreads >= (int64_t{1} << 32)) return hipErrorInvalidConfiguration;
-  join_kernel<D, In><<<dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream>>>(a, tile, a.slots == 0 ? kAll : few,
-                                                                                           16 * kTiles * kWaves);
+  join_kernel<D, In><<<dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream>>>(a, tile, a.slots == 0 ? kAll : few, many_tile);
   return hipGetLastError();
 }
 
@@ -1409,18 +1422,20 @@ hipError_t launch_type(const Attention& a, hipStream_t stream) {
 }  // namespace
 
 AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t n_seqs,
-                                   int64_t max_tokens, int64_t window) {
-  const int64_t group = q_heads / kv_heads, rows = M * group, mean = rows / n_seqs;
+                                   int64_t max_tokens, int64_t window, bool f16) {
+  const int64_t group = q_heads / kv_heads, rows = M * group;
   AttentionPlan p;
+  const int64_t wide_tile = 16 * kWidest * kWideTiles;
+  const int limit = few_rows(n_seqs, rows, tiles_bound(M, group, n_seqs, wide_tile) * kv_heads, max_tokens);
   // long prompts: as many as there can be
-  const int limit = few_rows(n_seqs, mean);
   const int64_t unit_bytes_ = static_cast<int64_t>(head_dim / 8) * 1024 + 16;
+  p.limit = limit;
   p.slot_units = (max_tokens + kUnit - 1) / kUnit + 4;          // and spare ones
-  p.slots = n_seqs == 1 ? (rows > limit ? 1 : 0) : std::min({n_seqs, rows / (limit + 1), int64_t{65535}});
-  if (mean <= 16 || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_) p.slots = 0;
+  p.slots = n_seqs == 1 ? (rows > limit ? 1 : 0) : std::min({n_seqs, rows / (int64_t{1} + limit), int64_t{65535}});
+  if (!by_operands(head_dim, f16) || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_) p.slots = 0;
   const size_t operands = static_cast<size_t>(p.slots) * kv_heads * p.slot_units * unit_bytes_;
   const bool wide = p.slots > 0;
-  const int64_t tile = wide ? 16 * kWidest * wide_tiles(head_dim) : few_tile(head_dim, mean);
+  const int64_t tile = wide ? wide_tile : few_tile(head_dim, rows / n_seqs);
   const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
   // Workgroups: few rows 1536, six a CU, which has room for three or four and finds many of
   // them short (64 chats of up to 8192 tokens, 8 key heads of 128: 70 us; 1024 72, 2048 76,

@@ -251,10 +251,11 @@ hipError_t launch_cache_copy(uint8_t* pages, int64_t layers, int64_t layer_bytes
 struct AttentionPlan {
   int splits, chunk;
   int64_t slots, slot_units;            // long prompts whose keys and values are made operands, units of each
+  int limit;                            // rows a key head that a sequence of them has more than
   size_t parts, workspace;              // bytes, of the parts' sums and of all
 };
 AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t n_seqs,
-                                   int64_t max_tokens, int64_t window);
+                                   int64_t max_tokens, int64_t window, bool f16);
 struct Attention {
   Cache cache;
   const void* q;
@@ -269,6 +270,7 @@ struct Attention {
   float* part;                          // workspace: [splits][M * q_heads][head_dim], then [splits][M * q_heads][2]
   uint8_t* operands;                    // behind it, for `slots` prompts
   int64_t slots, slot_units;
+  int limit;
 };
 hipError_t launch_cache_attention(const Attention& a, bool f16, hipStream_t stream);
 
