@@ -649,15 +649,16 @@ size_t convrot_cache_attention_workspace(int64_t M, int64_t q_heads, int64_t kv_
  *   t_j = scale * (q H / sqrt(D)) . (s_j c_j)      (the keys' scales and codes)
  *   out = rnd((sum_j softmax(t)_j s'_j c'_j) H / sqrt(D))     (the values')
  * and 0 where there is no such j.  Softmax statistics and sums are fp32.  Rounded to
- * fewer bits are a weight times its value's scale (fp16, 11 bits) and the rotated query
- * (15 bits of its row's largest value in one integer product; for long prompts fp16, the
- * sum of two for fp16 rows).  For long prompts the cached scales enter as fp16 relative
+ * fewer bits are a weight times its value's scale (fp16, 11 bits; for fp16 rows but those
+ * of long prompts the sum of two) and the rotated query (15 bits of its row's largest
+ * value in one integer product; for long prompts fp16, the sum of two for fp16 rows).
+ * For long prompts the cached scales enter as fp16 relative
  * to the largest of 32 tokens: those below 2^-14 of it lose bits.
  *   q    [M, q_heads, head_dim] in io_dtype, rows q_stride elements apart (at least
  *        q_heads * head_dim, a multiple of 8).
  *   out  [M, q_heads, head_dim] in io_dtype, contiguous; must not overlap q.
  *   workspace  at least convrot_cache_attention_workspace bytes: the parts' sums, and
- *        for prompts of several hundred rows a key head their sequences' keys and values as
+ *        for long prompts, up to head_dim 128, their sequences' keys and values as
  *        16-bit operands (4 head_dim bytes a token and key head, 8 GiB at most; past that
  *        they are read as they lie).  It must not be shared with a call that may run at
  *        the same time.

@@ -21,13 +21,15 @@
 // of, so that fp16 holds it whatever the scales are; it is a whole number, moves
 // only where a weight would pass 2^kRise times the last one, and the sums are
 // then rescaled by an exact power of two.  A weight times its value's scale is
-// rounded to fp16, 11 bits: more than an output of bf16 has and as many as one
-// of fp16.
+// rounded to fp16, 11 bits: more than an output of bf16 has; for one of fp16,
+// which has as many, it enters as the sum of two in the kernel for few rows (2.1e-4
+// off, which is the output's own rounding, for 3.0e-4 in one; 1 to 12 % of the time).
+// For long prompts, bound by the products, it stays one: 2.9e-4.
 //
 // Few rows (attend_few).  The units come from HBM once and bound the kernel, so
 // the codes enter as they lie: scores are int8 products of the codes and of the
 // rotated query in two digits of 8 bits, 15 bits together (one fp16, 11 bits,
-// was fewer than an fp16 output needs: 4.7e-4 off where 3.0e-4 is reached), with
+// was fewer than an fp16 output needs: 4.7e-4 off where 3.1e-4 was reached), with
 // the 8 that a code is held with taken off through the sum's first value.  The
 // weights' product takes the value codes as fp16: four bits under an exponent
 // read as 1024 + u or 1024 + 16 u, and one packed operation makes the code of it,
@@ -317,8 +319,9 @@ __device__ __forceinline__ void fetch_queries(const Attention& a, int group, int
   }
 }
 
-// 16 NT query columns of a wave: their queries, bounds and running sums.
-template <int D, int NT>
+// 16 NT query columns of a wave: their queries, bounds and running sums.  TWO: a weight times
+// its value's scale enters as the sum of two fp16.
+template <int D, int NT, bool TWO>
 struct Columns {
   v4i hi[NT][D / 64], lo[NT][D / 64];   // the queries as 256 hi + lo
   int eight[NT];                        // -8 times a column's sum of them: codes are held as c + 8
@@ -459,7 +462,7 @@ struct Columns {
         }
       }
     }
-    v8h p[NT];
+    v8h p[NT], rest[NT];
     auto weights = [&](auto hidden) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -479,6 +482,12 @@ struct Columns {
 #pragma unroll
         for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{v[i], v[i + 4]}), v2h);
         p[t] = __builtin_bit_cast(v8h, pairs);
+        if constexpr (TWO) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            pairs[i] = __builtin_convertvector((v2f{v[i] - static_cast<float>(pairs[i][0]), v[i + 4] - static_cast<float>(pairs[i][1])}), v2h);
+          rest[t] = __builtin_bit_cast(v8h, pairs);
+        }
       }
     };
     if (masked) weights(std::true_type{});
@@ -487,7 +496,10 @@ struct Columns {
     for (int d = 0; d < D / 16; ++d) {
       const v8h value = codes_of(w.v[d], spread);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[t], o[t][d], 0, 0, 0);
+      for (int t = 0; t < NT; ++t) {
+        o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[t], o[t][d], 0, 0, 0);
+        if constexpr (TWO) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, rest[t], o[t][d], 0, 0, 0);
+      }
     }
   }
 
@@ -940,7 +952,7 @@ __global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int f
 // next group comes straight into the other half while this one is worked on.
 template <int D, int WAVES>
 struct Staged {
-  static constexpr int kUnits = 4;      // a group
+  static constexpr int kUnits = 64 * WAVES / D;                  // a group: a half has 8 KB for each wave
   static constexpr int kPieces = StagedUnit<D>::kPieces, kMine = kUnits * kPieces / WAVES;
   uint4 piece[2][kUnits][kPieces][64];
 
@@ -1041,7 +1053,7 @@ __global__ __launch_bounds__(kAttnThreads, D * NT <= 64 ? 4 : D * NT <= 128 ? 3 
   int first, last;
   units_of(a, tile, group, kRows, part, tile.start, length, first, last);
   UnitReader<D> reader(a.cache, tile.b, kv_head, first >> (a.cache.page_shift - 5));
-  Columns<D, NT> c;
+  Columns<D, NT, std::is_same_v<In, _Float16>> c;
   UnitWords<D> words;
   bool there = false;
   c.template open<In>(a, group, kv_head, tile.off, tile.n, tile.start, length, tile.row0,
@@ -1320,12 +1332,10 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a, int few
   if (g == 0) finish<D, In>(v, l, piece, static_cast<In*>(a.out) + row * D);
 }
 
-// Which types and widths have the way by operands.  256 wide heads and fp16 queries of 128
-// wide ones are better off without: the one has no registers for more than a column tile a
-// wave (a prompt of 4608, 16 heads on 4: 346 us, 316 by the kernel for few; fp16 8 heads
-// 4440 and 2107), the other twice the products for its scores (four pieces of 250 behind
-// 16000 418 and 248, of 600 behind 8000 344 and 278; a prompt of 4608 alone 272 and 293).
-constexpr bool by_operands(int head_dim, bool f16) { return head_dim == 64 || (head_dim == 128 && !f16); }
+// Which widths have the way by operands.  256 wide heads are better off without: there are
+// no registers for more than a column tile a wave (a prompt of 4608, 16 heads on 4: 346 us,
+// 316 by the kernel for few; fp16, 8 heads: 4440 and 2107).
+constexpr bool by_operands(int head_dim) { return head_dim != 256; }
 // Rows (tokens times query heads a key head) above which a sequence goes that way, which
 // pays where many rows read the same keys.  One sequence: by what its tiles read in all (32
 // heads of 128 on 8: 1000 rows behind 16000 tokens 112 us, 120 by the other; 4000 alone 62
@@ -1346,9 +1356,11 @@ int few_rows(int64_t n_seqs, int64_t rows, int64_t tiles, int64_t max_tokens) {
 // which share what a unit costs (128 wide: with 8 rows of each of 16 sequences behind 4000
 // tokens 20.4 us and 25.5, with 30 31.8 and 29.7, with 150 80.6 and 78.5; 64 wide: with 30
 // 34.7 and 41.7, with 150 79 and 74).  Sums of 256 wide heads leave no registers for 32 (30
-// rows: 31 us, 48 with 32; 150: 78 and 111).
-constexpr int few_tile(int head_dim, int64_t mean) {
-  return head_dim == 256 || mean <= (head_dim == 64 ? 32 : 16) ? 16 : 32;
+// rows: 31 us, 48 with 32; 150: 78 and 111), nor do 64 wide ones in fp16, whose weights are
+// two terms (150: 103 with 32).
+constexpr bool small_tiles(int head_dim, bool f16) { return head_dim == 256 || (head_dim == 64 && f16); }
+constexpr int few_tile(int head_dim, bool f16, int64_t mean) {
+  return small_tiles(head_dim, f16) || mean <= (head_dim == 64 ? 32 : 16) ? 16 : 32;
 }
 // Column tiles of a wave of the kernel for many rows: two are what its registers hold of
 // 128 wide heads (256 and 40 bytes of scratch), and of 64 wide ones four spill (685 us
@@ -1356,11 +1368,12 @@ constexpr int few_tile(int head_dim, int64_t mean) {
 constexpr int kWideTiles = 2;
 // A workgroup of four waves has 64 KB of LDS at D = 64 and a CU two of them, out of step:
 // better where tiles are uneven and a wave's work on a unit is long (361 us against 435 with
-// eight for three pieces behind 16000 tokens, 143 against 164 for a prompt of 4608).  128 wide
-// heads have half the columns for as many bytes and are held back by the fetches of the
-// units, which eight waves share (four pieces behind 7000 tokens 354 us against 389, a
-// prompt of 4608 as fast).
-constexpr int wide_waves(int head_dim) { return head_dim == 128 ? 8 : 4; }
+// eight for three pieces behind 16000 tokens, 143 against 164 for a prompt of 4608; 128 wide
+// heads with fp16 queries in two terms 282 against 320).  128 wide heads with one term have
+// half the columns for as many bytes and are held back by the fetches of the units, which
+// eight waves share (four pieces behind 7000 tokens 354 us against 389, a prompt of 4608 as
+// fast).
+constexpr int wide_waves(int head_dim, bool f16) { return head_dim == 128 && !f16 ? 8 : 4; }
 constexpr int kWidest = 8;              // waves a CU
 constexpr int64_t kMostOperands = int64_t{8} << 30;             // bytes
 
@@ -1383,16 +1396,17 @@ hipError_t launch_heads(const Attention& a, hipStream_t stream) {
   constexpr int kAll = 0x7fffffff;
   const int64_t rows = static_cast<int64_t>(a.M) * (a.q_heads / a.cache.kv_heads);
   hipError_t e = hipSuccess;
-  const int tile = few_tile(D, rows / a.cache.n_seqs);
+  constexpr bool kF16 = std::is_same_v<In, _Float16>;
+  const int tile = few_tile(D, kF16, rows / a.cache.n_seqs);
   const int many = a.slots > 0 ? a.limit : kAll, few = a.cache.n_seqs > 1 ? a.limit : 0;
   if (a.slots == 0 || a.cache.n_seqs > 1) {
-    if constexpr (D == 256) e = launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream);
+    if constexpr (small_tiles(D, kF16)) e = launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream);
     else e = tile == 16 ? launch_tiles(attend_few<D, 1, In>, a, 16, kAttnWaves, 0, many, stream)
                         : launch_tiles(attend_few<D, 2, In>, a, 32, kAttnWaves, 0, many, stream);
   }
   int many_tile = tile;
-  if constexpr (by_operands(D, std::is_same_v<In, _Float16>)) {
-    constexpr int kWaves = wide_waves(D);
+  if constexpr (by_operands(D)) {
+    constexpr int kWaves = wide_waves(D, kF16);
     many_tile = 16 * kWideTiles * kWaves;
     if (a.slots > 0 && e == hipSuccess) {
       const int64_t units = (a.cache.max_tokens + kUnit - 1) / kUnit;
@@ -1432,10 +1446,10 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
   p.limit = limit;
   p.slot_units = (max_tokens + kUnit - 1) / kUnit + 4;          // and spare ones
   p.slots = n_seqs == 1 ? (rows > limit ? 1 : 0) : std::min({n_seqs, rows / (int64_t{1} + limit), int64_t{65535}});
-  if (!by_operands(head_dim, f16) || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_) p.slots = 0;
+  if (!by_operands(head_dim) || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_) p.slots = 0;
   const size_t operands = static_cast<size_t>(p.slots) * kv_heads * p.slot_units * unit_bytes_;
   const bool wide = p.slots > 0;
-  const int64_t tile = wide ? wide_tile : few_tile(head_dim, rows / n_seqs);
+  const int64_t tile = wide ? wide_tile : few_tile(head_dim, f16, rows / n_seqs);
   const int64_t work = std::max<int64_t>(1, tiles_bound(M, group, n_seqs, tile) * kv_heads);
   // Workgroups: few rows 1536, six a CU, which has room for three or four and finds many of
   // them short (64 chats of up to 8192 tokens, 8 key heads of 128: 70 us; 1024 72, 2048 76,
