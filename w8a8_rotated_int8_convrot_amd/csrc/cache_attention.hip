@@ -746,7 +746,7 @@ struct PromptColumns {
         for (int i = 0; i < 8; ++i)
           if ((facts.bad >> ((first + i) & 31) & 1) != 0 && s[t][i >> 2][i & 3] != kHidden) l[t] = __builtin_nanf("");
     }
-    raise(s, f);
+    raise<true>(s, f);
   }
 
   // The weights times the values' power of two over what the sums are in.
@@ -779,14 +779,18 @@ struct PromptColumns {
     }
   }
 
-  // Moves the references where a weight would get too large.
+  // Moves the references where a weight would get too large.  MASKED: some keys may be hidden; a
+  // column that sees none of a lane's keys has nothing there to move for (the mark of a hidden key
+  // is no score: times the unit's factor, 0 where no page or no key holds anything, it would be one).
+  template <bool MASKED>
   __device__ __forceinline__ void raise(const v4f (&s)[NT][2], const float (&f)[NT]) {
     float most[NT];
     bool move = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const v4f a = s[t][0], b = s[t][1];
-      most[t] = f[t] * max3(max3(max3(a[0], a[1], a[2]), a[3], b[0]), max3(b[1], b[2], b[3]), b[3]);
+      const float top = max3(max3(max3(a[0], a[1], a[2]), a[3], b[0]), max3(b[1], b[2], b[3]), b[3]);
+      most[t] = MASKED && top == kHidden ? kNoReference : f[t] * top;
       move = move || most[t] > m[t] + (kTop + kRise);
     }
     if (__any(move)) {
@@ -819,7 +823,7 @@ struct PromptColumns {
       float f[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) f[t] = qs[t] * group.key(i);
-      raise(s, f);
+      raise<false>(s, f);
       v8h p[NT];
       v4f next[NT][2];
       if (i + 1 < UNITS) scores(group.unit(i + 1), next);
