@@ -1132,7 +1132,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_many(Attention a, int fe
   const int part = static_cast<int>(blockIdx.y);
   Tile tile;
   if (!find_tile(a, group, kRows, few, many, static_cast<int>(blockIdx.x / static_cast<unsigned>(kv_heads)), tile)) return;
-  if (tile.slot >= a.slots) return;     // more long prompts than rows: the offsets rise and fall
+  // as many slots as rows allow: more long prompts are of offsets that rise and fall
+  if (tile.slot >= a.slots) return;
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int length = length_of(a, tile), all = tile.n * group;
   const int row0 = tile.row0 + 16 * NT * wave_index();
@@ -1380,6 +1381,7 @@ constexpr int kWideTiles = 2;
 constexpr int wide_waves(int head_dim, bool f16) { return head_dim == 128 && !f16 ? 8 : 4; }
 constexpr int kWidest = 8;              // waves a CU
 constexpr int64_t kMostOperands = int64_t{8} << 30;             // bytes
+constexpr int64_t kMostSlots = 65535;   // the third side of a grid
 
 int64_t tiles_bound(int64_t M, int64_t group, int64_t n_seqs, int64_t rows) {
   // one for every sequence that has rows, and one for every full tile
@@ -1449,8 +1451,10 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
   const int64_t unit_bytes_ = static_cast<int64_t>(head_dim / 8) * 1024 + 16;
   p.limit = limit;
   p.slot_units = (max_tokens + kUnit - 1) / kUnit + 4;          // and spare ones
-  p.slots = n_seqs == 1 ? (rows > limit ? 1 : 0) : std::min({n_seqs, rows / (int64_t{1} + limit), int64_t{65535}});
-  if (!by_operands(head_dim) || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_) p.slots = 0;
+  p.slots = n_seqs == 1 ? (rows > limit ? 1 : 0) : std::min(n_seqs, rows / (int64_t{1} + limit));
+  // all of them or none: what has no slot there would have no kernel
+  if (!by_operands(head_dim) || p.slots > kMostSlots || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_)
+    p.slots = 0;
   const size_t operands = static_cast<size_t>(p.slots) * kv_heads * p.slot_units * unit_bytes_;
   const bool wide = p.slots > 0;
   const int64_t tile = wide ? wide_tile : few_tile(head_dim, f16, rows / n_seqs);
