@@ -635,11 +635,26 @@ template <int D> struct StagedUnit {
   __device__ v8h value(int d) const { return __builtin_bit_cast(v8h, piece[(kKeys + d) * 64 + (threadIdx.x & 63)]); }
 };
 constexpr int kNoScale = -1000;
+// Powers of two of values below this count as it in the reference, as kLeastScale: the sum l, which
+// has no such factor, stays below 2^(80 + 14) a key.
+constexpr int kLeastLevel = -80;
+// Value scales that are closer than this share their unit's power of two: the reference, taken of the
+// largest score and the largest scale, is then six powers above the largest weight at most.
+constexpr float kSpread = 0x1p-6f;
+constexpr float kMostPower = 0x1p126f;  // its reciprocal is normal
+constexpr uint32_t kHeld = 1, kUneven = 2;
 struct UnitFacts {
   float key;                            // what a 1 of the key operand stands for
-  int value;                            // and of the value operand, as its logarithm
+  int value;                            // and of the value operand, as its logarithm; kNoScale: all are 0
   uint32_t bad;                         // tokens whose value is not finite
-  uint32_t held;                        // whether a page holds the unit
+  uint32_t flags;                       // kHeld: a page holds the unit.  kUneven: its tokens' scales are
+                                        // far apart, and each has a power of two of its own (Levels)
+};
+// How far below the unit's a token's power of two is, a byte a token, eight of each kind a lane.
+constexpr uint32_t kNothing = 255;      // a value of 0
+struct Levels {
+  uint32_t key[2], value[2];
+  static __device__ __forceinline__ uint32_t of(const uint32_t (&w)[2], int i) { return w[i >> 2] >> (8 * (i & 3)) & 255; }
 };
 
 // The state of 16 NT query columns of a wave whose keys and values come as operands
@@ -652,7 +667,6 @@ struct PromptColumns {
   int from[NT], to[NT];                 // visible keys of a column
   float m[NT], l[NT];                   // reference; sum of this lane's keys
   v4f o[NT][D / 16];                    // value dims 64 (t / 4) + 16 g + 4 i + t % 4 in o[][t][i]
-  int whole;                            // what a 1 of them stands for, as its logarithm
   int full_from, full_to;               // keys that every column sees
   int any_from, any_to;                 // keys that some column sees
 
@@ -667,7 +681,6 @@ struct PromptColumns {
     fetch_queries<D, NT, In>(a, group, kv_head, off, n, start, length, row0, raw, from, to);
     meanwhile();
     query_signs<In>(signs);
-    whole = kNoScale;
     const float unit = RootScale<D>::value * kLog2e * fabsf(a.scale);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -717,26 +730,15 @@ struct PromptColumns {
     }
   }
 
-  // Hides what a column does not see, and moves the references and what the sums are in
-  // where that is due.  `up`: what the sums are in, by the unit's values' power of two, as
-  // its logarithm.
-  __device__ __forceinline__ void settle(v4f (&s)[NT][2], const float (&f)[NT], int u, const UnitFacts& facts, float& up) {
+  // Hides what a column does not see.
+  __device__ __forceinline__ void hide(v4f (&s)[NT][2], int u, const UnitFacts& facts) {
     const int first = kUnit * u + 8 * static_cast<int>((threadIdx.x & 63) >> 4);
-    if (facts.value > whole) {
-      const float down = ldexpf(1.0f, max(whole, -200) - facts.value);  // 0 for the first
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) o[t][d] *= down;
-      whole = facts.value;
-    }
-    // past 2^40 a weight's fp16 is 0 either way
-    up = static_cast<float>(facts.value == kNoScale ? 0 : min(whole - facts.value, 40));
+    const bool held = (facts.flags & kHeld) != 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        s[t][i >> 2][i & 3] = facts.held && first + i >= from[t] && first + i < to[t] ? s[t][i >> 2][i & 3] : kHidden;
+        s[t][i >> 2][i & 3] = held && first + i >= from[t] && first + i < to[t] ? s[t][i >> 2][i & 3] : kHidden;
     if (facts.bad != 0) {
       // a value that is not finite: it is not in the product (there it would reach those
       // who do not see it), but in the sum of who sees it
@@ -746,28 +748,32 @@ struct PromptColumns {
         for (int i = 0; i < 8; ++i)
           if ((facts.bad >> ((first + i) & 31) & 1) != 0 && s[t][i >> 2][i & 3] != kHidden) l[t] = __builtin_nanf("");
     }
-    raise<true>(s, f);
   }
 
-  // The weights times the values' power of two over what the sums are in.
-  __device__ __forceinline__ void weights(const v4f (&s)[NT][2], const float (&f)[NT], float up, v8h (&p)[NT]) {
-    const float all = __builtin_amdgcn_exp2f(up);
+  // The logarithm of value i's power of two.
+  static __device__ __forceinline__ int level_of(const UnitFacts& facts, const Levels& levels, int i) {
+    const uint32_t down = Levels::of(levels.value, i);
+    return down == kNothing ? kNoScale : facts.value - static_cast<int>(down);
+  }
+
+  // The weights times their values' powers of two.
+  __device__ __forceinline__ void weights(const v4f (&s)[NT][2], const float (&f)[NT], const UnitFacts& facts,
+                                          const Levels& levels, v8h (&p)[NT]) {
+    v2h pairs[NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float low = -(m[t] + up);
-      float e[8];
+    for (int i = 0; i < 8; ++i) {
+      const int level = level_of(facts, levels, i), counted = level == kNoScale ? 0 : level;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int t = 0; t < NT; ++t) {
         const float x = s[t][i >> 2][i & 3];
-        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x, f[t], low));
-        e[i] = x == kHidden ? 0.0f : e[i];
+        float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x, f[t], static_cast<float>(counted) - m[t]));
+        e = x == kHidden ? 0.0f : e;
+        l[t] += ldexpf(e, -counted);
+        pairs[t][i & 3][i >> 2] = static_cast<_Float16>(level == kNoScale ? 0.0f : e);
       }
-      l[t] = __builtin_fmaf(((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])), all, l[t]);
-      v2h pairs[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pairs[i] = __builtin_convertvector((v2f{e[i], e[i + 4]}), v2h);
-      p[t] = __builtin_bit_cast(v8h, pairs);
     }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) p[t] = __builtin_bit_cast(v8h, pairs[t]);
   }
 
   __device__ __forceinline__ void add(const StagedUnit<D>& unit, const v8h (&p)[NT]) {
@@ -779,20 +785,12 @@ struct PromptColumns {
     }
   }
 
-  // Moves the references where a weight would get too large.  MASKED: some keys may be hidden; a
-  // column that sees none of a lane's keys has nothing there to move for (the mark of a hidden key
-  // is no score: times the unit's factor, 0 where no page or no key holds anything, it would be one).
-  template <bool MASKED>
-  __device__ __forceinline__ void raise(const v4f (&s)[NT][2], const float (&f)[NT]) {
-    float most[NT];
+  // The references to kTop below `most`, the logarithm of the largest weight times its value's
+  // power of two, where one would get too large.
+  __device__ __forceinline__ void raise(float (&most)[NT]) {
     bool move = false;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const v4f a = s[t][0], b = s[t][1];
-      const float top = max3(max3(max3(a[0], a[1], a[2]), a[3], b[0]), max3(b[1], b[2], b[3]), b[3]);
-      most[t] = MASKED && top == kHidden ? kNoReference : f[t] * top;
-      move = move || most[t] > m[t] + (kTop + kRise);
-    }
+    for (int t = 0; t < NT; ++t) move = move || most[t] > m[t] + (kTop + kRise);
     if (__any(move)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -808,31 +806,57 @@ struct PromptColumns {
       }
     }
   }
+  // What it takes of the keys that a column sees, one by one: the mark of a hidden one is no score
+  // (times the unit's factor, 0 where no page or no key holds anything, it would be one).
+  __device__ __forceinline__ void raise_seen(const v4f (&s)[NT][2], const float (&f)[NT], const UnitFacts& facts,
+                                             const Levels& levels) {
+    float most[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) most[t] = kNoReference;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float level = static_cast<float>(max(level_of(facts, levels, i), kLeastLevel));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float x = s[t][i >> 2][i & 3];
+        most[t] = __builtin_elementwise_maximum(most[t], x == kHidden ? kNoReference : __builtin_fmaf(x, f[t], level));
+      }
+    }
+    raise(most);
+  }
   // (NaN if one is: no canonical form is made of its operands first)
   static __device__ __forceinline__ float max3(float a, float b, float c) {
     return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
   }
 
-  // A whole group that every column sees all of, in the power of two that the sums are in.
+  // A whole group that every column sees all of, its units even.
   template <int UNITS, typename Group>
   __device__ __forceinline__ void whole_group(const Group& group) {
     v4f s[NT][2];
     scores(group.unit(0), s);
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
-      float f[NT];
+      const int value = group.value(i);
+      const float level = static_cast<float>(value);
+      float f[NT], most[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) f[t] = qs[t] * group.key(i);
-      raise<false>(s, f);
+      for (int t = 0; t < NT; ++t) {
+        const v4f a = s[t][0], b = s[t][1];
+        f[t] = qs[t] * group.key(i);
+        most[t] = __builtin_fmaf(max3(max3(max3(a[0], a[1], a[2]), a[3], b[0]), max3(b[1], b[2], b[3]), b[3]), f[t], level);
+      }
+      raise(most);
       v8h p[NT];
       v4f next[NT][2];
       if (i + 1 < UNITS) scores(group.unit(i + 1), next);
+      const float back = __uint_as_float(static_cast<uint32_t>(127 - value) << 23);   // 2^-value
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
+        const float low = level - m[t];
         float e[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][j >> 2][j & 3], f[t], -m[t]));
-        l[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+        for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][j >> 2][j & 3], f[t], low));
+        l[t] = __builtin_fmaf(((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])), back, l[t]);
         v2h pairs[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) pairs[j] = __builtin_convertvector((v2f{e[j], e[j + 4]}), v2h);
@@ -844,20 +868,33 @@ struct PromptColumns {
     }
   }
 
-  // Units [i0, i1) of a staged group, where something is hidden or not as usual.
-  template <typename Group>
-  __device__ __forceinline__ void steps(const Group& group, int u0, int i0, int i1) {
+  // Units [i0, i1) of a staged group, where something is hidden or not as usual; levels_of(i)
+  // where a unit's scales are far apart.
+  template <typename Group, typename F>
+  __device__ __forceinline__ void steps(const Group& group, int u0, int i0, int i1, F&& levels_of) {
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
       const UnitFacts facts = group.facts(i);
-      float f[NT], up;
+      const uint32_t down = facts.value == kNoScale ? ~0u : 0u;
+      Levels levels{{0, 0}, {down, down}};
+      float f[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) f[t] = qs[t] * facts.key;
       v4f s[NT][2];
       v8h p[NT];
       scores(group.unit(i), s);
-      settle(s, f, u0 + i, facts, up);
-      weights(s, f, up, p);
+      if ((facts.flags & kUneven) != 0) {
+        levels = levels_of(u0 + i);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int by = -static_cast<int>(Levels::of(levels.key, k));
+#pragma unroll
+          for (int t = 0; t < NT; ++t) s[t][k >> 2][k & 3] = ldexpf(s[t][k >> 2][k & 3], by);
+        }
+      }
+      hide(s, u0 + i, facts);
+      raise_seen(s, f, facts, levels);
+      weights(s, f, facts, levels, p);
       add(group.unit(i), p);
     }
   }
@@ -867,19 +904,27 @@ struct PromptColumns {
 __device__ inline float power_below(float v) { return __uint_as_float(__float_as_uint(v) & 0x7f800000u); }
 
 // A long prompt's keys and values as the operands of both products, made once in the
-// workspace for all of its tiles: [slot][key head][unit] of kPieces KB, and the facts of
-// as many units behind them.  A code times its scale is exact in fp16, 3 bits by 8, the
-// scales taken relative to a power of two of their unit (those below 2^-14 of it lose bits).
+// workspace for all of its tiles: [slot][key head][unit] of kPieces KB, and behind them the
+// facts of as many units, and their levels.  A code times its scale is exact in fp16, 3 bits by
+// 8, the scales taken relative to a power of two of their unit; where some lie more than kSpread
+// below the largest, each relative to one of its own.
 template <int D>
 struct Operands {
   static constexpr int kPieces = StagedUnit<D>::kPieces, kKeys = StagedUnit<D>::kKeys;
   uint4* piece;
   UnitFacts* facts;
+  uint8_t* levels;                      // [unit][64]: keys, values
   __device__ Operands(const Attention& a, int slot, int head) {
     const int64_t all = static_cast<int64_t>(a.slots) * a.cache.kv_heads * a.slot_units;
     const int64_t at = (static_cast<int64_t>(slot) * a.cache.kv_heads + head) * a.slot_units;
     piece = reinterpret_cast<uint4*>(a.operands) + at * (kPieces * 64);
     facts = reinterpret_cast<UnitFacts*>(a.operands + all * (kPieces * 1024)) + at;
+    levels = a.operands + all * (kPieces * 1024 + static_cast<int64_t>(sizeof(UnitFacts))) + at * 64;
+  }
+  __device__ Levels levels_of(int u) const {
+    const uint8_t* p = levels + static_cast<int64_t>(u) * 64 + 8 * ((threadIdx.x & 63) >> 4);
+    const uint2 k = *reinterpret_cast<const uint2*>(p), v = *reinterpret_cast<const uint2*>(p + 32);
+    return Levels{{k.x, k.y}, {v.x, v.y}};
   }
 };
 
@@ -909,19 +954,31 @@ __global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int f
   float scale = held && kUnit * u + (lane & 31) < length ? __uint_as_float(bits << 16) : 0.0f;
   const bool finite = fabsf(scale) < __builtin_inff();
   const uint64_t broken = __ballot(!finite);
-  float top = finite ? scale : 0.0f;
+  const float own = finite ? power_below(scale) : 0.0f;
+  float top = own;
   top = fmaxf(top, lane_xor<1>(top));
   top = fmaxf(top, lane_xor<2>(top));
   top = fmaxf(top, lane_xor<4>(top));
   top = fmaxf(top, lane_xor<8>(top));
   float other = top;
   swap_rows<16>(top, other);
-  top = power_below(fmaxf(top, other));
-  if (!finite && lane >= 32) scale = 0.0f;
-  scales[wave][lane] = static_cast<_Float16>(top > 0.0f ? scale * (1.0f / top) : scale * 0.0f);
+  top = fminf(fmaxf(top, other), kMostPower);
+  // keys by what fp16 holds of the small ones (none is lost where they are 0), values by how far the
+  // references may be above the weights of one that they are taken of
+  const bool is_key = lane < 32, there = held && finite && kUnit * u + (lane & 31) < length;
+  const bool uneven = __any(there && (is_key ? own > 0.0f && own < top * 0x1p-14f : own < top * kSpread));
+  if (!finite && !is_key) scale = 0.0f;
+  const float unit_of = uneven && own > 0.0f ? fminf(own, kMostPower) : top;
+  scales[wave][lane] = static_cast<_Float16>(unit_of > 0.0f ? scale * (1.0f / unit_of) : scale * 0.0f);
+  if (uneven) {
+    const uint32_t down = (__float_as_uint(top) - __float_as_uint(unit_of)) >> 23;
+    out.levels[static_cast<int64_t>(u) * 64 + lane] = static_cast<uint8_t>(own > 0.0f || is_key ? down : kNothing);
+  }
   const float key = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(top), 0));
   const int value = static_cast<int>(__builtin_amdgcn_readlane(__float_as_uint(top), 32) >> 23);
-  if (lane == 0) out.facts[u] = UnitFacts{key, value != 0 ? value - 127 : kNoScale, static_cast<uint32_t>(broken >> 32), held};
+  if (lane == 0)
+    out.facts[u] = UnitFacts{key, value != 0 ? value - 127 : kNoScale, static_cast<uint32_t>(broken >> 32),
+                             (held ? kHeld : 0) | (uneven ? kUneven : 0)};
   // lanes of this wave only read what it wrote itself
   __builtin_amdgcn_wave_barrier();
   uint4* to = out.piece + static_cast<int64_t>(u) * (O::kPieces * 64) + lane;
@@ -965,11 +1022,12 @@ struct Staged {
     int which;
     UnitFacts of;                       // unit lane % kUnits
     __device__ StagedUnit<D> unit(int i) const { return StagedUnit<D>{&s.piece[which][i][0][0]}; }
+    __device__ int value(int i) const { return __builtin_amdgcn_readlane(of.value, i); }
     __device__ float key(int i) const { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(of.key), i)); }
     __device__ UnitFacts facts(int i) const {
       auto one = [i](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), i)); };
       return UnitFacts{__uint_as_float(one(__float_as_uint(of.key))), static_cast<int>(one(static_cast<uint32_t>(of.value))),
-                       one(of.bad), one(of.held)};
+                       one(of.bad), one(of.flags)};
     }
   };
 
@@ -1006,11 +1064,11 @@ struct Staged {
       const int i0 = max(0, c.any_from / kUnit - u0);
       const int i1 = idle ? 0 : min(min(kUnits, last - u0), (c.any_to + kUnit - 1) / kUnit - u0);
       const Group group{*this, which, facts};
-      const bool usual = facts.held != 0 && facts.bad == 0 && facts.value == c.whole;
+      const bool usual = facts.flags == kHeld && facts.bad == 0 && facts.value >= kLeastLevel;
       if (i0 == 0 && i1 == kUnits && kUnit * u0 >= c.full_from && kUnit * (u0 + kUnits) <= c.full_to && __all(usual))
         c.template whole_group<kUnits>(group);
       else
-        c.steps(group, u0, i0, i1);
+        c.steps(group, u0, i0, i1, [&](int u) { return from.levels_of(u); });
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       facts = next;
@@ -1152,7 +1210,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_many(Attention a, int fe
   });
   staged.run(c, from, facts, first, last, idle);
   if (idle) return;
-  const float whole = c.whole == kNoScale ? 0.0f : ldexpf(1.0f, c.whole);
 
   const Rows row_of{tile.off, group, kv_head, a.q_heads};
   const int64_t rows = static_cast<int64_t>(a.M) * a.q_heads;
@@ -1166,7 +1223,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_many(Attention a, int fe
 #pragma unroll
     for (int d = 0; d < D / 64; ++d)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[d][e] = c.o[t][4 * d + (e & 3)][e >> 2] * whole;
+      for (int e = 0; e < 16; ++e) v[d][e] = c.o[t][4 * d + (e & 3)][e >> 2];
     if (a.splits != 1) {
       if (row < all) {
         const int64_t at = part * rows + row_of(row);
@@ -1448,7 +1505,7 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
   const int64_t wide_tile = 16 * kWidest * kWideTiles;
   const int limit = few_rows(n_seqs, rows, tiles_bound(M, group, n_seqs, wide_tile) * kv_heads, max_tokens);
   // long prompts: as many as there can be
-  const int64_t unit_bytes_ = static_cast<int64_t>(head_dim / 8) * 1024 + 16;
+  const int64_t unit_bytes_ = static_cast<int64_t>(head_dim / 8) * 1024 + 16 + 64;
   p.limit = limit;
   p.slot_units = (max_tokens + kUnit - 1) / kUnit + 4;          // and spare ones
   p.slots = n_seqs == 1 ? (rows > limit ? 1 : 0) : std::min(n_seqs, rows / (int64_t{1} + limit));
