@@ -119,3 +119,17 @@ def test_long_prompts(B, lens, G, H, D, page, kind, io):  # noqa: F811
     if io == "fp16" and kind in ("values of all sizes", "values of 0 seen first"):
         pytest.skip("results past fp16's largest value")
     check(B, kind, lens, G, H, D, page, torch.bfloat16 if io == "bf16" else torch.float16)
+
+
+FEW = [([(200, 3), (400, 1)], 4, 2, 128, 32), ([(150, 20), (1, 33)], 1, 3, 64, 64), ([(300, 1)], 8, 1, 256, 32),
+       ([(100, 40), (64, 1)], 1, 2, 256, 64), ([(260, 24), (90, 40)], 4, 1, 128, 128),
+       ([(40, 33), (50, 1), (500, 1100)], 2, 2, 64, 32)]          # both kernels
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp16"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens,G,H,D,page", FEW)
+def test_few_rows(B, lens, G, H, D, page, kind, io):  # noqa: F811
+    if io == "fp16" and kind in ("values of all sizes", "values of 0 seen first"):
+        pytest.skip("results past fp16's largest value")
+    check(B, kind, lens, G, H, D, page, torch.bfloat16 if io == "bf16" else torch.float16)

@@ -76,9 +76,13 @@ constexpr float kTop = 8.0f;
 constexpr float kRise = 6.0f;
 // A key that a column does not see; no score is as low.
 constexpr float kHidden = -0x1.fffffep127f;
-// Value scales below 2^-60 count as that in the reference: the sum l, which has
-// no such factor, then stays below 2^(60 + 14) a key.
-constexpr float kLeastScale = -60.0f;
+// Value scales below 2^-80 count as that in the reference: the sum l, which has
+// no such factor, then stays below 2^(80 + 14) a key.
+constexpr int kLeastLevel = -80;
+constexpr float kLeastScale = kLeastLevel;
+// Value scales that are closer than this share a place in the reference: taken of the largest score
+// and the largest scale, it is then six powers of two above the largest weight at most.
+constexpr float kSpread = 0x1p-6f;
 // Before the first key: below every score, and finite.
 constexpr float kNoReference = -0x1p120f;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -420,34 +424,37 @@ struct Columns {
         for (int i = 0; i < 4; ++i) y[t][4 * h + i] = static_cast<float>((high[i] << 8) + low[i]) * ks[4 * h + i];
       }
     }
-    float by[NT];
-    const float large = log_scale(vs);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) by[t] = large;
-    if (masked) {
+    // the reference, kTop below what the largest weight may be made of: the largest score and scale
+    // of an octet, or, where those may be far from any one key's, each key's own
+    const float large = fmaxf(fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])), fmaxf(fmaxf(vs[4], vs[5]), fmaxf(vs[6], vs[7])));
+    const float small = fminf(fminf(fminf(vs[0], vs[1]), fminf(vs[2], vs[3])), fminf(fminf(vs[4], vs[5]), fminf(vs[6], vs[7])));
+    float most[NT];
+    if (masked || __any(small < large * kSpread)) {
       const int first = kUnit * u + 8 * g;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float v[8];
+      for (int t = 0; t < NT; ++t) most[t] = kNoReference;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8; ++i) {
+        const float level = log_scale(vs[i]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
           const bool seen = first + i >= from[t] && first + i < to[t];
           y[t][i] = seen ? y[t][i] : kHidden;
-          v[i] = seen ? vs[i] : 0.0f;
+          most[t] = fmaxf(most[t], seen ? __builtin_fmaf(y[t][i], qs[t], level) : kNoReference);
         }
-        by[t] = log_scale(v);
+      }
+    } else {
+      const float level = log_scale(large);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float* x = y[t];
+        most[t] = __builtin_fmaf(fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))),
+                                 qs[t], level);
       }
     }
-    // the reference, kTop below what the largest weight may be made of
-    float most[NT];
     bool move = false;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float* x = y[t];
-      most[t] = __builtin_fmaf(fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))),
-                               qs[t], by[t]);
-      move = move || most[t] > m[t] + (kTop + kRise);
-    }
+    for (int t = 0; t < NT; ++t) move = move || most[t] > m[t] + (kTop + kRise);
     if (__any(move)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -503,11 +510,8 @@ struct Columns {
     }
   }
 
-  // log2 of the largest of a lane's value scales (of a NaN and a number, of the number).
-  static __device__ float log_scale(const float (&v)[8]) {
-    const float most = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-    return fmaxf(__builtin_amdgcn_logf(most), kLeastScale);
-  }
+  // log2 of a value scale (of NaN the least).
+  static __device__ float log_scale(float v) { return fmaxf(__builtin_amdgcn_logf(v), kLeastScale); }
 
   // Units first, first + by, ... below last, each loaded while the one before is worked on;
   // the first is in a already.
@@ -635,12 +639,6 @@ template <int D> struct StagedUnit {
   __device__ v8h value(int d) const { return __builtin_bit_cast(v8h, piece[(kKeys + d) * 64 + (threadIdx.x & 63)]); }
 };
 constexpr int kNoScale = -1000;
-// Powers of two of values below this count as it in the reference, as kLeastScale: the sum l, which
-// has no such factor, stays below 2^(80 + 14) a key.
-constexpr int kLeastLevel = -80;
-// Value scales that are closer than this share their unit's power of two: the reference, taken of the
-// largest score and the largest scale, is then six powers above the largest weight at most.
-constexpr float kSpread = 0x1p-6f;
 constexpr float kMostPower = 0x1p126f;  // its reciprocal is normal
 constexpr uint32_t kHeld = 1, kUneven = 2;
 struct UnitFacts {
