@@ -143,12 +143,17 @@ __device__ inline void decode(const uint32_t (&w)[E / 8], uint32_t scale, int c,
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[8 * j + i] = static_cast<float>(static_cast<int>((w[j] >> (4 * i)) & 15u) - 8);
   rotate_head(v, c);                    // whole numbers up to 2048
+  // (v s) / sqrt(D), the first product exact.  It may pass the largest fp32 where the second does not:
+  // scales from 1 on enter 2^-8 times as large, which they hold exactly
   const float s = __uint_as_float(scale << 16);
+  const bool large = s >= 1.0f;
+  const float by = large ? s * 0x1p-8f : s;
+  const float root = static_cast<float>(HeadScale<D>::value) * (large ? 0x1p8f : 1.0f);
 #pragma unroll
   for (int j = 0; j < E / 8; ++j) {
     float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (v[8 * j + i] * s) * static_cast<float>(HeadScale<D>::value);
+    for (int i = 0; i < 8; ++i) f[i] = (v[8 * j + i] * by) * root;
     raw[j] = narrow8<In>(f);
   }
 }
