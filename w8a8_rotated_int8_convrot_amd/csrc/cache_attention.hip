@@ -931,7 +931,7 @@ struct Operands {
 template <int D>
 __global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int few) {
   using O = Operands<D>;
-  __shared__ _Float16 scales[kAttnWaves][64];
+  __shared__ alignas(16) _Float16 scales[kAttnWaves][64];
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4, wave = wave_index();
   const int u = static_cast<int>(blockIdx.x) * kAttnWaves + wave, head = static_cast<int>(blockIdx.y);
   Tile tile;
@@ -977,7 +977,8 @@ __global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int f
   if (lane == 0)
     out.facts[u] = UnitFacts{key, value != 0 ? value - 127 : kNoScale, static_cast<uint32_t>(broken >> 32),
                              (held ? kHeld : 0) | (uneven ? kUneven : 0)};
-  // lanes of this wave only read what it wrote itself
+  // lanes of this wave only read what it wrote itself: its writes have to be done, no barrier is due
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   uint4* to = out.piece + static_cast<int64_t>(u) * (O::kPieces * 64) + lane;
   auto store = [&](int i, uint32_t word, const v2h (&by)[4]) {
@@ -995,7 +996,8 @@ __global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int f
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) store(h * (D / 32) + k, w.k[h][k], all);
   }
-  const uint4 eight = *reinterpret_cast<const uint4*>(&scales[wave][32 + 8 * g]);
+  uint4 eight;
+  __builtin_memcpy(&eight, __builtin_assume_aligned(&scales[wave][32 + 8 * g], 16), sizeof eight);
   // the scales of tokens 0 and 4, 1 and 5, 2 and 6, 3 and 7 of the octet
   const uint32_t by_token[4] = {__builtin_amdgcn_perm(eight.z, eight.x, 0x05040100u),
                                 __builtin_amdgcn_perm(eight.z, eight.x, 0x07060302u),
@@ -1125,7 +1127,7 @@ __global__ __launch_bounds__(kAttnThreads, D * NT <= 64 ? 4 : D * NT <= 128 ? 3 
 #pragma unroll
   for (int t = 0; t < NT; ++t) c.l[t] = column_sum(c.l[t]);
   constexpr int kStride = D + 4;
-  __shared__ float sums[kAttnWaves][16][kStride];
+  __shared__ alignas(16) float sums[kAttnWaves][16][kStride];
   __shared__ float refs[kAttnWaves][16], totals[kAttnWaves][16];
   const int mine = threadIdx.x >> 4, piece = threadIdx.x & 15;
   constexpr int E = D / 16;
