@@ -592,7 +592,8 @@ int convrot_rope(const void *q, int64_t q_heads, int64_t q_stride, void *q_out, 
  * with a code c held as c + 8: 32 D + 128 bytes.  Token t of sequence b lies in
  * page table[b][t / page].  The tokens of a call are rows: sequence b has rows
  * offsets[b] .. offsets[b + 1] - 1, and row i of it stands for its token
- * starts[b] + i - offsets[b]. */
+ * starts[b] + i - offsets[b].  A call of no rows (M = 0) is a no-op, and n_pages, n_seqs and max_pages
+ * may be 0 in it. */
 typedef struct convrot_cache {
     void          *pages;           /* [n_pages] of convrot_cache_page_bytes bytes, 16-byte aligned */
     int64_t        n_pages;         /* 1 to 2^31 - 1 */

@@ -42,7 +42,8 @@ int check_rows(int64_t M, const char* who) {
   return CONVROT_OK;
 }
 
-// The sizes of a cache; its pointers only where there are rows.
+// The sizes of a cache; its pointers, and that it holds pages, columns and sequences, only where
+// there are rows.
 int check_cache(const convrot_cache* c, int64_t M, const char* who) {
   if (!c) return fail(CONVROT_EINVAL, "%s: NULL pointer (cache)", who);
   if (!page_known(c->page))
@@ -52,11 +53,12 @@ int check_cache(const convrot_cache* c, int64_t M, const char* who) {
   if (c->kv_heads < 1 || c->kv_heads > kMaxKvHeads)
     return fail(CONVROT_EINVAL, "%s: kv_heads=%lld must be in [1, %lld]", who, static_cast<long long>(c->kv_heads),
                 static_cast<long long>(kMaxKvHeads));
-  if (c->n_pages < 1 || c->n_pages > 0x7fffffff)
+  const int64_t least = M == 0 ? 0 : 1;
+  if (c->n_pages < least || c->n_pages > 0x7fffffff)
     return fail(CONVROT_EINVAL, "%s: n_pages=%lld must be in [1, 2^31)", who, static_cast<long long>(c->n_pages));
-  if (c->n_seqs < 1 || c->n_seqs > kMaxSeqs)
+  if (c->n_seqs < least || c->n_seqs > kMaxSeqs)
     return fail(CONVROT_EINVAL, "%s: n_seqs=%lld must be in [1, 2^20]", who, static_cast<long long>(c->n_seqs));
-  if (c->max_pages < 1 || c->max_pages > kMaxCacheTokens / c->page)
+  if (c->max_pages < least || c->max_pages > kMaxCacheTokens / c->page)
     return fail(CONVROT_EINVAL, "%s: max_pages=%lld must be in [1, %lld]", who, static_cast<long long>(c->max_pages),
                 static_cast<long long>(kMaxCacheTokens / c->page));
   if (c->table_stride < c->max_pages || c->table_stride > kMaxStride)
