@@ -650,11 +650,12 @@ size_t convrot_cache_attention_workspace(int64_t M, int64_t q_heads, int64_t kv_
  *   t_j = scale * (q H / sqrt(D)) . (s_j c_j)      (the keys' scales and codes)
  *   out = rnd((sum_j softmax(t)_j s'_j c'_j) H / sqrt(D))     (the values')
  * and 0 where there is no such j.  Softmax statistics and sums are fp32.  Rounded to
- * fewer bits are a weight times its value's scale (fp16, 11 bits; for fp16 rows but those
- * of long prompts the sum of two) and the rotated query (15 bits of its row's largest
- * value in one integer product; for long prompts fp16, the sum of two for fp16 rows).
- * For long prompts the cached scales enter as fp16 relative
- * to the largest of 32 tokens: those below 2^-14 of it lose bits.
+ * fewer bits are a weight times its value's scale (fp16, 11 bits; for fp16 rows the sum
+ * of two) and the rotated query (15 bits of its row's largest value in one integer
+ * product; for long prompts fp16, the sum of two for fp16 rows): errors, in norm, of 1.01
+ * times the output's own rounding in bf16 (long prompts 1.03) and 1.03 in fp16 (1.00).
+ * Value scales below 2^-90 lose bits, and rows of bf16 whose rotated values pass 2^100
+ * may give NaN where the formula does not.
  *   q    [M, q_heads, head_dim] in io_dtype, rows q_stride elements apart (at least
  *        q_heads * head_dim, a multiple of 8).
  *   out  [M, q_heads, head_dim] in io_dtype, contiguous; must not overlap q.

@@ -22,9 +22,9 @@
 // only where a weight would pass 2^kRise times the last one, and the sums are
 // then rescaled by an exact power of two.  A weight times its value's scale is
 // rounded to fp16, 11 bits: more than an output of bf16 has; for one of fp16,
-// which has as many, it enters as the sum of two in the kernel for few rows (2.1e-4
-// off, which is the output's own rounding, for 3.0e-4 in one; 1 to 12 % of the time).
-// For long prompts, bound by the products, it stays one: 2.9e-4.
+// which has as many, it enters as the sum of two (2.1e-4 off, which is the output's
+// own rounding, for 2.9e-4 in one; 1 to 12 % of the time where rows are few, 6 % of
+// long prompts of 128 wide heads, 21 % of 64 wide ones).
 //
 // Few rows (attend_few).  The units come from HBM once and bound the kernel, so
 // the codes enter as they lie: scores are int8 products of the codes and of the
@@ -134,6 +134,12 @@ struct Spread {
     asm volatile("" : "+s"(low), "+s"(high));
   }
 };
+
+// a and b without what a pair of fp16 has of them: one instruction each, which takes an fp16 as it lies.
+__device__ inline void take_off(v2h pair, float& a, float& b) {
+  asm("v_fma_mix_f32 %0, %1, -1.0, %0 op_sel_hi:[1,0,0]" : "+v"(a) : "v"(pair));
+  asm("v_fma_mix_f32 %0, %1, -1.0, %0 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "+v"(b) : "v"(pair));
+}
 
 // Eight codes of a word as fp16, in the order of its nibbles 0 4 1 5 2 6 3 7.
 __device__ inline v8h codes_of(uint32_t w, const Spread& c) {
@@ -756,8 +762,8 @@ struct PromptColumns {
 
   // The weights times their values' powers of two.
   __device__ __forceinline__ void weights(const v4f (&s)[NT][2], const float (&f)[NT], const UnitFacts& facts,
-                                          const Levels& levels, v8h (&p)[NT]) {
-    v2h pairs[NT][4];
+                                          const Levels& levels, v8h (&p)[NT][TERMS]) {
+    v2h pairs[NT][TERMS][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int level = level_of(facts, levels, i), counted = level == kNoScale ? 0 : level;
@@ -767,19 +773,29 @@ struct PromptColumns {
         float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x, f[t], static_cast<float>(counted) - m[t]));
         e = x == kHidden ? 0.0f : e;
         l[t] += ldexpf(e, -counted);
-        pairs[t][i & 3][i >> 2] = static_cast<_Float16>(level == kNoScale ? 0.0f : e);
+        float w = level == kNoScale ? 0.0f : e;
+#pragma unroll
+        for (int r = 0; r < TERMS; ++r) {
+          const auto part = static_cast<_Float16>(w);
+          pairs[t][r][i & 3][i >> 2] = part;
+          w -= static_cast<float>(part);
+        }
       }
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) p[t] = __builtin_bit_cast(v8h, pairs[t]);
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < TERMS; ++r) p[t][r] = __builtin_bit_cast(v8h, pairs[t][r]);
   }
 
-  __device__ __forceinline__ void add(const StagedUnit<D>& unit, const v8h (&p)[NT]) {
+  __device__ __forceinline__ void add(const StagedUnit<D>& unit, const v8h (&p)[NT][TERMS]) {
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
       const v8h value = unit.value(d);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[t], o[t][d], 0, 0, 0);
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < TERMS; ++r) o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[t][r], o[t][d], 0, 0, 0);
     }
   }
 
@@ -844,7 +860,7 @@ struct PromptColumns {
         most[t] = __builtin_fmaf(max3(max3(max3(a[0], a[1], a[2]), a[3], b[0]), max3(b[1], b[2], b[3]), b[3]), f[t], level);
       }
       raise(most);
-      v8h p[NT];
+      v8h p[NT][TERMS];
       v4f next[NT][2];
       if (i + 1 < UNITS) scores(group.unit(i + 1), next);
       const float back = __uint_as_float(static_cast<uint32_t>(127 - value) << 23);   // 2^-value
@@ -855,10 +871,16 @@ struct PromptColumns {
 #pragma unroll
         for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][j >> 2][j & 3], f[t], low));
         l[t] = __builtin_fmaf(((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])), back, l[t]);
-        v2h pairs[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pairs[j] = __builtin_convertvector((v2f{e[j], e[j + 4]}), v2h);
-        p[t] = __builtin_bit_cast(v8h, pairs);
+        for (int r = 0; r < TERMS; ++r) {
+          v2h pairs[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            pairs[j] = __builtin_convertvector((v2f{e[j], e[j + 4]}), v2h);
+            if (r + 1 < TERMS) take_off(pairs[j], e[j], e[j + 4]);
+          }
+          p[t][r] = __builtin_bit_cast(v8h, pairs);
+        }
       }
       add(group.unit(i), p);
 #pragma unroll
@@ -879,7 +901,7 @@ struct PromptColumns {
 #pragma unroll
       for (int t = 0; t < NT; ++t) f[t] = qs[t] * facts.key;
       v4f s[NT][2];
-      v8h p[NT];
+      v8h p[NT][TERMS];
       scores(group.unit(i), s);
       if ((facts.flags & kUneven) != 0) {
         levels = levels_of(u0 + i);
