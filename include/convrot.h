@@ -660,9 +660,9 @@ size_t convrot_cache_attention_workspace(int64_t M, int64_t q_heads, int64_t kv_
  *        q_heads * head_dim, a multiple of 8).
  *   out  [M, q_heads, head_dim] in io_dtype, contiguous; must not overlap q.
  *   workspace  at least convrot_cache_attention_workspace bytes: the parts' sums, and
- *        for long prompts, up to head_dim 128, their sequences' keys and values as
- *        16-bit operands (4 head_dim bytes a token and key head, 8 GiB at most; past that
- *        they are read as they lie).  It must not be shared with a call that may run at
+ *        for long prompts of 64 wide heads, and of 128 wide ones in bf16, their sequences'
+ *        keys and values as 16-bit operands (4 head_dim bytes a token and key head, 8 GiB at
+ *        most; past that they are read as they lie).  It must not be shared with a call that may run at
  *        the same time.
  * The work is cut by M, n_seqs, max_pages and the window alone, which a host knows: a
  * table whose columns reach far past the tokens cuts too coarsely and asks for more

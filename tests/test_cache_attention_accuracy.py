@@ -7,7 +7,8 @@ errors, relative and in the mean (a value rounded to p bits is off by 2^-p / 12^
   and so weights off by 6 / 32512 / 12^1/2 1.05 = 5.6e-5; for bf16 rows the weight in one fp16, 2.8e-4 at most;
 - long prompts, bf16: the query in one fp16, 2.8e-4 of scores of 2.1, at most 5.9e-4 (2.1e-4 where its
   mantissas are spread as a normal value's are: 4.4e-4), and the weight, 2.1e-4: 4.9e-4 together;
-- long prompts, fp16: two terms of each, below 1e-6.
+- long prompts, fp16, 64 wide: two terms of each, below 1e-6 (128 and 256 wide fp16 heads, and 256 wide
+  ones of bf16, have the kernel for few rows only).
 Rounding the result costs at least 2^-11 / 12^1/2 = 1.4e-4 in fp16, 2^-8 / 12^1/2 = 1.13e-3 in bf16.
 So the ratios are at most (1 + (5.6 / 14)^2)^1/2 = 1.08, (1 + (2.9 / 11.3)^2)^1/2 = 1.04,
 (1 + (4.9 / 11.3)^2)^1/2 = 1.09 and 1.001.  A weight in one fp16 where two are due gives 1.4."""
@@ -22,11 +23,11 @@ from tests.test_cache_attention import DEV, B, filled, queries, wide_table  # no
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("io,many,most", [("fp16", False, 1.08), ("bf16", False, 1.04), ("bf16", True, 1.09), ("fp16", True, 1.002)])
-@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("D,io,many,most", [
+    (64, "fp16", False, 1.08), (128, "fp16", False, 1.08), (256, "fp16", False, 1.08), (64, "bf16", False, 1.04),
+    (128, "bf16", False, 1.04), (256, "bf16", False, 1.04), (64, "bf16", True, 1.09), (128, "bf16", True, 1.09),
+    (256, "bf16", True, 1.04), (64, "fp16", True, 1.002), (128, "fp16", True, 1.08), (256, "fp16", True, 1.08)])
 def test_error_beside_the_roundings(B, D, io, many, most):  # noqa: F811
-    if many and D == 256:
-        pytest.skip("256 wide heads have one kernel")
     dt = torch.bfloat16 if io == "bf16" else torch.float16
     H, G, page = 2, 4, 64
     lens = [(700, 300)] if many else [(900 + i, 1 + i % 3) for i in range(16)]

@@ -1417,9 +1417,11 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a, int few
 }
 
 // Which widths have the way by operands.  256 wide heads are better off without: there are
-// no registers for more than a column tile a wave (a prompt of 4608, 16 heads on 4: 346 us,
-// 316 by the kernel for few; fp16, 8 heads: 4440 and 2107).
-constexpr bool by_operands(int head_dim) { return head_dim != 256; }
+// no registers for more than a column tile a wave (a prompt of 4608, 16 heads on 4, bf16: 346
+// us, 316 by the kernel for few).  So are 128 wide ones of fp16, whose two terms of queries and
+// weights spill (32 heads on 8: 2000 rows behind 8000 tokens 217 us, 151 by the other; 8000 alone
+// 135 and 88, behind 8000 651 and 518; four of 2400 to 1500 behind 7000 490 and 297).
+constexpr bool by_operands(int head_dim, bool f16) { return head_dim == 64 || (head_dim == 128 && !f16); }
 // Rows (tokens times query heads a key head) above which a sequence goes that way, which
 // pays where many rows read the same keys.  One sequence: by what its tiles read in all (32
 // heads of 128 on 8: 1000 rows behind 16000 tokens 112 us, 120 by the other; 4000 alone 62
@@ -1457,7 +1459,7 @@ constexpr int kWideTiles = 2;
 // half the columns for as many bytes and are held back by the fetches of the units, which
 // eight waves share (four pieces behind 7000 tokens 354 us against 389, a prompt of 4608 as
 // fast).
-constexpr int wide_waves(int head_dim, bool f16) { return head_dim == 128 && !f16 ? 8 : 4; }
+constexpr int wide_waves(int head_dim) { return head_dim == 128 ? 8 : 4; }
 constexpr int kWidest = 8;              // waves a CU
 constexpr int64_t kMostOperands = int64_t{8} << 30;             // bytes
 constexpr int64_t kMostSlots = 65535;   // the third side of a grid
@@ -1490,8 +1492,8 @@ hipError_t launch_heads(const Attention& a, hipStream_t stream) {
                         : launch_tiles(attend_few<D, 2, In>, a, 32, kAttnWaves, 0, many, stream);
   }
   int many_tile = tile;
-  if constexpr (by_operands(D)) {
-    constexpr int kWaves = wide_waves(D, kF16);
+  if constexpr (by_operands(D, kF16)) {
+    constexpr int kWaves = wide_waves(D);
     many_tile = 16 * kWideTiles * kWaves;
     if (a.slots > 0 && e == hipSuccess) {
       const int64_t units = (a.cache.max_tokens + kUnit - 1) / kUnit;
@@ -1532,7 +1534,7 @@ AttentionPlan plan_cache_attention(int64_t M, int64_t q_heads, int64_t kv_heads,
   p.slot_units = (max_tokens + kUnit - 1) / kUnit + 4;          // and spare ones
   p.slots = n_seqs == 1 ? (rows > limit ? 1 : 0) : std::min(n_seqs, rows / (int64_t{1} + limit));
   // all of them or none: what has no slot there would have no kernel
-  if (!by_operands(head_dim) || p.slots > kMostSlots || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_)
+  if (!by_operands(head_dim, f16) || p.slots > kMostSlots || p.slots * kv_heads * p.slot_units > kMostOperands / unit_bytes_)
     p.slots = 0;
   const size_t operands = static_cast<size_t>(p.slots) * kv_heads * p.slot_units * unit_bytes_;
   const bool wide = p.slots > 0;
