@@ -652,18 +652,19 @@ size_t convrot_cache_attention_workspace(int64_t M, int64_t q_heads, int64_t kv_
  * and 0 where there is no such j.  Softmax statistics and sums are fp32.  Rounded to
  * fewer bits are a weight times its value's scale (fp16, 11 bits; for fp16 rows the sum
  * of two) and the rotated query (15 bits of its row's largest value in one integer
- * product; for long prompts fp16, the sum of two for fp16 rows): errors, in norm, of 1.01
- * times the output's own rounding in bf16 (long prompts 1.03) and 1.03 in fp16 (1.00).
- * Value scales below 2^-90 lose bits, and rows of bf16 whose rotated values pass 2^100
- * may give NaN where the formula does not.
+ * product; for long prompts of 64 wide heads, and of 128 wide ones in bf16, fp16, the sum
+ * of two for fp16 rows): errors, in norm, of 1.01 times the output's own rounding in bf16
+ * (such prompts 1.03) and 1.03 in fp16 (1.00), for ordinary rows.  Value scales below
+ * 2^-90 lose bits, and bf16 rows whose rotated values pass 2^100 may give NaN where the
+ * formula does not.
  *   q    [M, q_heads, head_dim] in io_dtype, rows q_stride elements apart (at least
  *        q_heads * head_dim, a multiple of 8).
  *   out  [M, q_heads, head_dim] in io_dtype, contiguous; must not overlap q.
  *   workspace  at least convrot_cache_attention_workspace bytes: the parts' sums, and
- *        for long prompts of 64 wide heads, and of 128 wide ones in bf16, their sequences'
- *        keys and values as 16-bit operands (4 head_dim bytes a token and key head, 8 GiB at
- *        most; past that they are read as they lie).  It must not be shared with a call that may run at
- *        the same time.
+ *        for such prompts their sequences' keys and values as 16-bit operands (4 head_dim
+ *        bytes a token and key head, 8 GiB and 65535 prompts at most; past that they are
+ *        read as they lie).  It must not be shared with a call that may run at the same
+ *        time.
  * The work is cut by M, n_seqs, max_pages and the window alone, which a host knows: a
  * table whose columns reach far past the tokens cuts too coarsely and asks for more
  * workspace than is used, so give the columns that are used (max_pages, with the table's

@@ -23,8 +23,10 @@
 // then rescaled by an exact power of two.  A weight times its value's scale is
 // rounded to fp16, 11 bits: more than an output of bf16 has; for one of fp16,
 // which has as many, it enters as the sum of two (2.1e-4 off, which is the output's
-// own rounding, for 2.9e-4 in one; 1 to 12 % of the time where rows are few, 6 % of
-// long prompts of 128 wide heads, 21 % of 64 wide ones).
+// own rounding, for 2.9e-4 in one; 1 to 12 % of the time where rows are few, 21 % of
+// long prompts).  Where one reference is taken for eight keys, or a unit, it is of
+// the largest t and the largest vs of them: six powers of two above the largest
+// weight at most, for where scales lie further apart keys go one by one.
 //
 // Few rows (attend_few).  The units come from HBM once and bound the kernel, so
 // the codes enter as they lie: scores are int8 products of the codes and of the
@@ -37,23 +39,23 @@
 // its loads one unit ahead, and join their sums in LDS; long sequences are cut
 // into parts, joined by a launch of their own.  64 tokens of 64 sequences of up
 // to 8192, 32 heads of 128 on 8: 70 us, 4.0 TB/s (5 of it the join); 4 of up to
-// 131000, 64 heads on 8: 104 us, 3.3 TB/s (7 the join; vector unit 36 %, matrix unit
-// 9 % busy: what is missing is bytes on their way, a unit a wave, 12 waves a CU, with
-// no registers for two); 1 of 1000: 10.8 us, latencies one behind the other: table,
+// 131000, 64 heads on 8: 106 us, 3.3 TB/s (8 the join; vector unit 38 %, matrix unit
+// 9 % busy: what is missing is bytes on their way, a unit a wave, 12 waves a CU, and
+// parts of even length); 1 of 1000: 11.0 us, latencies one behind the other: table,
 // unit, products, the waves' sums.
 //
 // Many rows (make_operands, attend_many).  A unit then serves hundreds of columns
 // and the products and exponentials bound the kernel.  Turning codes into operands
-// and scaling scores in every tile cost as much as the products (240 us where it is
-// 231 now), so one launch before writes keys and values as fp16 operands with
+// and scaling scores in every tile cost as much as the products (240 us where 231
+// were reached), so one launch before writes keys and values as fp16 operands with
 // their scales in them, and the tiles fetch those straight into LDS, two groups of
 // units in turn, one worked on while the next is on its way.  A query of bf16 enters
 // as one fp16, 11 bits for an output of 8; one of fp16 as the sum of two.  The scores
 // of the next unit are started beside the exponentials of this one.  A causal
-// prompt of 4608, 32 heads of 128 on 8: 231 us, 753 TFLOP/s counting visible keys
+// prompt of 4608, 32 heads of 128 on 8: 239 us, 727 TFLOP/s counting visible keys
 // (9 of it for the operands); three pieces of 667 to 1001 behind up to 16000, 24
-// heads of 64, fp16, two terms: 359 us, 505 TFLOP/s (44 for the operands, which is
-// their bytes at 6 TB/s).  Matrix and vector unit are busy 31 and 46 %, 35 and 52 %:
+// heads of 64, fp16, two terms: 454 us, 400 TFLOP/s (45 for the operands, which is
+// their bytes at 6 TB/s).  Matrix and vector unit are busy 30 and 45 %, 38 and 52 %:
 // a wave's products and exponentials follow each other, and two waves a SIMD, all
 // that the registers hold, cover little of that for each other.
 #include <algorithm>
@@ -949,7 +951,7 @@ struct Operands {
 };
 
 // One unit a wave: what it reads comes once, and what it writes bounds it (24 heads of 64,
-// 34000 tokens: 44 us, 6.1 TB/s).
+// 34000 tokens: 45 us, 5.9 TB/s).
 template <int D>
 __global__ __launch_bounds__(kAttnThreads) void make_operands(Attention a, int few) {
   using O = Operands<D>;
@@ -1344,8 +1346,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_many(Attention a, int fe
 
 // The parts of a row joined, a wave a row: first every part's reference and sum, a
 // part a lane, then four parts at a time by 16 lanes each.  Parts whose keys the row
-// does not see at all may not have been written, and are not read.  64 rows of 32 heads in
-// two parts: 4.9 us, a launch's length; 4 of 64 in 32 parts: 6.9.
+// does not see hold nothing of it and are not read.  64 rows of 32 heads in three parts:
+// 4.8 us, a launch's length; 4 of 64 in 43 parts: 8.0.
 template <int D, typename In>
 __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a, int few_rows, int many, int many_rows) {
   constexpr int E = D / 16;
@@ -1424,12 +1426,12 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(Attention a, int few
 constexpr bool by_operands(int head_dim, bool f16) { return head_dim == 64 || (head_dim == 128 && !f16); }
 // Rows (tokens times query heads a key head) above which a sequence goes that way, which
 // pays where many rows read the same keys.  One sequence: by what its tiles read in all (32
-// heads of 128 on 8: 1000 rows behind 16000 tokens 112 us, 120 by the other; 4000 alone 62
-// and 30, behind 8000 191 and 239).  Of more only the mean is known here, and the two kernels
+// heads of 128 on 8, bf16: 1000 rows behind 16000 tokens 111 us, 123 by the other; 4000 alone
+// 62 and 31, behind 8000 198 and 246).  Of more only the mean is known here, and the two kernels
 // run one after the other, so that a batch should go by one of them: by this one if the
-// mean is long and the tiles are more than the CUs, as their lengths differ (24 heads of 64:
-// 1001, 834 and 667 rows, 288 tiles, 362 us, 387 by the other, 496 by both; 8 heads of 128:
-// four of 4000 to 2500 rows, 440 tiles, 77 and 85, of 2400 to 1500, 280 tiles, 298 and 278, of
+// mean is long and the tiles are more than the CUs, as their lengths differ (24 heads of 64,
+// fp16: 1001, 834 and 667 rows, 288 tiles, 450 us, 519 by the other; 32 heads of 128 on 8, bf16:
+// four of 4000 to 2500 rows, 440 tiles, 81 and 87, of 2400 to 1500, 280 tiles, 276 and 255, of
 // 1000 to 625, 128 tiles, 325 and 248), else by the other but for prompts that are much
 // longer than the rest.
 constexpr int kNever = 0x7fffffff;
@@ -1449,16 +1451,15 @@ constexpr int few_tile(int head_dim, bool f16, int64_t mean) {
   return small_tiles(head_dim, f16) || mean <= (head_dim == 64 ? 32 : 16) ? 16 : 32;
 }
 // Column tiles of a wave of the kernel for many rows: two are what its registers hold of
-// 128 wide heads (256 and 40 bytes of scratch), and of 64 wide ones four spill (685 us
-// where two take 359).
+// 128 wide heads (256, and 28 bytes of scratch beside the loop), and of 64 wide ones four
+// spilled (685 us where two took 359).
 constexpr int kWideTiles = 2;
 // A workgroup of four waves has 64 KB of LDS at D = 64 and a CU two of them, out of step:
-// better where tiles are uneven and a wave's work on a unit is long (361 us against 435 with
-// eight for three pieces behind 16000 tokens, 143 against 164 for a prompt of 4608; 128 wide
-// heads with fp16 queries in two terms 282 against 320).  128 wide heads with one term have
-// half the columns for as many bytes and are held back by the fetches of the units, which
-// eight waves share (four pieces behind 7000 tokens 354 us against 389, a prompt of 4608 as
-// fast).
+// better where tiles are uneven and a wave's work on a unit is long (440 us against 514 with
+// eight for three pieces behind 16000 tokens, 188 against 215 for a prompt of 4608, 143 against
+// 168 in bf16).  128 wide heads have half the columns for as many bytes and are held back by the
+// fetches of the units, which eight waves share (four pieces of 1000 tokens behind 8000 400 us
+// against 436, of 600 behind 7000 277 against 249, a prompt of 4608 as fast).
 constexpr int wide_waves(int head_dim) { return head_dim == 128 ? 8 : 4; }
 constexpr int kWidest = 8;              // waves a CU
 constexpr int64_t kMostOperands = int64_t{8} << 30;             // bytes

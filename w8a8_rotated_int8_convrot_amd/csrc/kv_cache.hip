@@ -7,9 +7,10 @@
 // The rotation is the layer's own, with the head as its group: it spreads a
 // head's few large dims over all of them, and it is never taken back where the
 // attention reads, since (q H) . (k H) = D q . k.  The codes are taken in 64 bits:
-// the sums of 16-bit values are then exact, so that a code depends on nothing
-// but its row, and this card's 64-bit multiply-adds run at the rate of its 32-bit
-// ones.  A row that holds infinities or NaN gets the scale NaN.
+// the sums of 16-bit values are then exact (of bf16 where a row's values lie within
+// 2^37 of each other, else to 2^-53 of the largest), so that a code depends on
+// nothing but its row, and this card's 64-bit multiply-adds run at the rate of its
+// 32-bit ones.  A row that holds infinities or NaN gets the scale NaN.
 //
 // Eight tokens at multiples of eight share the words of their value codes, so
 // they are one wave's work: eight lanes a token, D / 8 dims a lane.  The wave that
@@ -18,8 +19,8 @@
 //
 // Bound by the vector unit where there are many tokens: six to eight stages of
 // 64-bit sums, three of them across lanes, then scale, code and check, some 37
-// instructions a value (10246 tokens of 16 heads of 64: append 26.5 us, 2.0 TB/s,
-// vector unit 64 % busy; read, without the check, 17.0, 3.2 TB/s, 54 %).  A
+// instructions a value (10246 tokens of 16 heads of 64: append 26.4 us, 2.0 TB/s,
+// vector unit 63 % busy; read, without the check, 17.2, 3.1 TB/s, 55 %).  A
 // division instead of the reciprocal: 38.  Several heads a wave, with the octet
 // found once: no faster (26), for more registers.  64 tokens of 8 heads: 6.1 and
 // 4.9 us, a launch and a chain of latencies (offsets, table, rows).
